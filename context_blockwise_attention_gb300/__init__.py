@@ -22,6 +22,14 @@ from .api import (  # noqa: F401
     NOALLOC_AUX_MAX_FLOATS,
     bwd_aux_floats,
     ulysses_reshard,
+    KV_MAX_SEQS,
+    KvCache,
+    kv_cache_empty,
+    kv_cache_write,
+    kv_cache_read,
+    kv_cache_attn,
+    kv_cache_attn_workspace,
+    rope_axes,
     library_path,
     load_library,
     version,
@@ -43,6 +51,14 @@ __all__ = [
     "NOALLOC_AUX_MAX_FLOATS",
     "bwd_aux_floats",
     "ulysses_reshard",
+    "KV_MAX_SEQS",
+    "KvCache",
+    "kv_cache_empty",
+    "kv_cache_write",
+    "kv_cache_read",
+    "kv_cache_attn",
+    "kv_cache_attn_workspace",
+    "rope_axes",
     "library_path",
     "load_library",
     "version",

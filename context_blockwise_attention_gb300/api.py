@@ -6,8 +6,10 @@ message.  The library must be built (``__graft_entry__.build()``); there is no f
 """
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -74,6 +76,27 @@ class _KvChunk(ctypes.Structure):
                 ("kv_pos", _PosMap)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int64)]
+
+
+class _KvAttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("cache", _KvCache), ("rows", _KvRows), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("q_first", ctypes.c_void_p), ("in_dtype", ctypes.c_int32),
+        ("o_dtype", ctypes.c_int32), ("hq", ctypes.c_int32), ("scale", ctypes.c_float), ("kv_pos", _PosMap),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p),
+        ("wait_timeout_ms", ctypes.c_int32), ("flags", ctypes.c_int32),
+    ]
+
+
 @dataclass(frozen=True)
 class PosMap:
     """Affine global positions of a shard or chunk: pos(i) = base + stride * i."""
@@ -125,6 +148,17 @@ def load_library():
     lib.cp_ulysses_reshard.restype = i32
     lib.cp_ulysses_reshard.argtypes = [i32, i32, i64, i32, ctypes.POINTER(i32), i32, i32, i32,
                                        ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
+    lib.cp_kv_cache_write.restype = i32
+    lib.cp_kv_cache_write.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvRows), vp, vp, i32, vp, vp]
+    lib.cp_kv_cache_read.restype = i32
+    lib.cp_kv_cache_read.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvRows), vp, vp, i32, vp, vp]
+    lib.cp_kv_cache_attn.restype = i32
+    lib.cp_kv_cache_attn.argtypes = [ctypes.POINTER(_KvAttnDesc), vp]
+    lib.cp_kv_cache_attn_workspace.restype = i32
+    lib.cp_kv_cache_attn_workspace.argtypes = [ctypes.POINTER(_KvAttnDesc), ctypes.POINTER(i64)]
+    lib.cp_rope_axes.restype = i32
+    lib.cp_rope_axes.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i32), i64, i32, i32,
+                                 i32, vp, i32, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double), i32, i32, vp]
     _lib = lib
     return lib
 
@@ -546,3 +580,279 @@ def ulysses_reshard(direction, tensors, cp, seq_len, layout="contiguous", out=No
     _check(lib.cp_ulysses_reshard(dirc, cp, seq_len, nt, arr_h, d, _dtype_code(dtype),
                                   _LAYOUTS[layout], arr_in, arr_out, _stream(stream)))
     return outs
+
+
+# ---------------------------------------------------------------- 8-bit KV cache
+# Largest number of sequences one call takes (``CP_KV_MAX_SEQS``).
+KV_MAX_SEQS = 4096
+
+
+class KvCache(NamedTuple):
+    """A paged 8-bit cache: ``k``, ``v`` float8_e4m3fn [pages, Hkv, page_size, D] and their
+    power-of-two scales ``k_scale``, ``v_scale`` fp32 [pages, Hkv]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache_empty(n_pages, page_size, hkv, d, device=None):
+    """Memory for a cache of ``n_pages`` pages; what it holds is undefined until it is written."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    shape = (n_pages, hkv, page_size, d)
+    return KvCache(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
+                   *(torch.empty((n_pages, hkv), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _invalid(message):
+    raise CpError(CP_ERR_INVALID_ARG, message)
+
+
+def _need(t, name, dtype, device):
+    """A contiguous CUDA tensor of ``dtype`` on ``device``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _invalid(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        _invalid(f"{name} must be contiguous")
+    if t.dtype != dtype:
+        _invalid(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        _invalid(f"{name} is on {t.device}, not on {device}")
+
+
+class _on_device:
+    """Makes ``device`` current for a call whose tensors live there."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _new(shape, dtype, device, stream):
+    """Memory that belongs to the stream the call runs on: when it is released, the allocator
+    gives it to later work of that stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cache_struct(cache):
+    k, v, k_scale, v_scale = cache
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        _invalid("cache.k must be a CUDA tensor")
+    dev = k.device
+    _need(k, "cache.k", torch.float8_e4m3fn, dev)
+    _need(v, "cache.v", torch.float8_e4m3fn, dev)
+    _need(k_scale, "cache.k_scale", torch.float32, dev)
+    _need(v_scale, "cache.v_scale", torch.float32, dev)
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
+        _invalid("cache.k and cache.v must be [pages, Hkv, page_size, D]")
+    n_pages, hkv, page_size, d = shape
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        _invalid("cache.k_scale and cache.v_scale must be [pages, Hkv]")
+    return _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page_size, hkv, d, 0)
+
+
+def _rows_struct(row_start, tokens, name, page_table, n_rows, device):
+    _need(row_start, "row_start", torch.int32, device)
+    _need(tokens, name, torch.int32, device)
+    _need(page_table, "page_table", torch.int32, device)
+    if row_start.dim() != 1 or tokens.dim() != 1 or page_table.dim() != 2:
+        _invalid(f"row_start must be [seqs + 1], {name} [seqs], page_table [seqs, pages]")
+    n_seqs, max_pages = page_table.shape
+    if row_start.shape[0] != n_seqs + 1 or tokens.shape[0] != n_seqs:
+        _invalid(f"row_start must be [seqs + 1], {name} [seqs], page_table [seqs, pages]")
+    return _KvRows(row_start.data_ptr(), tokens.data_ptr(), page_table.data_ptr(), n_seqs, max_pages, n_rows)
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    _need(status, "status", torch.int32, device)
+    if status.numel() < 1:
+        _invalid("status must hold one int32")
+    return status.data_ptr()
+
+
+def kv_cache_write(cache, k, v, row_start, cached, page_table, status=None, stream=None):
+    """Quantises new tokens into ``cache``: rows ``row_start[b] .. row_start[b + 1]`` of ``k``, ``v``
+    [rows, Hkv, D] become the tokens ``cached[b], cached[b] + 1, ...`` of sequence b, whose page of
+    tokens ``i * page_size ..`` is ``page_table[b, i]``.  ``row_start`` [seqs + 1], ``cached`` [seqs]
+    and ``page_table`` [seqs, pages] are int32 CUDA tensors.  Returns ``cache``."""
+    lib = load_library()
+    c = _cache_struct(cache)
+    dev = cache.k.device
+    dt = k.dtype if isinstance(k, torch.Tensor) else None
+    code = _dtype_code(dt)
+    _need(k, "k", dt, dev)
+    _need(v, "v", dt, dev)
+    if k.dim() != 3 or v.shape != k.shape or k.shape[1] != c.hkv or k.shape[2] != c.d:
+        _invalid("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
+    r = _rows_struct(row_start, cached, "cached", page_table, k.shape[0], dev)
+    with _on_device(dev):
+        _check(lib.cp_kv_cache_write(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), code,
+                                     _status_ptr(status, dev), _stream(stream)))
+    return cache
+
+
+def kv_cache_read(cache, row_start, first, page_table, n_rows, dtype=torch.bfloat16, k=None, v=None, status=None,
+                  stream=None):
+    """Reads tokens back: rows ``row_start[b] .. row_start[b + 1]`` of the returned ``k``, ``v``
+    [n_rows, Hkv, D] hold the tokens ``first[b], first[b] + 1, ...`` of sequence b.  Rows of no
+    sequence are left as they were (undefined where this call allocates them)."""
+    lib = load_library()
+    c = _cache_struct(cache)
+    dev = cache.k.device
+    if k is not None and isinstance(k, torch.Tensor):
+        dtype = k.dtype
+    code = _dtype_code(dtype)
+    shape = (int(n_rows), c.hkv, c.d)
+    r = _rows_struct(row_start, first, "first", page_table, int(n_rows), dev)
+    with _on_device(dev):
+        if k is None:
+            k = _new(shape, dtype, dev, stream)
+        if v is None:
+            v = _new(shape, dtype, dev, stream)
+        _need(k, "k", dtype, dev)
+        _need(v, "v", dtype, dev)
+        if tuple(k.shape) != shape or tuple(v.shape) != shape:
+            _invalid("k and v must be [n_rows, Hkv, D] with the cache's Hkv and D")
+        _check(lib.cp_kv_cache_read(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), code,
+                                    _status_ptr(status, dev), _stream(stream)))
+    return k, v
+
+
+def kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos=PosMap(0, 1), scale=0.0, o=None,
+                  lse=None, o_dtype=None, workspace=None, flags=0, status=None, wait_timeout_ms=0, stream=None):
+    """(O, LSE) partial of each sequence's new rows ``q`` [rows, Hq, D] over its ``kv_lens[b]`` cached
+    tokens (write the new tokens first if they are to be seen).
+
+    ``q_first`` (int32 [seqs]) makes it causal: row i of sequence b stands at position
+    ``q_first[b] + i`` and sees cached token j iff ``kv_pos.base + kv_pos.stride * j`` is not behind
+    it; without it every cached token is seen.  Rows that see nothing get O = 0, LSE = -inf; rows of
+    no sequence are left as they were.  ``workspace`` (uint8) may be given by callers that must not
+    allocate; it needs ``kv_cache_attn_workspace(...)`` bytes and belongs to one call at a time.
+    """
+    lib = load_library()
+    c = _cache_struct(cache)
+    dev = cache.k.device
+    dt = q.dtype if isinstance(q, torch.Tensor) else None
+    desc = _KvAttnDesc()
+    desc.in_dtype = _dtype_code(dt)
+    _need(q, "q", dt, dev)
+    if q.dim() != 3 or q.shape[2] != c.d:
+        _invalid("q must be [rows, Hq, D] with the cache's D")
+    rows, hq, d = q.shape
+    desc.cache = c
+    desc.rows = _rows_struct(row_start, kv_lens, "kv_lens", page_table, rows, dev)
+    if q_first is not None:
+        _need(q_first, "q_first", torch.int32, dev)
+        if q_first.dim() != 1 or q_first.shape[0] != kv_lens.shape[0]:
+            _invalid("q_first must be [seqs]")
+        desc.q_first = q_first.data_ptr()
+    desc.hq = hq
+    desc.scale = float(scale)
+    desc.kv_pos = _PosMap(kv_pos.base, kv_pos.stride)
+    desc.status = _status_ptr(status, dev)
+    desc.wait_timeout_ms = int(wait_timeout_ms)
+    desc.flags = int(flags)
+    with _on_device(dev):
+        if o is None:
+            o = _new((rows, hq, d), o_dtype or torch.float32, dev, stream)
+        else:
+            _need(o, "o", o.dtype if isinstance(o, torch.Tensor) else None, dev)
+        if lse is None:
+            lse = _new((rows, hq), torch.float32, dev, stream)
+        else:
+            _need(lse, "lse", torch.float32, dev)
+        if o.shape != q.shape or lse.shape != q.shape[:2]:
+            _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
+        desc.q, desc.o, desc.lse = q.data_ptr(), o.data_ptr(), lse.data_ptr()
+        desc.o_dtype = _dtype_code(o.dtype)
+        if workspace is None:
+            need = ctypes.c_int64(0)
+            _check(lib.cp_kv_cache_attn_workspace(ctypes.byref(desc), ctypes.byref(need)))
+            workspace = _new((need.value,), torch.uint8, dev, stream)
+        else:
+            _need(workspace, "workspace", torch.uint8, dev)
+        desc.workspace, desc.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        _check(lib.cp_kv_cache_attn(ctypes.byref(desc), _stream(stream)))
+    return o, lse
+
+
+def kv_cache_attn_workspace(cache, rows, hq, n_seqs, max_pages, dtype=torch.bfloat16, o_dtype=torch.float32):
+    """Bytes of workspace that ``kv_cache_attn`` needs for ``rows`` rows of ``hq`` heads over
+    ``n_seqs`` sequences with ``max_pages`` table entries each."""
+    desc = _KvAttnDesc()
+    desc.cache = _cache_struct(cache)
+    some = desc.cache.k  # the contents of the arrays do not matter here
+    desc.rows = _KvRows(some, some, some, int(n_seqs), int(max_pages), int(rows))
+    desc.in_dtype, desc.o_dtype, desc.hq = _dtype_code(dtype), _dtype_code(o_dtype), int(hq)
+    need = ctypes.c_int64(0)
+    with _on_device(cache.k.device):
+        _check(load_library().cp_kv_cache_attn_workspace(ctypes.byref(desc), ctypes.byref(need)))
+    return need.value
+
+
+# ---------------------------------------------------------------- rotary positions
+@functools.lru_cache(maxsize=64)
+def _rope_tables(inv_freq, sections):
+    return (ctypes.c_double * len(inv_freq))(*inv_freq), (ctypes.c_int32 * len(sections))(*sections)
+
+
+def rope_axes(xs, positions, inv_freq, sections=None, interleaved=False, inverse=False, out=None, stream=None):
+    """Rotary positions on the tensors ``xs`` (a list of up to four, each [tokens, H_t, D]), one launch.
+
+    ``positions``: int32 CUDA tensor [axes, tokens] (or [tokens] for one axis), global positions;
+    ``inv_freq``: rot/2 numbers (a tuple is fastest), ``rot`` <= D being the part of a head that is
+    turned; ``sections``: how many of the rot/2 pairs belong to each axis, in order.  Pairs are
+    (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  ``inverse`` turns back, which is also the
+    gradient.  ``out`` may be ``xs`` itself.  Returns the list of outputs.
+    """
+    lib = load_library()
+    n = len(xs)
+    if not 1 <= n <= 4:
+        _invalid("between 1 and 4 tensors")
+    x0 = xs[0]
+    if not isinstance(x0, torch.Tensor) or not x0.is_cuda:
+        _invalid("every tensor must be a CUDA tensor")
+    dev, dt = x0.device, x0.dtype
+    code = _dtype_code(dt)
+    if isinstance(inv_freq, torch.Tensor):
+        inv_freq = inv_freq.tolist()
+    inv_freq = tuple(inv_freq)
+    sections = (len(inv_freq),) if sections is None else tuple(sections)
+    _need(positions, "positions", torch.int32, dev)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if x0.dim() != 3 or positions.dim() not in (1, 2) or positions.shape[-1] != x0.shape[0] or axes != len(sections):
+        _invalid("tensors must be [tokens, H, D], positions [axes, tokens], sections one number for each axis")
+    tokens, _, d = x0.shape
+    with _on_device(dev):
+        if out is None:
+            out = [_new(x.shape, dt, dev, stream) for x in xs]
+        elif len(out) != n:
+            _invalid("one output for each tensor")
+        ins, outs, heads = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)(), (ctypes.c_int32 * n)()
+        for t in range(n):
+            x, y = xs[t], out[t]
+            _need(x, "x", dt, dev)
+            _need(y, "out", dt, dev)
+            if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != d or y.shape != x.shape:
+                _invalid("every tensor and its output must be [tokens, H, D] with the same tokens and D")
+            ins[t], outs[t], heads[t] = x.data_ptr(), y.data_ptr(), x.shape[1]
+        freq, cuts = _rope_tables(inv_freq, sections)
+        _check(lib.cp_rope_axes(n, ins, outs, heads, tokens, d, 2 * len(inv_freq), code, positions.data_ptr(), axes,
+                                cuts, freq, int(bool(interleaved)), int(bool(inverse)), _stream(stream)))
+    return list(out)

@@ -72,4 +72,28 @@ struct ReshardArgs {
 };
 cp_status launch_reshard(const ReshardArgs& a, int num_sms, cudaStream_t s);
 
+// 8-bit cache (n_rows and n_seqs > 0).
+cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
+                          int32_t* status, cudaStream_t s);
+cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,
+                         cudaStream_t s);
+int64_t kv_attn_workspace(const cp_kv_attn_desc& d, int num_sms);
+cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s);
+
+struct RopeArgs {
+  int32_t n_tensors;
+  const void* const* in;
+  void* const* out;
+  const int32_t* heads;
+  int64_t tokens;
+  int32_t d, rot;
+  bool bf16;
+  const int32_t* positions;
+  int32_t n_axes;
+  const int32_t* sections;
+  int32_t interleaved, inverse;
+  uint64_t turn[128];  // fraction of a turn per position, in units of 2^-64
+};
+cp_status launch_rope(const RopeArgs& a, cudaStream_t s);
+
 }  // namespace cpattn

@@ -388,6 +388,166 @@ cp_status cp_partial_attn_bwd_chunks(const cp_attn_bwd_desc* desc, int32_t n_chu
 cp_status cp_partial_attn_bwd_noalloc(const cp_attn_bwd_desc* desc, const void* o, int32_t o_dtype,
                                       const float* lse, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------- 8-bit KV cache
+ * A rank that serves keeps the keys and values of its share of every sequence in pages of 8-bit
+ * values.  The pages cited above only name the cache ([PCP/DCP] sections 2.1, 3.2); the format is
+ * this library's own:
+ *   values  e4m3 bytes [n_pages, hkv, page_size, d]: one page and head is one contiguous tile
+ *   scales  fp32 [n_pages, hkv], separate for K and V; the cached number is byte * scale.  Every
+ *           scale is a power of two, 2^e with e the smallest integer >= -64 for which the largest
+ *           finite magnitude of the page and head is <= 448 * 2^e.  A power of two costs e4m3 no
+ *           precision, makes byte * scale exact in bf16, and makes a later change of the scale
+ *           exact too, but for values that become subnormal.
+ * Token j of sequence b lives in page page_table[b][j / page_size], slot j % page_size.
+ */
+typedef struct {
+  void* k;        /* device e4m3 [n_pages, hkv, page_size, d], 16-byte aligned */
+  void* v;
+  float* k_scale; /* device fp32 [n_pages, hkv] */
+  float* v_scale;
+  int64_t n_pages;
+  int32_t page_size; /* 16, 32, 64 or 128 */
+  int32_t hkv;
+  int32_t d; /* 64 or 128 */
+  int32_t reserved;
+} cp_kv_cache;
+
+/* Largest number of sequences one call takes. */
+#define CP_KV_MAX_SEQS 4096
+
+/*
+ * The rows of a call: n_rows packed token rows, those of sequence b being
+ * [row_start[b], row_start[b+1]); rows behind row_start[n_seqs] are neither read nor written.
+ * All arrays are device memory, read by the kernels only, so that a captured graph can be
+ * replayed with other contents.
+ *   row_start   int32 [n_seqs + 1], non-decreasing, values in [0, n_rows]
+ *   tokens      int32 [n_seqs], >= 0; its meaning is given at each call
+ *   page_table  int32 [n_seqs, max_pages]; entries that hold no token of the call are not read
+ * Contents that break these rules are not followed out of bounds: the kernels clamp row_start,
+ * skip the entries of a sequence that need a page outside [0, n_pages) or behind max_pages (the
+ * attention answers NaN for the rows that see such a page), and record
+ * CP_ERR_INVALID_ARG | (site << 8) in *status where a status word is given.
+ */
+typedef struct {
+  const int32_t* row_start;
+  const int32_t* tokens;
+  const int32_t* page_table;
+  int32_t n_seqs;    /* 0 <= n_seqs <= CP_KV_MAX_SEQS */
+  int32_t max_pages; /* >= 1 where n_seqs > 0 */
+  int64_t n_rows;    /* >= 0, below 2^31 */
+} cp_kv_rows;
+
+/*
+ * cp_kv_cache_write -- quantises new tokens into the cache.  rows->tokens[b] is the number of
+ * tokens that sequence b already has: its rows become the tokens tokens[b], tokens[b] + 1, ...
+ * A page that is entered at slot 0 takes the scale of what this call writes into it.  A page that
+ * is continued at slot s > 0 takes the larger of its scale and the new tokens' scale; where it
+ * grows, the slots before s are rounded once more, e4m3(value * old / new).  Slots behind the
+ * written ones belong to no token; their bytes stay as they were.  Writing the same tokens to the
+ * same places again changes nothing.  Rounding is to nearest even; infinities become +-448 *
+ * scale, NaN stays NaN, and neither counts for the scale.  Numbers above 1.9375 * 2^127 read back
+ * as infinity.
+ * Two sequences of one call, or two overlapping calls, must not write the same page.
+ * Arguments: k, v device [n_rows, hkv, d] (in_dtype CP_F32 or CP_BF16), 16-byte aligned; status
+ * device int32 or NULL (see cp_kv_rows; the caller zeroes it).
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.
+ */
+cp_status cp_kv_cache_write(const cp_kv_cache* cache, const cp_kv_rows* rows, const void* k, const void* v,
+                            int32_t in_dtype, int32_t* status, cudaStream_t stream);
+
+/*
+ * cp_kv_cache_read -- the way back: rows [row_start[b], row_start[b+1]) receive the tokens
+ * rows->tokens[b], tokens[b] + 1, ... of sequence b as k, v device [n_rows, hkv, d] (out_dtype
+ * CP_F32 or CP_BF16; exact but for bf16's range).  The rows of one sequence are then a KV chunk
+ * for cp_partial_attn: this is the way a long prompt attends to a cached prefix.
+ * Rows whose page is bad (see cp_kv_rows) are left as they were.
+ * Errors: as cp_kv_cache_write.
+ */
+cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, void* k, void* v, int32_t out_dtype,
+                           int32_t* status, cudaStream_t stream);
+
+/*
+ * cp_kv_cache_attn -- attention of each sequence's new tokens over its cached ones (decoding: one
+ * row per sequence, or a few drafted tokens), as an (O, LSE) partial exactly like
+ * cp_partial_attn's: with the cache of one rank it is merged with the other ranks' partials by
+ * cp_merge_partials.
+ *   rows->tokens[b]  number of cached tokens of sequence b (its new ones included, if they are to
+ *                    be seen: write them first)
+ *   q_first          device int32 [n_seqs] or NULL.  NULL: every cached token is visible.
+ *                    Otherwise row i of sequence b stands at position q_first[b] + i and sees
+ *                    cached token j iff kv_pos.base + kv_pos.stride * j <= that (kv_pos: the
+ *                    rank's shard map, the same for all sequences; only differences matter, so a
+ *                    caller whose shards start elsewhere for each sequence shifts q_first[b])
+ *   q, o, lse        device [n_rows, hq, d] (in_dtype), [n_rows, hq, d] (o_dtype), fp32 [n_rows, hq]
+ *   scale            softmax scale; 0 means 1/sqrt(d)
+ *   workspace        device memory, 16-byte aligned, of at least cp_kv_cache_attn_workspace bytes;
+ *                    it need not be initialised and holds nothing afterwards.  Calls that may
+ *                    overlap need one each.
+ *   status           as cp_kv_rows; wait_timeout_ms as cp_attn_desc; flags must be 0
+ * A row that sees no token gets O = 0, LSE = -inf.  What unseen places hold (the rest of a page,
+ * tokens behind a row's position), NaN among it, has no influence.
+ * Rows of a sequence beyond a few dozen (long prompts) are answered, but cp_kv_cache_read followed
+ * by cp_partial_attn is the faster way for them.
+ * The split of the work, and with it the order of the sums, depends on the shapes, on row_start,
+ * tokens and q_first, and on the device's SM count alone: the same call gives the same bits.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.
+ */
+typedef struct {
+  cp_kv_cache cache;
+  cp_kv_rows rows;
+  const void* q;
+  void* o;
+  float* lse;
+  const int32_t* q_first;
+  int32_t in_dtype;
+  int32_t o_dtype;
+  int32_t hq;
+  float scale;
+  cp_posmap kv_pos;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;
+  int32_t wait_timeout_ms;
+  int32_t flags;
+} cp_kv_attn_desc;
+
+cp_status cp_kv_cache_attn(const cp_kv_attn_desc* desc, cudaStream_t stream);
+
+/* Bytes of workspace for a cp_kv_cache_attn call; reads the shapes and dtypes of desc only. */
+cp_status cp_kv_cache_attn_workspace(const cp_kv_attn_desc* desc, int64_t* bytes_out);
+
+/*
+ * ---------------------------------------------------------------- rotary positions
+ * cp_rope_axes -- rotary position embedding with one to four position axes (text, or time, height
+ * and width of a video token), of up to four tensors of the same tokens (queries and keys) in one
+ * launch; positions are global ([PCP/DCP] section 3.5, [Halo]), e.g. the ones cp_shard_layout writes.
+ *   pair i of a head (0 <= i < rot/2) belongs to the axis a whose section covers i: sections[0]
+ *   pairs, then sections[1], ...  Its angle is w = positions[a][token] * inv_freq[i];
+ *     (x_i, y_i) -> (x_i cos w - y_i sin w, x_i sin w + y_i cos w)
+ *   with (x_i, y_i) the elements (i, i + rot/2), or (2i, 2i + 1) where interleaved = 1.  Elements
+ *   [rot, d) are copied.  inverse = 1 turns by -w: the inverse rotation, which is also the
+ *   backward pass (the gradient of the inputs from that of the outputs).
+ * Angles are reduced exactly: the kernel multiplies the position by round(inv_freq / 2 pi * 2^64)
+ * modulo 2^64, so the fraction of a turn has no rounding that grows with the position (the angle
+ * is off by less than 2e-7 for any int32 position).
+ * Arguments:
+ *   n_tensors   1..4
+ *   in, out     host arrays [n_tensors] of device pointers, [tokens, heads[t], d], 16-byte
+ *               aligned; out[t] may be in[t]
+ *   heads       host array [n_tensors]
+ *   d, rot      d a multiple of 8, at most 256; rot a multiple of 16, 16 <= rot <= d
+ *   dtype       CP_F32 or CP_BF16 (arithmetic in fp32, rounded once)
+ *   positions   device int32 [n_axes, tokens], any sign
+ *   inv_freq    host fp64 [rot/2], finite, magnitudes at most 1e3
+ *   n_axes, sections  1..4; host int32 [n_axes], >= 0, sum rot/2
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.
+ */
+cp_status cp_rope_axes(int32_t n_tensors, const void* const* in, void* const* out, const int32_t* heads,
+                       int64_t tokens, int32_t d, int32_t rot, int32_t dtype, const int32_t* positions,
+                       int32_t n_axes, const int32_t* sections, const double* inv_freq, int32_t interleaved,
+                       int32_t inverse, cudaStream_t stream);
+
 /* Message for the calling thread's last non-OK status ("" if none).  Valid until the next call. */
 const char* cp_last_error(void);
 

@@ -1,0 +1,633 @@
+"""The 8-bit cache, attention over it and rotary positions on the GPU against the float64 oracle.
+
+Tolerances are per element and follow from the arithmetic:
+
+* cache bytes, scales and read-back values are equal to the oracle's.
+* rotation, fp32: the angle is off by at most 2e-7 (fraction of a turn to 24 bits), cos and sin by
+  2^-23, two products and a sum by 2^-24 each: 5e-7 (|a| + |b|) in all; bf16 outputs add half a step.
+* attention: a score is an fp32 sum of D products, off by at most 2^-20 of the sum of their
+  magnitudes A (D / 16 accumulations of 2^-23 at D = 128, and 2^-21 for the softmax scale and the
+  exponent's argument) plus 2^-22 |s|; weights have 22 bits for an fp32 output and 11 for a bf16
+  one, ex2 2^-22; sums over n keys add n / 16 accumulations of 2^-23.  So with delta the largest
+  score error of a row, |dO| <= (sum_j p_j |v_j|) (2 delta + w + n 2^-27 + 2^-20), w = 2^-21 or
+  2^-11, plus half a step of the output type, and |dLSE| <= delta + n 2^-24 + 2^-22 |LSE| + 2^-20.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import helpers
+import oracle
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    helpers.ensure_built()
+
+import context_blockwise_attention_gb300 as cpa  # noqa: E402
+from context_blockwise_attention_gb300 import PosMap, api  # noqa: E402
+
+DEV = torch.device("cuda", 0) if torch.cuda.is_available() else None
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def _starts(rows):
+    return np.concatenate([[0], np.cumsum(rows)]).astype(np.int64)
+
+
+class Pool:
+    """A cache and its host copy, with a page table that deals out pages in a random order."""
+
+    def __init__(self, seqs, tokens, page, hkv, d, seed, spare=2, fill=0x7F):
+        rng = np.random.default_rng(seed)
+        used = [max(0, -(-int(t) // page)) for t in tokens]
+        self.page, self.hkv, self.d = page, hkv, d
+        self.n_pages = sum(used) + spare
+        order = rng.permutation(self.n_pages)
+        self.width = max(1, max(used) if used else 1)
+        self.table = np.full((seqs, self.width), -1, dtype=np.int64)
+        at = 0
+        for b, u in enumerate(used):
+            self.table[b, :u] = order[at:at + u]
+            at += u
+        # every byte starts as NaN, every scale too: what nobody wrote must not show
+        self.bytes = [np.full((self.n_pages, hkv, page, d), fill, np.uint8) for _ in range(2)]
+        self.scale = [np.full((self.n_pages, hkv), np.nan, np.float32) for _ in range(2)]
+
+    def fill(self, tokens, seed, spread=3.0):
+        """Random tokens for each sequence, quantised by the oracle."""
+        rng = np.random.default_rng(seed)
+        for b, n in enumerate(tokens):
+            for which in range(2):
+                x = rng.standard_normal((int(n), self.hkv, self.d)) * 2.0 ** rng.uniform(-spread, spread, (int(n), self.hkv, 1))
+                oc.cache_write(self.bytes[which], self.scale[which], x.astype(np.float32).astype(np.float64), [0, int(n)],
+                               [0], self.table[b:b + 1])
+
+    def device(self):
+        f8 = [torch.from_numpy(b).to(DEV).view(torch.float8_e4m3fn) for b in self.bytes]
+        return cpa.KvCache(f8[0], f8[1], *(torch.from_numpy(s).to(DEV) for s in self.scale))
+
+    def tokens_of(self, b, n):
+        pages = self.table[b][:-(-int(n) // self.page)]
+        return [oc.cache_tokens(self.bytes[w], self.scale[w], pages, int(n)) for w in range(2)]
+
+
+def _same_cache(cache, pool):
+    for got, want in ((cache.k, pool.bytes[0]), (cache.v, pool.bytes[1])):
+        assert np.array_equal(got.view(torch.uint8).cpu().numpy(), want)
+    for got, want in ((cache.k_scale, pool.scale[0]), (cache.v_scale, pool.scale[1])):
+        assert np.array_equal(got.cpu().numpy(), want, equal_nan=True)
+
+
+# ------------------------------------------------------------------ writing and reading
+WRITES = [  # rows of each sequence, tokens before them, page, hkv, d, dtype
+    ([1], [0], 16, 1, 64, BF16),
+    ([1, 1, 1, 1], [15, 16, 17, 200], 16, 2, 128, BF16),
+    ([0, 3, 0, 1], [5, 30, 0, 63], 32, 3, 64, F32),
+    ([200, 0, 77, 64], [0, 9, 60, 64], 64, 2, 128, BF16),
+    ([129, 500], [127, 1], 128, 2, 64, F32),
+    ([33, 31, 16], [0, 1, 47], 16, 5, 128, F32),
+    ([257], [255], 128, 1, 128, BF16),
+    ([2] * 70, list(range(70)), 16, 2, 64, BF16),
+    ([40], [8], 64, 1, 64, BF16),
+]
+
+
+@pytest.mark.parametrize("rows,held,page,hkv,d,dtype", WRITES)
+def test_write_and_read_are_exact(rows, held, page, hkv, d, dtype):
+    total = [a + b for a, b in zip(rows, held)]
+    pool = Pool(len(rows), total, page, hkv, d, 1)
+    pool.fill(held, 2)
+    cache = pool.device()
+    start = _starts(rows)
+    extra = 5  # rows of no sequence
+    gen = torch.Generator().manual_seed(3)
+    # magnitudes from far below to far above what the continued pages hold
+    x = [(torch.randn((int(start[-1]) + extra, hkv, d), generator=gen) *
+          torch.exp2(torch.randint(-9, 9, (int(start[-1]) + extra, hkv, 1), generator=gen).float())).to(dtype)
+         for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = (_i32(start), _i32(held), _i32(pool.table))
+    for again in range(2):  # writing the same tokens again changes nothing
+        cpa.kv_cache_write(cache, x[0].to(DEV), x[1].to(DEV), *args, status=status)
+        if again == 0:
+            for w in range(2):
+                oc.cache_write(pool.bytes[w], pool.scale[w], x[w].double().numpy(), start, held, pool.table)
+        _same_cache(cache, pool)
+    # read the new rows, and everything from the first token on, in both types
+    for first, n in ((held, rows), ([0] * len(rows), total)):
+        s = _starts(n)
+        for out in (BF16, F32):
+            k = torch.full((int(s[-1]) + 3, hkv, d), 7.0, dtype=out, device=DEV)
+            v = torch.full_like(k, 7.0)
+            cpa.kv_cache_read(cache, _i32(s), _i32(first), args[2], k.shape[0], k=k, v=v, status=status)
+            for w, got in ((0, k), (1, v)):
+                assert bool((got[int(s[-1]):] == 7.0).all())
+                for b in range(len(rows)):
+                    want = pool.tokens_of(b, first[b] + n[b])[w][first[b]:]
+                    assert np.array_equal(got[int(s[b]):int(s[b + 1])].double().cpu().numpy(), want)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("rows", [[3], [100]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_write_special_values(rows, dtype):
+    pool = Pool(1, [120], 64, 2, 64, 5)
+    pool.fill([10], 6)
+    cache = pool.device()
+    x = torch.randn((rows[0], 2, 64), generator=torch.Generator().manual_seed(7)).to(dtype)
+    x[0, 0, :4] = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0])
+    x[1] = 0
+    x[2, 1, 5] = torch.finfo(dtype).max / 4
+    x[2, 1, 6] = 1e-39
+    cpa.kv_cache_write(cache, x.to(DEV), x.to(DEV), _i32([0, rows[0]]), _i32([10]), _i32(pool.table))
+    for w in range(2):
+        oc.cache_write(pool.bytes[w], pool.scale[w], x.double().numpy(), [0, rows[0]], [10], pool.table)
+    for got, want in ((cache.k, pool.bytes[0]), (cache.v, pool.bytes[1])):
+        got = got.view(torch.uint8).cpu().numpy()
+        nan = (want & 127) == 127  # a NaN's sign is free
+        assert np.array_equal((got & 127) == 127, nan) and np.array_equal(got[~nan], want[~nan])
+    assert np.array_equal(cache.k_scale.cpu().numpy(), pool.scale[0], equal_nan=True)
+    # a page of zeros takes the smallest scale
+    z = torch.zeros((5, 2, 64), dtype=dtype, device=DEV)
+    cpa.kv_cache_write(cache, z, z, _i32([0, 5]), _i32([64]), _i32(pool.table))
+    assert cache.k_scale[int(pool.table[0, 1])].tolist() == [2.0 ** -64] * 2
+
+
+def test_bad_pages_and_rows_are_skipped_and_reported():
+    pool = Pool(3, [64, 64, 64], 16, 2, 64, 8)
+    pool.fill([64, 64, 64], 9)
+    cache = pool.device()
+    bad = pool.table.copy()
+    bad[0, 1], bad[1, 2] = -7, pool.n_pages
+    start = [0, 64, 128, 192]
+    x = torch.randn((192, 2, 64), generator=torch.Generator().manual_seed(1)).to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    k = torch.full((192, 2, 64), 12345.0, device=DEV)  # no cached value
+    v = torch.full_like(k, 7.0)
+    cpa.kv_cache_read(cache, _i32(start), _i32([0, 0, 0]), _i32(bad), 192, k=k, v=v, status=status)
+    assert status.item() & 0xFF == api.CP_ERR_INVALID_ARG
+    skipped = [16 <= r < 32 or 64 + 32 <= r < 64 + 48 for r in range(192)]
+    assert bool((k[torch.tensor(skipped)] == 12345.0).all()) and not bool((k[~torch.tensor(skipped)] == 12345.0).any())
+    status.zero_()
+    cpa.kv_cache_write(cache, x, x, _i32(start), _i32([0, 0, 0]), _i32(bad), status=status)
+    assert status.item() & 0xFF == api.CP_ERR_INVALID_ARG
+    kept = pool.table[0, 1], pool.table[1, 2]
+    for page in kept:
+        assert np.array_equal(cache.k[int(page)].view(torch.uint8).cpu().numpy(), pool.bytes[0][page])
+    for n in range(len(pool.table[2])):
+        page = pool.table[2, n]
+        assert not np.array_equal(cache.k[int(page)].view(torch.uint8).cpu().numpy(), pool.bytes[0][page])
+    # behind the table, before the first token, rows out of order or out of range: nothing is written
+    _clean = pool.device()
+    for s, held in (([0, 64], [64]), ([0, 5], [-3]), ([64, 0], [0]), ([-100, -1], [0])):
+        cpa.kv_cache_write(_clean, x, x, _i32(s), _i32(held), _i32(pool.table[:1]), status=status)
+    _same_cache(_clean, pool)
+
+
+# ------------------------------------------------------------------ attention
+def _check_attn(pool, cache, q, rows, held, q_first, kv_pos, o_dtype, scale=0.0, poison=True):
+    start = _starts(rows)
+    n, hq, d = q.shape
+    o = torch.full((n, hq, d), float("nan"), dtype=o_dtype, device=DEV)
+    lse = torch.full((n, hq), float("nan"), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cpa.kv_cache_attn(q.to(DEV), cache, _i32(start), _i32(held), _i32(pool.table),
+                      q_first=None if q_first is None else _i32(q_first), kv_pos=kv_pos, scale=scale, o=o, lse=lse,
+                      status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    got_o, got_l = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isnan(got_o[int(start[-1]):]).all() and np.isnan(got_l[int(start[-1]):]).all()
+    sc = scale or d ** -0.5
+    qd = q.double().numpy()
+    worst = 0.0
+    for b in range(len(rows)):
+        r0, r1, m = int(start[b]), int(start[b + 1]), int(held[b])
+        if r1 == r0:
+            continue
+        k, v = pool.tokens_of(b, m)
+        kpos = kv_pos.base + kv_pos.stride * np.arange(m)
+        qpos = np.arange(r1 - r0) + (q_first[b] if q_first is not None else 0)
+        seen = kpos[None, :] <= qpos[:, None] if q_first is not None else np.ones((r1 - r0, m), bool)
+        group = hq // pool.hkv
+        for h in range(hq):
+            kh, vh = k[:, h // group], v[:, h // group]
+            for i in range(r1 - r0):
+                idx = np.nonzero(seen[i])[0]
+                go, gl = got_o[r0 + i, h], got_l[r0 + i, h]
+                if idx.size == 0:
+                    assert np.all(go == 0.0) and gl == -np.inf
+                    continue
+                s = sc * (kh[idx] @ qd[r0 + i, h])
+                a = sc * (np.abs(kh[idx]) @ np.abs(qd[r0 + i, h]))
+                top = s.max()
+                p = np.exp(s - top)
+                z = p.sum()
+                ref, ref_l = (p @ vh[idx]) / z, top + np.log(z)
+                delta = float((2.0 ** -20 * a + 2.0 ** -22 * np.abs(s)).max())
+                w = 2.0 ** -11 if o_dtype == BF16 else 2.0 ** -21
+                tol = (p @ np.abs(vh[idx])) / z * (2 * delta + w + idx.size * 2.0 ** -27 + 2.0 ** -20)
+                tol = tol + np.abs(ref) * (2.0 ** -8 if o_dtype == BF16 else 2.0 ** -24) * 1.01 + 1e-30
+                err = np.abs(go - ref)
+                assert np.all(err <= tol), (b, i, h, float((err / tol).max()), float(err.max()))
+                tol_l = delta + idx.size * 2.0 ** -24 + 2.0 ** -22 * abs(ref_l) + 2.0 ** -20
+                assert abs(gl - ref_l) <= tol_l, (b, i, h, gl, ref_l)
+                worst = max(worst, float((err / tol).max()), abs(gl - ref_l) / tol_l)
+    return o, lse, worst
+
+
+ATTN = [  # rows, held, page, hq, hkv, d, in, out, stride of the shard or None (not causal)
+    ([1], [1], 16, 1, 1, 64, BF16, F32, 1),
+    ([1], [1], 128, 8, 8, 128, F32, BF16, None),
+    ([1, 1, 1], [0, 33, 31], 16, 8, 1, 128, BF16, BF16, None),
+    ([1], [1000], 64, 32, 8, 128, BF16, BF16, 1),
+    ([1] * 9, [1, 15, 16, 17, 32, 64, 65, 500, 129], 16, 8, 2, 64, BF16, F32, 1),
+    ([1] * 9, [1, 15, 16, 17, 32, 64, 65, 500, 129], 32, 8, 2, 128, F32, F32, 1),
+    ([2, 0, 5, 1], [300, 40, 5, 7], 64, 8, 2, 128, BF16, F32, 1),
+    ([4, 8, 3], [4, 513, 260], 128, 16, 2, 64, BF16, BF16, 1),
+    ([17, 1], [300, 3], 32, 10, 2, 128, BF16, BF16, 1),
+    ([7, 33], [100, 90], 16, 12, 1, 64, F32, F32, 1),
+    ([3, 40], [1200, 64], 64, 16, 1, 128, BF16, F32, 1),
+    ([3, 40], [1200, 64], 64, 16, 1, 128, BF16, BF16, 1),
+    ([5, 9], [700, 1100], 128, 32, 2, 64, F32, BF16, 1),
+    ([2, 3], [90, 1000], 64, 4, 4, 128, BF16, F32, 8),
+    ([6, 2], [31, 640], 32, 8, 1, 64, BF16, BF16, 3),
+    ([1, 1], [5000, 4097], 128, 4, 2, 64, BF16, F32, 1),
+    ([2, 1], [2500, 3333], 16, 5, 1, 128, F32, F32, None),
+]
+
+
+@pytest.mark.parametrize("rows,held,page,hq,hkv,d,din,dout,stride", ATTN)
+def test_attention(rows, held, page, hq, hkv, d, din, dout, stride):
+    pool = Pool(len(rows), held, page, hkv, d, 11)
+    pool.fill(held, 12)
+    q = (torch.randn((sum(rows) + 2, hq, d), generator=torch.Generator().manual_seed(13)) *
+         torch.exp2(torch.randint(-3, 2, (sum(rows) + 2, hq, 1), generator=torch.Generator().manual_seed(14)).float())).to(din)
+    base = 0 if stride is None else stride - 1
+    first = None
+    if stride is not None:  # the last row sees everything
+        first = [base + stride * (m - 1) - (n - 1) for n, m in zip(rows, held)]
+    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(base, stride or 1), dout)
+
+
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_attention_rows_that_see_little_or_nothing(dout):
+    rows, held = [6, 3, 2, 4], [50, 200, 0, 31]
+    pool = Pool(4, held, 16, 2, 64, 21)
+    pool.fill(held, 22)
+    q = torch.randn((15, 8, 64), generator=torch.Generator().manual_seed(23)).to(BF16)
+    # a shard at positions 5, 9, 13, ...: the first rows stand before it, a later one in its middle
+    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(5, 4), dout)
+    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(0, 1), dout, scale=0.7)
+
+
+@pytest.mark.parametrize("g", [1, 8, 16])
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_attention_ignores_nan_and_infinity_behind_a_row(g, dout):
+    """Tokens that some rows see and others do not hold NaN values (and keys): the rows before them
+    are as if they were not there, the others are NaN in those columns."""
+    held, rows = [70], [4]
+    pool = Pool(1, held, 32, 1, 64, 31)
+    pool.fill(held, 32)
+    q = torch.randn((4, g, 64), generator=torch.Generator().manual_seed(33)).to(BF16)
+    page, slot = pool.table[0, 2], 69 - 64  # the last token: row 3 alone sees it
+    pool.bytes[1][page, 0, slot, :7] = 0x7F
+    pool.bytes[1][page, 0, slot, 9] = 0xFF
+    cache = pool.device()
+    start, first = _i32([0, 4]), _i32([66])
+    o, lse = cpa.kv_cache_attn(q.to(DEV), cache, start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
+    clean = Pool(1, held, 32, 1, 64, 31)
+    clean.fill(held, 32)
+    o2, l2 = cpa.kv_cache_attn(q.to(DEV), clean.device(), start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
+    assert torch.equal(o[:3], o2[:3]) and torch.equal(lse, l2)
+    nan = torch.zeros(64, dtype=torch.bool, device=DEV)
+    nan[:7] = True
+    nan[9] = True
+    assert bool(o[3][:, nan].isnan().all()) and torch.equal(o[3][:, ~nan], o2[3][:, ~nan])
+    # a NaN key: the scores of the rows that see it are NaN
+    pool.bytes[0][page, 0, slot, 3] = 0x7F
+    o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
+    assert torch.equal(o[:3], o2[:3]) and torch.equal(lse[:3], l2[:3])
+    assert bool(o[3].isnan().all()) and bool(lse[3].isnan().all())
+    # an infinite query spoils its own row alone
+    q[1, 0, 5] = float("inf")
+    o, lse = cpa.kv_cache_attn(q.to(DEV), clean.device(), start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
+    keep = torch.ones((4, g), dtype=torch.bool, device=DEV)
+    keep[1, 0] = False
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], l2[keep])
+    assert bool(o[1, 0].isnan().all())
+
+
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_attention_scales_far_apart(dout):
+    """Value pages whose scales differ by 2^40, and keys that make one token far heavier than the rest."""
+    held = [160]
+    pool = Pool(1, held, 16, 1, 128, 41)
+    rng = np.random.default_rng(42)
+    for which in range(2):
+        x = rng.standard_normal((160, 1, 128))
+        if which:
+            x *= 2.0 ** np.repeat([0, -40, 20, -20, 0, 5, -5, 30, -30, 1], 16)[:, None, None]
+        else:
+            x[3] *= 30
+            x[77] *= 40
+        oc.cache_write(pool.bytes[which], pool.scale[which], x, [0, 160], [0], pool.table)
+    q = torch.randn((2, 4, 128), generator=torch.Generator().manual_seed(43)).to(BF16)
+    _check_attn(pool, pool.device(), q, [2], held, [158], PosMap(0, 1), dout)
+
+
+def test_attention_bad_pages_answer_nan_and_report():
+    held, rows = [100, 100, 100], [2, 2, 2]
+    pool = Pool(3, held, 16, 2, 64, 51)
+    pool.fill(held, 52)
+    bad = pool.table.copy()
+    bad[0, 4], bad[1, 0] = pool.n_pages + 3, -1
+    q = torch.randn((6, 4, 64), generator=torch.Generator().manual_seed(53)).to(BF16).to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = (pool.device(), _i32([0, 2, 4, 6]))
+    good, lgood = cpa.kv_cache_attn(q, *args, _i32(held), _i32(pool.table))
+    o, lse = cpa.kv_cache_attn(q, *args, _i32(held), _i32(bad), status=status)
+    assert status.item() & 0xFF == api.CP_ERR_INVALID_ARG
+    assert bool(o[:4].isnan().all()) and bool(lse[:4].isnan().all())
+    assert torch.equal(o[4:], good[4:]) and torch.equal(lse[4:], lgood[4:])
+    # causal rows that do not reach the bad page are right
+    status.zero_()
+    o, lse = cpa.kv_cache_attn(q, *args, _i32(held), _i32(bad), q_first=_i32([62, 98, 98]), status=status)
+    ref, lref = cpa.kv_cache_attn(q, *args, _i32(held), _i32(pool.table), q_first=_i32([62, 98, 98]))
+    assert torch.equal(o[0], ref[0]) and torch.equal(o[1], ref[1]) and bool(o[2:4].isnan().all())
+    # more tokens than the table has pages for
+    status.zero_()
+    o, lse = cpa.kv_cache_attn(q, *args, _i32([100, 2 ** 31 - 1, 100]), _i32(pool.table), status=status)
+    assert status.item() & 0xFF == api.CP_ERR_INVALID_ARG
+    assert torch.equal(o[:2], good[:2]) and bool(o[2:4].isnan().all()) and torch.equal(o[4:], good[4:])
+    # a negative count is an empty cache
+    o, lse = cpa.kv_cache_attn(q, *args, _i32([100, -5, 100]), _i32(pool.table))
+    assert bool((o[2:4] == 0).all()) and bool((lse[2:4] == -float("inf")).all()) and torch.equal(o[4:], good[4:])
+
+
+def test_attention_offsets_beyond_32_bits():
+    """Pages whose bytes begin beyond 2^32, in a pool of more than 4 GiB for K and for V."""
+    page, hkv, d = 128, 4, 128
+    n_pages = (5 << 30) // (page * hkv * d)
+    k = torch.zeros((n_pages, hkv, page, d), dtype=torch.uint8, device=DEV)
+    v = torch.zeros_like(k)
+    ks = torch.ones((n_pages, hkv), device=DEV)
+    vs = torch.ones((n_pages, hkv), device=DEV)
+    pool = Pool(1, [500], page, hkv, d, 61, spare=0)
+    pool.fill([500], 62)
+    far = [n_pages - 1, n_pages - 77, 3, n_pages // 2 + 1]
+    for i, p in enumerate(pool.table[0]):
+        for dst, src in ((k, pool.bytes[0]), (v, pool.bytes[1])):
+            dst[far[i]] = torch.from_numpy(src[p]).to(DEV)
+        for dst, src in ((ks, pool.scale[0]), (vs, pool.scale[1])):
+            dst[far[i]] = torch.from_numpy(src[p]).to(DEV)
+    cache = cpa.KvCache(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), ks, vs)
+    q = torch.randn((3, 8, d), generator=torch.Generator().manual_seed(63)).to(BF16).to(DEV)
+    o, lse = cpa.kv_cache_attn(q, cache, _i32([0, 3]), _i32([500]), _i32([far]))
+    want, lwant = cpa.kv_cache_attn(q, pool.device(), _i32([0, 3]), _i32([500]), _i32(pool.table))
+    assert torch.equal(o, want) and torch.equal(lse, lwant)
+    kk, vv = cpa.kv_cache_read(cache, _i32([0, 500]), _i32([0]), _i32([far]), 500, dtype=F32)
+    cpa.kv_cache_write(cache, kk * 3, vv * 3, _i32([0, 500]), _i32([0]), _i32([far]))
+    k3, _ = cpa.kv_cache_read(cache, _i32([0, 500]), _i32([0]), _i32([far]), 500, dtype=F32)
+    assert bool(((k3 - 3 * kk).abs() <= 3 * kk.abs() * 2.0 ** -4 + 1e-3).all())
+
+
+def _serving_case(seed, rows, held, page=32, hq=8, hkv=2, d=64):
+    pool = Pool(len(rows), held, page, hkv, d, seed)
+    pool.fill(held, seed + 1)
+    q = torch.randn((sum(rows), hq, d), generator=torch.Generator().manual_seed(seed + 2)).to(BF16).to(DEV)
+    return pool, pool.device(), q, _i32(_starts(rows)), _i32(held), _i32(pool.table)
+
+
+def test_attention_same_bits_on_streams_at_once_and_in_graphs():
+    cases = [_serving_case(70, [1, 2, 1], [900, 40, 333]), _serving_case(80, [4], [2000], page=128, hq=16, d=128)]
+    alone = [cpa.kv_cache_attn(q, c, s, h, t) for _, c, q, s, h, t in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):  # both at once; one by the stream argument, one by the current stream
+        (_, c, q, s, h, t) = cases[0]
+        r0 = cpa.kv_cache_attn(q, c, s, h, t, stream=streams[0])
+        (_, c, q, s, h, t) = cases[1]
+        with torch.cuda.stream(streams[1]):
+            r1 = cpa.kv_cache_attn(q, c, s, h, t)
+        raw = cpa.kv_cache_attn(q, c, s, h, t, stream=streams[1].cuda_stream)
+        torch.cuda.synchronize()
+        for got, want in ((r0, alone[0]), (r1, alone[1]), (raw, alone[1])):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # a captured step replayed with other lengths, positions and pages
+    pool, cache, q, s, h, t = _serving_case(90, [1, 1, 1], [700, 64, 257], page=16)
+    h0, s0 = h.clone(), s.clone()
+    first = _i32([699, 63, 256])
+    o = torch.empty((3, 8, 64), device=DEV)
+    lse = torch.empty((3, 8), device=DEV)
+    ws = torch.empty(cpa.kv_cache_attn_workspace(cache, 3, 8, 3, t.shape[1]), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        cpa.kv_cache_attn(q, cache, s, h, t, q_first=first, o=o, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cpa.kv_cache_attn(q, cache, s, h, t, q_first=first, o=o, lse=lse, workspace=ws)
+    for lens, starts in (([700, 64, 257], [0, 1, 2, 3]), ([1, 60, 0], [0, 0, 2, 3]), ([650, 3, 256], [0, 3, 3, 3])):
+        h.copy_(_i32(lens))
+        s.copy_(_i32(starts))
+        first.copy_(_i32([max(0, x - 1) for x in lens]))
+        ws.fill_(0xFF)
+        g.replay()
+        want = cpa.kv_cache_attn(q, cache, s, h, t, q_first=first)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    h.copy_(h0)
+    s.copy_(s0)
+
+
+def test_calls_refuse_wrong_tensors():
+    pool, cache, q, s, h, t = _serving_case(99, [1, 1], [40, 30])
+    x = torch.zeros((2, 2, 64), dtype=BF16, device=DEV)
+    for call in (
+            lambda: cpa.kv_cache_attn(q.double(), cache, s, h, t),
+            lambda: cpa.kv_cache_attn(q.transpose(0, 1), cache, s, h, t),
+            lambda: cpa.kv_cache_attn(q[:, :, :32].contiguous(), cache, s, h, t),
+            lambda: cpa.kv_cache_attn(q[:, :3].contiguous(), cache, s, h, t),
+            lambda: cpa.kv_cache_attn(q, cache, s.long(), h, t),
+            lambda: cpa.kv_cache_attn(q, cache, s, h[:1], t),
+            lambda: cpa.kv_cache_attn(q, cache, s, h, t, q_first=h[:1]),
+            lambda: cpa.kv_cache_attn(q, cache, s, h, t, o=torch.empty((2, 8, 32), device=DEV)),
+            lambda: cpa.kv_cache_attn(q, cache._replace(k=cache.k.view(torch.uint8)), s, h, t),
+            lambda: cpa.kv_cache_attn(q, cache._replace(v_scale=cache.v_scale[1:]), s, h, t),
+            lambda: cpa.kv_cache_write(cache, x[:, :1].contiguous(), x, s, h, t),
+            lambda: cpa.kv_cache_write(cache, x, x.float(), s, h, t),
+            lambda: cpa.kv_cache_read(cache, s, h, t, 2, dtype=torch.float16),
+            lambda: cpa.kv_cache_read(cache, s, h, t, 2, k=x[:1], v=x[:1]),
+            lambda: cpa.rope_axes([x], h, (1.0,) * 16, (9, 9)),
+            lambda: cpa.rope_axes([x], h[:1], (1.0,) * 16),
+            lambda: cpa.rope_axes([x, x.float()], h, (1.0,) * 16),
+            lambda: cpa.rope_axes([x], h, (1.0,) * 16, out=[x.float()]),
+            lambda: cpa.rope_axes([x], h, (1.0,) * 12),
+    ):
+        with pytest.raises(cpa.CpError):
+            call()
+
+
+# ------------------------------------------------------------------ rotary positions
+ROPE = [  # tokens, heads, d, rot, sections, interleaved, dtype, largest position
+    (1, (1,), 64, 64, (32,), False, BF16, 10),
+    (7, (4, 2), 64, 64, (32,), True, F32, 1 << 30),
+    (33, (32, 8), 128, 128, (16, 24, 24), False, BF16, 5000),
+    (5, (3, 1, 1, 2), 128, 64, (8, 12, 12), True, BF16, 300),
+    (129, (5,), 64, 16, (2, 2, 2, 2), False, F32, 70000),
+    (64, (64, 8), 64, 32, (0, 16), False, F32, 1 << 20),
+    (3, (2,), 256, 256, (128,), False, F32, 100),
+    (9, (1, 1), 24, 16, (8,), True, F32, (1 << 31) - 2),
+    (2, (130,), 40, 32, (5, 11), False, BF16, 999),
+    (2000, (2, 1), 128, 96, (16, 16, 16), False, BF16, 1 << 18),
+]
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("tokens,heads,d,rot,sections,interleaved,dtype,far", ROPE)
+def test_rope(tokens, heads, d, rot, sections, interleaved, dtype, far, inverse):
+    gen = torch.Generator().manual_seed(5)
+    xs = [torch.randn((tokens, h, d), generator=gen).to(dtype) for h in heads]
+    pos = torch.randint(-far, far + 1, (len(sections), tokens), generator=gen)
+    pos[:, -1] = far
+    freq = [1.3 * 10000.0 ** (-2 * i / rot) * (-1 if i % 5 == 4 else 1) for i in range(rot // 2)]
+    dev = [x.to(DEV) for x in xs]
+    ys = cpa.rope_axes(dev, pos.int().to(DEV), freq, sections, interleaved, inverse)
+    for x, y in zip(xs, ys):
+        ref = oc.rotate(x.double().numpy(), pos.numpy(), freq, sections, interleaved, inverse)
+        a = np.abs(x.double().numpy())
+        lo, hi = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+        tol = np.zeros_like(a)
+        tol[..., lo] = tol[..., hi] = 5e-7 * (a[..., lo] + a[..., hi])
+        if dtype == BF16:
+            tol[..., :rot] += 2.0 ** -8 * 1.01 * np.abs(ref[..., :rot])
+        got = y.double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) - tol).max())
+        assert np.array_equal(got[..., rot:], x.double().numpy()[..., rot:])
+    # in place gives the same bits, and the other direction leads back
+    same = [x.clone() for x in dev]
+    cpa.rope_axes(same, pos.int().to(DEV), freq, sections, interleaved, inverse, out=same)
+    assert all(torch.equal(a, b) for a, b in zip(same, ys))
+    back = cpa.rope_axes(ys, pos.int().to(DEV), freq, sections, interleaved, not inverse)
+    for x, y in zip(dev, back):
+        # twice 5e-7 (|a| + |b|) in fp32; in bf16 the two roundings of a pair's elements, half a step each
+        lim = (2.0 ** -6 if dtype == BF16 else 3e-6) * x.float().abs().amax(-1, keepdim=True)
+        assert bool(((x.float() - y.float()).abs() <= lim).all())
+
+
+def test_rope_is_its_gradient():
+    """The gradient of sum(w * rope(x)) by the formula (rotate w back) against differences."""
+    gen = torch.Generator().manual_seed(6)
+    x = torch.randn((4, 2, 32), generator=gen)
+    w = torch.randn((4, 2, 32), generator=gen)
+    pos = torch.tensor([[3, 1000, -7, 50000], [1, 2, 3, 4]], dtype=torch.int32, device=DEV)
+    freq = [100.0 ** (-i / 8) for i in range(8)]
+    args = (pos, freq, (3, 5))
+    grad = cpa.rope_axes([w.to(DEV)], *args, inverse=True)[0].double().cpu()
+
+    def loss(z):
+        return float((w.double() * torch.from_numpy(oc.rotate(z.double().numpy(), pos.cpu().numpy(), freq, (3, 5)))).sum())
+    for at in [(0, 0, 0), (1, 1, 11), (2, 0, 12), (3, 1, 23), (3, 0, 24), (1, 0, 31), (2, 1, 5)]:
+        e = torch.zeros((4, 2, 32), dtype=torch.float64)
+        e[at] = 1.0  # the loss is linear in x: any step gives the exact slope
+        diff = loss(x.double() + e) - loss(x.double() - e)
+        assert abs(diff / 2 - float(grad[at])) <= 5e-7 * 2 * float(w.abs().max()) + 1e-12
+    y = cpa.rope_axes([x.to(DEV)], *args)[0]
+    assert abs(float((y.double().cpu() * w).sum()) - float((x * grad).sum())) <= 1e-4
+
+
+def test_rope_takes_the_shard_layout_s_positions_and_graphs():
+    qmap, pos = cpa.shard_layout(4096, 8, 5, "strided", positions=True)
+    x = torch.randn((512, 3, 64), generator=torch.Generator().manual_seed(7)).to(BF16).to(DEV)
+    freq = tuple(10000.0 ** (-i / 32) for i in range(32))
+    y = cpa.rope_axes([x], pos, freq)[0]
+    ref = oc.rotate(x.double().cpu().numpy(), [qmap.base + qmap.stride * np.arange(512)], freq, (32,))
+    assert np.abs(y.double().cpu().numpy() - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 1e-5
+    out = torch.empty_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cpa.rope_axes([x], pos, freq, out=[out])
+    g.replay()
+    assert torch.equal(out, y)
+    pos += 1
+    g.replay()
+    assert torch.equal(out, cpa.rope_axes([x], pos, freq)[0]) and not torch.equal(out, y)
+    assert torch.equal(cpa.rope_axes([x], pos, freq, stream=torch.cuda.Stream())[0].cpu(), out.cpu())
+
+
+# ------------------------------------------------------------------ together
+def test_prompt_then_decoding_over_four_ranks():
+    """Two sequences served by four ranks with strided shards: the prompt's keys are rotated and
+    written into each rank's cache, read back for the prompt's tensor-core attention, then two
+    tokens are decoded, each rank over its own cache, and the ranks' partials merged."""
+    cp, hq, hkv, d, page = 4, 8, 2, 64, 16
+    prompt, steps = [140, 64], 2
+    total = [p + steps for p in prompt]
+    gen = torch.Generator().manual_seed(8)
+    freq = tuple(10000.0 ** (-i / 32) for i in range(32))
+    raw = [[torch.randn((n, h, d), generator=gen).to(BF16).to(DEV) for h in (hq, hkv, hkv)] for n in total]
+    qk = []
+    for b, n in enumerate(total):
+        pos = torch.arange(n, dtype=torch.int32, device=DEV)
+        q, k = cpa.rope_axes(raw[b][:2], pos, freq)
+        qk.append((q, k, raw[b][2]))
+    width = 12
+    caches, tables = [], []
+    for r in range(cp):
+        caches.append(cpa.kv_cache_empty(2 * width, page, hkv, d))
+        tables.append(torch.randperm(2 * width, generator=gen).reshape(2, width).int().to(DEV))
+
+    def local(n, r):  # tokens of the first n that rank r holds
+        return max(0, -(-(n - r) // cp))
+
+    def put(lo, hi):
+        for r in range(cp):
+            have = [local(x, r) for x in lo]
+            new = [local(x, r) - y for x, y in zip(hi, have)]
+            k, v = (torch.cat([qk[b][w][[r + cp * j for j in range(have[b], have[b] + new[b])]] for b in range(2)])
+                    for w in (1, 2))
+            cpa.kv_cache_write(caches[r], k, v, _i32(_starts(new)), _i32(have), tables[r])
+    put([0, 0], prompt)
+    kept = []
+    for b in range(2):  # every rank's keys and values as the cache holds them
+        parts = []
+        for r in range(cp):
+            n = local(prompt[b], r)
+            parts.append(cpa.kv_cache_read(caches[r], _i32([0, n]), _i32([0]), tables[r][b:b + 1], n))
+        kept.append(parts)
+        # the prompt's own attention: rank 1's queries against every rank's chunk
+        q = qk[b][0][1:prompt[b]:cp].contiguous()
+        o, lse = cpa.partial_attn_chunks(q, [(parts[r][0], parts[r][1], PosMap(r, cp)) for r in range(cp)], PosMap(1, cp))
+        kpos = np.concatenate([r + cp * np.arange(local(prompt[b], r)) for r in range(cp)])
+        o_ref, l_ref = oracle.attention(q.cpu(), torch.cat([p[0] for p in parts]).cpu(), torch.cat([p[1] for p in parts]).cpu(),
+                                        1 + cp * np.arange(q.shape[0]), kpos, causal=True)
+        helpers.compare_partial(o.cpu().numpy(), lse.cpu().numpy(), o_ref, l_ref, helpers.TOL_BF16_O, helpers.TOL_BF16_LSE)
+    for step in range(steps):
+        now = [p + step for p in prompt]
+        put(now, [n + 1 for n in now])
+        q = torch.cat([qk[b][0][now[b]:now[b] + 1] for b in range(2)])
+        parts = []
+        for r in range(cp):
+            lens = _i32([local(n + 1, r) for n in now])
+            parts.append(cpa.kv_cache_attn(q, caches[r], _i32([0, 1, 2]), lens, tables[r], q_first=_i32(now),
+                                           kv_pos=PosMap(r, cp)))
+        o, lse = cpa.merge_partials([p[0] for p in parts], [p[1] for p in parts], out_dtype=F32)
+        for b in range(2):
+            ks, vs, ps = [], [], []
+            for r in range(cp):
+                n = local(now[b] + 1, r)
+                k, v = cpa.kv_cache_read(caches[r], _i32([0, n]), _i32([0]), tables[r][b:b + 1], n, dtype=F32)
+                ks.append(k.cpu())
+                vs.append(v.cpu())
+                ps.append(r + cp * np.arange(n))
+            o_ref, l_ref = oracle.attention(q[b:b + 1].cpu(), torch.cat(ks), torch.cat(vs), [now[b]], np.concatenate(ps))
+            assert np.abs(o[b:b + 1].cpu().numpy() - o_ref).max() <= 2e-5
+            assert np.abs(lse[b:b + 1].cpu().numpy() - l_ref).max() <= 2e-5
