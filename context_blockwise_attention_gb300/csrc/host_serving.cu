@@ -134,10 +134,11 @@ CP_API cp_status cp_kv_cache_attn(const cp_kv_attn_desc* desc, cudaStream_t stre
   if (d.kv_pos.base < 0) CP_INVALID("%s: positions must be >= 0", who);
   if (d.kv_pos.stride > 2000000000 || d.kv_pos.base > 2000000000) CP_INVALID("%s: global positions exceed 2e9", who);
   if (!(d.scale >= 0.0f) || isinf(d.scale)) CP_INVALID("%s: scale must be finite and >= 0", who);
-  if (d.flags != 0) CP_INVALID("%s: unknown flag bits 0x%x", who, d.flags);
+  if (d.flags & ~CP_FLAG_TEST_STALL) CP_INVALID("%s: unknown flag bits 0x%x", who, d.flags);
   if (d.wait_timeout_ms < 0) CP_INVALID("%s: wait_timeout_ms must be >= 0", who);
   if (!aligned(d.status, 4) || !aligned(d.q_first, 4)) CP_INVALID("%s: status and q_first must be 4-byte aligned", who);
   if (d.rows.n_rows == 0 || d.rows.n_seqs == 0) return CP_OK;
+  if (d.cache.n_pages == 0) CP_INVALID("%s: the cache has no pages", who);
   if (d.q == nullptr || d.o == nullptr || d.lse == nullptr) CP_INVALID("%s: q, o and lse must not be NULL", who);
   if (!aligned(d.q, 16) || !aligned(d.o, 16) || !aligned(d.lse, 4))
     CP_INVALID("%s: q and o must be 16-byte aligned, lse 4-byte aligned", who);

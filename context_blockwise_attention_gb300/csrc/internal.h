@@ -27,6 +27,9 @@ cp_status cuda_fail(cudaError_t e, const char* what);
 bool encode_map_2d(CUtensorMap* m, const void* base, int64_t tokens, int64_t row_elems, bool fp32,
                    int box_rows);
 
+// 2-D tensor map over bytes seen as [lines, 128]: box = 128 bytes x box_lines, 128-byte swizzle.
+bool encode_map_bytes(CUtensorMap* m, const void* base, int64_t lines, int box_lines);
+
 // ---- launchers (arguments already validated by the C entry points) ----
 cp_status launch_fill_positions(int32_t* out, int64_t n, int64_t base, int64_t stride,
                                 cudaStream_t s);

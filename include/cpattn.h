@@ -484,7 +484,8 @@ cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, voi
  *   workspace        device memory, 16-byte aligned, of at least cp_kv_cache_attn_workspace bytes;
  *                    it need not be initialised and holds nothing afterwards.  Calls that may
  *                    overlap need one each.
- *   status           as cp_kv_rows; wait_timeout_ms as cp_attn_desc; flags must be 0
+ *   status, wait_timeout_ms, flags  as cp_attn_desc (flags: 0 or CP_FLAG_TEST_STALL); status also
+ *                    reports bad pages (cp_kv_rows)
  * A row that sees no token gets O = 0, LSE = -inf.  What unseen places hold (the rest of a page,
  * tokens behind a row's position), NaN among it, has no influence.
  * Rows of a sequence beyond a few dozen (long prompts) are answered, but cp_kv_cache_read followed

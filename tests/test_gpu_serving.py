@@ -362,6 +362,13 @@ def test_attention_bad_pages_answer_nan_and_report():
     o, lse = cpa.kv_cache_attn(q, *args, _i32(held), _i32(bad), q_first=_i32([62, 98, 98]), status=status)
     ref, lref = cpa.kv_cache_attn(q, *args, _i32(held), _i32(pool.table), q_first=_i32([62, 98, 98]))
     assert torch.equal(o[0], ref[0]) and torch.equal(o[1], ref[1]) and bool(o[2:4].isnan().all())
+    # nor those that only share a tile with it: page 5 is bad, positions 71 and 72 end in page 4
+    bad[0, 4], bad[0, 5] = pool.table[0, 4], -1
+    o, lse = cpa.kv_cache_attn(q, *args, _i32(held), _i32(bad), q_first=_i32([71, 98, 98]))
+    ref, lref = cpa.kv_cache_attn(q, *args, _i32(held), _i32(pool.table), q_first=_i32([71, 98, 98]))
+    assert torch.equal(o[:2], ref[:2]) and torch.equal(lse[:2], lref[:2])
+    o, lse = cpa.kv_cache_attn(q, *args, _i32(held), _i32(bad), q_first=_i32([79, 98, 98]))
+    assert bool(o[0].isfinite().all()) and bool(o[1].isnan().all())
     # more tokens than the table has pages for
     status.zero_()
     o, lse = cpa.kv_cache_attn(q, *args, _i32([100, 2 ** 31 - 1, 100]), _i32(pool.table), status=status)
@@ -446,6 +453,25 @@ def test_attention_same_bits_on_streams_at_once_and_in_graphs():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     h.copy_(h0)
     s.copy_(s0)
+
+
+def test_attention_wait_runs_out():
+    pool, cache, q, s, h, t = _serving_case(95, [1, 1], [400, 300])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cpa.kv_cache_attn(q, cache, s, h, t, status=status, flags=api.CP_FLAG_TEST_STALL, wait_timeout_ms=20)
+    torch.cuda.synchronize()
+    assert status.item() & 0xFF == api.CP_ERR_TIMEOUT
+    want = _check_attn(pool, cache, q.cpu(), [1, 1], [400, 300], None, PosMap(0, 1), F32)
+    assert want[0].isfinite().all()
+
+
+def test_workspace_is_checked():
+    pool, cache, q, s, h, t = _serving_case(97, [1, 1], [4000, 300])
+    need = cpa.kv_cache_attn_workspace(cache, 2, 8, 2, t.shape[1])
+    with pytest.raises(cpa.CpError):
+        cpa.kv_cache_attn(q, cache, s, h, t, workspace=torch.empty(need - 16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(cpa.CpError):
+        cpa.kv_cache_attn(q, cache, s, h, t, workspace=torch.empty(need + 16, dtype=torch.uint8, device=DEV)[8:])
 
 
 def test_calls_refuse_wrong_tensors():

@@ -101,6 +101,7 @@ def test_attention_refuses():
         assert lib.cp_last_error()
     assert lib.cp_kv_cache_attn(None, None) == BAD
     assert call(workspace=0) == BAD
+    assert call(cache=_cache(n_pages=0)) == BAD
     assert call(rows=_rows(n_rows=0), q=0) == api.CP_OK
     need = ctypes.c_int64()
     assert lib.cp_kv_cache_attn_workspace(None, ctypes.byref(need)) == BAD
