@@ -584,7 +584,7 @@ def ulysses_reshard(direction, tensors, cp, seq_len, layout="contiguous", out=No
 
 # ---------------------------------------------------------------- 8-bit KV cache
 # Largest number of sequences one call takes (``CP_KV_MAX_SEQS``).
-KV_MAX_SEQS = 4096
+KV_MAX_SEQS = 2048
 
 
 class KvCache(NamedTuple):

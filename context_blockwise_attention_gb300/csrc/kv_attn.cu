@@ -8,26 +8,29 @@
 // bound for up to a few dozen rows; the design is about keeping loads in flight and splitting the
 // keys evenly, not about the tensor rate.
 //
-// Work split.  The unit is a granule of 32 keys of one item (sequence, KV head, block of RT query
-// rows); granules are numbered item after item.  Every warp of the grid is a worker on its own,
-// with an equal share of consecutive granules, whatever the sequences' lengths: no barrier between
-// warps, and a worker's copies run ahead across item borders.  An item that lies within one share is
-// finished there; of the others each worker leaves a partial (O unnormalised, m, l), at most two per
-// worker (the item its share begins in and the one it ends in), and a second kernel, launched as
-// a programmatic dependent, combines them in the order of the workers.
+// Work split.  The unit is a granule of 4096 / D keys (8 KB of cache) of one item (sequence, KV head,
+// block of RT query rows); granules are numbered item after item, each item beginning with kSetup
+// numbers that stand for the time its start and end take.  Every warp of the grid is a worker on its
+// own, with an equal share of consecutive numbers, whatever the sequences' lengths: no barrier
+// between warps, and a worker's copies run ahead across item borders.  An item that lies within one
+// share is finished there; of the others each worker leaves a partial (O unnormalised, m, l), at most
+// two per worker (the item its share begins inside of and the one it ends in), and a second kernel,
+// launched as a programmatic dependent, combines them in the order of the workers.  That kernel also
+// answers the rows of sequences without visible tokens, which are no items.
 //
 // Products.  mma.sync m16n8k16 with f16 operands: e4m3 -> f16 is exact and one instruction for two
-// values, and with 8 to 32 query rows the 128-row tiles of tcgen05 would be mostly empty.  Rows of
-// S are query rows, so that the accumulator layout of S is the operand layout of P.  The orders of
-// keys and dimensions inside the products are free as long as both operands agree; they are chosen
-// so that every lane reads 16 consecutive bytes of a key or value row, without bank conflicts under
-// the 128-byte swizzle that the copies apply.
+// values, and the 128-row tiles of tcgen05 would be mostly empty with 8 to 32 query rows.  Both
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and head dimensions fill the 16
+// rows of an operand tile, query rows its 8 columns, so that 8 rows waste nothing and O takes
+// D / 4 registers; P^T gets from the accumulator's layout into the operand's by one 8x8 transpose
+// for 8 keys.  The orders of keys and dimensions inside the products are free as long as both
+// operands agree; they are chosen so that every lane reads 16 consecutive bytes of a key or value
+// row, without bank conflicts under the 128-byte swizzle that the copies apply.
 //
-// Precision.  A query row is scaled by a power of two to at most 2^15 and split into f16 parts, high
-// and low; P likewise (times 2^15).  With up to 8 rows (kTwo) the unused upper half of the 16-row
-// operand holds the low parts: 22 bits at no cost.  With more rows and bf16 in and out, one f16
-// part is enough: bf16 queries are exact, and P's 2^-12 is far below the output's 2^-9.  Sums,
-// maxima and the accumulators are fp32.
+// Precision.  A query row is scaled by a power of two to at most 2^15; as f16 a bf16 row is then
+// exact (over 2^28 of range), an fp32 row is split into a high and a low part, 22 bits.  P, times
+// 2^15, is one f16 part for a bf16 output (2^-12, against the output's 2^-9) and two parts for an
+// fp32 one.  Sums, maxima and the accumulators are fp32.
 #include "internal.h"
 #include "kv_common.cuh"
 #include "ptx.cuh"
@@ -39,31 +42,39 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.0f;  // largest P operand
-constexpr int kKeys = 32;            // keys of a granule
+constexpr int kSetup = 1;            // what an item costs besides its granules
+constexpr int kFlush = 64;           // granules summed before they are put aside
 constexpr unsigned kFull = 0xffffffffu;
 
-struct Yes {
-  static constexpr bool value = true;
-};
-struct No {
-  static constexpr bool value = false;
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
 
-template <int D, int NT, bool TWO>
+// QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
+template <int D>
+constexpr int kKeysOf = 4096 / D;  // keys of a granule
+
+template <int D, int NT, int QP, int PP>
 struct Shape {
-  static constexpr int kWarps = 8;
-  static constexpr int kRows = NT * (TWO ? 8 : 16);  // RT
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 2) : 4;
+  // More warps hide more latency; registers (O takes NT D / 4) and shared memory bound their number.
+  static constexpr bool kHeavy = NT * D >= 256 || NT * QP >= 4;
+  static constexpr int kWarps = kHeavy ? 8 : 12;
+  static constexpr int kRows = NT * 8;  // RT
+  static constexpr int kKeys = kKeysOf<D>;
+  static constexpr int kSteps = kKeys / 16;          // steps of 16 keys
   static constexpr int kHalf = kKeys * D;            // bytes of K (or V) of a granule
   static constexpr int kStage = 2 * kHalf;
-  static constexpr bool kQSmem = NT > 1;             // query operands in shared memory
-  static constexpr int kQBytes = kQSmem ? NT * (D / 16) * 512 : 0;
+  static constexpr bool kQSmem = D == 128 && NT * QP >= 4;  // query operands in shared memory
+  static constexpr int kStages = kHeavy && !kQSmem ? 3 : 2;
+  static constexpr int kQBytes = kQSmem ? NT * QP * (D / 16) * 256 : 0;
   static constexpr int kWarpBytes = kStages * kStage + kQBytes;
   // behind the warps' parts (1024-byte aligned for the swizzle): scales, barriers, control, plan
-  static constexpr int kScaleOff = kWarps * kWarpBytes;               // [warp][stage][4] fp32
-  static constexpr int kBarOff = kScaleOff + kWarps * kStages * 16;   // [warp][stage] + stall
+  static constexpr int kScaleOff = kWarps * kWarpBytes;               // [warp][stage][8] fp32
+  static constexpr int kBarOff = kScaleOff + kWarps * kStages * 32;   // [warp][stage] + stall
   static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
-  static constexpr int kPlanOff = (kCtlOff + 8 + 15) / 16 * 16 + 16 * 16;  // 16 x 8 B scan scratch before it
+  static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;       // [warp] 8 bytes
+  static constexpr int kPlanOff = kScanOff + 16 * 8;
 };
 
 struct Params {
@@ -83,6 +94,7 @@ struct Params {
   int64_t* plan;   // [n_seqs + 1] granules before each sequence (workspace)
   float* part_o;   // [workers][2][RT][D]
   float2* part_ml; // [workers][2][RT]: m (base 2), l
+  float* aside;    // [workers][RT][D]: accumulators put aside
 };
 
 // What a sequence asks for.
@@ -92,21 +104,21 @@ struct Seq {
   int32_t rows;
   int32_t tokens;  // cached tokens, as far as the page table reaches
   int32_t keys;    // tokens that its last row sees
-  int32_t gpi;     // granules of an item, at least 1
-  int32_t blocks;  // blocks of RT query rows
+  int32_t gpi;     // granules of an item
+  int32_t blocks;  // blocks of RT query rows; 0 where no row sees a token
   bool over;       // more tokens than the table has pages for
 };
 
 // Number of tokens that a row at position `pos` sees: token j stands at base + stride * j.
 __device__ __forceinline__ int32_t visible(const Params& p, int32_t tokens, int64_t pos) {
   if (p.q_first == nullptr) return tokens;
-  const int64_t off = pos - p.kv_pos.base;
+  const int64_t off = pos - p.kv_pos.base;  // below 2^32
   if (off < 0) return 0;
-  const int64_t n = off / p.kv_pos.stride + 1;
-  return n < tokens ? static_cast<int32_t>(n) : tokens;
+  const uint32_t n = static_cast<uint32_t>(off) / static_cast<uint32_t>(p.kv_pos.stride);
+  return n < static_cast<uint32_t>(tokens) ? static_cast<int32_t>(n) + 1 : tokens;
 }
 
-template <int RT>
+template <int D, int RT>
 __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   Seq s;
   s.r0 = kv::row_at(p.rows, b);
@@ -119,15 +131,15 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   s.tokens = t < 0 ? 0 : static_cast<int32_t>(t);
   s.pos0 = p.q_first != nullptr ? __ldg(p.q_first + b) : 0;
   s.keys = s.rows > 0 ? visible(p, s.tokens, s.pos0 + s.rows - 1) : 0;
-  s.gpi = s.keys > kKeys ? (s.keys + kKeys - 1) / kKeys : 1;
-  s.blocks = static_cast<int32_t>((static_cast<int64_t>(s.rows) * p.group + RT - 1) / RT);
+  s.gpi = (s.keys + kKeysOf<D> - 1) / kKeysOf<D>;
+  s.blocks = s.keys > 0 ? (s.rows * p.group + RT - 1) / RT : 0;
   return s;
 }
-__device__ __forceinline__ int64_t granules(const Params& p, const Seq& s) {
-  return static_cast<int64_t>(s.blocks) * p.hkv * s.gpi;
+__device__ __forceinline__ int64_t numbers(const Params& p, const Seq& s) {
+  return static_cast<int64_t>(s.blocks) * p.hkv * (s.gpi + kSetup);
 }
 
-// Shares of W granules among n workers: worker w has [share(w), share(w + 1)).
+// Shares of W numbers among n workers: worker w has [share(w), share(w + 1)).
 __device__ __forceinline__ int64_t share(int64_t W, int64_t n, int64_t w) { return W * w / n; }
 __device__ __forceinline__ int64_t worker_of(int64_t W, int64_t n, int64_t x) { return ((x + 1) * n - 1) / W; }
 __device__ __forceinline__ int64_t workers(int64_t W, int64_t most) { return W < most ? W : most; }
@@ -174,8 +186,8 @@ __device__ __forceinline__ void store_row4(const Params& p, int64_t at, float a,
   }
 }
 
-// Granules before each sequence, in shared memory: plan[0 .. n_seqs].
-template <int RT, int THREADS>
+// Numbers before each sequence, in shared memory: plan[0 .. n_seqs].
+template <int D, int RT, int THREADS>
 __device__ __forceinline__ void make_plan(const Params& p, int64_t* plan, int64_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.rows.n_seqs;
@@ -184,8 +196,8 @@ __device__ __forceinline__ void make_plan(const Params& p, int64_t* plan, int64_
     const int b = base + tid;
     int64_t x = 0;
     if (b < n) {
-      const Seq s = seq_of<RT>(p, b);
-      x = granules(p, s);
+      const Seq s = seq_of<D, RT>(p, b);
+      x = numbers(p, s);
       if (s.over && s.rows > 0 && blockIdx.x == 0) kv::report(p.status, kv::kSiteTokens);
     }
 #pragma unroll
@@ -215,28 +227,28 @@ struct Cursor {
   int gpi, blocks;
 };
 
-// Moves to the first sequence at or behind c.b + 1 that has rows.
-template <int RT>
+// Moves to the first sequence behind c.b that has items.
+template <int D, int RT>
 __device__ __forceinline__ void next_seq(const Params& p, Cursor& c, Seq& s) {
   do {
     ++c.b;
     if (c.b >= p.rows.n_seqs) return;
-    s = seq_of<RT>(p, c.b);
+    s = seq_of<D, RT>(p, c.b);
   } while (s.blocks == 0);
   c.head = c.block = c.g = 0;
   c.gpi = s.gpi;
   c.blocks = s.blocks;
 }
 
-template <int D, int NT, bool TWO>
-__global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
+template <int D, int NT, int QP, int PP>
+__global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     kv_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v) {
-  using S = Shape<D, NT, TWO>;
+  using S = Shape<D, NT, QP, PP>;
   constexpr int RT = S::kRows;
-  constexpr int kNd = D / 8;          // 8-column tiles of O; also the columns of a lane's V chunk
-  constexpr int kRl = TWO ? 1 : 2;    // query rows of a lane per row tile
-  constexpr int kSt = S::kStages;
+  constexpr int kMt = D / 16;  // 16-row tiles of O^T; also steps of 16 dimensions of S
+  constexpr int kCols = D / 8; // columns of O that a lane holds, for two query rows
+  constexpr int kSt = S::kStages, kSteps = S::kSteps, kKeys = S::kKeys;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -246,13 +258,13 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
   const uint32_t base = ptx::smem_u32(smem);
   const uint32_t ring = base + warp * S::kWarpBytes;
   const uint32_t q_smem = ring + kSt * S::kStage;
-  const uint32_t scales = base + S::kScaleOff + warp * kSt * 16;
+  const uint32_t scales = base + S::kScaleOff + warp * kSt * 32;
   const uint32_t bars = base + S::kBarOff + warp * kSt * 8;
   const uint32_t stall_bar = base + S::kBarOff + S::kWarps * kSt * 8;
 
   if (lane == 0) {
-    // one arrival for the copies' bytes, four for the lanes that copy the scales
-    for (int i = 0; i < kSt; ++i) ptx::mbar_init(bars + i * 8, 5);
+    // one arrival for the copies' bytes, and one for each lane that copies a scale
+    for (int i = 0; i < kSt; ++i) ptx::mbar_init(bars + i * 8, 1 + 2 * kSteps);
     if (warp == 0) {
       ptx::mbar_init(stall_bar, 1);
       *abort_flag = 0;
@@ -262,7 +274,8 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
-  make_plan<RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kPlanOff - 16 * 16));
+  ptx::wait_dependencies();  // launched early: what was in the stream before is complete from here on
+  make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
   const int n_seqs = p.rows.n_seqs;
   if (blockIdx.x == 0)
     for (int i = tid; i <= n_seqs; i += S::kWarps * 32) p.plan[i] = plan[i];
@@ -278,117 +291,143 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
   if (worker >= n_workers) return;
   const int64_t lo = share(W, n_workers, worker), hi = share(W, n_workers, worker + 1);
-  int64_t left = hi - lo, to_issue = left;
+  int64_t left = hi - lo;  // numbers of the share from the cursor on
 
   Cursor c;  // where the products are
   Seq seq;
+  bool inside;  // the share begins inside of an item
   {
-    int a = 0, z = n_seqs - 1;  // the last sequence whose granules begin at or before lo
+    int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
     while (a < z) {
       const int mid = (a + z + 1) >> 1;
       if (plan[mid] <= lo) a = mid;
       else z = mid - 1;
     }
     c.b = a;
-    seq = seq_of<RT>(p, a);
+    seq = seq_of<D, RT>(p, a);
     const int64_t off = lo - plan[a];
-    const int64_t item = off / seq.gpi;
-    c.g = static_cast<int>(off - item * seq.gpi);
+    const int64_t item = off / (seq.gpi + kSetup);
+    const int at = static_cast<int>(off - item * (seq.gpi + kSetup));
+    inside = at >= kSetup;
+    c.g = inside ? at - kSetup : 0;
+    if (!inside) left -= kSetup - at;
     c.head = static_cast<int>(item / seq.blocks);
     c.block = static_cast<int>(item - static_cast<int64_t>(c.head) * seq.blocks);
     c.gpi = seq.gpi;
     c.blocks = seq.blocks;
   }
+  if (left <= 0) return;
   Cursor f = c;  // where the copies are
+  int64_t to_issue = left;
   int f_keys = seq.keys;
-  bool f_over = seq.over;
-  int64_t page_first = -1;  // lane i holds the (page_first + i)-th page of sequence f.b
+  int f_last = seq.over ? p.rows.max_pages - 1 : -1;  // a page that counts as bad
+  int window = -32;        // lane i holds page window + i of sequence f.b
   int pages = -1;
 
-  auto page_of = [&](int64_t ord) -> int64_t {
-    if (page_first < 0 || ord < page_first || ord >= page_first + 32) {
-      page_first = ord;
-      const int64_t mine = ord + lane;
-      int64_t id = kv::page_at(p.rows, p.n_pages, f.b, mine);
-      if (f_over && mine == p.rows.max_pages - 1) id = -1;
-      pages = id < 0 ? -1 : static_cast<int>(id);
+  auto page_of = [&](int ord) -> int {
+    if (static_cast<unsigned>(ord - window) >= 32u) {
+      window = ord;
+      const int64_t id = kv::page_at(p.rows, p.n_pages, f.b, ord + lane);
+      pages = id < 0 || ord + lane == f_last ? -1 : static_cast<int>(id);
     }
-    return __shfl_sync(kFull, pages, static_cast<int>(ord - page_first));
+    return __shfl_sync(kFull, pages, ord - window);
+  };
+  // Starts the copies of one page's part of K and V (`lines` lines of the maps from `page` on).
+  auto copy = [&](int page, int slot, uint32_t dst, uint32_t bar) {
+    const int row = (page * p.hkv + f.head) * p.page + slot;  // below 2^31: checked on the host
+    const int line = D == 128 ? row : row >> 1;
+    ptx::tma_load_2d(dst, &map_k, 0, line, bar);
+    ptx::tma_load_2d(dst + S::kHalf, &map_v, 0, line, bar);
+  };
+  // Copies the scale of K (even lane) or V (odd lane), or stands in for it: where there is no
+  // token the smallest scale, for a bad page NaN, which reaches the rows that see it.
+  auto copy_scale = [&](int page, bool need, uint32_t to) {
+    if (page >= 0) ptx::cp_async4(to, p.scale[lane & 1] + (page * p.hkv + f.head));
+    else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(need ? 0x7fffffffu : 0x1f800000u) : "memory");
   };
 
   // Starts the copies of the next granule into stage `st`.
   auto issue = [&](int st) {
     const uint32_t bar = bars + st * 8, dst = ring + st * S::kStage;
     const int key0 = f.g * kKeys;
-    const int parts = p.page < kKeys ? 2 : 1;       // pages of 16 tokens: two to a granule
-    const int part_bytes = S::kHalf / parts;
-    int64_t page[2] = {-1, -1};
-    bool want[2];
-    uint32_t tx = 0;
+    const int mine = key0 + (lane >> 1) * 16;  // lane 2 i + w copies the scale of step i of K (w = 0) or V (w = 1)
+    int my_page = -1;
+    bool bad = false;
+    if (p.page >= kKeys) {
+      const int page = page_of(key0 >> p.page_log2);
+      bad = page < 0;
+      my_page = page;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, bad ? 0 : S::kStage);
+        if (!bad) copy(page, key0 & (p.page - 1), dst, bar);
+      }
+    } else {  // several pages, as far as there are tokens
+      const int part = p.page * D;
+      uint32_t tx = 0;
+      int page[kSteps];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = key0 + i * 16;
-      want[i] = i < parts && k < f_keys;
-      if (want[i]) {
-        page[i] = page_of(static_cast<int64_t>(k) >> p.page_log2);
-        if (page[i] >= 0) tx += 2 * part_bytes;
-        else if (lane == 0) kv::report(p.status, kv::kSitePage);
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = key0 + i * p.page;
+        page[i] = -1;
+        if (i * p.page < kKeys && k < f_keys) {
+          page[i] = page_of(k >> p.page_log2);
+          if (page[i] >= 0) tx += 2 * part;
+          else bad = true;
+          if (mine >= k && mine < k + p.page) my_page = page[i];
+        }
+      }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, tx);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          if (page[i] >= 0) copy(page[i], 0, dst + i * part, bar);
       }
     }
-    if (lane == 0) {
-      ptx::mbar_arrive_expect_tx(bar, tx);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (want[i] && page[i] >= 0) {
-          const int64_t row = (page[i] * p.hkv + f.head) * p.page + ((key0 + i * 16) & (p.page - 1));
-          const int line = static_cast<int>(D == 128 ? row : row >> 1);
-          ptx::tma_load_2d(dst + i * part_bytes, &map_k, 0, line, bar);
-          ptx::tma_load_2d(dst + S::kHalf + i * part_bytes, &map_v, 0, line, bar);
-        }
-    }
-    if (lane < 4) {  // lane 2 i + w: scale of part i of K (w = 0) or V (w = 1)
-      const int i = parts == 2 ? lane >> 1 : 0;
-      const int64_t pg = i ? page[1] : page[0];
-      const bool need = i ? want[1] : want[0];
-      const uint32_t to = scales + st * 16 + lane * 4;
-      if (need && pg >= 0)
-        ptx::cp_async4(to, p.scale[lane & 1] + pg * p.hkv + f.head);
-      else  // no token: the smallest scale; a bad page: NaN, which reaches the rows that see it
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(need ? 0x7fffffffu : 0x1f800000u) : "memory");
+    if (lane < 2 * kSteps) {
+      copy_scale(my_page, mine < f_keys, scales + st * 32 + lane * 4);
       ptx::cp_async_arrive(bar);
     }
+    if (bad && lane == 0) kv::report(p.status, kv::kSitePage);
     --to_issue;
-    if (++f.g == f.gpi) {
+    if (++f.g == f.gpi && to_issue > kSetup) {
+      to_issue -= kSetup;
       f.g = 0;
       if (++f.block == f.blocks) {
         f.block = 0;
-        if (++f.head == p.hkv && to_issue > 0) {
+        if (++f.head == p.hkv) {
           Seq s{};
-          next_seq<RT>(p, f, s);
+          next_seq<D, RT>(p, f, s);
           f_keys = s.keys;
-          f_over = s.over;
-          page_first = -1;
+          f_last = s.over ? p.rows.max_pages - 1 : -1;
+          window = -32;
         }
       }
+    } else if (f.g == f.gpi) {
+      to_issue = 0;
     }
   };
 
+  int in_flight = 0;
   for (int i = 0; i < kSt; ++i)
-    if (to_issue > 0) issue(i);
+    if (to_issue > 0) {
+      issue(i);
+      ++in_flight;
+    }
 
   // lane's offsets inside a stage.  128-byte lines; 16-byte chunk x of line y sits at x ^ (y & 7).
-  // D = 128: a line is a key.  Key tile t holds keys 8 t + g; lane (gid, tig) reads dimensions
-  //   32 tig .. + 31 of key 8 t + gid, and dimensions 16 gid .. + 15 of four values a step of 16.
-  // D = 64: a line is two keys.  Column (2 x + y) of key tile 2 i + u is key 16 i + 4 x + 2 u + y, so
-  //   that the four values of a lane are 16 i + 4 tig + (0 .. 3), two lines.
+  // A step of 16 keys has two groups u = 0, 1 of 8, group u being rows 8 u .. 8 u + 7 of the operand.
+  // D = 128: a line is a key; row c of group u is key 8 u + c.  Lane (gid, tig) reads dimensions
+  //   32 tig .. + 31 of key c = gid, and dimensions 16 gid .. + 15 of the values of c = 2 tig, 2 tig + 1.
+  // D = 64: a line is two keys; row c of group u is key 4 (c >> 1) + 2 u + (c & 1), so that the four
+  //   values of a lane, 4 tig .. 4 tig + 3, are two lines that no other tig shares a bank with.
   uint32_t k_off[2], v_off[4];
   if (D == 128) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) k_off[j] = gid * 128 + (((2 * tig + j) ^ gid) << 4);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int r = 2 * tig + (x & 1);
-      v_off[x] = S::kHalf + (r + 8 * (x >> 1)) * 128 + ((gid ^ r) << 4);
+      const int c0 = 2 * tig + (x & 1);
+      v_off[x] = S::kHalf + (c0 + 8 * (x >> 1)) * 128 + ((gid ^ c0) << 4);
     }
   } else {
 #pragma unroll
@@ -402,219 +441,229 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
       v_off[x] = S::kHalf + line * 128 + ((((x & 1) * 4 + (gid >> 1)) ^ line) << 4) + (gid & 1) * 8;
     }
   }
-  // first of the two keys of a lane in key tile t
-  auto key_of = [&](int t) { return D == 128 ? 8 * t + 2 * tig : 16 * (t >> 1) + 4 * tig + 2 * (t & 1); };
+  // key of row c of group u in a step
+  auto key_at = [](int u, int c0) { return D == 128 ? 8 * u + c0 : 4 * (c0 >> 1) + 2 * u + (c0 & 1); };
 
-  uint32_t qf[S::kQSmem ? 1 : NT][S::kQSmem ? 1 : D / 16][4];
-  float fac[NT][kRl], m[NT][kRl], l[NT][kRl];
-  int lim[NT][kRl];
-  float acc[NT][kNd][4];
+  uint32_t qf[S::kQSmem ? 1 : NT * QP][S::kQSmem ? 1 : kMt][2];
+  // of the lane's two query rows 2 tig, 2 tig + 1 in each tile
+  float fac[NT][2], m[NT][2], l[NT][2];
+  int lim[NT][2];
+  float acc[NT][kMt][4];
   float v_ref = 1e-37f;  // largest V scale so far: P is held relative to it
+  float inv_ref = 0.0f;  // kPScale / v_ref
   int lim_min = 0, lim_max = 0;
-  int64_t row_q = 0;  // first query row (token row * group + head in group) of the block
+  int live = NT;         // tiles that have rows
+  int row_q = 0;         // first query row (token row * group + head in group) of the block
+  float* const aside = p.aside + worker * (RT * D);
+  float m_aside[NT][2], v_aside = 0.0f;  // what the values put aside refer to
+  bool flushed = false;
+  int since = 0;         // granules since then
 
   auto begin_item = [&]() {
-    row_q = static_cast<int64_t>(c.block) * RT;
-    const int64_t n_rows = static_cast<int64_t>(seq.rows) * p.group;
+    row_q = c.block * RT;
+    const int n_rows = seq.rows * p.group;
+    live = min(NT, (n_rows - row_q + 7) / 8);
     int lmin = 0x7fffffff, lmax = 0;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      // the lane's part of query row gid of the tile
+      const int rho = row_q + n * 8 + gid;
+      const bool live = rho < n_rows;
+      const int t = live ? rho / p.group : 0;
+      const int64_t at = ((seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group)) * D + tig * (D / 4);
+      int lm = live ? visible(p, seq.tokens, seq.pos0 + t) : -1;
+      if (live) {
+        lmin = min(lmin, lm);
+        lmax = max(lmax, lm);
+      }
+      float x[kMt][4];
+      float top = 0.0f;
 #pragma unroll
-      for (int r = 0; r < kRl; ++r) {
-        const int64_t rho = row_q + n * (TWO ? 8 : 16) + r * 8 + gid;
-        const bool live = rho < n_rows;
-        const int64_t t = live ? rho / p.group : 0;
-        const int64_t at = ((seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group)) * D + tig * (D / 4);
-        lim[n][r] = live ? visible(p, seq.tokens, seq.pos0 + t) : -1;
-        if (live) {
-          lmin = min(lmin, lim[n][r]);
-          lmax = max(lmax, lim[n][r]);
+      for (int j = 0; j < kMt; ++j) {
+        if (live) load4(p, at + j * 4, x[j]);
+        else x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[j][e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      // 2^e <= top < 2^(e + 1) goes to [2^14, 2^15); rows of (almost) zeros keep a finite factor
+      const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = kv::pow2(14 - e), f = p.scale_log2 * kv::pow2(e - 14);
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) {
+        uint32_t h[2], w[2];
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const float a = x[j][2 * e2] * up, b = x[j][2 * e2 + 1] * up;
+          h[e2] = to_f16x2(a, b);
+          const float2 back = from_f16x2(h[e2]);
+          w[e2] = to_f16x2(a - back.x, b - back.y);
         }
-        float x[D / 16][4];
-        float top = 0.0f;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          if (live) load4(p, at + s * 4, x[s]);
-          else x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[s][e]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^e <= top < 2^(e + 1) goes to [2^14, 2^15); rows of (almost) zeros keep a finite factor
-        const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
-        const float up = kv::pow2(14 - e);
-        fac[n][r] = p.scale_log2 * kv::pow2(e - 14);
-        m[n][r] = -INFINITY;
-        l[n][r] = 0.0f;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          uint32_t h[2], w[2];
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const float a = x[s][2 * e2] * up, b = x[s][2 * e2 + 1] * up;
-            h[e2] = to_f16x2(a, b);
-            if (TWO) {
-              const float2 back = from_f16x2(h[e2]);
-              w[e2] = to_f16x2(a - back.x, b - back.y);
-            }
-          }
-          if constexpr (S::kQSmem) {
-            const uint32_t to = q_smem + ((n * (D / 16) + s) * 32 + lane) * 16;
-            if constexpr (TWO) {
-              ptx::sts128(to, h[0], w[0], h[1], w[1]);
-            } else {
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + r * 4), "r"(h[0]) : "memory");
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 8 + r * 4), "r"(h[1]) : "memory");
-            }
-          } else if constexpr (TWO) {
-            qf[n][s][0] = h[0], qf[n][s][1] = w[0], qf[n][s][2] = h[1], qf[n][s][3] = w[1];
-          } else {
-            qf[n][s][r] = h[0], qf[n][s][2 + r] = h[1];
-          }
+        if constexpr (S::kQSmem) {
+          const uint32_t to = q_smem + ((n * QP * kMt + j) * 32 + lane) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
+          if (QP == 2)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + kMt * 256), "r"(w[0]), "r"(w[1]) : "memory");
+        } else {
+          qf[n * QP][j][0] = h[0], qf[n * QP][j][1] = h[1];
+          if (QP == 2) qf[n * QP + QP - 1][j][0] = w[0], qf[n * QP + QP - 1][j][1] = w[1];
         }
       }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);
+        lim[n][r] = __shfl_sync(kFull, lm, (2 * tig + r) * 4);
+        m[n][r] = -INFINITY;
+        l[n][r] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
     lim_min = __reduce_min_sync(kFull, lmin);
     lim_max = __reduce_max_sync(kFull, lmax);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int r = 0; r < kRl; ++r)
-        if (lim[n][r] < 0) lim[n][r] = lim_max;  // rows of nobody must not make the tile a masked one
-#pragma unroll
-      for (int j = 0; j < kNd; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
-    }
-    v_ref = 1e-37f;
-  };
-
-  // One granule; kMask: some of its keys are not seen by some row.
-  auto granule = [&](int st, auto mask_tag) {
-    constexpr bool kMask = decltype(mask_tag)::value;
-    const uint32_t tile = ring + st * S::kStage;
-    const int key0 = c.g * kKeys;
-    const uint4 sc4 = ptx::lds128u(scales + st * 16);
-    const float ks[2] = {__uint_as_float(sc4.x), __uint_as_float(sc4.z)};
-    const float vs[2] = {__uint_as_float(sc4.y), __uint_as_float(sc4.w)};
-    float s[NT][4][4];
-#pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) s[n][t][0] = s[n][t][1] = s[n][t][2] = s[n][t][3] = 0.0f;
-    {
-      // words of K: step j of 16 dimensions is the lane's j-th word of a key
-      uint32_t kw[4][D / 16];
+      for (int r = 0; r < 2; ++r)
+        if (lim[n][r] < 0) lim[n][r] = lim_max;  // rows of nobody must not make the tile a masked one
+    v_ref = 1e-37f;
+    flushed = false;
+    since = 0;
+  };
+
+  // One granule for the first kLive tiles of query rows; kMask: some of its keys are not seen by some row.
+  auto granule = [&](int st, auto live_tag, auto mask_tag) {
+    constexpr int kLive = decltype(live_tag)::value;
+    constexpr bool kMask = decltype(mask_tag)::value != 0;
+    const uint32_t tile = ring + st * S::kStage;
+    const int key0 = c.g * kKeys;
+    float ks[kSteps], vs[kSteps];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+    for (int i = 0; i < kSteps; i += 2) {
+      const uint4 v = ptx::lds128u(scales + st * 32 + i * 8);
+      ks[i] = __uint_as_float(v.x), vs[i] = __uint_as_float(v.y);
+      ks[i + 1] = __uint_as_float(v.z), vs[i + 1] = __uint_as_float(v.w);
+    }
+    // S^T: s[n][i][2 u + r] is key key_at(u, gid) of step i for query row 2 tig + r of tile n
+    float s[kLive][kSteps][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t kw[2][kMt];  // word j of the lane's part of a key: dimensions of step j
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         if (D == 128) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 v = ptx::lds128u(tile + t * 1024 + k_off[j]);
-            kw[t][4 * j] = v.x, kw[t][4 * j + 1] = v.y, kw[t][4 * j + 2] = v.z, kw[t][4 * j + 3] = v.w;
+            const uint4 v = ptx::lds128u(tile + (2 * i + u) * 1024 + k_off[j]);
+            kw[u][4 * j] = v.x, kw[u][4 * j + 1] = v.y, kw[u][4 * j + 2] = v.z, kw[u][4 * j + 3] = v.w;
           }
         } else {
-          const uint4 v = ptx::lds128u(tile + (t >> 1) * 1024 + k_off[t & 1]);
-          kw[t][0] = v.x, kw[t][1] = v.y, kw[t][2] = v.z, kw[t][3] = v.w;
+          const uint4 v = ptx::lds128u(tile + i * 1024 + k_off[u]);
+          kw[u][0] = v.x, kw[u][1] = v.y, kw[u][2] = v.z, kw[u][3] = v.w;
         }
       }
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t a[NT][4];
+      for (int n = 0; n < kLive; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+      for (int j = 0; j < kMt; ++j) {
+        const uint32_t a[4] = {kv::e4m3x2_to_f16x2(kw[0][j]), kv::e4m3x2_to_f16x2(kw[1][j]),
+                               kv::e4m3x2_to_f16x2(kw[0][j] >> 16), kv::e4m3x2_to_f16x2(kw[1][j] >> 16)};
+#pragma unroll
+        for (int n = 0; n < kLive * QP; ++n) {
           if constexpr (S::kQSmem) {
-            const uint4 v = ptx::lds128u(q_smem + ((n * (D / 16) + j) * 32 + lane) * 16);
-            a[n][0] = v.x, a[n][1] = v.y, a[n][2] = v.z, a[n][3] = v.w;
+            const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
+            ptx::mma_f16(s[n / QP][i], a, b.x, b.y);
           } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[n][e] = qf[n][j][e];
+            ptx::mma_f16(s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
           }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t b0 = kv::e4m3x2_to_f16x2(kw[t][j]), b1 = kv::e4m3x2_to_f16x2(kw[t][j] >> 16);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) ptx::mma_f16(s[n][t], a[n], b0, b1);
         }
       }
     }
-    // scores, maxima
-    float corr[NT][kRl];
+    // Maxima.  s keeps the products; a score is s * f2 (f2 > 0), and only masked tiles, where an unseen
+    // page's scale may be anything, hold scores themselves.
+    float corr[kLive][2], f2[kLive][2][kSteps];
     bool grew = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < kLive; ++n)
 #pragma unroll
-      for (int r = 0; r < kRl; ++r) {
+      for (int r = 0; r < 2; ++r) {
         float top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float f2 = fac[n][r] * ks[t >> 1];
+        for (int i = 0; i < kSteps; ++i) {
+          f2[n][r][i] = fac[n][r] * ks[i];
+          if (kMask) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float z = TWO ? s[n][t][e] + s[n][t][2 + e] : s[n][t][2 * r + e];
-            z *= f2;
-            if (kMask && key0 + key_of(t) + e >= lim[n][r]) z = -INFINITY;
-            s[n][t][2 * r + e] = z;
-            top = fmaxf(top, z);
+            for (int u = 0; u < 2; ++u) {
+              float& z = s[n][i][2 * u + r];
+              z = key0 + 16 * i + key_at(u, gid) >= lim[n][r] ? -INFINITY : z * f2[n][r][i];
+            }
           }
+          const float top2 = fmaxf(s[n][i][r], s[n][i][2 + r]);
+          top = fmaxf(top, kMask ? top2 : top2 * f2[n][r][i]);
         }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
         const bool up = top > m[n][r];
         grew |= up;
         const float now = up ? top : m[n][r];
         corr[n][r] = now == -INFINITY ? 1.0f : ex2(m[n][r] - now);
         m[n][r] = now;
       }
-    const float v_top = fmaxf(v_ref, fmaxf(vs[0], vs[1]));
+    float v_top = v_ref;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) v_top = fmaxf(v_top, vs[i]);
     if (__any_sync(kFull, grew || v_top > v_ref)) {
       const float rr = v_ref / v_top;
       v_ref = v_top;
+      inv_ref = kPScale / v_top;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < kLive; ++n) {
+        l[n][0] *= corr[n][0];
+        l[n][1] *= corr[n][1];
+        const float c0 = corr[n][0] * rr, c1 = corr[n][1] * rr;
 #pragma unroll
-        for (int r = 0; r < kRl; ++r) l[n][r] *= corr[n][r];
-        const float c0 = corr[n][0] * rr, c1 = corr[n][kRl - 1] * rr;
-#pragma unroll
-        for (int j = 0; j < kNd; ++j) {
+        for (int j = 0; j < kMt; ++j) {
           acc[n][j][0] *= c0;
-          acc[n][j][1] *= c0;
-          acc[n][j][2] *= c1;
+          acc[n][j][1] *= c1;
+          acc[n][j][2] *= c0;
           acc[n][j][3] *= c1;
         }
       }
     }
-    // weights and their operands
-    uint32_t pa[NT][2][4];
-    const float inv_ref = kPScale / v_ref;
-    const float vf[2] = {vs[0] * inv_ref, vs[1] * inv_ref};
+    // Weights as operands: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid
+    uint32_t pb[kLive][PP][kSteps][2];
+    float vf[kSteps];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < kSteps; ++i) vf[i] = vs[i] * inv_ref;
 #pragma unroll
-      for (int r = 0; r < kRl; ++r) {
-        const float ref = m[n][r] == -INFINITY ? 0.0f : m[n][r];
+    for (int n = 0; n < kLive; ++n) {
+      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float a = ex2(s[n][t][2 * r] - ref), b = ex2(s[n][t][2 * r + 1] - ref);
-          l[n][r] += a + b;
-          float av = a * vf[t >> 1], bv = b * vf[t >> 1];
-          if (kMask) {  // an unseen page's scale may be NaN
-            if (s[n][t][2 * r] == -INFINITY) av = 0.0f;
-            if (s[n][t][2 * r + 1] == -INFINITY) bv = 0.0f;
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float pv[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float z = s[n][i][2 * u + r];
+            const float w = ex2(kMask ? z - ref[r] : fmaf(z, f2[n][r][i], -ref[r]));
+            l[n][r] += w;
+            pv[r] = w * vf[i];
+            if (kMask && z == -INFINITY) pv[r] = 0.0f;  // an unseen page's scale may be NaN
           }
-          const uint32_t h = to_f16x2(av, bv);
-          // operand register: row gid (+ 8) of the even or odd key tile of a step
-          if constexpr (TWO) {
+          const uint32_t h = to_f16x2(pv[0], pv[1]);
+          pb[n][0][i][u] = ptx::transpose8x8(h);
+          if constexpr (PP == 2) {
             const float2 back = from_f16x2(h);
-            pa[n][t >> 1][2 * (t & 1)] = h;
-            pa[n][t >> 1][2 * (t & 1) + 1] = to_f16x2(av - back.x, bv - back.y);
-          } else {
-            pa[n][t >> 1][2 * (t & 1) + r] = h;
+            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(pv[0] - back.x, pv[1] - back.y));
           }
         }
-      }
-    // O += P V
+    }
+    // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
       uint32_t vw[4][D / 32];
       bool odd = false;
 #pragma unroll
@@ -628,7 +677,7 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
         }
         if (kMask) {
           // what no row sees counts as zero: 0 * NaN would not vanish
-          const int key = key0 + 16 * i + (D == 128 ? 2 * tig + (x & 1) + 8 * (x >> 1) : 4 * tig + x);
+          const int key = key0 + 16 * i + key_at(x >> 1, 2 * tig + (x & 1));
           if (key >= lim_max) {
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) vw[x][w] = 0u;
@@ -640,19 +689,18 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
       }
       if (kMask && __any_sync(kFull, odd)) {
         // NaN among values that only some of the rows see: those rows get NaN by a product of the
-        // rows' visibility with the places of the NaN, and the NaN are taken out of V.
-        uint32_t va[NT][4];
+        // places of the NaN with the rows' visibility, and the NaN are taken out of V.
+        uint32_t vis[kLive][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < kLive; ++n) {
+          const int l0 = __shfl_sync(kFull, lim[n][0], gid >> 1), l1 = __shfl_sync(kFull, lim[n][1], gid >> 1);
+          const int lm = (gid & 1) ? l1 : l0;  // of query row gid
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int k = key0 + key_of(2 * i + u);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int lm = r < kRl ? lim[n][r < kRl ? r : 0] : 0;
-              va[n][2 * u + r] = (k < lm ? 0x3c00u : 0u) | (k + 1 < lm ? 0x3c000000u : 0u);
-            }
+            const int k = key0 + 16 * i + key_at(u, 2 * tig);
+            vis[n][u] = (k < lm ? 0x3c00u : 0u) | (k + 1 < lm ? 0x3c000000u : 0u);
           }
+        }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           uint32_t at[4];
@@ -663,93 +711,146 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
             vw[x][w] &= ~nan;
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t sel = (e & 1) * 0x11u + (e >> 1) * 0x22u;
-            const uint32_t b0 = kv::e4m3x2_to_f16x2(__byte_perm(at[0], at[1], 0x40u + sel));
-            const uint32_t b1 = kv::e4m3x2_to_f16x2(__byte_perm(at[2], at[3], 0x40u + sel));
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a = __byte_perm(at[0], at[1], half ? 0x7362 : 0x5140);
+            const uint32_t b = __byte_perm(at[2], at[3], half ? 0x7362 : 0x5140);
+            const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
+                                    kv::e4m3x2_to_f16x2(b >> 16)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < kLive; ++n) {
               float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              ptx::mma_f16(hit, va[n], b0, b1);
+              ptx::mma_f16(hit, av, vis[n][0], vis[n][1]);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (hit[k] > 0.0f) acc[n][4 * w + e][k] = __int_as_float(0x7fffffff);
+                if (hit[k] > 0.0f) acc[n][2 * w + half][k] = __int_as_float(0x7fffffff);
             }
           }
         }
       }
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        // bytes of two keys side by side: columns 4 w, 4 w + 1 and 4 w + 2, 4 w + 3
-        const uint32_t a01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), b01 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-        const uint32_t a23 = __byte_perm(vw[0][w], vw[1][w], 0x7362), b23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        const uint32_t b0[4] = {kv::e4m3x2_to_f16x2(a01), kv::e4m3x2_to_f16x2(a01 >> 16), kv::e4m3x2_to_f16x2(a23),
-                                kv::e4m3x2_to_f16x2(a23 >> 16)};
-        const uint32_t b1[4] = {kv::e4m3x2_to_f16x2(b01), kv::e4m3x2_to_f16x2(b01 >> 16), kv::e4m3x2_to_f16x2(b23),
-                                kv::e4m3x2_to_f16x2(b23 >> 16)};
+      for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int half = 0; half < 2; ++half) {  // columns 4 w + 2 half, + 1: bytes of two keys side by side
+          const uint32_t a = __byte_perm(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
+          const uint32_t b = __byte_perm(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
+          const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
+                                  kv::e4m3x2_to_f16x2(b >> 16)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) ptx::mma_f16(acc[n][4 * w + e], pa[n][i], b0[e], b1[e]);
-      }
+          for (int n = 0; n < kLive; ++n)
+#pragma unroll
+            for (int part = 0; part < PP; ++part)
+              ptx::mma_f16(acc[n][2 * w + half], av, pb[n][part][i][0], pb[n][part][i][1]);
+        }
     }
   };
 
-  // The lane's part of a row: columns tig * D / 4 .. + D / 4 - 1, the first half from the even
-  // column of the accumulators, the second from the odd one.
+  // The same for the tiles that the block has: sequences differ in their rows.
+  auto granule_live = [&](int st, auto mask_tag) {
+    if constexpr (NT == 1) {
+      granule(st, Int<1>{}, mask_tag);
+    } else if constexpr (NT == 2) {
+      if (live == 1) granule(st, Int<1>{}, mask_tag);
+      else granule(st, Int<2>{}, mask_tag);
+    } else {
+      if (live == 1) granule(st, Int<1>{}, mask_tag);
+      else if (live == 2) granule(st, Int<2>{}, mask_tag);
+      else if (live == 3) granule(st, Int<3>{}, mask_tag);
+      else granule(st, Int<4>{}, mask_tag);
+    }
+  };
+
+  // Columns 4 j .. 4 j + 3 of the lane's part of query row 2 tig + r of tile n: the accumulators, with
+  // what was put aside (`from`) at weight `keep`.
+  auto four = [&](int n, int r, int j, const float* from, float keep, float (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = acc[n][2 * j + (e >> 1)][2 * (e & 1) + r];
+    if (flushed) {
+      const float4 y = *reinterpret_cast<const float4*>(from + 4 * j);
+      x[0] = fmaf(y.x, keep, x[0]), x[1] = fmaf(y.y, keep, x[1]);
+      x[2] = fmaf(y.z, keep, x[2]), x[3] = fmaf(y.w, keep, x[3]);
+    }
+  };
+
+  // Puts the accumulators aside: adds them to the worker's rows in the workspace and clears them.
+  // The tensor cores' fp32 sums are truncated, which adds up to 1e-5 over a thousand granules; with
+  // kFlush granules to a sum it stays near 1e-6, however long the cache.
+  auto flush = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float* const at = aside + (n * 8 + 2 * tig + r) * D + gid * kCols;
+        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, at, keep, x);
+          *reinterpret_cast<float4*>(at + 4 * j) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        m_aside[n][r] = m[n][r];
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
+    v_aside = v_ref;
+    flushed = true;
+    since = 0;
+  };
+
+  // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial.
   auto end_item = [&](bool whole, int slot) {
-    const int64_t n_rows = static_cast<int64_t>(seq.rows) * p.group;
+    const int n_rows = seq.rows * p.group;
     const float back = v_ref * (1.0f / kPScale);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < kRl; ++r) {
+      for (int r = 0; r < 2; ++r) {
         float sum = l[n][r];
-        sum += __shfl_xor_sync(kFull, sum, 1);
-        sum += __shfl_xor_sync(kFull, sum, 2);
-        const int local = n * (TWO ? 8 : 16) + r * 8 + gid;
-        const int64_t rho = row_q + local;
+        sum += __shfl_xor_sync(kFull, sum, 4);
+        sum += __shfl_xor_sync(kFull, sum, 8);
+        sum += __shfl_xor_sync(kFull, sum, 16);
+        const int local = n * 8 + 2 * tig + r;
+        const int rho = row_q + local;
         if (rho >= n_rows) continue;
-        const float f2 = whole ? (sum == 0.0f ? 0.0f : back / sum) : back;
-        float* const part =
-            p.part_o + ((worker * 2 + slot) * RT + local) * D + tig * (D / 4);
-        const int64_t t = rho / p.group;
+        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
+        const float f = whole ? (sum == 0.0f ? 0.0f : back / sum) : back;
+        float* const part = p.part_o + ((worker * 2 + slot) * RT + local) * D + gid * kCols;
+        const int t = rho / p.group;
         const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
 #pragma unroll
-        for (int odd = 0; odd < 2; ++odd)
-#pragma unroll
-          for (int j = 0; j < kNd; j += 4) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = (TWO ? acc[n][j + e][odd] + acc[n][j + e][2 + odd] : acc[n][j + e][2 * r + odd]) * f2;
-            const int col = odd * kNd + j;
-            if (whole) store_row4(p, out * D + tig * (D / 4) + col, x[0], x[1], x[2], x[3]);
-            else *reinterpret_cast<float4*>(part + col) = make_float4(x[0], x[1], x[2], x[3]);
-          }
-        if (tig == 0) {
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, aside + local * D + gid * kCols, keep, x);
+          if (whole) store_row4(p, out * D + gid * kCols + 4 * j, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+          else *reinterpret_cast<float4*>(part + 4 * j) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        }
+        if (gid == 0) {
           if (whole) p.lse[out] = sum == 0.0f ? -INFINITY : (m[n][r] + log2f(sum)) * kLn2;
           else p.part_ml[(worker * 2 + slot) * RT + local] = make_float2(m[n][r], sum);
         }
       }
   };
 
+  // A stage is mostly there already: the clock that bounds the wait is read only where it is not.
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+  };
   int st = 0;
   uint32_t parity = 0;
-  bool first = true;       // the item at hand is the one the share begins in
-  int item_from = c.g;     // first granule of it that is ours
+  bool from_start = c.g == 0;  // the item at hand is ours from its first granule on
   bool ok = true;
   begin_item();
-  while (left > 0) {
-    if (!sync::wait_warp(bars + st * 8, parity, ctl, kv::kSiteWait)) {
+  while (true) {
+    if (!wait(bars + st * 8, parity)) {
       ok = false;
       break;
     }
     const int key0 = c.g * kKeys;
-    if (key0 + kKeys <= lim_min) granule(st, No{});
-    else if (key0 < lim_max) granule(st, Yes{});
+    if (key0 + kKeys <= lim_min) granule_live(st, Int<0>{});
+    else if (key0 < lim_max) granule_live(st, Int<1>{});
     __syncwarp();
     if (to_issue > 0) issue(st);
+    else --in_flight;
     if (++st == kSt) {
       st = 0;
       parity ^= 1u;
@@ -757,24 +858,25 @@ __global__ void __launch_bounds__(Shape<D, NT, TWO>::kWarps * 32, 1)
     --left;
     ++c.g;
     if (c.g == c.gpi || left == 0) {
-      const bool whole = item_from == 0 && c.g == c.gpi;
-      end_item(whole, first || item_from != 0 ? 0 : 1);
-      if (left > 0) {
-        c.g = 0;
-        item_from = 0;
-        // the first item keeps slot 0 even where the share begins at its first granule
-        first = false;
-        if (++c.block == c.blocks) {
-          c.block = 0;
-          if (++c.head == p.hkv) next_seq<RT>(p, c, seq);
-        }
-        begin_item();
+      end_item(from_start && c.g == c.gpi, inside ? 0 : 1);
+      left -= kSetup;  // of the next item
+      if (left <= 0) break;
+      c.g = 0;
+      from_start = true;
+      inside = false;
+      if (++c.block == c.blocks) {
+        c.block = 0;
+        if (++c.head == p.hkv) next_seq<D, RT>(p, c, seq);
       }
+      begin_item();
+    } else if (++since == kFlush) {
+      flush();
     }
   }
   if (!ok) {
-    // copies in flight must not outlive the block: `left` granules are waited for, as many as stages
-    for (int i = 0; i < kSt && i < left; ++i) {
+    // copies in flight must not outlive the block: those of this granule and, where there was more to
+    // copy, of the next
+    for (int i = 0; i < in_flight; ++i) {
       sync::wait_drain(bars + st * 8, parity, p.timeout_ns);
       if (++st == kSt) {
         st = 0;
@@ -800,20 +902,30 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) kv_attn_combine_ker
   const int64_t id = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
   const int64_t row = id / p.hq;
   const int h = static_cast<int>(id - row * p.hq);
-  if (row >= p.rows.n_rows) return;
-  const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
-  const Seq seq = seq_of<RT>(p, b);
+  int b = 0;
+  Seq seq{};
+  if (row < p.rows.n_rows) {
+    b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+    seq = seq_of<D, RT>(p, b);
+  }
+  // Every thread waits, also one without work: the kernel behind this one may begin once this grid is
+  // through, and must not meet the first kernel's blocks.
+  ptx::wait_dependencies();
   if (row < seq.r0 || row >= seq.r0 + seq.rows) return;
   const int head = h / p.group;
-  const int64_t rho = (row - seq.r0) * p.group + (h - head * p.group);
-  const int64_t block = rho / RT;
-  const int local = static_cast<int>(rho - block * RT);
-  ptx::wait_dependencies();
-  const int64_t W = p.plan[p.rows.n_seqs], n = workers(W, cp.most);
-  const int64_t from = p.plan[b] + (head * static_cast<int64_t>(seq.blocks) + block) * seq.gpi;
-  const int64_t w0 = worker_of(W, n, from), w1 = worker_of(W, n, from + seq.gpi - 1);
-  if (w0 == w1) return;  // finished by its worker
-  auto place = [&](int64_t w) { return (w * 2 + (share(W, n, w) < from ? 1 : 0)) * RT + local; };
+  const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
+  const int block = rho / RT, local = rho - block * RT;
+  int64_t w0 = 0, w1 = -1;
+  int slot0 = 0;
+  if (seq.blocks > 0) {
+    const int64_t W = p.plan[p.rows.n_seqs], n = workers(W, cp.most);
+    const int64_t from = p.plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
+    w0 = worker_of(W, n, from);
+    w1 = worker_of(W, n, from + seq.gpi - 1);
+    if (w0 == w1) return;  // finished by its worker
+    slot0 = share(W, n, w0) < from ? 1 : 0;  // the later ones begin inside of the item
+  }
+  auto place = [&](int64_t w) { return (w * 2 + (w == w0 ? slot0 : 0)) * RT + local; };
 
   const int sub = WPR == 1 ? 0 : warp;
   float top = -INFINITY, sum = 0.0f;
@@ -887,43 +999,41 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) kv_attn_combine_ker
 
 // The variant for a call: by the query rows that a sequence has on average.
 struct Plan {
-  int nt;
-  bool two;
+  int nt, qp, pp;
   int rows;      // RT
+  int warps;     // of a block
   int64_t grid;
-  int64_t plan_off, ml_off, o_off, bytes;
+  int64_t plan_off, ml_off, o_off, aside_off, bytes;
 };
 Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   Plan r;
   const int64_t group = d.hq / d.cache.hkv, seqs = d.rows.n_seqs > 0 ? d.rows.n_seqs : 1;
   const int64_t per = (d.rows.n_rows + seqs - 1) / seqs * group;
-  const bool narrow = d.in_dtype == CP_BF16 && d.o_dtype == CP_BF16;
-  r.two = per <= 8 || !narrow;
-  r.nt = per <= (r.two ? 8 : 16) ? 1 : 2;
-  r.rows = r.nt * (r.two ? 8 : 16);
-  const int64_t most = ((static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size + kKeys - 1) / kKeys) * d.cache.hkv *
+  r.qp = d.in_dtype == CP_BF16 ? 1 : 2;
+  r.pp = d.in_dtype == CP_BF16 && d.o_dtype == CP_BF16 ? 1 : 2;
+  r.nt = per <= (d.cache.d == 128 ? 8 : 32) ? 1 : 2;
+  r.rows = r.nt * 8;
+  r.warps = r.nt * d.cache.d >= 256 || r.nt * r.qp >= 4 ? 8 : 12;
+  const int64_t most = ((static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096 + kSetup) * d.cache.hkv *
                        (seqs + d.rows.n_rows * group / r.rows);
   r.grid = most < sms ? (most < 1 ? 1 : most) : sms;
-  const int64_t slots = r.grid * 8 * 2 * r.rows;
+  const int64_t slots = r.grid * r.warps * 2 * r.rows;
   r.plan_off = 0;
   r.ml_off = (seqs + 1) * 8;
   r.o_off = (r.ml_off + slots * 8 + 255) / 256 * 256;
-  r.bytes = r.o_off + slots * d.cache.d * 4;
+  r.aside_off = r.o_off + slots * d.cache.d * 4;
+  r.bytes = r.aside_off + slots / 2 * d.cache.d * 4;
   return r;
 }
 
-template <int D, int NT, bool TWO>
+template <int D, int NT, int QP, int PP>
 cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
               cudaStream_t s) {
-  using S = Shape<D, NT, TWO>;
+  using S = Shape<D, NT, QP, PP>;
+  static_assert(1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8 <= 232448, "shared memory of a block");
   const int smem = 1024 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, NT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, NT, QP, PP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel attribute");
-  kv_attn_kernel<D, NT, TWO><<<static_cast<unsigned>(pl.grid), S::kWarps * 32, smem, s>>>(p, mk, mv);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
-  CombineParams cp{p, pl.grid * S::kWarps};
-  // with few items each is cut into many partials: more warps for each output row
-  const int64_t parts = cp.most / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -931,13 +1041,21 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  if (parts > 16) {
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid));
+  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT, QP, PP>, p, mk, mv)) != cudaSuccess)
+    return cuda_fail(e, "kv_attn_kernel launch");
+  CombineParams cp{p, pl.grid * S::kWarps};
+  // Eight warps an output row while there are few rows, or many partials to a row; else one.
+  const int64_t parts = cp.most / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
+  cfg.dynamicSmemBytes = 0;
+  cfg.blockDim = dim3(256);
+  if (parts > 16 || outs <= 1024) {
     cfg.gridDim = dim3(static_cast<unsigned>(outs));
-    cfg.blockDim = dim3(256);
     e = cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 8>, cp);
   } else {
     cfg.gridDim = dim3(static_cast<unsigned>((outs + 7) / 8));
-    cfg.blockDim = dim3(256);
     e = cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 1>, cp);
   }
   return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv_attn_combine_kernel launch");
@@ -946,8 +1064,13 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
 template <int D>
 cp_status run_d(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
                 cudaStream_t s) {
-  if (pl.two) return pl.nt == 1 ? run<D, 1, true>(p, pl, mk, mv, items, s) : run<D, 2, true>(p, pl, mk, mv, items, s);
-  return pl.nt == 1 ? run<D, 1, false>(p, pl, mk, mv, items, s) : run<D, 2, false>(p, pl, mk, mv, items, s);
+  if (pl.pp == 1)
+    return pl.nt == 1   ? run<D, 1, 1, 1>(p, pl, mk, mv, items, s)
+           : pl.nt == 2 ? run<D, 2, 1, 1>(p, pl, mk, mv, items, s)
+                        : run<D, 4, 1, 1>(p, pl, mk, mv, items, s);
+  if (pl.qp == 1)
+    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, s) : run<D, 2, 1, 2>(p, pl, mk, mv, items, s);
+  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, s) : run<D, 2, 2, 2>(p, pl, mk, mv, items, s);
 }
 
 }  // namespace
@@ -958,7 +1081,8 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   const Plan pl = plan_of(d, num_sms);
   const cp_kv_cache& c = d.cache;
   const int64_t lines = c.n_pages * c.hkv * c.page_size * c.d / 128;
-  const int box = (c.page_size < kKeys ? c.page_size : kKeys) * c.d / 128;
+  const int keys = 4096 / c.d;
+  const int box = (c.page_size < keys ? c.page_size : keys) * c.d / 128;
   CUtensorMap mk, mv;
   if (!encode_map_bytes(&mk, c.k, lines, box) || !encode_map_bytes(&mv, c.v, lines, box)) {
     set_error("cp_kv_cache_attn: tensor map encoding failed");
@@ -993,6 +1117,7 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   p.plan = reinterpret_cast<int64_t*>(ws + pl.plan_off);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + pl.o_off);
+  p.aside = reinterpret_cast<float*>(ws + pl.aside_off);
   const int64_t seqs = d.rows.n_seqs;
   const int64_t items = (seqs + d.rows.n_rows * p.group / pl.rows) * c.hkv;
   return c.d == 128 ? run_d<128>(p, pl, mk, mv, items, s) : run_d<64>(p, pl, mk, mv, items, s);

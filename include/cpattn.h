@@ -414,7 +414,7 @@ typedef struct {
 } cp_kv_cache;
 
 /* Largest number of sequences one call takes. */
-#define CP_KV_MAX_SEQS 4096
+#define CP_KV_MAX_SEQS 2048
 
 /*
  * The rows of a call: n_rows packed token rows, those of sequence b being
