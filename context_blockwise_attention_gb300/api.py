@@ -8,6 +8,7 @@ message.  The library must be built (``__graft_entry__.build()``); there is no f
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -149,16 +150,15 @@ def load_library():
     lib.cp_ulysses_reshard.argtypes = [i32, i32, i64, i32, ctypes.POINTER(i32), i32, i32, i32,
                                        ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
     lib.cp_kv_cache_write.restype = i32
-    lib.cp_kv_cache_write.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvRows), vp, vp, i32, vp, vp]
+    lib.cp_kv_cache_write.argtypes = [vp, vp, vp, vp, i32, vp, vp]
     lib.cp_kv_cache_read.restype = i32
-    lib.cp_kv_cache_read.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvRows), vp, vp, i32, vp, vp]
+    lib.cp_kv_cache_read.argtypes = [vp, vp, vp, vp, i32, vp, vp]
     lib.cp_kv_cache_attn.restype = i32
-    lib.cp_kv_cache_attn.argtypes = [ctypes.POINTER(_KvAttnDesc), vp]
+    lib.cp_kv_cache_attn.argtypes = [vp, vp]
     lib.cp_kv_cache_attn_workspace.restype = i32
-    lib.cp_kv_cache_attn_workspace.argtypes = [ctypes.POINTER(_KvAttnDesc), ctypes.POINTER(i64)]
+    lib.cp_kv_cache_attn_workspace.argtypes = [vp, ctypes.POINTER(i64)]
     lib.cp_rope_axes.restype = i32
-    lib.cp_rope_axes.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i32), i64, i32, i32,
-                                 i32, vp, i32, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double), i32, i32, vp]
+    lib.cp_rope_axes.argtypes = [i32, vp, vp, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, i32, vp]
     _lib = lib
     return lib
 
@@ -608,32 +608,46 @@ def _invalid(message):
     raise CpError(CP_ERR_INVALID_ARG, message)
 
 
-def _need(t, name, dtype, device):
-    """A contiguous CUDA tensor of ``dtype`` on ``device``."""
+# The calls below serve single tokens, where the time on the host counts: one check a tensor, and the
+# descriptors packed in one go.
+_CACHE_ROWS = struct.Struct("@4Pq4i3P2iq")                  # cp_kv_cache, cp_kv_rows
+_KV_ATTN = struct.Struct("@4Pq4i3P2iq4P3if2qPqP2i")         # cp_kv_attn_desc
+_CODES = {torch.float32: CP_F32, torch.bfloat16: CP_BF16}
+
+
+def _ptr(t, name, dtype, index):
+    """The address of a contiguous tensor of ``dtype`` on CUDA device ``index``."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _invalid(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         _invalid(f"{name} must be contiguous")
     if t.dtype != dtype:
         _invalid(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        _invalid(f"{name} is on {t.device}, not on {device}")
+    _invalid(f"{name} is on device {t.get_device()}, not on device {index}")
 
 
-class _on_device:
-    """Makes ``device`` current for a call whose tensors live there."""
-    __slots__ = ("guard",)
+def _index(t, name):
+    """The CUDA device of ``t``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _invalid(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+def _elsewhere(index):
+    """Whether another device than ``index`` is the current one."""
+    return index != torch._C._cuda_getDevice()
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _stream_of(stream, index):
+    """The raw stream of a call: the one given, or the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _new(shape, dtype, device, stream):
@@ -647,43 +661,41 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _cache_struct(cache):
+def _cache_fields(cache, index):
     k, v, k_scale, v_scale = cache
-    if not isinstance(k, torch.Tensor) or not k.is_cuda:
-        _invalid("cache.k must be a CUDA tensor")
-    dev = k.device
-    _need(k, "cache.k", torch.float8_e4m3fn, dev)
-    _need(v, "cache.v", torch.float8_e4m3fn, dev)
-    _need(k_scale, "cache.k_scale", torch.float32, dev)
-    _need(v_scale, "cache.v_scale", torch.float32, dev)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    ptrs = (_ptr(k, "cache.k", f8, index), _ptr(v, "cache.v", f8, index),
+            _ptr(k_scale, "cache.k_scale", f32, index), _ptr(v_scale, "cache.v_scale", f32, index))
     shape = k.shape
     if len(shape) != 4 or v.shape != shape:
         _invalid("cache.k and cache.v must be [pages, Hkv, page_size, D]")
     n_pages, hkv, page_size, d = shape
-    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+    if k_scale.shape != (n_pages, hkv) or v_scale.shape != (n_pages, hkv):
         _invalid("cache.k_scale and cache.v_scale must be [pages, Hkv]")
-    return _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page_size, hkv, d, 0)
+    return (*ptrs, n_pages, page_size, hkv, d, 0)
 
 
-def _rows_struct(row_start, tokens, name, page_table, n_rows, device):
-    _need(row_start, "row_start", torch.int32, device)
-    _need(tokens, name, torch.int32, device)
-    _need(page_table, "page_table", torch.int32, device)
-    if row_start.dim() != 1 or tokens.dim() != 1 or page_table.dim() != 2:
+def _rows_fields(row_start, tokens, name, page_table, n_rows, index):
+    i32 = torch.int32
+    ptrs = (_ptr(row_start, "row_start", i32, index), _ptr(tokens, name, i32, index),
+            _ptr(page_table, "page_table", i32, index))
+    table = page_table.shape
+    if len(table) != 2 or row_start.shape != (table[0] + 1,) or tokens.shape != (table[0],):
         _invalid(f"row_start must be [seqs + 1], {name} [seqs], page_table [seqs, pages]")
-    n_seqs, max_pages = page_table.shape
-    if row_start.shape[0] != n_seqs + 1 or tokens.shape[0] != n_seqs:
-        _invalid(f"row_start must be [seqs + 1], {name} [seqs], page_table [seqs, pages]")
-    return _KvRows(row_start.data_ptr(), tokens.data_ptr(), page_table.data_ptr(), n_seqs, max_pages, n_rows)
+    return (*ptrs, table[0], table[1], n_rows)
 
 
-def _status_ptr(status, device):
+def _status_ptr(status, index):
     if status is None:
-        return None
-    _need(status, "status", torch.int32, device)
+        return 0
     if status.numel() < 1:
         _invalid("status must hold one int32")
-    return status.data_ptr()
+    return _ptr(status, "status", torch.int32, index)
+
+
+def _code(dtype):
+    code = _CODES.get(dtype)
+    return _dtype_code(dtype) if code is None else code
 
 
 def kv_cache_write(cache, k, v, row_start, cached, page_table, status=None, stream=None):
@@ -692,18 +704,20 @@ def kv_cache_write(cache, k, v, row_start, cached, page_table, status=None, stre
     tokens ``i * page_size ..`` is ``page_table[b, i]``.  ``row_start`` [seqs + 1], ``cached`` [seqs]
     and ``page_table`` [seqs, pages] are int32 CUDA tensors.  Returns ``cache``."""
     lib = load_library()
-    c = _cache_struct(cache)
-    dev = cache.k.device
-    dt = k.dtype if isinstance(k, torch.Tensor) else None
-    code = _dtype_code(dt)
-    _need(k, "k", dt, dev)
-    _need(v, "v", dt, dev)
-    if k.dim() != 3 or v.shape != k.shape or k.shape[1] != c.hkv or k.shape[2] != c.d:
+    index = _index(k, "k")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv_cache_write(cache, k, v, row_start, cached, page_table, status, stream)
+    dt = k.dtype
+    code = _code(dt)
+    pk, pv = _ptr(k, "k", dt, index), _ptr(v, "v", dt, index)
+    c = _cache_fields(cache, index)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != c[6] or shape[2] != c[7]:
         _invalid("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
-    r = _rows_struct(row_start, cached, "cached", page_table, k.shape[0], dev)
-    with _on_device(dev):
-        _check(lib.cp_kv_cache_write(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), code,
-                                     _status_ptr(status, dev), _stream(stream)))
+    desc = _CACHE_ROWS.pack(*c, *_rows_fields(row_start, cached, "cached", page_table, shape[0], index))
+    _check(lib.cp_kv_cache_write(desc, desc[56:], pk, pv, code, _status_ptr(status, index),
+                                 _stream_of(stream, index)))
     return cache
 
 
@@ -713,28 +727,30 @@ def kv_cache_read(cache, row_start, first, page_table, n_rows, dtype=torch.bfloa
     [n_rows, Hkv, D] hold the tokens ``first[b], first[b] + 1, ...`` of sequence b.  Rows of no
     sequence are left as they were (undefined where this call allocates them)."""
     lib = load_library()
-    c = _cache_struct(cache)
-    dev = cache.k.device
-    if k is not None and isinstance(k, torch.Tensor):
+    index = _index(cache[0], "cache.k")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv_cache_read(cache, row_start, first, page_table, n_rows, dtype, k, v, status, stream)
+    if isinstance(k, torch.Tensor):
         dtype = k.dtype
-    code = _dtype_code(dtype)
-    shape = (int(n_rows), c.hkv, c.d)
-    r = _rows_struct(row_start, first, "first", page_table, int(n_rows), dev)
-    with _on_device(dev):
-        if k is None:
-            k = _new(shape, dtype, dev, stream)
-        if v is None:
-            v = _new(shape, dtype, dev, stream)
-        _need(k, "k", dtype, dev)
-        _need(v, "v", dtype, dev)
-        if tuple(k.shape) != shape or tuple(v.shape) != shape:
-            _invalid("k and v must be [n_rows, Hkv, D] with the cache's Hkv and D")
-        _check(lib.cp_kv_cache_read(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), code,
-                                    _status_ptr(status, dev), _stream(stream)))
+    code = _code(dtype)
+    c = _cache_fields(cache, index)
+    shape = (n_rows, c[6], c[7])
+    desc = _CACHE_ROWS.pack(*c, *_rows_fields(row_start, first, "first", page_table, n_rows, index))
+    dev = cache[0].device
+    k = _new(shape, dtype, dev, stream) if k is None else k
+    v = _new(shape, dtype, dev, stream) if v is None else v
+    pk, pv = _ptr(k, "k", dtype, index), _ptr(v, "v", dtype, index)
+    if k.shape != shape or v.shape != shape:
+        _invalid("k and v must be [n_rows, Hkv, D] with the cache's Hkv and D")
+    _check(lib.cp_kv_cache_read(desc, desc[56:], pk, pv, code, _status_ptr(status, index), _stream_of(stream, index)))
     return k, v
 
 
-def kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos=PosMap(0, 1), scale=0.0, o=None,
+_POS0 = PosMap(0, 1)
+
+
+def kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos=_POS0, scale=0.0, o=None,
                   lse=None, o_dtype=None, workspace=None, flags=0, status=None, wait_timeout_ms=0, stream=None):
     """(O, LSE) partial of each sequence's new rows ``q`` [rows, Hq, D] over its ``kv_lens[b]`` cached
     tokens (write the new tokens first if they are to be seen).
@@ -746,64 +762,63 @@ def kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos
     allocate; it needs ``kv_cache_attn_workspace(...)`` bytes and belongs to one call at a time.
     """
     lib = load_library()
-    c = _cache_struct(cache)
-    dev = cache.k.device
-    dt = q.dtype if isinstance(q, torch.Tensor) else None
-    desc = _KvAttnDesc()
-    desc.in_dtype = _dtype_code(dt)
-    _need(q, "q", dt, dev)
-    if q.dim() != 3 or q.shape[2] != c.d:
+    index = _index(q, "q")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first, kv_pos, scale, o, lse, o_dtype,
+                                 workspace, flags, status, wait_timeout_ms, stream)
+    dt, dev = q.dtype, q.device
+    code = _code(dt)
+    pq = _ptr(q, "q", dt, index)
+    c = _cache_fields(cache, index)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != c[7]:
         _invalid("q must be [rows, Hq, D] with the cache's D")
-    rows, hq, d = q.shape
-    desc.cache = c
-    desc.rows = _rows_struct(row_start, kv_lens, "kv_lens", page_table, rows, dev)
+    rows, hq, _ = shape
+    r = _rows_fields(row_start, kv_lens, "kv_lens", page_table, rows, index)
+    first = 0
     if q_first is not None:
-        _need(q_first, "q_first", torch.int32, dev)
-        if q_first.dim() != 1 or q_first.shape[0] != kv_lens.shape[0]:
+        first = _ptr(q_first, "q_first", torch.int32, index)
+        if q_first.shape != kv_lens.shape:
             _invalid("q_first must be [seqs]")
-        desc.q_first = q_first.data_ptr()
-    desc.hq = hq
-    desc.scale = float(scale)
-    desc.kv_pos = _PosMap(kv_pos.base, kv_pos.stride)
-    desc.status = _status_ptr(status, dev)
-    desc.wait_timeout_ms = int(wait_timeout_ms)
-    desc.flags = int(flags)
-    with _on_device(dev):
-        if o is None:
-            o = _new((rows, hq, d), o_dtype or torch.float32, dev, stream)
-        else:
-            _need(o, "o", o.dtype if isinstance(o, torch.Tensor) else None, dev)
-        if lse is None:
-            lse = _new((rows, hq), torch.float32, dev, stream)
-        else:
-            _need(lse, "lse", torch.float32, dev)
-        if o.shape != q.shape or lse.shape != q.shape[:2]:
-            _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
-        desc.q, desc.o, desc.lse = q.data_ptr(), o.data_ptr(), lse.data_ptr()
-        desc.o_dtype = _dtype_code(o.dtype)
-        if workspace is None:
-            need = ctypes.c_int64(0)
-            _check(lib.cp_kv_cache_attn_workspace(ctypes.byref(desc), ctypes.byref(need)))
-            workspace = _new((need.value,), torch.uint8, dev, stream)
-        else:
-            _need(workspace, "workspace", torch.uint8, dev)
-        desc.workspace, desc.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        _check(lib.cp_kv_cache_attn(ctypes.byref(desc), _stream(stream)))
+    if o is None:
+        o = _new(shape, o_dtype or torch.float32, dev, stream)
+    elif not isinstance(o, torch.Tensor) or o.shape != shape:
+        _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
+    if lse is None:
+        lse = _new(shape[:2], torch.float32, dev, stream)
+    elif not isinstance(lse, torch.Tensor) or lse.shape != shape[:2]:
+        _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
+    odt = o.dtype
+    ocode = _code(odt)
+    if workspace is None:
+        workspace = _new((_attn_workspace(index, *c[4:8], *r[3:], hq, code, ocode),), torch.uint8, dev, stream)
+    _check(lib.cp_kv_cache_attn(
+        _KV_ATTN.pack(*c, *r, pq, _ptr(o, "o", odt, index), _ptr(lse, "lse", torch.float32, index), first, code, ocode,
+                      hq, scale, kv_pos.base, kv_pos.stride, _ptr(workspace, "workspace", torch.uint8, index),
+                      workspace.numel(), _status_ptr(status, index), wait_timeout_ms, flags),
+        _stream_of(stream, index)))
     return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(index, n_pages, page_size, hkv, d, n_seqs, max_pages, n_rows, hq, code, ocode):
+    """Bytes of workspace by the shapes of a call; device ``index`` is the current one."""
+    some = 16  # the contents of the arrays do not matter here
+    need = ctypes.c_int64(0)
+    _check(load_library().cp_kv_cache_attn_workspace(
+        _KV_ATTN.pack(some, some, some, some, n_pages, page_size, hkv, d, 0, some, some, some, n_seqs, max_pages, n_rows,
+                      0, 0, 0, 0, code, ocode, hq, 0.0, 0, 1, 0, 0, 0, 0, 0), ctypes.byref(need)))
+    return need.value
 
 
 def kv_cache_attn_workspace(cache, rows, hq, n_seqs, max_pages, dtype=torch.bfloat16, o_dtype=torch.float32):
     """Bytes of workspace that ``kv_cache_attn`` needs for ``rows`` rows of ``hq`` heads over
     ``n_seqs`` sequences with ``max_pages`` table entries each."""
-    desc = _KvAttnDesc()
-    desc.cache = _cache_struct(cache)
-    some = desc.cache.k  # the contents of the arrays do not matter here
-    desc.rows = _KvRows(some, some, some, int(n_seqs), int(max_pages), int(rows))
-    desc.in_dtype, desc.o_dtype, desc.hq = _dtype_code(dtype), _dtype_code(o_dtype), int(hq)
-    need = ctypes.c_int64(0)
-    with _on_device(cache.k.device):
-        _check(load_library().cp_kv_cache_attn_workspace(ctypes.byref(desc), ctypes.byref(need)))
-    return need.value
+    index = _index(cache[0], "cache.k")
+    with torch.cuda.device(index):
+        return _attn_workspace(index, *_cache_fields(cache, index)[4:8], int(n_seqs), int(max_pages), int(rows), int(hq),
+                               _code(dtype), _code(o_dtype))
 
 
 # ---------------------------------------------------------------- rotary positions
@@ -826,33 +841,36 @@ def rope_axes(xs, positions, inv_freq, sections=None, interleaved=False, inverse
     if not 1 <= n <= 4:
         _invalid("between 1 and 4 tensors")
     x0 = xs[0]
-    if not isinstance(x0, torch.Tensor) or not x0.is_cuda:
-        _invalid("every tensor must be a CUDA tensor")
-    dev, dt = x0.device, x0.dtype
-    code = _dtype_code(dt)
+    index = _index(x0, "x")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return rope_axes(xs, positions, inv_freq, sections, interleaved, inverse, out, stream)
+    dt = x0.dtype
+    code = _code(dt)
     if isinstance(inv_freq, torch.Tensor):
         inv_freq = inv_freq.tolist()
     inv_freq = tuple(inv_freq)
     sections = (len(inv_freq),) if sections is None else tuple(sections)
-    _need(positions, "positions", torch.int32, dev)
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if x0.dim() != 3 or positions.dim() not in (1, 2) or positions.shape[-1] != x0.shape[0] or axes != len(sections):
+    ppos = _ptr(positions, "positions", torch.int32, index)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    shape = x0.shape
+    if len(shape) != 3 or positions.dim() not in (1, 2) or positions.shape[-1] != shape[0] or axes != len(sections):
         _invalid("tensors must be [tokens, H, D], positions [axes, tokens], sections one number for each axis")
-    tokens, _, d = x0.shape
-    with _on_device(dev):
-        if out is None:
-            out = [_new(x.shape, dt, dev, stream) for x in xs]
-        elif len(out) != n:
-            _invalid("one output for each tensor")
-        ins, outs, heads = (ctypes.c_void_p * n)(), (ctypes.c_void_p * n)(), (ctypes.c_int32 * n)()
-        for t in range(n):
-            x, y = xs[t], out[t]
-            _need(x, "x", dt, dev)
-            _need(y, "out", dt, dev)
-            if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != d or y.shape != x.shape:
-                _invalid("every tensor and its output must be [tokens, H, D] with the same tokens and D")
-            ins[t], outs[t], heads[t] = x.data_ptr(), y.data_ptr(), x.shape[1]
-        freq, cuts = _rope_tables(inv_freq, sections)
-        _check(lib.cp_rope_axes(n, ins, outs, heads, tokens, d, 2 * len(inv_freq), code, positions.data_ptr(), axes,
-                                cuts, freq, int(bool(interleaved)), int(bool(inverse)), _stream(stream)))
+    tokens, _, d = shape
+    if out is None:
+        out = [_new(x.shape, dt, x0.device, stream) for x in xs]
+    elif len(out) != n:
+        _invalid("one output for each tensor")
+    ins, outs, heads = [], [], []
+    for x, y in zip(xs, out):
+        ins.append(_ptr(x, "x", dt, index))
+        outs.append(_ptr(y, "out", dt, index))
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != d or y.shape != shape:
+            _invalid("every tensor and its output must be [tokens, H, D] with the same tokens and D")
+        heads.append(shape[1])
+    freq, cuts = _rope_tables(inv_freq, sections)
+    ptrs = struct.pack(f"@{n}P", *ins), struct.pack(f"@{n}P", *outs), struct.pack(f"@{n}i", *heads)
+    _check(lib.cp_rope_axes(n, *ptrs, tokens, d, 2 * len(inv_freq), code, ppos, axes, cuts, freq,
+                            1 if interleaved else 0, 1 if inverse else 0, _stream_of(stream, index)))
     return list(out)

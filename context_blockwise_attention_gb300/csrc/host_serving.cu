@@ -107,8 +107,9 @@ CP_API cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* ro
   cp_status st = validate_copy("cp_kv_cache_read", cache, rows, k, v, out_dtype, status);
   if (st != CP_OK) return st;
   if (rows->n_rows == 0 || rows->n_seqs == 0) return CP_OK;
-  if ((st = require_sm103(nullptr, nullptr)) != CP_OK) return st;
-  return launch_kv_read(*cache, *rows, k, v, out_dtype == CP_BF16, status, stream);
+  int sms = 0;
+  if ((st = require_sm103(nullptr, &sms)) != CP_OK) return st;
+  return launch_kv_read(*cache, *rows, k, v, out_dtype == CP_BF16, status, sms, stream);
 }
 
 CP_API cp_status cp_kv_cache_attn_workspace(const cp_kv_attn_desc* desc, int64_t* bytes_out) {
@@ -180,9 +181,10 @@ CP_API cp_status cp_rope_axes(int32_t n_tensors, const void* const* in, void* co
   if (sum != rot / 2) CP_INVALID("%s: the sections cover %lld pairs, not rot/2 = %d", who, (long long)sum, rot / 2);
   int64_t all = 0;
   for (int t = 0; t < n_tensors; ++t) {
-    if (heads[t] <= 0 || heads[t] > (1 << 20)) CP_INVALID("%s: head counts must be positive (and at most 2^20)", who);
+    if (heads[t] <= 0) CP_INVALID("%s: head counts must be positive", who);
     all += heads[t];
   }
+  if (all > 65536) CP_INVALID("%s: more than 65536 heads in all", who);
   RopeArgs a{n_tensors, in, out, heads, tokens, d, rot, dtype == CP_BF16, positions, n_axes, sections,
              interleaved, inverse, {}};
   for (int i = 0; i < rot / 2; ++i) {
@@ -195,7 +197,8 @@ CP_API cp_status cp_rope_axes(int32_t n_tensors, const void* const* in, void* co
     if (in[t] == nullptr || out[t] == nullptr) CP_INVALID("%s: in[%d] and out[%d] must not be NULL", who, t, t);
     if (!aligned(in[t], 16) || !aligned(out[t], 16)) CP_INVALID("%s: every tensor must be 16-byte aligned", who);
   }
-  cp_status st = require_sm103(nullptr, nullptr);
+  int sms = 0;
+  cp_status st = require_sm103(nullptr, &sms);
   if (st != CP_OK) return st;
-  return launch_rope(a, stream);
+  return launch_rope(a, sms, stream);
 }

@@ -79,7 +79,7 @@ cp_status launch_reshard(const ReshardArgs& a, int num_sms, cudaStream_t s);
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
                           int32_t* status, cudaStream_t s);
 cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,
-                         cudaStream_t s);
+                         int num_sms, cudaStream_t s);
 int64_t kv_attn_workspace(const cp_kv_attn_desc& d, int num_sms);
 cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s);
 
@@ -97,6 +97,6 @@ struct RopeArgs {
   int32_t interleaved, inverse;
   uint64_t turn[128];  // fraction of a turn per position, in units of 2^-64
 };
-cp_status launch_rope(const RopeArgs& a, cudaStream_t s);
+cp_status launch_rope(const RopeArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace cpattn

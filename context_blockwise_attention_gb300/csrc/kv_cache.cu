@@ -1,6 +1,7 @@
 // Writing tokens into the paged e4m3 cache and reading them back (cp_kv_cache_write / _read).
 #include "internal.h"
 #include "kv_common.cuh"
+#include "ptx.cuh"
 
 namespace cpattn {
 
@@ -64,6 +65,14 @@ __device__ __forceinline__ bool span_of(const cp_kv_rows& r, int64_t n_pages, in
   return true;
 }
 
+// Four cached bytes at a larger scale: old scale / new scale is `ratio`.
+__device__ __forceinline__ void requantise4(uint8_t* q, float ratio) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(q);
+  const float2 a = kv::e4m3x2_to_float2(v), b = kv::e4m3x2_to_float2(v >> 16);
+  *reinterpret_cast<uint32_t*>(q) =
+      kv::to_e4m3x2(a.x * ratio, a.y * ratio) | (kv::to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+}
+
 struct WriteParams {
   cp_kv_cache c;
   cp_kv_rows rows;
@@ -75,7 +84,7 @@ struct WriteParams {
 // One warp per (page, head, K or V): it goes over the page's new rows twice, first for the largest
 // magnitude and then to convert them, and over the older slots where the scale grew.
 template <int D, class T>
-__global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kN = D / 32;  // elements of a row per lane
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -84,6 +93,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const WritePara
   if (unit >= p.units) return;
   const int sub = static_cast<int>(w - unit * (2 * hkv));
   const int which = sub & 1, head = sub >> 1;
+  ptx::wait_dependencies();
   PageSpan s;
   if (!span_of(p.rows, p.c.n_pages, P, unit, lane, s)) return;
   if (s.page < 0) {
@@ -115,10 +125,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const WritePara
       for (int i = 0; i < s.slot; ++i) {
         uint8_t* q = out + i * D;
         if constexpr (kN == 4) {
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(q);
-          const float2 a = kv::e4m3x2_to_float2(v), b = kv::e4m3x2_to_float2(v >> 16);
-          *reinterpret_cast<uint32_t*>(q) =
-              kv::to_e4m3x2(a.x * ratio, a.y * ratio) | (kv::to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+          requantise4(q, ratio);
         } else {
           const float2 a = kv::e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(q));
           *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(kv::to_e4m3x2(a.x * ratio, a.y * ratio));
@@ -139,59 +146,242 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const WritePara
   if (lane == 0 && now != old) *scale = now;
 }
 
+// 16 bytes of a row as fp32: 8 bf16 or 4 fp32.
+template <class T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+  unpack_bf16x2(v.x, x[0], x[1]);
+  unpack_bf16x2(v.y, x[2], x[3]);
+  unpack_bf16x2(v.z, x[4], x[5]);
+  unpack_bf16x2(v.w, x[6], x[7]);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+
+// Prompts: the threads of a tile (page, head, K or V) hold its new rows in registers between the
+// largest magnitude and the conversion, so that they are read once.  A block takes as many heads of
+// one page as fit.  Bound by memory: 2 or 4 bytes in and 1 out per number; 16-byte loads, all of a
+// thread's in flight at once.
+template <int D, int P>
+constexpr int kTileThreads = P * D / 16 < kThreads ? P * D / 16 : kThreads;
+template <int D, int P, class T>
+__global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_constant__ WriteParams p) {
+  constexpr int kV = kVec<T>, kTT = kTileThreads<D, P>, kTiles = kThreads / kTT;
+  constexpr int kPerRow = D / kV, kRowsAtOnce = kTT / kPerRow, kPasses = P / kRowsAtOnce;
+  __shared__ float tops[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hkv = p.c.hkv;
+  const int groups = (hkv + kTiles - 1) / kTiles;
+  const int64_t unit = blockIdx.x / (2 * groups);
+  const int sub = static_cast<int>(blockIdx.x - unit * (2 * groups));
+  const int which = sub & 1, head = (sub >> 1) * kTiles + tid / kTT;
+  const int at = tid % kTT, row0 = at / kPerRow, col = at % kPerRow * kV;
+  ptx::wait_dependencies();
+  PageSpan s;
+  if (!span_of(p.rows, p.c.n_pages, P, unit, lane, s)) return;  // the same for the whole block
+  if (s.page < 0) {
+    if (tid == 0) kv::report(p.status, kv::kSitePage);
+    return;
+  }
+  const bool mine = head < hkv;
+  const T* x = static_cast<const T*>(p.x[which]) + (s.row * hkv + head) * D + col;
+  const int64_t tile = s.page * hkv + head;
+  uint8_t* out = static_cast<uint8_t*>(which ? p.c.v : p.c.k) + tile * P * D + col;
+  float* scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
+  const float old = mine && s.slot > 0 ? *scale : 0.0f;
+  uint4 held[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + i * kRowsAtOnce;
+    held[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (mine && r < s.n) held[i] = __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * hkv * D));
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    float e[kV];
+    unpack(held[i], e);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) amax = fmaxf(amax, kv::magnitude(e[j]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) tops[warp] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kTT / 32; ++i) amax = fmaxf(amax, tops[warp / (kTT / 32) * (kTT / 32) + i]);
+  if (!mine) return;
+  const int ex = kv::scale_exp(amax);
+  float now = kv::pow2(ex), inv = kv::pow2(-ex);
+  if (old >= now) {
+    now = old;
+    inv = 1.0f / old;  // exact: a power of two
+  } else if (s.slot > 0) {
+    const float ratio = old / now;
+    for (int r = row0; r < s.slot; r += kRowsAtOnce)
+#pragma unroll
+      for (int j = 0; j < kV; j += 4) requantise4(out + r * D + j, ratio);
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + i * kRowsAtOnce;
+    if (r >= s.n) break;
+    float e[kV];
+    unpack(held[i], e);
+    uint32_t w[kV / 4];
+#pragma unroll
+    for (int j = 0; j < kV; j += 4)
+      w[j / 4] = kv::to_e4m3x2(e[j] * inv, e[j + 1] * inv) | (kv::to_e4m3x2(e[j + 2] * inv, e[j + 3] * inv) << 16);
+    uint8_t* q = out + (s.slot + r) * D;
+    if constexpr (kV == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(q) = w[0];
+  }
+  if (at == 0 && now != old) *scale = now;
+}
+
 struct ReadParams {
   cp_kv_cache c;
   cp_kv_rows rows;
   void* x[2];
   int32_t* status;
+  int32_t heads;  // of a block
 };
 
-// One warp per (row, head).
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A thread keeps one row and 16 of its columns (16 bytes of cache) and goes over the heads: where its
+// token lives is looked up once.  Bound by memory: 1 byte in and 2 or 4 out per number; the loads of
+// kAhead heads are in flight together.
 template <int D, class T>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
-  constexpr int kN = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kCols = D / 16, kRows = kThreads / kCols, kAhead = 4;
+  __shared__ int seqs[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = p.c.hkv, P = p.c.page_size;
-  const int64_t row = w / hkv;
-  const int head = static_cast<int>(w - row * hkv);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int64_t row = row0 + tid / kCols;
+  ptx::wait_dependencies();
+  if (warp < 2) {  // the sequences of the block's first and last row
+    const int64_t last = row0 + kRows - 1;
+    const int64_t r = warp == 0 ? row0 : last < p.rows.n_rows ? last : p.rows.n_rows - 1;
+    const int b = find_seq(p.rows.n_seqs, r, lane, [&](int i) { return kv::row_at(p.rows, i); });
+    if (lane == 0) seqs[warp] = b;
+  }
+  __syncthreads();
   if (row >= p.rows.n_rows) return;
-  const int b = find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+  int b = seqs[0], z = seqs[1];
+  while (b < z) {  // the last one that begins at or before the row
+    const int mid = (b + z + 1) >> 1;
+    if (kv::row_at(p.rows, mid) <= row) b = mid;
+    else z = mid - 1;
+  }
   const int64_t r0 = kv::row_at(p.rows, b), r1 = kv::row_at(p.rows, b + 1);
   const int64_t first = __ldg(p.rows.tokens + b);
   if (row < r0 || row >= r1) return;
   const int64_t token = first + (row - r0);
-  const int64_t page = first < 0 ? -1 : kv::page_at(p.rows, p.c.n_pages, b, token / P);
+  const int64_t ord = first < 0 ? -1 : token / P;
+  const int64_t page = kv::page_at(p.rows, p.c.n_pages, b, ord);
   if (page < 0) {
-    if (lane == 0) kv::report(p.status, kv::kSitePage);
+    kv::report(p.status, kv::kSitePage);
     return;
   }
-  const int64_t tile = page * hkv + head;
+  const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
+  const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
+  const int col = tid % kCols * 16;
+  const uint8_t* src = static_cast<const uint8_t*>(which ? p.c.v : p.c.k) +
+                       ((page * hkv + h0) * P + (token - ord * P)) * D + col;
+  const float* scale = (which ? p.c.v_scale : p.c.k_scale) + page * hkv;
+  T* dst = static_cast<T*>(p.x[which]) + (row * hkv + h0) * D + col;
+  for (int h = h0; h < h1; h += kAhead) {
+    uint4 v[kAhead];
+    float f[kAhead];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const uint8_t* q =
-        static_cast<const uint8_t*>(which ? p.c.v : p.c.k) + (tile * P + token % P) * D + lane * kN;
-    const float scale = __ldg((which ? p.c.v_scale : p.c.k_scale) + tile);
-    T* out = static_cast<T*>(p.x[which]) + (row * hkv + head) * D + lane * kN;
+    for (int i = 0; i < kAhead; ++i)
+      if (h + i < h1) {
+        v[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * P * D));
+        f[i] = __ldg(scale + h + i);
+      }
 #pragma unroll
-    for (int j = 0; j < kN; j += 2) {
-      const float2 f = kv::e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(q + j));
-      out[j] = static_cast<T>(f.x * scale);
-      out[j + 1] = static_cast<T>(f.y * scale);
-    }
+    for (int i = 0; i < kAhead; ++i)
+      if (h + i < h1) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 lo = kv::e4m3x2_to_float2(w[j]), hi = kv::e4m3x2_to_float2(w[j] >> 16);
+          x[4 * j] = lo.x * f[i], x[4 * j + 1] = lo.y * f[i];
+          x[4 * j + 2] = hi.x * f[i], x[4 * j + 3] = hi.y * f[i];
+        }
+        T* to = dst + i * D;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8)
+            __stcs(reinterpret_cast<uint4*>(to + j),
+                   make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]),
+                              pack_bf16x2(x[j + 4], x[j + 5]), pack_bf16x2(x[j + 6], x[j + 7])));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            __stcs(reinterpret_cast<float4*>(to + j), make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
+        }
+      }
+    src += static_cast<int64_t>(kAhead) * P * D;
+    dst += kAhead * D;
   }
 }
 
 template <class K, class P>
-cp_status launch(K kernel, const P& p, int64_t warps, const char* what, cudaStream_t s) {
-  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 0x7fffffff) {
-    set_error("%s: too many rows", what);
+cp_status launch(K kernel, const P& p, int64_t bx, int64_t by, const char* what, cudaStream_t s) {
+  if (bx > 0x7fffffff || by > 65535) {
+    set_error("%s: too many rows or heads", what);
     return CP_ERR_INVALID_ARG;
   }
-  kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by));
+  cfg.blockDim = dim3(kThreads);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? CP_OK : cuda_fail(e, what);
+}
+
+template <int D, int P, class T>
+cp_status write_tiles(const WriteParams& p, cudaStream_t s) {
+  constexpr int kTiles = kThreads / kTileThreads<D, P>;
+  return launch(kv_write_tile_kernel<D, P, T>, p, p.units * 2 * ((p.c.hkv + kTiles - 1) / kTiles), 1,
+                "kv_write_tile_kernel launch", s);
+}
+template <int D, class T>
+cp_status write(const WriteParams& p, cudaStream_t s) {
+  // Few new rows in a page: a warp a tile (one token each of 128 sequences: 4.1 us).  Many: a block's
+  // threads hold the page's new rows.
+  if (p.rows.n_rows < 8 * static_cast<int64_t>(p.rows.n_seqs))
+    return launch(kv_write_warp_kernel<D, T>, p, (p.units * p.c.hkv * 2 + kThreads / 32 - 1) / (kThreads / 32), 1,
+                  "kv_write_warp_kernel launch", s);
+  switch (p.c.page_size) {
+    case 16: return write_tiles<D, 16, T>(p, s);
+    case 32: return write_tiles<D, 32, T>(p, s);
+    case 64: return write_tiles<D, 64, T>(p, s);
+    default: return write_tiles<D, 128, T>(p, s);
+  }
+}
+template <int D, class T>
+cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
+  constexpr int kRows = kThreads / (D / 16);
+  // all heads to a block, or fewer where the rows alone do not make four blocks an SM
+  const int64_t bx = (p.rows.n_rows + kRows - 1) / kRows;
+  const int64_t cut = (2 * num_sms + bx - 1) / bx;
+  p.heads = static_cast<int32_t>((p.c.hkv + cut - 1) / cut);
+  return launch(kv_read_kernel<D, T>, p, bx, 2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_read_kernel launch", s);
 }
 
 }  // namespace
@@ -199,25 +389,15 @@ cp_status launch(K kernel, const P& p, int64_t warps, const char* what, cudaStre
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
                           int32_t* status, cudaStream_t s) {
   WriteParams p{c, rows, {k, v}, status, rows.n_rows / c.page_size + 2 * static_cast<int64_t>(rows.n_seqs)};
-  const int64_t warps = p.units * c.hkv * 2;
-  const char* what = "kv_write_warp_kernel launch";
-  if (c.d == 128)
-    return bf16 ? launch(kv_write_warp_kernel<128, __nv_bfloat16>, p, warps, what, s)
-                : launch(kv_write_warp_kernel<128, float>, p, warps, what, s);
-  return bf16 ? launch(kv_write_warp_kernel<64, __nv_bfloat16>, p, warps, what, s)
-              : launch(kv_write_warp_kernel<64, float>, p, warps, what, s);
+  if (c.d == 128) return bf16 ? write<128, __nv_bfloat16>(p, s) : write<128, float>(p, s);
+  return bf16 ? write<64, __nv_bfloat16>(p, s) : write<64, float>(p, s);
 }
 
 cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,
-                         cudaStream_t s) {
-  ReadParams p{c, rows, {k, v}, status};
-  const int64_t warps = rows.n_rows * c.hkv;
-  const char* what = "kv_read_kernel launch";
-  if (c.d == 128)
-    return bf16 ? launch(kv_read_kernel<128, __nv_bfloat16>, p, warps, what, s)
-                : launch(kv_read_kernel<128, float>, p, warps, what, s);
-  return bf16 ? launch(kv_read_kernel<64, __nv_bfloat16>, p, warps, what, s)
-              : launch(kv_read_kernel<64, float>, p, warps, what, s);
+                         int num_sms, cudaStream_t s) {
+  ReadParams p{c, rows, {k, v}, status, 0};
+  if (c.d == 128) return bf16 ? read<128, __nv_bfloat16>(p, num_sms, s) : read<128, float>(p, num_sms, s);
+  return bf16 ? read<64, __nv_bfloat16>(p, num_sms, s) : read<64, float>(p, num_sms, s);
 }
 
 }  // namespace cpattn

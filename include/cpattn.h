@@ -535,8 +535,8 @@ cp_status cp_kv_cache_attn_workspace(const cp_kv_attn_desc* desc, int64_t* bytes
  * Arguments:
  *   n_tensors   1..4
  *   in, out     host arrays [n_tensors] of device pointers, [tokens, heads[t], d], 16-byte
- *               aligned; out[t] may be in[t]
- *   heads       host array [n_tensors]
+ *               aligned; out[t] may be in[t], and overlaps no other tensor
+ *   heads       host array [n_tensors], 65536 in all at most
  *   d, rot      d a multiple of 8, at most 256; rot a multiple of 16, 16 <= rot <= d
  *   dtype       CP_F32 or CP_BF16 (arithmetic in fp32, rounded once)
  *   positions   device int32 [n_axes, tokens], any sign

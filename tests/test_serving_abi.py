@@ -122,7 +122,7 @@ def test_rope_refuses():
     for kw in [dict(n=0), dict(n=5), dict(ins=None), dict(outs=None), dict(heads=None), dict(tokens=-1), dict(d=60),
                dict(d=264), dict(d=0), dict(rot=24), dict(rot=0), dict(rot=80), dict(dtype=2), dict(positions=None),
                dict(positions=0x3002), dict(axes=0), dict(axes=5), dict(sections=(10, 7)), dict(sections=(20, -4)),
-               dict(heads=(8, 0)), dict(interleaved=2), dict(inverse=-1), dict(ins=(0x1000, 0)),
+               dict(heads=(8, 0)), dict(heads=(65536, 1)), dict(interleaved=2), dict(inverse=-1), dict(ins=(0x1000, 0)),
                dict(ins=(0x1008, 0x2000)), dict(outs=(0x1000, 0x2004)), dict(freq=[float("nan")] * 16),
                dict(freq=[1e4] * 16), dict(freq=[float("inf")] * 16)]:
         assert call(**kw) == BAD, kw
