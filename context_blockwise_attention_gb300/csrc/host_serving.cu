@@ -97,8 +97,9 @@ CP_API cp_status cp_kv_cache_write(const cp_kv_cache* cache, const cp_kv_rows* r
   cp_status st = validate_copy("cp_kv_cache_write", cache, rows, k, v, in_dtype, status);
   if (st != CP_OK) return st;
   if (rows->n_rows == 0 || rows->n_seqs == 0) return CP_OK;
-  if ((st = require_sm103(nullptr, nullptr)) != CP_OK) return st;
-  return launch_kv_write(*cache, *rows, k, v, in_dtype == CP_BF16, status, stream);
+  int sms = 0;
+  if ((st = require_sm103(nullptr, &sms)) != CP_OK) return st;
+  return launch_kv_write(*cache, *rows, k, v, in_dtype == CP_BF16, status, sms, stream);
 }
 
 CP_API cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, void* k, void* v,

@@ -42,26 +42,28 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[N]) 
 // begin at, so that the grid's size follows from the row count alone and no prefix sum over the
 // sequences is needed.
 struct PageSpan {
-  int64_t page;  // -1: bad
-  int64_t row;   // first row of the call that goes into it
-  int slot, n;   // slots [slot, slot + n)
+  int page;     // -1: bad
+  int row;      // first row of the call that goes into it
+  int slot, n;  // slots [slot, slot + n)
 };
-__device__ __forceinline__ bool span_of(const cp_kv_rows& r, int64_t n_pages, int P, int64_t unit, int lane,
+__device__ __forceinline__ bool span_of(const cp_kv_rows& r, int64_t n_pages, int P, uint32_t unit, int lane,
                                         PageSpan& out) {
-  const int b = find_seq(r.n_seqs, unit, lane, [&](int i) { return kv::row_at(r, i) / P + 2 * static_cast<int64_t>(i); });
-  const int64_t r0 = kv::row_at(r, b), r1 = kv::row_at(r, b + 1);
-  const int64_t first = __ldg(r.tokens + b);
-  const int64_t k = unit - (r0 / P + 2 * static_cast<int64_t>(b));
-  if (r1 <= r0 || first < 0 || k < 0) return false;
-  const int64_t ord = first / P + k;
-  const int64_t begin = k == 0 ? first : ord * P;  // first token of the call in this page
-  const int64_t end = first + (r1 - r0);
-  if (begin >= end) return false;
-  out.page = kv::page_at(r, n_pages, b, ord);
-  out.row = r0 + (begin - first);
-  out.slot = static_cast<int>(begin - ord * P);
-  const int64_t room = P - out.slot, left = end - begin;
-  out.n = static_cast<int>(room < left ? room : left);
+  const int shift = 31 - __clz(P);
+  auto begin = [&](int i) { return (static_cast<uint32_t>(kv::row_at(r, i)) >> shift) + 2u * i; };
+  const int b = find_seq(r.n_seqs, unit, lane, [&](int i) { return static_cast<int64_t>(begin(i)); });
+  const int r0 = static_cast<int>(kv::row_at(r, b)), r1 = static_cast<int>(kv::row_at(r, b + 1));
+  const int first = __ldg(r.tokens + b);
+  const uint32_t at = begin(b);
+  if (r1 <= r0 || first < 0 || unit < at) return false;
+  const int64_t ord = (first >> shift) + static_cast<int64_t>(unit - at);
+  const int64_t from = unit == at ? first : ord << shift;  // first token of the call in this page
+  const int64_t end = static_cast<int64_t>(first) + (r1 - r0);
+  if (from >= end) return false;
+  out.page = static_cast<int>(kv::page_at(r, n_pages, b, ord));
+  out.row = r0 + static_cast<int>(from - first);
+  out.slot = static_cast<int>(from - (ord << shift));
+  const int64_t left = end - from;
+  out.n = static_cast<int>(P - out.slot < left ? P - out.slot : left);
   return true;
 }
 
@@ -78,7 +80,8 @@ struct WriteParams {
   cp_kv_rows rows;
   const void* x[2];  // k, v
   int32_t* status;
-  int64_t units;
+  uint32_t units;
+  int32_t heads;  // of a block of the tile kernel
 };
 
 // One warp per (page, head, K or V): it goes over the page's new rows twice, first for the largest
@@ -87,11 +90,10 @@ template <int D, class T>
 __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kN = D / 32;  // elements of a row per lane
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int hkv = p.c.hkv, P = p.c.page_size;
-  const int64_t unit = w / (2 * hkv);
+  const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), unit = w / (2u * hkv);
   if (unit >= p.units) return;
-  const int sub = static_cast<int>(w - unit * (2 * hkv));
+  const int sub = static_cast<int>(w - unit * (2u * hkv));
   const int which = sub & 1, head = sub >> 1;
   ptx::wait_dependencies();
   PageSpan s;
@@ -100,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const __grid_co
     if (lane == 0) kv::report(p.status, kv::kSitePage);
     return;
   }
-  const T* x = static_cast<const T*>(p.x[which]) + (s.row * hkv + head) * D + lane * kN;
-  const int64_t tile = s.page * hkv + head;
+  const T* x = static_cast<const T*>(p.x[which]) + (static_cast<int64_t>(s.row) * hkv + head) * D + lane * kN;
+  const int64_t tile = static_cast<int64_t>(s.page) * hkv + head;
   uint8_t* out = static_cast<uint8_t*>(which ? p.c.v : p.c.k) + tile * P * D + lane * kN;
   float* scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
   const float old = s.slot > 0 ? *scale : 0.0f;
@@ -160,85 +162,110 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
   x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
 }
 
+// Largest counting magnitude of 16 bytes.  The maximum passes over NaN by itself; where it finds an
+// infinity it is taken again without.
+__device__ __forceinline__ float top_of(const uint4& v, const __nv_bfloat16*) {
+  auto abs2 = [](uint32_t u) {
+    u &= 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&u);
+  };
+  const __nv_bfloat162 m = __hmax2(__hmax2(abs2(v.x), abs2(v.y)), __hmax2(abs2(v.z), abs2(v.w)));
+  float top = fmaxf(__low2float(m), __high2float(m));
+  if (!(top < INFINITY)) {
+    float e[8];
+    unpack(v, e);
+    top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, kv::magnitude(e[j]));
+  }
+  return top;
+}
+__device__ __forceinline__ float top_of(const uint4& v, const float*) {
+  float e[4];
+  unpack(v, e);
+  float top = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
+  if (!(top < INFINITY))
+    top = fmaxf(fmaxf(kv::magnitude(e[0]), kv::magnitude(e[1])), fmaxf(kv::magnitude(e[2]), kv::magnitude(e[3])));
+  return top;
+}
+
 // Prompts: the threads of a tile (page, head, K or V) hold its new rows in registers between the
 // largest magnitude and the conversion, so that they are read once.  A block takes as many heads of
-// one page as fit.  Bound by memory: 2 or 4 bytes in and 1 out per number; 16-byte loads, all of a
-// thread's in flight at once.
+// one page at once as fit, and goes over p.heads of them, so that where the page lies is looked up
+// once.  Bound by memory: 2 or 4 bytes in and 1 out per number; 16-byte loads, all of a thread's in
+// flight at once.
 template <int D, int P>
 constexpr int kTileThreads = P * D / 16 < kThreads ? P * D / 16 : kThreads;
 template <int D, int P, class T>
 __global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kV = kVec<T>, kTT = kTileThreads<D, P>, kTiles = kThreads / kTT;
   constexpr int kPerRow = D / kV, kRowsAtOnce = kTT / kPerRow, kPasses = P / kRowsAtOnce;
-  __shared__ float tops[kThreads / 32];
+  __shared__ float tops[2][kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = p.c.hkv;
-  const int groups = (hkv + kTiles - 1) / kTiles;
-  const int64_t unit = blockIdx.x / (2 * groups);
-  const int sub = static_cast<int>(blockIdx.x - unit * (2 * groups));
-  const int which = sub & 1, head = (sub >> 1) * kTiles + tid / kTT;
+  const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
+  const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
   const int at = tid % kTT, row0 = at / kPerRow, col = at % kPerRow * kV;
   ptx::wait_dependencies();
   PageSpan s;
-  if (!span_of(p.rows, p.c.n_pages, P, unit, lane, s)) return;  // the same for the whole block
+  if (!span_of(p.rows, p.c.n_pages, P, blockIdx.x, lane, s)) return;  // the same for the whole block
   if (s.page < 0) {
     if (tid == 0) kv::report(p.status, kv::kSitePage);
     return;
   }
-  const bool mine = head < hkv;
-  const T* x = static_cast<const T*>(p.x[which]) + (s.row * hkv + head) * D + col;
-  const int64_t tile = s.page * hkv + head;
-  uint8_t* out = static_cast<uint8_t*>(which ? p.c.v : p.c.k) + tile * P * D + col;
-  float* scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
-  const float old = mine && s.slot > 0 ? *scale : 0.0f;
-  uint4 held[kPasses];
+  int turn = 0;
+  for (int h = h0; h < h1; h += kTiles, turn ^= 1) {
+    const int head = h + tid / kTT;
+    const bool mine = head < h1;
+    const T* x = static_cast<const T*>(p.x[which]) + (static_cast<int64_t>(s.row) * hkv + head) * D + col;
+    const int64_t tile = static_cast<int64_t>(s.page) * hkv + head;
+    uint8_t* out = static_cast<uint8_t*>(which ? p.c.v : p.c.k) + tile * P * D + col;
+    float* scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
+    const float old = mine && s.slot > 0 ? *scale : 0.0f;
+    uint4 held[kPasses];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = row0 + i * kRowsAtOnce;
-    held[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (mine && r < s.n) held[i] = __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * hkv * D));
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = row0 + i * kRowsAtOnce;
+      held[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine && r < s.n) held[i] = __ldcs(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * hkv * D));
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) amax = fmaxf(amax, top_of(held[i], x));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) tops[turn][warp] = amax;
+    __syncthreads();  // two sets of maxima: the next head's do not wait for these to be read
+#pragma unroll
+    for (int i = 0; i < kTT / 32; ++i) amax = fmaxf(amax, tops[turn][warp / (kTT / 32) * (kTT / 32) + i]);
+    if (!mine) continue;
+    const int ex = kv::scale_exp(amax);
+    float now = kv::pow2(ex), inv = kv::pow2(-ex);
+    if (old >= now) {
+      now = old;
+      inv = 1.0f / old;  // exact: a power of two
+    } else if (s.slot > 0) {
+      const float ratio = old / now;
+      for (int r = row0; r < s.slot; r += kRowsAtOnce)
+#pragma unroll
+        for (int j = 0; j < kV; j += 4) requantise4(out + r * D + j, ratio);
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = row0 + i * kRowsAtOnce;
+      if (r >= s.n) break;
+      float e[kV];
+      unpack(held[i], e);
+      uint32_t w[kV / 4];
+#pragma unroll
+      for (int j = 0; j < kV; j += 4)
+        w[j / 4] = kv::to_e4m3x2(e[j] * inv, e[j + 1] * inv) | (kv::to_e4m3x2(e[j + 2] * inv, e[j + 3] * inv) << 16);
+      uint8_t* q = out + (s.slot + r) * D;
+      if constexpr (kV == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(q) = w[0];
+    }
+    if (at == 0 && now != old) *scale = now;
   }
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    float e[kV];
-    unpack(held[i], e);
-#pragma unroll
-    for (int j = 0; j < kV; ++j) amax = fmaxf(amax, kv::magnitude(e[j]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) tops[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kTT / 32; ++i) amax = fmaxf(amax, tops[warp / (kTT / 32) * (kTT / 32) + i]);
-  if (!mine) return;
-  const int ex = kv::scale_exp(amax);
-  float now = kv::pow2(ex), inv = kv::pow2(-ex);
-  if (old >= now) {
-    now = old;
-    inv = 1.0f / old;  // exact: a power of two
-  } else if (s.slot > 0) {
-    const float ratio = old / now;
-    for (int r = row0; r < s.slot; r += kRowsAtOnce)
-#pragma unroll
-      for (int j = 0; j < kV; j += 4) requantise4(out + r * D + j, ratio);
-  }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = row0 + i * kRowsAtOnce;
-    if (r >= s.n) break;
-    float e[kV];
-    unpack(held[i], e);
-    uint32_t w[kV / 4];
-#pragma unroll
-    for (int j = 0; j < kV; j += 4)
-      w[j / 4] = kv::to_e4m3x2(e[j] * inv, e[j + 1] * inv) | (kv::to_e4m3x2(e[j + 2] * inv, e[j + 3] * inv) << 16);
-    uint8_t* q = out + (s.slot + r) * D;
-    if constexpr (kV == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(q) = w[0];
-  }
-  if (at == 0 && now != old) *scale = now;
 }
 
 struct ReadParams {
@@ -246,7 +273,7 @@ struct ReadParams {
   cp_kv_rows rows;
   void* x[2];
   int32_t* status;
-  int32_t heads;  // of a block
+  int32_t heads, reps;  // of a block: heads, and rows for each thread
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
@@ -254,84 +281,86 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// A thread keeps one row and 16 of its columns (16 bytes of cache) and goes over the heads: where its
-// token lives is looked up once.  Bound by memory: 1 byte in and 2 or 4 out per number; the loads of
-// kAhead heads are in flight together.
+// A thread writes 16 bytes at a time (so that a warp's stores fill whole lines; with 32 bytes a thread
+// they were half-filled and the kernel 10 % slower) and goes over the heads of its row: where a token
+// lives is looked up once.  Bound by memory: 1 byte in and 2 or 4 out per number; the loads of kAhead
+// heads are in flight together.
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kCols = D / 16, kRows = kThreads / kCols, kAhead = 4;
+  constexpr int kV = kVec<T>, kCols = D / kV, kRows = kThreads / kCols, kAhead = 8;
   __shared__ int seqs[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hkv = p.c.hkv, P = p.c.page_size;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int64_t row = row0 + tid / kCols;
+  const int hkv = p.c.hkv, P = p.c.page_size, shift = 31 - __clz(P);
+  const int n_rows = static_cast<int>(p.rows.n_rows);
+  const int row0 = blockIdx.x * (kRows * p.reps);
+  const int row_end = n_rows - row0 < kRows * p.reps ? n_rows : row0 + kRows * p.reps;
+  const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
+  const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
+  const int col = tid % kCols * kV;
   ptx::wait_dependencies();
   if (warp < 2) {  // the sequences of the block's first and last row
-    const int64_t last = row0 + kRows - 1;
-    const int64_t r = warp == 0 ? row0 : last < p.rows.n_rows ? last : p.rows.n_rows - 1;
-    const int b = find_seq(p.rows.n_seqs, r, lane, [&](int i) { return kv::row_at(p.rows, i); });
+    const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
+                           [&](int i) { return kv::row_at(p.rows, i); });
     if (lane == 0) seqs[warp] = b;
   }
   __syncthreads();
-  if (row >= p.rows.n_rows) return;
-  int b = seqs[0], z = seqs[1];
-  while (b < z) {  // the last one that begins at or before the row
-    const int mid = (b + z + 1) >> 1;
-    if (kv::row_at(p.rows, mid) <= row) b = mid;
-    else z = mid - 1;
-  }
-  const int64_t r0 = kv::row_at(p.rows, b), r1 = kv::row_at(p.rows, b + 1);
-  const int64_t first = __ldg(p.rows.tokens + b);
-  if (row < r0 || row >= r1) return;
-  const int64_t token = first + (row - r0);
-  const int64_t ord = first < 0 ? -1 : token / P;
-  const int64_t page = kv::page_at(p.rows, p.c.n_pages, b, ord);
-  if (page < 0) {
-    kv::report(p.status, kv::kSitePage);
-    return;
-  }
-  const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
-  const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
-  const int col = tid % kCols * 16;
-  const uint8_t* src = static_cast<const uint8_t*>(which ? p.c.v : p.c.k) +
-                       ((page * hkv + h0) * P + (token - ord * P)) * D + col;
-  const float* scale = (which ? p.c.v_scale : p.c.k_scale) + page * hkv;
-  T* dst = static_cast<T*>(p.x[which]) + (row * hkv + h0) * D + col;
-  for (int h = h0; h < h1; h += kAhead) {
-    uint4 v[kAhead];
-    float f[kAhead];
+  const uint8_t* const cache = static_cast<const uint8_t*>(which ? p.c.v : p.c.k);
+  const float* const scales = which ? p.c.v_scale : p.c.k_scale;
+  for (int row = row0 + tid / kCols; row < row_end; row += kRows) {
+    int b = seqs[0], z = seqs[1];
+    while (b < z) {  // the last one that begins at or before the row
+      const int mid = (b + z + 1) >> 1;
+      if (kv::row_at(p.rows, mid) <= row) b = mid;
+      else z = mid - 1;
+    }
+    const int r0 = static_cast<int>(kv::row_at(p.rows, b)), r1 = static_cast<int>(kv::row_at(p.rows, b + 1));
+    const int first = __ldg(p.rows.tokens + b);
+    if (row < r0 || row >= r1) continue;
+    const int64_t token = static_cast<int64_t>(first) + (row - r0);
+    const int64_t page = first < 0 ? -1 : kv::page_at(p.rows, p.c.n_pages, b, token >> shift);
+    if (page < 0) {
+      kv::report(p.status, kv::kSitePage);
+      continue;
+    }
+    const uint8_t* src = cache + ((page * hkv + h0) * P + (token & (P - 1))) * D + col;
+    const float* scale = scales + page * hkv;
+    T* dst = static_cast<T*>(p.x[which]) + (static_cast<int64_t>(row) * hkv + h0) * D + col;
+    for (int h = h0; h < h1; h += kAhead) {
+      uint32_t v[kAhead][kV / 4];
+      float f[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (h + i < h1) {
-        v[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(i) * P * D));
-        f[i] = __ldg(scale + h + i);
-      }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (h + i < h1) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        float x[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 lo = kv::e4m3x2_to_float2(w[j]), hi = kv::e4m3x2_to_float2(w[j] >> 16);
-          x[4 * j] = lo.x * f[i], x[4 * j + 1] = lo.y * f[i];
-          x[4 * j + 2] = hi.x * f[i], x[4 * j + 3] = hi.y * f[i];
+      for (int i = 0; i < kAhead; ++i)
+        if (h + i < h1) {
+          const uint8_t* q = src + static_cast<int64_t>(i) * P * D;
+          if constexpr (kV == 8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(q));
+            v[i][0] = u.x, v[i][kV / 4 - 1] = u.y;
+          } else {
+            v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+          }
+          f[i] = __ldg(scale + h + i);
         }
-        T* to = dst + i * D;
-        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 8)
-            __stcs(reinterpret_cast<uint4*>(to + j),
-                   make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]),
-                              pack_bf16x2(x[j + 4], x[j + 5]), pack_bf16x2(x[j + 6], x[j + 7])));
-        } else {
+      for (int i = 0; i < kAhead; ++i)
+        if (h + i < h1) {
+          float x[kV];
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            __stcs(reinterpret_cast<float4*>(to + j), make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
+          for (int j = 0; j < kV / 4; ++j) {
+            const float2 lo = kv::e4m3x2_to_float2(v[i][j]), hi = kv::e4m3x2_to_float2(v[i][j] >> 16);
+            x[4 * j] = lo.x * f[i], x[4 * j + 1] = lo.y * f[i];
+            x[4 * j + 2] = hi.x * f[i], x[4 * j + 3] = hi.y * f[i];
+          }
+          T* to = dst + i * D;
+          if constexpr (kV == 8)
+            __stcs(reinterpret_cast<uint4*>(to), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                            pack_bf16x2(x[kV - 4], x[kV - 3]),
+                                                            pack_bf16x2(x[kV - 2], x[kV - 1])));
+          else
+            __stcs(reinterpret_cast<float4*>(to), make_float4(x[0], x[1], x[2], x[3]));
         }
-      }
-    src += static_cast<int64_t>(kAhead) * P * D;
-    dst += kAhead * D;
+      src += static_cast<int64_t>(kAhead) * P * D;
+      dst += kAhead * D;
+    }
   }
 }
 
@@ -354,48 +383,62 @@ cp_status launch(K kernel, const P& p, int64_t bx, int64_t by, const char* what,
   return e == cudaSuccess ? CP_OK : cuda_fail(e, what);
 }
 
+// Heads of a block, so that `blocks` blocks a head make at least `want` blocks in all.
+int32_t heads_of(int32_t hkv, int64_t blocks, int64_t want) {
+  const int64_t cut = (want + blocks - 1) / blocks;
+  return static_cast<int32_t>((hkv + cut - 1) / cut);
+}
+
 template <int D, int P, class T>
-cp_status write_tiles(const WriteParams& p, cudaStream_t s) {
+cp_status write_tiles(WriteParams& p, int num_sms, cudaStream_t s) {
   constexpr int kTiles = kThreads / kTileThreads<D, P>;
-  return launch(kv_write_tile_kernel<D, P, T>, p, p.units * 2 * ((p.c.hkv + kTiles - 1) / kTiles), 1,
+  int32_t heads = heads_of(p.c.hkv, 2 * p.units, 8 * num_sms);
+  p.heads = (heads + kTiles - 1) / kTiles * kTiles;
+  return launch(kv_write_tile_kernel<D, P, T>, p, p.units, 2 * ((p.c.hkv + p.heads - 1) / p.heads),
                 "kv_write_tile_kernel launch", s);
 }
 template <int D, class T>
-cp_status write(const WriteParams& p, cudaStream_t s) {
+cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
   // Few new rows in a page: a warp a tile (one token each of 128 sequences: 4.1 us).  Many: a block's
   // threads hold the page's new rows.
-  if (p.rows.n_rows < 8 * static_cast<int64_t>(p.rows.n_seqs))
-    return launch(kv_write_warp_kernel<D, T>, p, (p.units * p.c.hkv * 2 + kThreads / 32 - 1) / (kThreads / 32), 1,
+  if (p.rows.n_rows < 8 * static_cast<int64_t>(p.rows.n_seqs)) {
+    const int64_t warps = static_cast<int64_t>(p.units) * p.c.hkv * 2;
+    return launch(kv_write_warp_kernel<D, T>, p, (warps + kThreads / 32 - 1) / (kThreads / 32), 1,
                   "kv_write_warp_kernel launch", s);
+  }
   switch (p.c.page_size) {
-    case 16: return write_tiles<D, 16, T>(p, s);
-    case 32: return write_tiles<D, 32, T>(p, s);
-    case 64: return write_tiles<D, 64, T>(p, s);
-    default: return write_tiles<D, 128, T>(p, s);
+    case 16: return write_tiles<D, 16, T>(p, num_sms, s);
+    case 32: return write_tiles<D, 32, T>(p, num_sms, s);
+    case 64: return write_tiles<D, 64, T>(p, num_sms, s);
+    default: return write_tiles<D, 128, T>(p, num_sms, s);
   }
 }
 template <int D, class T>
 cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
-  constexpr int kRows = kThreads / (D / 16);
-  // all heads to a block, or fewer where the rows alone do not make four blocks an SM
-  const int64_t bx = (p.rows.n_rows + kRows - 1) / kRows;
-  const int64_t cut = (2 * num_sms + bx - 1) / bx;
-  p.heads = static_cast<int32_t>((p.c.hkv + cut - 1) / cut);
+  // Four rows a thread, or as few as make four blocks an SM; then fewer heads a block.
+  constexpr int kRows = kThreads / (D / kVec<T>);
+  const int64_t all = (p.rows.n_rows + kRows - 1) / kRows;
+  int64_t reps = all * 2 / (4 * num_sms);
+  reps = reps < 1 ? 1 : reps > 4 ? 4 : reps;
+  p.reps = static_cast<int32_t>(reps);
+  const int64_t bx = (all + reps - 1) / reps;
+  p.heads = heads_of(p.c.hkv, 2 * bx, 4 * num_sms);
   return launch(kv_read_kernel<D, T>, p, bx, 2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_read_kernel launch", s);
 }
 
 }  // namespace
 
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
-                          int32_t* status, cudaStream_t s) {
-  WriteParams p{c, rows, {k, v}, status, rows.n_rows / c.page_size + 2 * static_cast<int64_t>(rows.n_seqs)};
-  if (c.d == 128) return bf16 ? write<128, __nv_bfloat16>(p, s) : write<128, float>(p, s);
-  return bf16 ? write<64, __nv_bfloat16>(p, s) : write<64, float>(p, s);
+                          int32_t* status, int num_sms, cudaStream_t s) {
+  const int64_t units = rows.n_rows / c.page_size + 2 * static_cast<int64_t>(rows.n_seqs);
+  WriteParams p{c, rows, {k, v}, status, static_cast<uint32_t>(units), 0};
+  if (c.d == 128) return bf16 ? write<128, __nv_bfloat16>(p, num_sms, s) : write<128, float>(p, num_sms, s);
+  return bf16 ? write<64, __nv_bfloat16>(p, num_sms, s) : write<64, float>(p, num_sms, s);
 }
 
 cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,
                          int num_sms, cudaStream_t s) {
-  ReadParams p{c, rows, {k, v}, status, 0};
+  ReadParams p{c, rows, {k, v}, status, 0, 0};
   if (c.d == 128) return bf16 ? read<128, __nv_bfloat16>(p, num_sms, s) : read<128, float>(p, num_sms, s);
   return bf16 ? read<64, __nv_bfloat16>(p, num_sms, s) : read<64, float>(p, num_sms, s);
 }
