@@ -43,7 +43,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.0f;  // largest P operand
 constexpr int kSetup = 1;            // what an item costs besides its granules
-constexpr int kFlush = 64;           // granules summed before they are put aside
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int N>
@@ -61,6 +60,12 @@ struct Shape {
   static constexpr bool kHeavy = NT * D >= 256 || NT * QP >= 4;
   static constexpr int kWarps = kHeavy ? 8 : 12;
   static constexpr int kRows = NT * 8;  // RT
+  // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: 5e-6 of O after
+  // 64 granules of rows over 1e5 tokens, 1e-6 after 8.  So the accumulators are added to others every
+  // kFlush granules: in registers where there are some left (kHold), else in the workspace (every 8
+  // granules that took 5 %).  bf16 outputs can wait longer.
+  static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
+  static constexpr int kFlush = PP == 1 ? 64 : kHold ? 4 : D == 128 ? 16 : 8;
   static constexpr int kKeys = kKeysOf<D>;
   static constexpr int kSteps = kKeys / 16;          // steps of 16 keys
   static constexpr int kHalf = kKeys * D;            // bytes of K (or V) of a granule
@@ -91,7 +96,6 @@ struct Params {
   cp_posmap kv_pos;
   int32_t* status;
   int64_t timeout_ns;
-  int64_t* plan;   // [n_seqs + 1] granules before each sequence (workspace)
   float* part_o;   // [workers][2][RT][D]
   float2* part_ml; // [workers][2][RT]: m (base 2), l
   float* aside;    // [workers][RT][D]: accumulators put aside
@@ -277,8 +281,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   ptx::wait_dependencies();  // launched early: what was in the stream before is complete from here on
   make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
   const int n_seqs = p.rows.n_seqs;
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= n_seqs; i += S::kWarps * 32) p.plan[i] = plan[i];
   ptx::launch_dependents();
   const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
   if (p.stall && blockIdx.x == 0 && warp == 0) {
@@ -458,6 +460,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   float m_aside[NT][2], v_aside = 0.0f;  // what the values put aside refer to
   bool flushed = false;
   int since = 0;         // granules since then
+  constexpr bool kHold = S::kHold;
+  float held[kHold ? kMt : 1][4];  // of the one tile
 
   auto begin_item = [&]() {
     row_q = c.block * RT;
@@ -530,6 +534,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     v_ref = 1e-37f;
     flushed = false;
     since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) held[j][0] = held[j][1] = held[j][2] = held[j][3] = 0.0f;
+    }
   };
 
   // One granule for the first kLive tiles of query rows; kMask: some of its keys are not seen by some row.
@@ -629,6 +637,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
           acc[n][j][1] *= c1;
           acc[n][j][2] *= c0;
           acc[n][j][3] *= c1;
+          if constexpr (kHold) {
+            held[j][0] *= c0;
+            held[j][1] *= c1;
+            held[j][2] *= c0;
+            held[j][3] *= c1;
+          }
         }
       }
     }
@@ -748,14 +762,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   auto granule_live = [&](int st, auto mask_tag) {
     if constexpr (NT == 1) {
       granule(st, Int<1>{}, mask_tag);
-    } else if constexpr (NT == 2) {
-      if (live == 1) granule(st, Int<1>{}, mask_tag);
-      else granule(st, Int<2>{}, mask_tag);
     } else {
       if (live == 1) granule(st, Int<1>{}, mask_tag);
-      else if (live == 2) granule(st, Int<2>{}, mask_tag);
-      else if (live == 3) granule(st, Int<3>{}, mask_tag);
-      else granule(st, Int<4>{}, mask_tag);
+      else granule(st, Int<NT>{}, mask_tag);
     }
   };
 
@@ -763,7 +772,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   // what was put aside (`from`) at weight `keep`.
   auto four = [&](int n, int r, int j, const float* from, float keep, float (&x)[4]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = acc[n][2 * j + (e >> 1)][2 * (e & 1) + r];
+    for (int e = 0; e < 4; ++e) {
+      x[e] = acc[n][2 * j + (e >> 1)][2 * (e & 1) + r];
+      if constexpr (kHold) x[e] += held[2 * j + (e >> 1)][2 * (e & 1) + r];
+    }
     if (flushed) {
       const float4 y = *reinterpret_cast<const float4*>(from + 4 * j);
       x[0] = fmaf(y.x, keep, x[0]), x[1] = fmaf(y.y, keep, x[1]);
@@ -771,10 +783,19 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
   };
 
-  // Puts the accumulators aside: adds them to the worker's rows in the workspace and clears them.
-  // The tensor cores' fp32 sums are truncated, which adds up to 1e-5 over a thousand granules; with
-  // kFlush granules to a sum it stays near 1e-6, however long the cache.
+  // Puts the accumulators aside: adds them to the others and clears them.
   auto flush = [&]() {
+    since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          held[j][e] += acc[0][j][e];
+          acc[0][j][e] = 0.0f;
+        }
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -794,7 +815,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
     v_aside = v_ref;
     flushed = true;
-    since = 0;
   };
 
   // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial.
@@ -869,7 +889,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         if (++c.head == p.hkv) next_seq<D, RT>(p, c, seq);
       }
       begin_item();
-    } else if (++since == kFlush) {
+    } else if (++since == S::kFlush) {
       flush();
     }
   }
@@ -886,115 +906,139 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   }
 }
 
-struct CombineParams {
-  Params p;
-  int64_t most;  // workers of the first kernel
-};
-
-// WPR warps per (row, query head): each goes over every WPR-th partial.
+// Sums the partials of the items that several workers shared, and answers the rows that see nothing.
+// WPR warps per (row, query head), each going over every WPR-th partial.  What depends on the shapes
+// alone is worked out before the wait for the first kernel, while its last blocks still run.
+constexpr int kSumThreads = 256;
 template <int D, int RT, int WPR>
-__global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) kv_attn_combine_kernel(const __grid_constant__ CombineParams cp) {
-  const Params& p = cp.p;
-  constexpr int kN = D / 32;
-  __shared__ float sh_o[WPR][D];
+__global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
+  constexpr int kN = D / 32, kPer = kSumThreads / 32 / WPR;  // rows of a block at a time
+  extern __shared__ int64_t plan[];
+  __shared__ int64_t scratch[kSumThreads / 32];
+  __shared__ float sh_o[WPR > 1 ? WPR : 1][D];
   __shared__ float2 sh_ml[WPR];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t id = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
-  const int64_t row = id / p.hq;
-  const int h = static_cast<int>(id - row * p.hq);
-  int b = 0;
-  Seq seq{};
-  if (row < p.rows.n_rows) {
-    b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
-    seq = seq_of<D, RT>(p, b);
-  }
-  // Every thread waits, also one without work: the kernel behind this one may begin once this grid is
-  // through, and must not meet the first kernel's blocks.
-  ptx::wait_dependencies();
-  if (row < seq.r0 || row >= seq.r0 + seq.rows) return;
-  const int head = h / p.group;
-  const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
-  const int block = rho / RT, local = rho - block * RT;
-  int64_t w0 = 0, w1 = -1;
-  int slot0 = 0;
-  if (seq.blocks > 0) {
-    const int64_t W = p.plan[p.rows.n_seqs], n = workers(W, cp.most);
-    const int64_t from = p.plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
-    w0 = worker_of(W, n, from);
-    w1 = worker_of(W, n, from + seq.gpi - 1);
-    if (w0 == w1) return;  // finished by its worker
-    slot0 = share(W, n, w0) < from ? 1 : 0;  // the later ones begin inside of the item
-  }
-  auto place = [&](int64_t w) { return (w * 2 + (w == w0 ? slot0 : 0)) * RT + local; };
-
-  const int sub = WPR == 1 ? 0 : warp;
-  float top = -INFINITY, sum = 0.0f;
-  float acc[kN];
-#pragma unroll
-  for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-  for (int64_t base = w0 + sub; base <= w1; base += 32 * WPR) {
-    const int64_t mine = base + static_cast<int64_t>(lane) * WPR;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (mine <= w1) ml = p.part_ml[place(mine)];
-    float t = ml.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
-    const float now = fmaxf(top, t);
-    const float ref = now == -INFINITY ? 0.0f : now;
-    const float old = ex2(top - ref);
-    const float wt = ex2(ml.x - ref);
-    float z = ml.y * wt;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-    sum = sum * old + z;
-#pragma unroll
-    for (int j = 0; j < kN; ++j) acc[j] *= old;
-    top = now;
-    const int64_t many = (w1 - base) / WPR + 1;
-    const int count = many < 32 ? static_cast<int>(many) : 32;
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const float wi = __shfl_sync(kFull, wt, i);
-      const float* src = p.part_o + place(base + static_cast<int64_t>(i) * WPR) * D + lane * kN;
-      if constexpr (kN == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
-        acc[2] = fmaf(wi, v.z, acc[2]), acc[kN - 1] = fmaf(wi, v.w, acc[kN - 1]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
+  const int sub = warp % WPR;
+  const int64_t outs = p.rows.n_rows * p.hq;
+  make_plan<D, RT, kSumThreads>(p, plan, scratch);
+  const int64_t W = plan[p.rows.n_seqs], n = workers(W, most);
+  bool waited = false;
+  for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kPer; id0 < outs; id0 += static_cast<int64_t>(gridDim.x) * kPer) {
+    const int64_t id = id0 + warp / WPR;
+    const int64_t row = id / p.hq;
+    const int h = static_cast<int>(id - row * p.hq);
+    int local = 0, parts = -1;  // -1: nothing to write here
+    int64_t w0 = 0;
+    int slot0 = 0;
+    if (id < outs) {
+      const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+      const Seq seq = seq_of<D, RT>(p, b);
+      if (row >= seq.r0 && row < seq.r0 + seq.rows) {
+        parts = 0;
+        if (seq.blocks > 0) {
+          const int head = h / p.group;
+          const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
+          const int block = rho / RT;
+          local = rho - block * RT;
+          const int64_t from =
+              plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
+          w0 = worker_of(W, n, from);
+          const int64_t w1 = worker_of(W, n, from + seq.gpi - 1);
+          slot0 = share(W, n, w0) < from ? 1 : 0;  // the later ones begin inside of the item
+          parts = w0 == w1 ? -1 : static_cast<int>(w1 - w0) + 1;  // one: finished by its worker
+        }
       }
     }
-  }
-  if constexpr (WPR > 1) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j) sh_o[warp][lane * kN + j] = acc[j];
-    if (lane == 0) sh_ml[warp] = make_float2(top, sum);
-    __syncthreads();
-    if (warp != 0) return;
-    float all = -INFINITY;
-    for (int w = 0; w < WPR; ++w) all = fmaxf(all, sh_ml[w].x);
-    const float ref = all == -INFINITY ? 0.0f : all;
-    sum = 0.0f;
+    if (!waited) ptx::wait_dependencies();
+    waited = true;
+    auto place = [&](int i) { return ((w0 + i) * 2 + (i == 0 ? slot0 : 0)) * RT + local; };
+    float top = -INFINITY, sum = 0.0f;
+    float acc[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-    for (int w = 0; w < WPR; ++w) {
-      const float wt = ex2(sh_ml[w].x - ref);
-      sum = fmaf(wt, sh_ml[w].y, sum);
+    for (int base = sub; base < parts; base += 32 * WPR) {
+      const int mine = base + lane * WPR;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (mine < parts) ml = p.part_ml[place(mine)];
+      float t = ml.x;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) acc[j] = fmaf(wt, sh_o[w][lane * kN + j], acc[j]);
+      for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+      const float now = fmaxf(top, t);
+      const float ref = now == -INFINITY ? 0.0f : now;
+      const float old = ex2(top - ref);
+      const float wt = ex2(ml.x - ref);
+      float z = ml.y * wt;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+      sum = sum * old + z;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) acc[j] *= old;
+      top = now;
+      const int many = (parts - 1 - base) / WPR + 1;
+      const int count = many < 32 ? many : 32;
+      for (int i0 = 0; i0 < count; i0 += 4) {
+        float v[4][kN];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i0 + u < count) {
+            const float* src = p.part_o + place(base + (i0 + u) * WPR) * D + lane * kN;
+            if constexpr (kN == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][kN - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[u][0] = x.x, v[u][1] = x.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float wi = __shfl_sync(kFull, wt, (i0 + u) & 31);
+          if (i0 + u < count) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) acc[j] = fmaf(wi, v[u][j], acc[j]);
+          }
+        }
+      }
     }
-    top = all;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t out = row * p.hq + h;
+    if constexpr (WPR > 1) {
+      __syncthreads();  // the row before has been read
 #pragma unroll
-  for (int j = 0; j < kN; ++j) {
-    const int64_t at = out * D + lane * kN + j;
-    if (p.o_bf16) static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(acc[j] * inv);
-    else static_cast<float*>(p.o)[at] = acc[j] * inv;
+      for (int j = 0; j < kN; ++j) sh_o[warp][lane * kN + j] = acc[j];
+      if (lane == 0) sh_ml[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (warp == 0) {
+        float all = -INFINITY;
+        for (int w = 0; w < WPR; ++w) all = fmaxf(all, sh_ml[w].x);
+        const float ref = all == -INFINITY ? 0.0f : all;
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+        for (int w = 0; w < WPR; ++w) {
+          const float wt = ex2(sh_ml[w].x - ref);
+          sum = fmaf(wt, sh_ml[w].y, sum);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) acc[j] = fmaf(wt, sh_o[w][lane * kN + j], acc[j]);
+        }
+        top = all;
+      }
+    }
+    if (parts >= 0 && sub == 0) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t at = id * D + lane * kN;
+      if constexpr (kN == 4) {
+        store_row4(p, at, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[kN - 1] * inv);
+      } else if (p.o_bf16) {
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+            __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+      } else {
+        *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(acc[0] * inv, acc[1] * inv);
+      }
+      if (lane == 0) p.lse[id] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
   }
-  if (lane == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  // A block without rows waits too: the kernel behind this one may begin once this grid is through,
+  // and must not meet the blocks of the one before.
+  if (!waited) ptx::wait_dependencies();
 }
 
 // The variant for a call: by the query rows that a sequence has on average.
@@ -1003,7 +1047,7 @@ struct Plan {
   int rows;      // RT
   int warps;     // of a block
   int64_t grid;
-  int64_t plan_off, ml_off, o_off, aside_off, bytes;
+  int64_t ml_off, o_off, aside_off, bytes;
 };
 Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   Plan r;
@@ -1018,8 +1062,7 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
                        (seqs + d.rows.n_rows * group / r.rows);
   r.grid = most < sms ? (most < 1 ? 1 : most) : sms;
   const int64_t slots = r.grid * r.warps * 2 * r.rows;
-  r.plan_off = 0;
-  r.ml_off = (seqs + 1) * 8;
+  r.ml_off = 0;
   r.o_off = (r.ml_off + slots * 8 + 255) / 256 * 256;
   r.aside_off = r.o_off + slots * d.cache.d * 4;
   r.bytes = r.aside_off + slots / 2 * d.cache.d * 4;
@@ -1028,7 +1071,7 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
 
 template <int D, int NT, int QP, int PP>
 cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
-              cudaStream_t s) {
+              int num_sms, cudaStream_t s) {
   using S = Shape<D, NT, QP, PP>;
   static_assert(1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8 <= 232448, "shared memory of a block");
   const int smem = 1024 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
@@ -1046,31 +1089,26 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
   cfg.dynamicSmemBytes = smem;
   if ((e = cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NT, QP, PP>, p, mk, mv)) != cudaSuccess)
     return cuda_fail(e, "kv_attn_kernel launch");
-  CombineParams cp{p, pl.grid * S::kWarps};
   // Eight warps an output row while there are few rows, or many partials to a row; else one.
-  const int64_t parts = cp.most / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
-  cfg.dynamicSmemBytes = 0;
-  cfg.blockDim = dim3(256);
-  if (parts > 16 || outs <= 1024) {
-    cfg.gridDim = dim3(static_cast<unsigned>(outs));
-    e = cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 8>, cp);
-  } else {
-    cfg.gridDim = dim3(static_cast<unsigned>((outs + 7) / 8));
-    e = cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 1>, cp);
-  }
+  const int64_t workers = pl.grid * S::kWarps, parts = workers / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
+  const bool wide = parts > 16 || outs <= 1024;
+  const int64_t blocks = wide ? outs : (outs + 7) / 8, resident = 4 * static_cast<int64_t>(num_sms);
+  cfg.dynamicSmemBytes = (p.rows.n_seqs + 1) * 8;
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < resident ? blocks : resident));
+  e = wide ? cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 8>, p, workers)
+           : cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 1>, p, workers);
   return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv_attn_combine_kernel launch");
 }
 
 template <int D>
 cp_status run_d(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
-                cudaStream_t s) {
+                int num_sms, cudaStream_t s) {
   if (pl.pp == 1)
-    return pl.nt == 1   ? run<D, 1, 1, 1>(p, pl, mk, mv, items, s)
-           : pl.nt == 2 ? run<D, 2, 1, 1>(p, pl, mk, mv, items, s)
-                        : run<D, 4, 1, 1>(p, pl, mk, mv, items, s);
+    return pl.nt == 1 ? run<D, 1, 1, 1>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 1>(p, pl, mk, mv, items, num_sms, s);
   if (pl.qp == 1)
-    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, s) : run<D, 2, 1, 2>(p, pl, mk, mv, items, s);
-  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, s) : run<D, 2, 2, 2>(p, pl, mk, mv, items, s);
+    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 2>(p, pl, mk, mv, items, num_sms, s);
+  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 2, 2>(p, pl, mk, mv, items, num_sms, s);
 }
 
 }  // namespace
@@ -1114,13 +1152,12 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   p.kv_pos = d.kv_pos;
   p.status = d.status;
   p.timeout_ns = timeout_ns;
-  p.plan = reinterpret_cast<int64_t*>(ws + pl.plan_off);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + pl.o_off);
   p.aside = reinterpret_cast<float*>(ws + pl.aside_off);
   const int64_t seqs = d.rows.n_seqs;
   const int64_t items = (seqs + d.rows.n_rows * p.group / pl.rows) * c.hkv;
-  return c.d == 128 ? run_d<128>(p, pl, mk, mv, items, s) : run_d<64>(p, pl, mk, mv, items, s);
+  return c.d == 128 ? run_d<128>(p, pl, mk, mv, items, num_sms, s) : run_d<64>(p, pl, mk, mv, items, num_sms, s);
 }
 
 }  // namespace cpattn

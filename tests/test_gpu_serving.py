@@ -96,6 +96,8 @@ WRITES = [  # rows of each sequence, tokens before them, page, hkv, d, dtype
     ([257], [255], 128, 1, 128, BF16),
     ([2] * 70, list(range(70)), 16, 2, 64, BF16),
     ([40], [8], 64, 1, 64, BF16),
+    ([3] * 700, [i % 37 for i in range(700)], 16, 1, 64, BF16),
+    ([20, 0, 0, 0, 9] * 30, [i % 50 for i in range(150)], 16, 3, 128, BF16),
 ]
 
 
@@ -343,6 +345,47 @@ def test_attention_scales_far_apart(dout):
     _check_attn(pool, pool.device(), q, [2], held, [158], PosMap(0, 1), dout)
 
 
+@pytest.mark.parametrize("d,page,dout", [(128, 128, F32), (128, 64, BF16), (64, 128, F32)])
+def test_attention_very_long_rows(d, page, dout):
+    """Millions of cached tokens, the same pages over and over: the softmax of the repeated keys is that
+    of the keys, and LSE grows by ln(repeats).  The sums are put aside on the way: at most A truncated
+    accumulations of 2^-23 to a sum (64 granules of 4 for bf16 outputs, 64 or 32 in all for fp32 ones), whatever
+    the length; 2^-19 for the fp32 sums of the parts."""
+    once, repeats = 1024, 4096
+    pool = Pool(1, [once], page, 2, d, 45)
+    pool.fill([once], 46, spread=1.0)
+    q = torch.randn((2, 6, d), generator=torch.Generator().manual_seed(47)).to(BF16)
+    table = np.tile(pool.table, (1, repeats))
+    o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), _i32([0, 2]), _i32([once * repeats]), _i32(table), o_dtype=dout)
+    k, v = pool.tokens_of(0, once)
+    acc = 256 if dout == BF16 else 64
+    for i in range(2):
+        for h in range(6):
+            kh, vh, x = k[:, h // 3], v[:, h // 3], q[i, h].double().numpy()
+            s = kh @ x * d ** -0.5
+            p = np.exp(s - s.max())
+            z = p.sum()
+            delta = float((2.0 ** -20 * (np.abs(kh) @ np.abs(x)) * d ** -0.5 + 2.0 ** -22 * np.abs(s)).max())
+            ref = p @ vh / z
+            w = 2.0 ** -11 if dout == BF16 else 2.0 ** -21
+            tol = p @ np.abs(vh) / z * (2 * delta + w + acc * 2.0 ** -23 + 2.0 ** -19)
+            tol = tol + np.abs(ref) * (2.0 ** -8 if dout == BF16 else 2.0 ** -24) * 1.01
+            assert np.all(np.abs(o[i, h].double().cpu().numpy() - ref) <= tol)
+            ref_l = s.max() + np.log(z) + np.log(repeats)
+            assert abs(float(lse[i, h]) - ref_l) <= delta + 2.0 ** -19 + 2.0 ** -22 * abs(ref_l)
+
+
+def test_attention_many_sequences():
+    n = cpa.KV_MAX_SEQS
+    held = [(7 * i) % 41 for i in range(n)]
+    rows = [1 if i % 5 else 0 for i in range(n)]
+    pool = Pool(n, held, 16, 1, 64, 48)
+    pool.fill(held, 49)
+    q = torch.randn((sum(rows) + 1, 2, 64), generator=torch.Generator().manual_seed(50)).to(BF16)
+    first = [m - 1 - (i % 3) for i, m in enumerate(held)]
+    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(0, 1), F32)
+
+
 def test_attention_bad_pages_answer_nan_and_report():
     held, rows = [100, 100, 100], [2, 2, 2]
     pool = Pool(3, held, 16, 2, 64, 51)
@@ -453,6 +496,50 @@ def test_attention_same_bits_on_streams_at_once_and_in_graphs():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     h.copy_(h0)
     s.copy_(s0)
+
+
+def test_a_decoding_step_in_a_graph():
+    """Rotation, write and attention captured as one step and replayed for the next tokens."""
+    seqs, hq, hkv, d, page = 3, 4, 2, 64, 16
+    held = [15, 32, 40]
+    pool = Pool(seqs, [64] * seqs, page, hkv, d, 101)
+    pool.fill(held, 102)
+    eager, graphed = pool.device(), pool.device()
+    gen = torch.Generator().manual_seed(103)
+    freq = tuple(100.0 ** (-i / 32) for i in range(32))
+    table, start = _i32(pool.table), _i32(range(seqs + 1))
+    q, k, v = (torch.empty((seqs, h, d), dtype=BF16, device=DEV) for h in (hq, hkv, hkv))
+    n, pos = _i32(held), _i32(held)
+    after = n + 1
+
+    def step(cache, out=None):
+        qr, kr = cpa.rope_axes([q, k], pos, freq)
+        cpa.kv_cache_write(cache, kr, v, start, n, table)
+        return cpa.kv_cache_attn(qr, cache, start, after, table, q_first=pos, o_dtype=BF16)
+
+    def load(i):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=gen).to(BF16) * 2.0 ** (i % 4))
+        for t in (n, pos):
+            t.copy_(_i32([h + i for h in held]))
+        after.copy_(n + 1)
+    load(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(graphed)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = step(graphed)
+    for i in range(20):
+        load(i)
+        want = step(eager)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        for a, b in zip(eager, graphed):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 def test_attention_wait_runs_out():
