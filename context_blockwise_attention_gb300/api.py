@@ -612,6 +612,7 @@ def _invalid(message):
 # descriptors packed in one go.
 _CACHE_ROWS = struct.Struct("@4Pq4i3P2iq")                  # cp_kv_cache, cp_kv_rows
 _KV_ATTN = struct.Struct("@4Pq4i3P2iq4P3if2qPqP2i")         # cp_kv_attn_desc
+_CACHE_BYTES = ctypes.sizeof(_KvCache)
 _CODES = {torch.float32: CP_F32, torch.bfloat16: CP_BF16}
 
 
@@ -688,9 +689,10 @@ def _rows_fields(row_start, tokens, name, page_table, n_rows, index):
 def _status_ptr(status, index):
     if status is None:
         return 0
+    ptr = _ptr(status, "status", torch.int32, index)
     if status.numel() < 1:
         _invalid("status must hold one int32")
-    return _ptr(status, "status", torch.int32, index)
+    return ptr
 
 
 def _code(dtype):
@@ -716,7 +718,7 @@ def kv_cache_write(cache, k, v, row_start, cached, page_table, status=None, stre
     if len(shape) != 3 or v.shape != shape or shape[1] != c[6] or shape[2] != c[7]:
         _invalid("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
     desc = _CACHE_ROWS.pack(*c, *_rows_fields(row_start, cached, "cached", page_table, shape[0], index))
-    _check(lib.cp_kv_cache_write(desc, desc[56:], pk, pv, code, _status_ptr(status, index),
+    _check(lib.cp_kv_cache_write(desc, desc[_CACHE_BYTES:], pk, pv, code, _status_ptr(status, index),
                                  _stream_of(stream, index)))
     return cache
 
@@ -743,7 +745,7 @@ def kv_cache_read(cache, row_start, first, page_table, n_rows, dtype=torch.bfloa
     pk, pv = _ptr(k, "k", dtype, index), _ptr(v, "v", dtype, index)
     if k.shape != shape or v.shape != shape:
         _invalid("k and v must be [n_rows, Hkv, D] with the cache's Hkv and D")
-    _check(lib.cp_kv_cache_read(desc, desc[56:], pk, pv, code, _status_ptr(status, index), _stream_of(stream, index)))
+    _check(lib.cp_kv_cache_read(desc, desc[_CACHE_BYTES:], pk, pv, code, _status_ptr(status, index), _stream_of(stream, index)))
     return k, v
 
 

@@ -74,6 +74,10 @@ cp_status validate_attn(const char* who, const cp_kv_attn_desc& d) {
     CP_INVALID("%s: o_dtype %d is not CP_F32 or CP_BF16", who, d.o_dtype);
   if (d.hq <= 0) CP_INVALID("%s: head counts must be positive", who);
   if (d.hq % d.cache.hkv != 0) CP_INVALID("%s: hq %d is not a multiple of hkv %d", who, d.hq, d.cache.hkv);
+  if (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size > 2000000000)
+    CP_INVALID("%s: max_pages * page_size exceeds 2e9 tokens", who);
+  if (d.rows.n_rows * d.hq > 0x7fffff00)  // query rows, rounded up to their blocks, stay int32
+    CP_INVALID("%s: n_rows * hq must stay below 2^31", who);
   return CP_OK;
 }
 

@@ -1046,6 +1046,7 @@ struct Plan {
   int nt, qp, pp;
   int rows;      // RT
   int warps;     // of a block
+  double most;
   int64_t grid;
   int64_t ml_off, o_off, aside_off, bytes;
 };
@@ -1058,9 +1059,10 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   r.nt = per <= (d.cache.d == 128 ? 8 : 32) ? 1 : 2;
   r.rows = r.nt * 8;
   r.warps = r.nt * d.cache.d >= 256 || r.nt * r.qp >= 4 ? 8 : 12;
-  const int64_t most = ((static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096 + kSetup) * d.cache.hkv *
-                       (seqs + d.rows.n_rows * group / r.rows);
-  r.grid = most < sms ? (most < 1 ? 1 : most) : sms;
+  // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
+  r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
+           static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
+  r.grid = r.most < sms ? static_cast<int64_t>(r.most) : sms;
   const int64_t slots = r.grid * r.warps * 2 * r.rows;
   r.ml_off = 0;
   r.o_off = (r.ml_off + slots * 8 + 255) / 256 * 256;
@@ -1117,6 +1119,10 @@ int64_t kv_attn_workspace(const cp_kv_attn_desc& d, int num_sms) { return plan_o
 
 cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s) {
   const Plan pl = plan_of(d, num_sms);
+  if (pl.most > 1e12) {  // their products with a worker's number stay int64
+    set_error("cp_kv_cache_attn: max_pages * page_size * hkv * n_seqs is too large for one call");
+    return CP_ERR_INVALID_ARG;
+  }
   const cp_kv_cache& c = d.cache;
   const int64_t lines = c.n_pages * c.hkv * c.page_size * c.d / 128;
   const int keys = 4096 / c.d;
@@ -1125,10 +1131,6 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   if (!encode_map_bytes(&mk, c.k, lines, box) || !encode_map_bytes(&mv, c.v, lines, box)) {
     set_error("cp_kv_cache_attn: tensor map encoding failed");
     return CP_ERR_CUDA;
-  }
-  if (d.rows.n_rows * d.hq > 0x7fffffff) {
-    set_error("cp_kv_cache_attn: too many rows");
-    return CP_ERR_INVALID_ARG;
   }
   uint8_t* const ws = static_cast<uint8_t*>(d.workspace);
   Params p{};

@@ -490,6 +490,7 @@ cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, voi
  * tokens behind a row's position), NaN among it, has no influence.
  * Rows of a sequence beyond a few dozen (long prompts) are answered, but cp_kv_cache_read followed
  * by cp_partial_attn is the faster way for them.
+ * max_pages * page_size is at most 2e9, n_rows * hq below 2^31.
  * The split of the work, and with it the order of the sums, depends on the shapes, on row_start,
  * tokens and q_first, and on the device's SM count alone: the same call gives the same bits.
  * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.

@@ -290,31 +290,31 @@ def test_attention_rows_that_see_little_or_nothing(dout):
     _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(0, 1), dout, scale=0.7)
 
 
-@pytest.mark.parametrize("g", [1, 8, 16])
+@pytest.mark.parametrize("g,d,page", [(1, 64, 32), (8, 64, 16), (16, 64, 128), (3, 128, 32), (16, 128, 16)])
 @pytest.mark.parametrize("dout", [BF16, F32])
-def test_attention_ignores_nan_and_infinity_behind_a_row(g, dout):
+def test_attention_ignores_nan_and_infinity_behind_a_row(g, d, page, dout):
     """Tokens that some rows see and others do not hold NaN values (and keys): the rows before them
     are as if they were not there, the others are NaN in those columns."""
     held, rows = [70], [4]
-    pool = Pool(1, held, 32, 1, 64, 31)
+    pool = Pool(1, held, page, 1, d, 31)
     pool.fill(held, 32)
-    q = torch.randn((4, g, 64), generator=torch.Generator().manual_seed(33)).to(BF16)
-    page, slot = pool.table[0, 2], 69 - 64  # the last token: row 3 alone sees it
-    pool.bytes[1][page, 0, slot, :7] = 0x7F
-    pool.bytes[1][page, 0, slot, 9] = 0xFF
+    q = torch.randn((4, g, d), generator=torch.Generator().manual_seed(33)).to(BF16)
+    last, slot = pool.table[0, 69 // page], 69 % page  # the last token: row 3 alone sees it
+    pool.bytes[1][last, 0, slot, :7] = 0x7F
+    pool.bytes[1][last, 0, slot, 9] = 0xFF
     cache = pool.device()
     start, first = _i32([0, 4]), _i32([66])
     o, lse = cpa.kv_cache_attn(q.to(DEV), cache, start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
-    clean = Pool(1, held, 32, 1, 64, 31)
+    clean = Pool(1, held, page, 1, d, 31)
     clean.fill(held, 32)
     o2, l2 = cpa.kv_cache_attn(q.to(DEV), clean.device(), start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
     assert torch.equal(o[:3], o2[:3]) and torch.equal(lse, l2)
-    nan = torch.zeros(64, dtype=torch.bool, device=DEV)
+    nan = torch.zeros(d, dtype=torch.bool, device=DEV)
     nan[:7] = True
     nan[9] = True
     assert bool(o[3][:, nan].isnan().all()) and torch.equal(o[3][:, ~nan], o2[3][:, ~nan])
     # a NaN key: the scores of the rows that see it are NaN
-    pool.bytes[0][page, 0, slot, 3] = 0x7F
+    pool.bytes[0][last, 0, slot, 3] = 0x7F
     o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), start, _i32(held), _i32(pool.table), q_first=first, o_dtype=dout)
     assert torch.equal(o[:3], o2[:3]) and torch.equal(lse[:3], l2[:3])
     assert bool(o[3].isnan().all()) and bool(lse[3].isnan().all())

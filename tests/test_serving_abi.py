@@ -48,6 +48,7 @@ def test_structs_match_the_header():
     assert ctypes.sizeof(api._KvCache) == 56
     assert ctypes.sizeof(api._KvRows) == 40
     assert ctypes.sizeof(api._KvAttnDesc) == 192
+    assert api._CACHE_ROWS.size == 96 and api._KV_ATTN.size == 192
     assert api._KvAttnDesc.q.offset == 96 and api._KvAttnDesc.kv_pos.offset == 144
     assert api._KvAttnDesc.workspace.offset == 160 and api._KvAttnDesc.flags.offset == 188
 
@@ -102,6 +103,8 @@ def test_attention_refuses():
     assert lib.cp_kv_cache_attn(None, None) == BAD
     assert call(workspace=0) == BAD
     assert call(cache=_cache(n_pages=0)) == BAD
+    assert call(rows=_rows(max_pages=1 << 26)) == BAD       # 2^32 tokens a sequence
+    assert call(rows=_rows(n_rows=1 << 27)) == BAD          # 2^32 query rows
     assert call(rows=_rows(n_rows=0), q=0) == api.CP_OK
     need = ctypes.c_int64()
     assert lib.cp_kv_cache_attn_workspace(None, ctypes.byref(need)) == BAD
