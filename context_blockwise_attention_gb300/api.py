@@ -794,11 +794,14 @@ def kv_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos
     odt = o.dtype
     ocode = _code(odt)
     if workspace is None:
-        workspace = _new((_attn_workspace(index, *c[4:8], *r[3:], hq, code, ocode),), torch.uint8, dev, stream)
+        need = _attn_workspace(index, *c[4:8], *r[3:], hq, code, ocode)
+        workspace = _new((need,), torch.uint8, dev, stream) if need else None
     _check(lib.cp_kv_cache_attn(
         _KV_ATTN.pack(*c, *r, pq, _ptr(o, "o", odt, index), _ptr(lse, "lse", torch.float32, index), first, code, ocode,
-                      hq, scale, kv_pos.base, kv_pos.stride, _ptr(workspace, "workspace", torch.uint8, index),
-                      workspace.numel(), _status_ptr(status, index), wait_timeout_ms, flags),
+                      hq, scale, kv_pos.base, kv_pos.stride,
+                      _ptr(workspace, "workspace", torch.uint8, index) if workspace is not None else 0,
+                      workspace.numel() if workspace is not None else 0, _status_ptr(status, index), wait_timeout_ms,
+                      flags),
         _stream_of(stream, index)))
     return o, lse
 

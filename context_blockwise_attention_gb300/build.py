@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libcpattn.so")
 
 SOURCES = ["host.cu", "layout.cu", "merge.cu", "reshard.cu", "attn_simt.cu", "attn_tc.cu", "tmap.cu",
            "bwd_prep.cu", "bwd_simt.cu", "bwd_tc.cu", "noalloc.cu", "host_serving.cu", "kv_cache.cu", "kv_attn.cu",
-           "rope.cu"]
+           "kv_attn_d64.cu", "kv_attn_d128.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",

@@ -1,0 +1,1179 @@
+// Attention of a batch's new tokens over the paged 8-bit cache (cp_kv_cache_attn): the kernels and their
+// launches.  kv_attn.cu chooses among them; kv_attn_d64.cu and kv_attn_d128.cu compile them.
+//
+// Per (sequence, KV head) the g = hq / hkv query heads of the sequence's rows are one block of
+// query rows that share keys and values:
+//   s_ij = scale * ks(page of j) * (q_i . k8_j),  p_ij = 2^(s_ij log2 e - m_i),
+//   O_i = sum_j p_ij vs(page of j) v8_j / l_i,    LSE_i = ln 2 (m_i + log2 l_i),  l_i = sum_j p_ij.
+// Bound: every cached byte is read once for 2 g rows' worth of products per byte, so it is memory
+// bound for up to a few dozen rows; the design is about keeping loads in flight and splitting the
+// keys evenly, not about the tensor rate.
+//
+// Work split.  The unit is a granule of 4096 / D keys (8 KB of cache) of one item (sequence, KV head,
+// block of RT query rows); granules are numbered item after item, each item beginning with kSetup
+// numbers that stand for the time its start and end take.  Every warp of the grid is a worker on its
+// own, with an equal share of consecutive numbers, whatever the sequences' lengths: no barrier
+// between warps, and a worker's copies run ahead across item borders.  An item that lies within one
+// share is finished there; of the others each worker leaves a partial (O unnormalised, m, l), at most
+// two per worker (the item its share begins inside of and the one it ends in), and a second kernel,
+// launched as a programmatic dependent, combines them in the order of the workers.  That kernel also
+// answers the rows of sequences without visible tokens, which are no items.
+//
+// Few short rows (SOLO): one block per (sequence, KV head), its warps share the granules, and the
+// partials meet in shared memory: one launch and no workspace.
+//
+// Products.  mma.sync m16n8k16 with f16 operands: e4m3 -> f16 is exact and one instruction for two
+// values, and the 128-row tiles of tcgen05 would be mostly empty with 8 to 32 query rows.  Both
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys and head dimensions fill the 16
+// rows of an operand tile, query rows its 8 columns, so that 8 rows waste nothing and O takes
+// D / 4 registers; P^T gets from the accumulator's layout into the operand's by one 8x8 transpose
+// for 8 keys.  The orders of keys and dimensions inside the products are free as long as both
+// operands agree; they are chosen so that every lane reads 16 consecutive bytes of a key or value
+// row, without bank conflicts under the 128-byte swizzle that the copies apply.
+//
+// Precision.  A query row is scaled by a power of two to at most 2^15; as f16 a bf16 row is then
+// exact (over 2^28 of range), an fp32 row is split into a high and a low part, 22 bits.  P, times
+// 2^15, is one f16 part for a bf16 output (2^-12, against the output's 2^-9) and two parts for an
+// fp32 one.  Sums, maxima and the accumulators are fp32.
+#pragma once
+
+#include "internal.h"
+#include "kv_common.cuh"
+#include "ptx.cuh"
+#include "sync.cuh"
+
+namespace cpattn {
+namespace kvattn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kPScale = 32768.0f;  // largest P operand
+constexpr int kSetup = 1;            // what an item costs besides its granules
+constexpr unsigned kFull = 0xffffffffu;
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+// QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
+template <int D>
+constexpr int kKeysOf = 4096 / D;  // keys of a granule
+
+template <int D, int NT, int QP, int PP>
+struct Shape {
+  // More warps hide more latency; registers (O takes NT D / 4) and shared memory bound their number.
+  static constexpr bool kHeavy = NT * D >= 256 || NT * QP >= 4;
+  static constexpr int kWarps = kHeavy ? 8 : 12;
+  static constexpr int kRows = NT * 8;  // RT
+  // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: 5e-6 of O after
+  // 64 granules of rows over 1e5 tokens, 1e-6 after 8.  So the accumulators are added to others every
+  // kFlush granules: in registers where there are some left (kHold), else in the workspace (every 8
+  // granules that took 5 %).  bf16 outputs can wait longer.
+  static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
+  static constexpr int kFlush = PP == 1 ? 64 : kHold ? 4 : D == 128 ? 16 : 8;
+  static constexpr int kKeys = kKeysOf<D>;
+  static constexpr int kSteps = kKeys / 16;          // steps of 16 keys
+  static constexpr int kHalf = kKeys * D;            // bytes of K (or V) of a granule
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr bool kQSmem = D == 128 && NT * QP >= 4;  // query operands in shared memory
+  static constexpr int kStages = kHeavy && !kQSmem ? 3 : 2;
+  static constexpr int kQBytes = kQSmem ? NT * QP * (D / 16) * 256 : 0;
+  static constexpr int kWarpBytes = kStages * kStage + kQBytes;
+  // behind the warps' parts (1024-byte aligned for the swizzle): scales, barriers, control, plan
+  static constexpr int kScaleOff = kWarps * kWarpBytes;               // [warp][stage][8] fp32
+  static constexpr int kBarOff = kScaleOff + kWarps * kStages * 32;   // [warp][stage] + stall
+  static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
+  static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;       // [warp] 8 bytes
+  static constexpr int kPlanOff = kScanOff + 16 * 8;
+};
+
+struct Params {
+  const float* scale[2];  // K, V
+  cp_kv_rows rows;
+  int64_t n_pages;
+  const void* q;
+  void* o;
+  float* lse;
+  const int32_t* q_first;
+  int32_t hq, hkv, group, page, page_log2;
+  int32_t q_bf16, o_bf16, stall;
+  float scale_log2;
+  cp_posmap kv_pos;
+  int32_t* status;
+  int64_t timeout_ns;
+  float* part_o;   // [workers][2][RT][D]
+  float2* part_ml; // [workers][2][RT]: m (base 2), l
+  float* aside;    // [workers][RT][D]: accumulators put aside
+};
+
+// What a sequence asks for.
+struct Seq {
+  int64_t r0;      // first row
+  int64_t pos0;    // position of its first row
+  int32_t rows;
+  int32_t tokens;  // cached tokens, as far as the page table reaches
+  int32_t keys;    // tokens that its last row sees
+  int32_t gpi;     // granules of an item
+  int32_t blocks;  // blocks of RT query rows; 0 where no row sees a token
+  bool over;       // more tokens than the table has pages for
+};
+
+// Number of tokens that a row at position `pos` sees: token j stands at base + stride * j.
+__device__ __forceinline__ int32_t visible(const Params& p, int32_t tokens, int64_t pos) {
+  if (p.q_first == nullptr) return tokens;
+  const int64_t off = pos - p.kv_pos.base;  // below 2^32
+  if (off < 0) return 0;
+  const uint32_t n = static_cast<uint32_t>(off) / static_cast<uint32_t>(p.kv_pos.stride);
+  return n < static_cast<uint32_t>(tokens) ? static_cast<int32_t>(n) + 1 : tokens;
+}
+
+template <int D, int RT>
+__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
+  Seq s;
+  s.r0 = kv::row_at(p.rows, b);
+  const int64_t r1 = kv::row_at(p.rows, b + 1);
+  s.rows = r1 > s.r0 ? static_cast<int32_t>(r1 - s.r0) : 0;
+  int64_t t = __ldg(p.rows.tokens + b);
+  const int64_t room = static_cast<int64_t>(p.rows.max_pages) << p.page_log2;
+  s.over = t > room;
+  if (s.over) t = room;
+  s.tokens = t < 0 ? 0 : static_cast<int32_t>(t);
+  s.pos0 = p.q_first != nullptr ? __ldg(p.q_first + b) : 0;
+  s.keys = s.rows > 0 ? visible(p, s.tokens, s.pos0 + s.rows - 1) : 0;
+  s.gpi = (s.keys + kKeysOf<D> - 1) / kKeysOf<D>;
+  s.blocks = s.keys > 0 ? (s.rows * p.group + RT - 1) / RT : 0;
+  return s;
+}
+__device__ __forceinline__ int64_t numbers(const Params& p, const Seq& s) {
+  return static_cast<int64_t>(s.blocks) * p.hkv * (s.gpi + kSetup);
+}
+
+// Shares of W numbers among n workers: worker w has [share(w), share(w + 1)).
+__device__ __forceinline__ int64_t share(int64_t W, int64_t n, int64_t w) { return W * w / n; }
+__device__ __forceinline__ int64_t worker_of(int64_t W, int64_t n, int64_t x) { return ((x + 1) * n - 1) / W; }
+__device__ __forceinline__ int64_t workers(int64_t W, int64_t most) { return W < most ? W : most; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t to_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 from_f16x2(uint32_t h) {
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// Four consecutive query elements as fp32.
+__device__ __forceinline__ void load4(const Params& p, int64_t at, float (&x)[4]) {
+  if (p.q_bf16) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + at));
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  }
+}
+
+__device__ __forceinline__ void store_row4(const Params& p, int64_t at, float a, float b, float c, float d) {
+  if (p.o_bf16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+    uint2 pk;
+    pk.x = *reinterpret_cast<const uint32_t*>(&x);
+    pk.y = *reinterpret_cast<const uint32_t*>(&y);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at) = pk;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = make_float4(a, b, c, d);
+  }
+}
+
+// A lane's consecutive part of a row.
+__device__ __forceinline__ void store_lane(const Params& p, int64_t at, const float (&x)[4]) {
+  store_row4(p, at, x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_lane(const Params& p, int64_t at, const float (&x)[2]) {
+  if (p.o_bf16)
+    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + at) = __floats2bfloat162_rn(x[0], x[1]);
+  else
+    *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(x[0], x[1]);
+}
+
+// Numbers before each sequence, in shared memory: plan[0 .. n_seqs].
+template <int D, int RT, int THREADS>
+__device__ __forceinline__ void make_plan(const Params& p, int64_t* plan, int64_t* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = p.rows.n_seqs;
+  int64_t before = 0;
+  for (int base = 0; base < n; base += THREADS) {
+    const int b = base + tid;
+    int64_t x = 0;
+    if (b < n) {
+      const Seq s = seq_of<D, RT>(p, b);
+      x = numbers(p, s);
+      if (s.over && s.rows > 0 && blockIdx.x == 0) kv::report(p.status, kv::kSiteTokens);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t add = before, all = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) add += scratch[i];
+      all += scratch[i];
+    }
+    if (b < n) plan[b + 1] = add + x;
+    before += all;
+    __syncthreads();
+  }
+  if (tid == 0) plan[0] = 0;
+  __syncthreads();
+}
+
+// A place in the numbering of granules.
+struct Cursor {
+  int b, head, block, g;
+  int gpi, blocks;
+};
+
+// Moves to the first sequence behind c.b that has items.
+template <int D, int RT>
+__device__ __forceinline__ void next_seq(const Params& p, Cursor& c, Seq& s) {
+  do {
+    ++c.b;
+    if (c.b >= p.rows.n_seqs) return;
+    s = seq_of<D, RT>(p, c.b);
+  } while (s.blocks == 0);
+  c.head = c.block = c.g = 0;
+  c.gpi = s.gpi;
+  c.blocks = s.blocks;
+}
+
+template <int D, int NT, int QP, int PP, bool SOLO>
+__global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
+    kv_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v) {
+  using S = Shape<D, NT, QP, PP>;
+  constexpr int RT = S::kRows;
+  constexpr int kMt = D / 16;  // 16-row tiles of O^T; also steps of 16 dimensions of S
+  constexpr int kCols = D / 8; // columns of O that a lane holds, for two query rows
+  constexpr int kSt = S::kStages, kSteps = S::kSteps, kKeys = S::kKeys;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  int64_t* const plan = reinterpret_cast<int64_t*>(smem + S::kPlanOff);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + S::kCtlOff);
+  const uint32_t base = ptx::smem_u32(smem);
+  const uint32_t ring = base + warp * S::kWarpBytes;
+  const uint32_t q_smem = ring + kSt * S::kStage;
+  const uint32_t scales = base + S::kScaleOff + warp * kSt * 32;
+  const uint32_t bars = base + S::kBarOff + warp * kSt * 8;
+  const uint32_t stall_bar = base + S::kBarOff + S::kWarps * kSt * 8;
+
+  if (lane == 0) {
+    // one arrival for the copies' bytes, and one for each lane that copies a scale
+    for (int i = 0; i < kSt; ++i) ptx::mbar_init(bars + i * 8, 1 + 2 * kSteps);
+    if (warp == 0) {
+      ptx::mbar_init(stall_bar, 1);
+      *abort_flag = 0;
+      ptx::tma_prefetch_desc(&map_k);
+      ptx::tma_prefetch_desc(&map_v);
+    }
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  ptx::wait_dependencies();  // launched early: what was in the stream before is complete from here on
+  const int n_seqs = p.rows.n_seqs;
+  const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
+  Cursor c;  // where the products are
+  Seq seq;
+  int64_t left;  // numbers of the share from the cursor on
+  bool inside;   // the share begins inside of an item
+  const bool stalled = p.stall && blockIdx.x == 0 && warp == 0;  // test only
+  if constexpr (SOLO) {
+    c.b = blockIdx.x / p.hkv;
+    c.head = blockIdx.x - c.b * p.hkv;
+    seq = seq_of<D, RT>(p, c.b);
+    if (seq.over && seq.rows > 0 && tid == 0) kv::report(p.status, kv::kSiteTokens);
+    if (seq.blocks == 0) {  // nothing to see
+      for (int i = tid; i < seq.rows * p.group * (D / 4); i += S::kWarps * 32) {
+        const int rho = i / (D / 4), t = rho / p.group;
+        const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+        store_row4(p, out * D + (i & (D / 4 - 1)) * 4, 0.0f, 0.0f, 0.0f, 0.0f);
+        if ((i & (D / 4 - 1)) == 0) p.lse[out] = -INFINITY;
+      }
+      return;
+    }
+    __syncthreads();  // the abort flag is set up
+    c.block = 0;
+    c.gpi = seq.gpi;
+    c.blocks = seq.blocks;
+    c.g = seq.gpi * warp / S::kWarps;
+    left = seq.gpi * (warp + 1) / S::kWarps - c.g;
+    inside = false;
+  } else {
+    make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
+    ptx::launch_dependents();
+    if (stalled) {
+      sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+      return;
+    }
+    const int64_t W = plan[n_seqs];
+    const int64_t n_workers = workers(W, static_cast<int64_t>(gridDim.x) * S::kWarps);
+    if (worker >= n_workers) return;
+    const int64_t lo = share(W, n_workers, worker), hi = share(W, n_workers, worker + 1);
+    left = hi - lo;
+    int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (plan[mid] <= lo) a = mid;
+      else z = mid - 1;
+    }
+    c.b = a;
+    seq = seq_of<D, RT>(p, a);
+    const int64_t off = lo - plan[a];
+    const int64_t item = off / (seq.gpi + kSetup);
+    const int at = static_cast<int>(off - item * (seq.gpi + kSetup));
+    inside = at >= kSetup;
+    c.g = inside ? at - kSetup : 0;
+    if (!inside) left -= kSetup - at;
+    c.head = static_cast<int>(item / seq.blocks);
+    c.block = static_cast<int>(item - static_cast<int64_t>(c.head) * seq.blocks);
+    c.gpi = seq.gpi;
+    c.blocks = seq.blocks;
+    if (left <= 0) return;
+  }
+  bool ok = true;
+  if (stalled) {  // the block's other warps still meet it
+    ok = sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+    left = 0;
+  }
+  const int g_first = c.g, solo_left = static_cast<int>(left);  // of a block of rows, where SOLO
+  Cursor f = c;  // where the copies are
+  int64_t to_issue = left;
+  int f_keys = seq.keys;
+  int f_last = seq.over ? p.rows.max_pages - 1 : -1;  // a page that counts as bad
+  int window = -32;        // lane i holds page window + i of sequence f.b
+  int pages = -1;
+
+  auto page_of = [&](int ord) -> int {
+    if (static_cast<unsigned>(ord - window) >= 32u) {
+      window = ord;
+      const int64_t id = kv::page_at(p.rows, p.n_pages, f.b, ord + lane);
+      pages = id < 0 || ord + lane == f_last ? -1 : static_cast<int>(id);
+    }
+    return __shfl_sync(kFull, pages, ord - window);
+  };
+  // Starts the copies of one page's part of K and V (`lines` lines of the maps from `page` on).
+  auto copy = [&](int page, int slot, uint32_t dst, uint32_t bar) {
+    const int row = (page * p.hkv + f.head) * p.page + slot;  // below 2^31: checked on the host
+    const int line = D == 128 ? row : row >> 1;
+    ptx::tma_load_2d(dst, &map_k, 0, line, bar);
+    ptx::tma_load_2d(dst + S::kHalf, &map_v, 0, line, bar);
+  };
+  // Copies the scale of K (even lane) or V (odd lane), or stands in for it: where there is no
+  // token the smallest scale, for a bad page NaN, which reaches the rows that see it.
+  auto copy_scale = [&](int page, bool need, uint32_t to) {
+    if (page >= 0) ptx::cp_async4(to, p.scale[lane & 1] + (page * p.hkv + f.head));
+    else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(need ? 0x7fffffffu : 0x1f800000u) : "memory");
+  };
+
+  // Starts the copies of the next granule into stage `st`.
+  auto issue = [&](int st) {
+    const uint32_t bar = bars + st * 8, dst = ring + st * S::kStage;
+    const int key0 = f.g * kKeys;
+    const int mine = key0 + (lane >> 1) * 16;  // lane 2 i + w copies the scale of step i of K (w = 0) or V (w = 1)
+    int my_page = -1;
+    bool bad = false;
+    if (p.page >= kKeys) {
+      const int page = page_of(key0 >> p.page_log2);
+      bad = page < 0;
+      my_page = page;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, bad ? 0 : S::kStage);
+        if (!bad) copy(page, key0 & (p.page - 1), dst, bar);
+      }
+    } else {  // several pages, as far as there are tokens
+      const int part = p.page * D;
+      uint32_t tx = 0;
+      int page[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = key0 + i * p.page;
+        page[i] = -1;
+        if (i * p.page < kKeys && k < f_keys) {
+          page[i] = page_of(k >> p.page_log2);
+          if (page[i] >= 0) tx += 2 * part;
+          else bad = true;
+          if (mine >= k && mine < k + p.page) my_page = page[i];
+        }
+      }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, tx);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          if (page[i] >= 0) copy(page[i], 0, dst + i * part, bar);
+      }
+    }
+    if (lane < 2 * kSteps) {
+      copy_scale(my_page, mine < f_keys, scales + st * 32 + lane * 4);
+      ptx::cp_async_arrive(bar);
+    }
+    if (bad && lane == 0) kv::report(p.status, kv::kSitePage);
+    --to_issue;
+    if (++f.g == f.gpi && to_issue > kSetup) {
+      to_issue -= kSetup;
+      f.g = 0;
+      if (++f.block == f.blocks) {
+        f.block = 0;
+        if (++f.head == p.hkv) {
+          Seq s{};
+          next_seq<D, RT>(p, f, s);
+          f_keys = s.keys;
+          f_last = s.over ? p.rows.max_pages - 1 : -1;
+          window = -32;
+        }
+      }
+    } else if (f.g == f.gpi) {
+      to_issue = 0;
+    }
+  };
+
+  // lane's offsets inside a stage.  128-byte lines; 16-byte chunk x of line y sits at x ^ (y & 7).
+  // A step of 16 keys has two groups u = 0, 1 of 8, group u being rows 8 u .. 8 u + 7 of the operand.
+  // D = 128: a line is a key; row c of group u is key 8 u + c.  Lane (gid, tig) reads dimensions
+  //   32 tig .. + 31 of key c = gid, and dimensions 16 gid .. + 15 of the values of c = 2 tig, 2 tig + 1.
+  // D = 64: a line is two keys; row c of group u is key 4 (c >> 1) + 2 u + (c & 1), so that the four
+  //   values of a lane, 4 tig .. 4 tig + 3, are two lines that no other tig shares a bank with.
+  uint32_t k_off[2], v_off[4];
+  if (D == 128) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) k_off[j] = gid * 128 + (((2 * tig + j) ^ gid) << 4);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int c0 = 2 * tig + (x & 1);
+      v_off[x] = S::kHalf + (c0 + 8 * (x >> 1)) * 128 + ((gid ^ c0) << 4);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int line = 2 * (gid >> 1) + u;
+      k_off[u] = line * 128 + ((((gid & 1) * 4 + tig) ^ line) << 4);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int line = 2 * tig + (x >> 1);
+      v_off[x] = S::kHalf + line * 128 + ((((x & 1) * 4 + (gid >> 1)) ^ line) << 4) + (gid & 1) * 8;
+    }
+  }
+  // key of row c of group u in a step
+  auto key_at = [](int u, int c0) { return D == 128 ? 8 * u + c0 : 4 * (c0 >> 1) + 2 * u + (c0 & 1); };
+
+  uint32_t qf[S::kQSmem ? 1 : NT * QP][S::kQSmem ? 1 : kMt][2];
+  // of the lane's two query rows 2 tig, 2 tig + 1 in each tile
+  float fac[NT][2], m[NT][2], l[NT][2];
+  int lim[NT][2];
+  float acc[NT][kMt][4];
+  float v_ref = 1e-37f;  // largest V scale so far: P is held relative to it
+  float inv_ref = 0.0f;  // kPScale / v_ref
+  int lim_min = 0, lim_max = 0;
+  int live = NT;         // tiles that have rows
+  int row_q = 0;         // first query row (token row * group + head in group) of the block
+  float* const aside = p.aside + worker * (RT * D);
+  float m_aside[NT][2], v_aside = 0.0f;  // what the values put aside refer to
+  bool flushed = false;
+  int since = 0;         // granules since then
+  constexpr bool kHold = S::kHold;
+  float held[kHold ? kMt : 1][4];  // of the one tile
+
+  auto begin_item = [&]() {
+    row_q = c.block * RT;
+    const int n_rows = seq.rows * p.group;
+    live = min(NT, (n_rows - row_q + 7) / 8);
+    int lmin = 0x7fffffff, lmax = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // the lane's part of query row gid of the tile
+      const int rho = row_q + n * 8 + gid;
+      const bool live = rho < n_rows;
+      const int t = live ? rho / p.group : 0;
+      const int64_t at = ((seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group)) * D + tig * (D / 4);
+      int lm = live ? visible(p, seq.tokens, seq.pos0 + t) : -1;
+      if (live) {
+        lmin = min(lmin, lm);
+        lmax = max(lmax, lm);
+      }
+      float x[kMt][4];
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) {
+        if (live) load4(p, at + j * 4, x[j]);
+        else x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[j][e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      // 2^e <= top < 2^(e + 1) goes to [2^14, 2^15); rows of (almost) zeros keep a finite factor
+      const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = kv::pow2(14 - e), f = p.scale_log2 * kv::pow2(e - 14);
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) {
+        uint32_t h[2], w[2];
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const float a = x[j][2 * e2] * up, b = x[j][2 * e2 + 1] * up;
+          h[e2] = to_f16x2(a, b);
+          const float2 back = from_f16x2(h[e2]);
+          w[e2] = to_f16x2(a - back.x, b - back.y);
+        }
+        if constexpr (S::kQSmem) {
+          const uint32_t to = q_smem + ((n * QP * kMt + j) * 32 + lane) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
+          if (QP == 2)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + kMt * 256), "r"(w[0]), "r"(w[1]) : "memory");
+        } else {
+          qf[n * QP][j][0] = h[0], qf[n * QP][j][1] = h[1];
+          if (QP == 2) qf[n * QP + QP - 1][j][0] = w[0], qf[n * QP + QP - 1][j][1] = w[1];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);
+        lim[n][r] = __shfl_sync(kFull, lm, (2 * tig + r) * 4);
+        m[n][r] = -INFINITY;
+        l[n][r] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
+    lim_min = __reduce_min_sync(kFull, lmin);
+    lim_max = __reduce_max_sync(kFull, lmax);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (lim[n][r] < 0) lim[n][r] = lim_max;  // rows of nobody must not make the tile a masked one
+    v_ref = 1e-37f;
+    flushed = false;
+    since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) held[j][0] = held[j][1] = held[j][2] = held[j][3] = 0.0f;
+    }
+  };
+
+  // One granule for the first kLive tiles of query rows; kMask: some of its keys are not seen by some row.
+  auto granule = [&](int st, auto live_tag, auto mask_tag) {
+    constexpr int kLive = decltype(live_tag)::value;
+    constexpr bool kMask = decltype(mask_tag)::value != 0;
+    const uint32_t tile = ring + st * S::kStage;
+    const int key0 = c.g * kKeys;
+    float ks[kSteps], vs[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; i += 2) {
+      const uint4 v = ptx::lds128u(scales + st * 32 + i * 8);
+      ks[i] = __uint_as_float(v.x), vs[i] = __uint_as_float(v.y);
+      ks[i + 1] = __uint_as_float(v.z), vs[i + 1] = __uint_as_float(v.w);
+    }
+    // S^T: s[n][i][2 u + r] is key key_at(u, gid) of step i for query row 2 tig + r of tile n
+    float s[kLive][kSteps][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t kw[2][kMt];  // word j of the lane's part of a key: dimensions of step j
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (D == 128) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 v = ptx::lds128u(tile + (2 * i + u) * 1024 + k_off[j]);
+            kw[u][4 * j] = v.x, kw[u][4 * j + 1] = v.y, kw[u][4 * j + 2] = v.z, kw[u][4 * j + 3] = v.w;
+          }
+        } else {
+          const uint4 v = ptx::lds128u(tile + i * 1024 + k_off[u]);
+          kw[u][0] = v.x, kw[u][1] = v.y, kw[u][2] = v.z, kw[u][3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kLive; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) {
+        const uint32_t a[4] = {kv::e4m3x2_to_f16x2(kw[0][j]), kv::e4m3x2_to_f16x2(kw[1][j]),
+                               kv::e4m3x2_to_f16x2(kw[0][j] >> 16), kv::e4m3x2_to_f16x2(kw[1][j] >> 16)};
+#pragma unroll
+        for (int n = 0; n < kLive * QP; ++n) {
+          if constexpr (S::kQSmem) {
+            const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
+            ptx::mma_f16(s[n / QP][i], a, b.x, b.y);
+          } else {
+            ptx::mma_f16(s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
+          }
+        }
+      }
+    }
+    // Maxima.  s keeps the products; a score is s * f2 (f2 > 0), and only masked tiles, where an unseen
+    // page's scale may be anything, hold scores themselves.
+    float corr[kLive][2], f2[kLive][2][kSteps];
+    bool grew = false;
+#pragma unroll
+    for (int n = 0; n < kLive; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          f2[n][r][i] = fac[n][r] * ks[i];
+          if (kMask) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float& z = s[n][i][2 * u + r];
+              z = key0 + 16 * i + key_at(u, gid) >= lim[n][r] ? -INFINITY : z * f2[n][r][i];
+            }
+          }
+          const float top2 = fmaxf(s[n][i][r], s[n][i][2 + r]);
+          top = fmaxf(top, kMask ? top2 : top2 * f2[n][r][i]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+        const bool up = top > m[n][r];
+        grew |= up;
+        const float now = up ? top : m[n][r];
+        corr[n][r] = now == -INFINITY ? 1.0f : ex2(m[n][r] - now);
+        m[n][r] = now;
+      }
+    float v_top = v_ref;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) v_top = fmaxf(v_top, vs[i]);
+    if (__any_sync(kFull, grew || v_top > v_ref)) {
+      const float rr = v_ref / v_top;
+      v_ref = v_top;
+      inv_ref = kPScale / v_top;
+#pragma unroll
+      for (int n = 0; n < kLive; ++n) {
+        l[n][0] *= corr[n][0];
+        l[n][1] *= corr[n][1];
+        const float c0 = corr[n][0] * rr, c1 = corr[n][1] * rr;
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) {
+          acc[n][j][0] *= c0;
+          acc[n][j][1] *= c1;
+          acc[n][j][2] *= c0;
+          acc[n][j][3] *= c1;
+          if constexpr (kHold) {
+            held[j][0] *= c0;
+            held[j][1] *= c1;
+            held[j][2] *= c0;
+            held[j][3] *= c1;
+          }
+        }
+      }
+    }
+    // Weights as operands: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid
+    uint32_t pb[kLive][PP][kSteps][2];
+    float vf[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) vf[i] = vs[i] * inv_ref;
+#pragma unroll
+    for (int n = 0; n < kLive; ++n) {
+      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float pv[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float z = s[n][i][2 * u + r];
+            const float w = ex2(kMask ? z - ref[r] : fmaf(z, f2[n][r][i], -ref[r]));
+            l[n][r] += w;
+            pv[r] = w * vf[i];
+            if (kMask && z == -INFINITY) pv[r] = 0.0f;  // an unseen page's scale may be NaN
+          }
+          const uint32_t h = to_f16x2(pv[0], pv[1]);
+          pb[n][0][i][u] = ptx::transpose8x8(h);
+          if constexpr (PP == 2) {
+            const float2 back = from_f16x2(h);
+            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(pv[0] - back.x, pv[1] - back.y));
+          }
+        }
+    }
+    // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      uint32_t vw[4][D / 32];
+      bool odd = false;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (D == 128) {
+          const uint4 v = ptx::lds128u(tile + i * 2048 + v_off[x]);
+          vw[x][0] = v.x, vw[x][1] = v.y, vw[x][D / 32 - 2] = v.z, vw[x][D / 32 - 1] = v.w;
+        } else {
+          const uint2 v = ptx::lds64(tile + i * 1024 + v_off[x]);
+          vw[x][0] = v.x, vw[x][1] = v.y;
+        }
+        if (kMask) {
+          // what no row sees counts as zero: 0 * NaN would not vanish
+          const int key = key0 + 16 * i + key_at(x >> 1, 2 * tig + (x & 1));
+          if (key >= lim_max) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) vw[x][w] = 0u;
+          } else if (key >= lim_min) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) odd |= __vcmpeq4(vw[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+          }
+        }
+      }
+      if (kMask && __any_sync(kFull, odd)) {
+        // NaN among values that only some of the rows see: those rows get NaN by a product of the
+        // places of the NaN with the rows' visibility, and the NaN are taken out of V.
+        uint32_t vis[kLive][2];
+#pragma unroll
+        for (int n = 0; n < kLive; ++n) {
+          const int l0 = __shfl_sync(kFull, lim[n][0], gid >> 1), l1 = __shfl_sync(kFull, lim[n][1], gid >> 1);
+          const int lm = (gid & 1) ? l1 : l0;  // of query row gid
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int k = key0 + 16 * i + key_at(u, 2 * tig);
+            vis[n][u] = (k < lm ? 0x3c00u : 0u) | (k + 1 < lm ? 0x3c000000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t at[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t nan = __vcmpeq4(vw[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            at[x] = nan & 0x38383838u;  // e4m3 one
+            vw[x][w] &= ~nan;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a = __byte_perm(at[0], at[1], half ? 0x7362 : 0x5140);
+            const uint32_t b = __byte_perm(at[2], at[3], half ? 0x7362 : 0x5140);
+            const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
+                                    kv::e4m3x2_to_f16x2(b >> 16)};
+#pragma unroll
+            for (int n = 0; n < kLive; ++n) {
+              float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              ptx::mma_f16(hit, av, vis[n][0], vis[n][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (hit[k] > 0.0f) acc[n][2 * w + half][k] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // columns 4 w + 2 half, + 1: bytes of two keys side by side
+          const uint32_t a = __byte_perm(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
+          const uint32_t b = __byte_perm(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
+          const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
+                                  kv::e4m3x2_to_f16x2(b >> 16)};
+#pragma unroll
+          for (int n = 0; n < kLive; ++n)
+#pragma unroll
+            for (int part = 0; part < PP; ++part)
+              ptx::mma_f16(acc[n][2 * w + half], av, pb[n][part][i][0], pb[n][part][i][1]);
+        }
+    }
+  };
+
+  // The same for the tiles that the block has: sequences differ in their rows.
+  auto granule_live = [&](int st, auto mask_tag) {
+    if constexpr (NT == 1) {
+      granule(st, Int<1>{}, mask_tag);
+    } else {
+      if (live == 1) granule(st, Int<1>{}, mask_tag);
+      else granule(st, Int<NT>{}, mask_tag);
+    }
+  };
+
+  // Columns 4 j .. 4 j + 3 of the lane's part of query row 2 tig + r of tile n: the accumulators, with
+  // what was put aside (`from`) at weight `keep`.
+  auto four = [&](int n, int r, int j, const float* from, float keep, float (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = acc[n][2 * j + (e >> 1)][2 * (e & 1) + r];
+      if constexpr (kHold) x[e] += held[2 * j + (e >> 1)][2 * (e & 1) + r];
+    }
+    if (flushed) {
+      const float4 y = *reinterpret_cast<const float4*>(from + 4 * j);
+      x[0] = fmaf(y.x, keep, x[0]), x[1] = fmaf(y.y, keep, x[1]);
+      x[2] = fmaf(y.z, keep, x[2]), x[3] = fmaf(y.w, keep, x[3]);
+    }
+  };
+
+  // Puts the accumulators aside: adds them to the others and clears them.
+  auto to_workspace = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float* const at = aside + (n * 8 + 2 * tig + r) * D + gid * kCols;
+        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, at, keep, x);
+          *reinterpret_cast<float4*>(at + 4 * j) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        m_aside[n][r] = m[n][r];
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
+    v_aside = v_ref;
+    flushed = true;
+  };
+  auto flush = [&]() {
+    since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          held[j][e] += acc[0][j][e];
+          acc[0][j][e] = 0.0f;
+        }
+    } else {
+      to_workspace();
+    }
+  };
+
+  // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial at
+  // part_o [RT][D], part_ml [RT].
+  auto end_item = [&](bool whole, float* part_o, float2* part_ml) {
+    const int n_rows = seq.rows * p.group;
+    const float back = v_ref * (1.0f / kPScale);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[n][r];
+        sum += __shfl_xor_sync(kFull, sum, 4);
+        sum += __shfl_xor_sync(kFull, sum, 8);
+        sum += __shfl_xor_sync(kFull, sum, 16);
+        const int local = n * 8 + 2 * tig + r;
+        const int rho = row_q + local;
+        if (rho >= n_rows) continue;
+        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
+        const float f = whole ? (sum == 0.0f ? 0.0f : back / sum) : back;
+        float* const part = part_o + local * D + gid * kCols;
+        const int t = rho / p.group;
+        const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, aside + local * D + gid * kCols, keep, x);
+          if (whole) store_row4(p, out * D + gid * kCols + 4 * j, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+          else *reinterpret_cast<float4*>(part + 4 * j) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        }
+        if (gid == 0) {
+          if (whole) p.lse[out] = sum == 0.0f ? -INFINITY : (m[n][r] + log2f(sum)) * kLn2;
+          else part_ml[local] = make_float2(m[n][r], sum);
+        }
+      }
+  };
+
+  // A stage is mostly there already: the clock that bounds the wait is read only where it is not.
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+  };
+  int st = 0, in_flight = 0;
+  uint32_t parity = 0;
+  bool from_start = c.g == 0;  // the item at hand is ours from its first granule on
+  while (true) {  // once; for each block of rows where SOLO
+    for (int i = 0; i < kSt; ++i)
+      if (to_issue > 0) {
+        issue(st + i < kSt ? st + i : st + i - kSt);
+        ++in_flight;
+      }
+    begin_item();
+    while (left > 0) {
+      if (!wait(bars + st * 8, parity)) {
+        ok = false;
+        break;
+      }
+      const int key0 = c.g * kKeys;
+      if (key0 + kKeys <= lim_min) granule_live(st, Int<0>{});
+      else if (key0 < lim_max) granule_live(st, Int<1>{});
+      __syncwarp();
+      if (to_issue > 0) issue(st);
+      else --in_flight;
+      if (++st == kSt) {
+        st = 0;
+        parity ^= 1u;
+      }
+      --left;
+      ++c.g;
+      if (c.g == c.gpi || left == 0) {
+        if (SOLO) break;
+        const int64_t slot = worker * 2 + (inside ? 0 : 1);
+        end_item(from_start && c.g == c.gpi, p.part_o + slot * (RT * D), p.part_ml + slot * RT);
+        left -= kSetup;  // of the next item
+        if (left <= 0) break;
+        c.g = 0;
+        from_start = true;
+        inside = false;
+        if (++c.block == c.blocks) {
+          c.block = 0;
+          if (++c.head == p.hkv) next_seq<D, RT>(p, c, seq);
+        }
+        begin_item();
+      } else if (++since == S::kFlush && (kHold || !SOLO)) {  // 16 granules need no more
+        flush();
+      }
+    }
+    if (!SOLO) break;
+    // The warps' partials meet where their stages were; a warp of no granules leaves an empty one.
+    static_assert(S::kStages * S::kStage >= RT * (D * 4 + 8), "a warp's partial fits its stages");
+    float* const mine = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);
+    __syncwarp();
+    end_item(false, mine, reinterpret_cast<float2*>(mine + RT * D));
+    __syncthreads();
+    for (int i = warp; i < RT; i += S::kWarps) {
+      const int rho = row_q + i;
+      if (rho >= seq.rows * p.group) break;
+      float top = -INFINITY;
+      for (int w = 0; w < S::kWarps; ++w)
+        top = fmaxf(top, reinterpret_cast<const float2*>(smem + w * S::kWarpBytes + RT * D * 4)[i].x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, x[D / 32];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] = 0.0f;
+      for (int w = 0; w < S::kWarps; ++w) {
+        const float2 ml = reinterpret_cast<const float2*>(smem + w * S::kWarpBytes + RT * D * 4)[i];
+        const float wt = ex2(ml.x - ref);
+        sum = fmaf(wt, ml.y, sum);
+        const float* const from = reinterpret_cast<const float*>(smem + w * S::kWarpBytes) + i * D + lane * (D / 32);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = fmaf(wt, from[j], x[j]);
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] *= inv;
+      const int t = rho / p.group;
+      const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+      store_lane(p, out * D + lane * (D / 32), x);
+      if (lane == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    ptx::fence_proxy_async_smem();  // the next block's copies write where the partials were
+    __syncthreads();
+    if (++c.block == c.blocks || *abort_flag) break;
+    f.block = c.block;
+    f.g = c.g = g_first;
+    left = to_issue = solo_left;
+  }
+  if (!ok) {
+    // copies in flight must not outlive the block: those of this granule and, where there was more to
+    // copy, of the next
+    for (int i = 0; i < in_flight; ++i) {
+      sync::wait_drain(bars + st * 8, parity, p.timeout_ns);
+      if (++st == kSt) {
+        st = 0;
+        parity ^= 1u;
+      }
+    }
+  }
+}
+
+// Sums the partials of the items that several workers shared, and answers the rows that see nothing.
+// WPR warps per (row, query head), each going over every WPR-th partial.  What depends on the shapes
+// alone is worked out before the wait for the first kernel, while its last blocks still run.
+constexpr int kSumThreads = 256;
+template <int D, int RT, int WPR>
+__global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
+  constexpr int kN = D / 32, kPer = kSumThreads / 32 / WPR;  // rows of a block at a time
+  extern __shared__ int64_t plan[];
+  __shared__ int64_t scratch[kSumThreads / 32];
+  __shared__ float sh_o[WPR > 1 ? WPR : 1][D];
+  __shared__ float2 sh_ml[WPR];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % WPR;
+  const int64_t outs = p.rows.n_rows * p.hq;
+  make_plan<D, RT, kSumThreads>(p, plan, scratch);
+  const int64_t W = plan[p.rows.n_seqs], n = workers(W, most);
+  bool waited = false;
+  for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kPer; id0 < outs; id0 += static_cast<int64_t>(gridDim.x) * kPer) {
+    const int64_t id = id0 + warp / WPR;
+    const int64_t row = id / p.hq;
+    const int h = static_cast<int>(id - row * p.hq);
+    int local = 0, parts = -1;  // -1: nothing to write here
+    int64_t w0 = 0;
+    int slot0 = 0;
+    if (id < outs) {
+      const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+      const Seq seq = seq_of<D, RT>(p, b);
+      if (row >= seq.r0 && row < seq.r0 + seq.rows) {
+        parts = 0;
+        if (seq.blocks > 0) {
+          const int head = h / p.group;
+          const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
+          const int block = rho / RT;
+          local = rho - block * RT;
+          const int64_t from =
+              plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
+          w0 = worker_of(W, n, from);
+          const int64_t w1 = worker_of(W, n, from + seq.gpi - 1);
+          slot0 = share(W, n, w0) < from ? 1 : 0;  // the later ones begin inside of the item
+          parts = w0 == w1 ? -1 : static_cast<int>(w1 - w0) + 1;  // one: finished by its worker
+        }
+      }
+    }
+    if (!waited) ptx::wait_dependencies();
+    waited = true;
+    auto place = [&](int i) { return ((w0 + i) * 2 + (i == 0 ? slot0 : 0)) * RT + local; };
+    float top = -INFINITY, sum = 0.0f;
+    float acc[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+    for (int base = sub; base < parts; base += 32 * WPR) {
+      const int mine = base + lane * WPR;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (mine < parts) ml = p.part_ml[place(mine)];
+      float t = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+      const float now = fmaxf(top, t);
+      const float ref = now == -INFINITY ? 0.0f : now;
+      const float old = ex2(top - ref);
+      const float wt = ex2(ml.x - ref);
+      float z = ml.y * wt;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+      sum = sum * old + z;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) acc[j] *= old;
+      top = now;
+      const int many = (parts - 1 - base) / WPR + 1;
+      const int count = many < 32 ? many : 32;
+      for (int i0 = 0; i0 < count; i0 += 4) {
+        float v[4][kN];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i0 + u < count) {
+            const float* src = p.part_o + place(base + (i0 + u) * WPR) * D + lane * kN;
+            if constexpr (kN == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][kN - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[u][0] = x.x, v[u][1] = x.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float wi = __shfl_sync(kFull, wt, (i0 + u) & 31);
+          if (i0 + u < count) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) acc[j] = fmaf(wi, v[u][j], acc[j]);
+          }
+        }
+      }
+    }
+    if constexpr (WPR > 1) {
+      __syncthreads();  // the row before has been read
+#pragma unroll
+      for (int j = 0; j < kN; ++j) sh_o[warp][lane * kN + j] = acc[j];
+      if (lane == 0) sh_ml[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (warp == 0) {
+        float all = -INFINITY;
+        for (int w = 0; w < WPR; ++w) all = fmaxf(all, sh_ml[w].x);
+        const float ref = all == -INFINITY ? 0.0f : all;
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+        for (int w = 0; w < WPR; ++w) {
+          const float wt = ex2(sh_ml[w].x - ref);
+          sum = fmaf(wt, sh_ml[w].y, sum);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) acc[j] = fmaf(wt, sh_o[w][lane * kN + j], acc[j]);
+        }
+        top = all;
+      }
+    }
+    if (parts >= 0 && sub == 0) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) acc[j] *= inv;
+      store_lane(p, id * D + lane * kN, acc);
+      if (lane == 0) p.lse[id] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+  }
+  // A block without rows waits too: the kernel behind this one may begin once this grid is through,
+  // and must not meet the blocks of the one before.
+  if (!waited) ptx::wait_dependencies();
+}
+
+// The variant for a call: by the query rows that a sequence has on average.
+struct Plan {
+  int nt, qp, pp;
+  int rows;      // RT
+  int warps;     // of a block
+  bool solo;     // one block per (sequence, KV head), no workspace
+  double most;
+  int64_t grid;
+  int64_t ml_off, o_off, aside_off, bytes;
+};
+template <int D, int NT, int QP, int PP>
+cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
+              int num_sms, cudaStream_t s) {
+  using S = Shape<D, NT, QP, PP>;
+  static_assert(1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8 <= 232448, "shared memory of a block");
+  const int smem = 1024 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
+  const auto kernel = pl.solo ? kv_attn_kernel<D, NT, QP, PP, true> : kv_attn_kernel<D, NT, QP, PP, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel attribute");
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid));
+  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p, mk, mv)) != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
+  if (pl.solo) return CP_OK;
+  // Eight warps an output row while there are few rows, or many partials to a row; else one.
+  const int64_t workers = pl.grid * S::kWarps, parts = workers / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
+  const bool wide = parts > 16 || outs <= 1024;
+  const int64_t blocks = wide ? outs : (outs + 7) / 8, resident = 4 * static_cast<int64_t>(num_sms);
+  cfg.dynamicSmemBytes = (p.rows.n_seqs + 1) * 8;
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < resident ? blocks : resident));
+  e = wide ? cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 8>, p, workers)
+           : cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 1>, p, workers);
+  return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv_attn_combine_kernel launch");
+}
+
+template <int D>
+cp_status run_d(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
+                int num_sms, cudaStream_t s) {
+  if (pl.pp == 1)
+    return pl.nt == 1 ? run<D, 1, 1, 1>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 1>(p, pl, mk, mv, items, num_sms, s);
+  if (pl.qp == 1)
+    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 2>(p, pl, mk, mv, items, num_sms, s);
+  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 2, 2>(p, pl, mk, mv, items, num_sms, s);
+}
+
+}  // namespace kvattn
+}  // namespace cpattn

@@ -194,13 +194,14 @@ def test_bad_pages_and_rows_are_skipped_and_reported():
 
 
 # ------------------------------------------------------------------ attention
-def _check_attn(pool, cache, q, rows, held, q_first, kv_pos, o_dtype, scale=0.0, poison=True):
+def _check_attn(pool, cache, q, rows, held, q_first, kv_pos, o_dtype, scale=0.0, wide=0):
     start = _starts(rows)
     n, hq, d = q.shape
     o = torch.full((n, hq, d), float("nan"), dtype=o_dtype, device=DEV)
     lse = torch.full((n, hq), float("nan"), device=DEV)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    cpa.kv_cache_attn(q.to(DEV), cache, _i32(start), _i32(held), _i32(pool.table),
+    table = pool.table if wide == 0 else np.concatenate([pool.table, np.full((len(rows), wide), -1)], 1)
+    cpa.kv_cache_attn(q.to(DEV), cache, _i32(start), _i32(held), _i32(table),
                       q_first=None if q_first is None else _i32(q_first), kv_pos=kv_pos, scale=scale, o=o, lse=lse,
                       status=status)
     torch.cuda.synchronize()
@@ -266,8 +267,11 @@ ATTN = [  # rows, held, page, hq, hkv, d, in, out, stride of the shard or None (
 ]
 
 
+# a table as wide as the longest sequence needs, and a much wider one: short rows take one block a sequence and
+# head by the first, and are split by the second
+@pytest.mark.parametrize("wide", [0, 600])
 @pytest.mark.parametrize("rows,held,page,hq,hkv,d,din,dout,stride", ATTN)
-def test_attention(rows, held, page, hq, hkv, d, din, dout, stride):
+def test_attention(rows, held, page, hq, hkv, d, din, dout, stride, wide):
     pool = Pool(len(rows), held, page, hkv, d, 11)
     pool.fill(held, 12)
     q = (torch.randn((sum(rows) + 2, hq, d), generator=torch.Generator().manual_seed(13)) *
@@ -276,18 +280,19 @@ def test_attention(rows, held, page, hq, hkv, d, din, dout, stride):
     first = None
     if stride is not None:  # the last row sees everything
         first = [base + stride * (m - 1) - (n - 1) for n, m in zip(rows, held)]
-    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(base, stride or 1), dout)
+    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(base, stride or 1), dout, wide=wide)
 
 
+@pytest.mark.parametrize("wide", [0, 600])
 @pytest.mark.parametrize("dout", [BF16, F32])
-def test_attention_rows_that_see_little_or_nothing(dout):
+def test_attention_rows_that_see_little_or_nothing(dout, wide):
     rows, held = [6, 3, 2, 4], [50, 200, 0, 31]
     pool = Pool(4, held, 16, 2, 64, 21)
     pool.fill(held, 22)
     q = torch.randn((15, 8, 64), generator=torch.Generator().manual_seed(23)).to(BF16)
     # a shard at positions 5, 9, 13, ...: the first rows stand before it, a later one in its middle
-    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(5, 4), dout)
-    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(0, 1), dout, scale=0.7)
+    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(5, 4), dout, wide=wide)
+    _check_attn(pool, pool.device(), q, rows, held, [2, 300, 7, -100], PosMap(0, 1), dout, scale=0.7, wide=wide)
 
 
 @pytest.mark.parametrize("g,d,page", [(1, 64, 32), (8, 64, 16), (16, 64, 128), (3, 128, 32), (16, 128, 16)])
@@ -542,8 +547,10 @@ def test_a_decoding_step_in_a_graph():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
-def test_attention_wait_runs_out():
+@pytest.mark.parametrize("width", [13, 400])  # a table of few pages: one block a sequence and head; of many: split
+def test_attention_wait_runs_out(width):
     pool, cache, q, s, h, t = _serving_case(95, [1, 1], [400, 300])
+    t = torch.cat([t, t.new_full((2, width - t.shape[1]), -1)], 1)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     cpa.kv_cache_attn(q, cache, s, h, t, status=status, flags=api.CP_FLAG_TEST_STALL, wait_timeout_ms=20)
     torch.cuda.synchronize()
@@ -554,7 +561,9 @@ def test_attention_wait_runs_out():
 
 def test_workspace_is_checked():
     pool, cache, q, s, h, t = _serving_case(97, [1, 1], [4000, 300])
+    t = torch.cat([t, t.new_full((2, 400), -1)], 1)
     need = cpa.kv_cache_attn_workspace(cache, 2, 8, 2, t.shape[1])
+    assert need > 0
     with pytest.raises(cpa.CpError):
         cpa.kv_cache_attn(q, cache, s, h, t, workspace=torch.empty(need - 16, dtype=torch.uint8, device=DEV))
     with pytest.raises(cpa.CpError):
