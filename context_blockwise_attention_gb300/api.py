@@ -662,28 +662,45 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
 def _cache_fields(cache, index):
-    k, v, k_scale, v_scale = cache
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    ptrs = (_ptr(k, "cache.k", f8, index), _ptr(v, "cache.v", f8, index),
-            _ptr(k_scale, "cache.k_scale", f32, index), _ptr(v_scale, "cache.v_scale", f32, index))
+    """The fields of cp_kv_cache."""
+    k, v, ks, vs = cache
+    try:
+        fine = (k.dtype is _F8 and v.dtype is _F8 and ks.dtype is _F32 and vs.dtype is _F32
+                and k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == index
+                and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, name, dtype in ((k, "k", _F8), (v, "v", _F8), (ks, "k_scale", _F32), (vs, "v_scale", _F32)):
+            _ptr(t, "cache." + name, dtype, index)
     shape = k.shape
     if len(shape) != 4 or v.shape != shape:
         _invalid("cache.k and cache.v must be [pages, Hkv, page_size, D]")
     n_pages, hkv, page_size, d = shape
-    if k_scale.shape != (n_pages, hkv) or v_scale.shape != (n_pages, hkv):
+    if ks.shape != (n_pages, hkv) or vs.shape != (n_pages, hkv):
         _invalid("cache.k_scale and cache.v_scale must be [pages, Hkv]")
-    return (*ptrs, n_pages, page_size, hkv, d, 0)
+    return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page_size, hkv, d, 0
 
 
 def _rows_fields(row_start, tokens, name, page_table, n_rows, index):
-    i32 = torch.int32
-    ptrs = (_ptr(row_start, "row_start", i32, index), _ptr(tokens, name, i32, index),
-            _ptr(page_table, "page_table", i32, index))
+    """The fields of cp_kv_rows."""
+    try:
+        fine = (row_start.dtype is _I32 and tokens.dtype is _I32 and page_table.dtype is _I32
+                and row_start.get_device() == tokens.get_device() == page_table.get_device() == index
+                and row_start.is_contiguous() and tokens.is_contiguous() and page_table.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, label in ((row_start, "row_start"), (tokens, name), (page_table, "page_table")):
+            _ptr(t, label, _I32, index)
     table = page_table.shape
     if len(table) != 2 or row_start.shape != (table[0] + 1,) or tokens.shape != (table[0],):
         _invalid(f"row_start must be [seqs + 1], {name} [seqs], page_table [seqs, pages]")
-    return (*ptrs, table[0], table[1], n_rows)
+    return row_start.data_ptr(), tokens.data_ptr(), page_table.data_ptr(), table[0], table[1], n_rows
 
 
 def _status_ptr(status, index):

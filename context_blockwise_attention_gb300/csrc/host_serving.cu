@@ -86,10 +86,11 @@ cp_status validate_attn(const char* who, const cp_kv_attn_desc& d) {
 // would show in the result.
 uint64_t turn_of(double inv_freq) {
   const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
-  const double f = fabs(inv_freq), w = f * hi;
+  const double f = fabs(inv_freq), w = f * hi;  // below 2^8
   const double rest = fma(f, hi, -w) + f * lo;
-  uint64_t u = static_cast<uint64_t>(ldexp(w - floor(w), 64));  // exact: below 2^64
-  u += static_cast<uint64_t>(static_cast<int64_t>(llrint(ldexp(rest, 64))));
+  const double part = w - static_cast<double>(static_cast<int64_t>(w));
+  uint64_t u = static_cast<uint64_t>(part * 0x1p64);  // exact: part is below 1
+  u += static_cast<uint64_t>(static_cast<int64_t>(rest * 0x1p64));
   return inv_freq < 0.0 ? uint64_t(0) - u : u;
 }
 
