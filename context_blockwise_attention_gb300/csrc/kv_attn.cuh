@@ -315,11 +315,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     seq = seq_of<D, RT>(p, c.b);
     if (seq.over && seq.rows > 0 && tid == 0) kv::report(p.status, kv::kSiteTokens);
     if (seq.blocks == 0) {  // nothing to see
-      for (int i = tid; i < seq.rows * p.group * (D / 4); i += S::kWarps * 32) {
-        const int rho = i / (D / 4), t = rho / p.group;
+      for (int rho = warp; rho < seq.rows * p.group; rho += S::kWarps) {
+        const int t = rho / p.group;
         const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
-        store_row4(p, out * D + (i & (D / 4 - 1)) * 4, 0.0f, 0.0f, 0.0f, 0.0f);
-        if ((i & (D / 4 - 1)) == 0) p.lse[out] = -INFINITY;
+        const float zero[D / 32] = {};
+        store_lane(p, out * D + lane * (D / 32), zero);
+        if (lane == 0) p.lse[out] = -INFINITY;
       }
       return;
     }

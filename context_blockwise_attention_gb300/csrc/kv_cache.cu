@@ -197,9 +197,10 @@ __device__ __forceinline__ float top_of(const uint4& v, const float*) {
 // largest magnitude and the conversion, so that they are read once.  A block takes as many heads of
 // one page at once as fit, and goes over p.heads of them, so that where the page lies is looked up
 // once.  Bound by memory: 2 or 4 bytes in and 1 out per number; 16-byte loads, all of a thread's in
-// flight at once.  29 k tokens of 8 x 128 bf16 (178 MB): 30.8 us, 5.8 TB/s.
+// flight at once: 64 numbers a thread, 32 in small pages (29 k tokens of 8 x 128 bf16, pages of 64, 178 MB:
+// 28.7 us, 6.2 TB/s, with 32 a thread 30.8; 32 k tokens, pages of 16: 34 us with 32, 36 with 64, 40 with 16).
 template <int D, int P>
-constexpr int kTileThreads = P * D / 16 < kThreads ? P * D / 16 : kThreads;
+constexpr int kTileThreads = P >= 64 ? P * D / 64 : P * D / 32;
 template <int D, int P, class T>
 __global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kV = kVec<T>, kTT = kTileThreads<D, P>, kTiles = kThreads / kTT;
@@ -403,8 +404,8 @@ cp_status write_tiles(WriteParams& p, int num_sms, cudaStream_t s) {
 }
 template <int D, class T>
 cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
-  // A block a tile pays where its threads have rows to hold: 64 sequences of 512 rows 35 against 60 us (pages of
-  // 64; of 16 40 each), of 128 rows 12 against 18 (pages of 16: 14 against 11), 512 sequences of 8 rows 23 to 32
+  // A block a tile pays where its threads have rows to hold: 64 sequences of 512 rows 34 against 60 us (pages of
+  // 64; of 16 34 against 41), of 128 rows 12 against 18 (pages of 16: 14 against 11), 512 sequences of 8 rows 23 to 32
   // against 10; and where the tiles are few and a warp would take their rows one after the other: one sequence
   // of 512 rows 2.3 against 8.5.
   const int64_t tiles = static_cast<int64_t>(p.units) * p.c.hkv * 2, seqs = p.rows.n_seqs;

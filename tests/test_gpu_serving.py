@@ -503,6 +503,36 @@ def test_attention_same_bits_on_streams_at_once_and_in_graphs():
     s.copy_(s0)
 
 
+@pytest.mark.parametrize("wide", [0, 500])
+def test_rows_before_the_first_and_behind_the_last_sequence(wide):
+    """row_start may begin behind row 0: the rows before it belong to nobody, in all three calls."""
+    rows, held, total = [2, 0, 1], [40, 9, 100], [42, 9, 101]
+    pool = Pool(3, total, 16, 2, 64, 105)
+    pool.fill(total, 106)
+    cache = pool.device()
+    table = torch.cat([_i32(pool.table), torch.full((3, wide), -1, dtype=torch.int32, device=DEV)], 1)
+    start = _i32([3, 5, 5, 6])
+    q = torch.randn((8, 8, 64), generator=torch.Generator().manual_seed(107)).to(BF16).to(DEV)
+    o = torch.full((8, 8, 64), 12345.0, device=DEV)
+    lse = torch.full((8, 8), 12345.0, device=DEV)
+    cpa.kv_cache_attn(q, cache, start, _i32(total), table, q_first=_i32(held), o=o, lse=lse)
+    want = cpa.kv_cache_attn(q[3:6].contiguous(), cache, start - 3, _i32(total), table, q_first=_i32(held))
+    assert torch.equal(o[3:6], want[0]) and torch.equal(lse[3:6], want[1])
+    for x in (o, lse):
+        assert bool((x[:3] == 12345.0).all()) and bool((x[6:] == 12345.0).all())
+    k = torch.full((8, 2, 64), 12345.0, device=DEV)
+    v = torch.full_like(k, 12345.0)
+    cpa.kv_cache_read(cache, start, _i32(held), table, 8, k=k, v=v)
+    for x in (k, v):
+        assert bool((x[:3] == 12345.0).all()) and bool((x[6:] == 12345.0).all())
+    cpa.kv_cache_write(cache, k, v, start, _i32(held), table)  # what was read goes back to its place
+    for got, was in ((cache.k, pool.bytes[0]), (cache.v, pool.bytes[1])):
+        now = oc.e4m3_decode(got.view(torch.uint8).cpu().numpy())
+        assert np.array_equal(np.isnan(now), np.isnan(oc.e4m3_decode(was)))
+    k2, v2 = cpa.kv_cache_read(cache, start - 3, _i32(held), table, 3, dtype=F32)
+    assert torch.equal(k2, k[3:6]) and torch.equal(v2, v[3:6])
+
+
 def test_a_decoding_step_in_a_graph():
     """Rotation, write and attention captured as one step and replayed for the next tokens."""
     seqs, hq, hkv, d, page = 3, 4, 2, 64, 16

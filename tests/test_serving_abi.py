@@ -81,6 +81,7 @@ def test_write_and_read_refuse(name):
     # nothing to do: no launch, no error
     assert call(_cache(), _rows(n_rows=0), k=None, v=None) == api.CP_OK
     assert call(_cache(n_pages=0, k=0, v=0, k_scale=0, v_scale=0), _rows(n_rows=0)) == api.CP_OK
+    assert call(_cache(), _rows(n_seqs=0, max_pages=0, row_start=0, tokens=0, page_table=0)) == api.CP_OK
 
 
 def test_attention_refuses():
@@ -106,6 +107,7 @@ def test_attention_refuses():
     assert call(rows=_rows(max_pages=1 << 26)) == BAD       # 2^32 tokens a sequence
     assert call(rows=_rows(n_rows=1 << 27)) == BAD          # 2^32 query rows
     assert call(rows=_rows(n_rows=0), q=0) == api.CP_OK
+    assert call(rows=_rows(n_seqs=0, max_pages=0, row_start=0, tokens=0, page_table=0)) == api.CP_OK
     need = ctypes.c_int64()
     assert lib.cp_kv_cache_attn_workspace(None, ctypes.byref(need)) == BAD
     assert lib.cp_kv_cache_attn_workspace(ctypes.byref(_attn()), None) == BAD
