@@ -56,11 +56,6 @@ constexpr float kPScale = 32768.0f;  // largest P operand
 constexpr int kSetup = 1;            // what an item costs besides its granules
 constexpr unsigned kFull = 0xffffffffu;
 
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-
 template <int D>
 constexpr int kKeysOf = 4096 / D;  // keys of a granule
 
@@ -583,12 +578,73 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
   };
 
-  // One granule for the first kLive tiles of query rows; kMask: some of its keys are not seen by some row.
-  auto granule = [&](int st, auto live_tag, auto mask_tag) {
-    constexpr int kLive = decltype(live_tag)::value;
-    constexpr bool kMask = decltype(mask_tag)::value != 0;
+  // Where some row of the block does not see all keys of the granule: values that no row sees count as zero,
+  // since 0 * NaN would not vanish, and NaN among values that only some of the rows see go to those rows'
+  // accumulators and are taken out.  Rolled up, as a granule's other code has to stay in the instruction cache.
+  auto mask_values = [&](uint32_t tile) {
+    constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;  // 16-byte chunks of a key, keys of a pass
+    const int key0 = c.g * kKeys;
+    auto value_at = [&](int k, int chunk) {  // address of a chunk of key key0 + k
+      const int line = D == 128 ? k : k >> 1;
+      return tile + S::kHalf + line * 128 + ((((D == 128 ? 0 : (k & 1) * 4) + chunk) ^ (line & 7)) << 4);
+    };
+    const int first = max(lim_min - key0, 0);  // below kKeys
+    bool odd = false;
+#pragma unroll 1
+    for (int k0 = first & ~(kAtOnce - 1); k0 < kKeys; k0 += kAtOnce) {
+      const int k = k0 + lane / kChunks;
+      const uint32_t at = value_at(k, lane % kChunks);
+      if (key0 + k >= lim_max) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+      } else if (k >= first) {
+        const uint4 v = ptx::lds128u(at);
+        const uint32_t nan = __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                             __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        odd |= nan != 0u;
+      }
+    }
+    if (__any_sync(kFull, odd)) {
+#pragma unroll 1
+      for (int k = first; k < kKeys && key0 + k < lim_max; ++k) {
+        const uint32_t at = D == 128 ? value_at(k, gid) : value_at(k, gid >> 1) + (gid & 1) * 8;
+        uint32_t v[kCols / 4];
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          const uint2 x = ptx::lds64(at + 8 * i);
+          v[2 * i] = x.x, v[2 * i + 1] = x.y;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i) {
+          const uint32_t nan = __vcmpeq4(v[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(v[i] & ~nan) : "memory");
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if ((nan >> (8 * e) & 1u) && key0 + k < lim[n][r])
+                  acc[n][2 * i + (e >> 1)][2 * (e & 1) + r] = __int_as_float(0x7fffffff);
+        }
+      }
+    }
+    ptx::fence_proxy_async_smem();  // before the next copies into the stage
+    __syncwarp();
+  };
+
+  // One granule; masked: some of its keys are not seen by some row.  Masks and tiles without rows are uniform
+  // branches and predicates, not variants: with four variants a warp's items of a few granules ran at the
+  // speed of the instruction cache (62 x 16 items of some 3 granules, up to 60 rows, D = 64: 86 us, more than half
+  // of the stalls; now 55, and 16-row items of 8192 tokens 102 against 106).
+  auto granule = [&](int st, bool masked) {
     const uint32_t tile = ring + st * S::kStage;
     const int key0 = c.g * kKeys;
+    const bool both = NT == 1 || live > 1;
+    auto product = [&](int n, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+      if (n == 0) ptx::mma_f16(d, a, b0, b1);
+      else ptx::mma_f16_if(d, a, b0, b1, both);
+    };
     float ks[kSteps], vs[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; i += 2) {
@@ -596,8 +652,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       ks[i] = __uint_as_float(v.x), vs[i] = __uint_as_float(v.y);
       ks[i + 1] = __uint_as_float(v.z), vs[i + 1] = __uint_as_float(v.w);
     }
+    if (masked) {
+      mask_values(tile);
+      // a value scale that is not finite comes in by the scores, which rows that do not see it leave out
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (!(vs[i] < INFINITY)) ks[i] = __int_as_float(0x7fffffff), vs[i] = 1e-37f;
+    }
     // S^T: s[n][i][2 u + r] is key key_at(u, gid) of step i for query row 2 tig + r of tile n
-    float s[kLive][kSteps][4];
+    float s[NT][kSteps][4];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint32_t kw[2][kMt];  // word j of the lane's part of a key: dimensions of step j
@@ -615,44 +678,54 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         }
       }
 #pragma unroll
-      for (int n = 0; n < kLive; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
+      for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
 #pragma unroll
       for (int j = 0; j < kMt; ++j) {
         const uint32_t a[4] = {kv::e4m3x2_to_f16x2(kw[0][j]), kv::e4m3x2_to_f16x2(kw[1][j]),
                                kv::e4m3x2_to_f16x2(kw[0][j] >> 16), kv::e4m3x2_to_f16x2(kw[1][j] >> 16)};
 #pragma unroll
-        for (int n = 0; n < kLive * QP; ++n) {
+        for (int n = 0; n < NT * QP; ++n) {
           if constexpr (S::kQSmem) {
             const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
-            ptx::mma_f16(s[n / QP][i], a, b.x, b.y);
+            product(n / QP, s[n / QP][i], a, b.x, b.y);
           } else {
-            ptx::mma_f16(s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
+            product(n / QP, s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
           }
         }
       }
     }
     // Maxima.  s keeps the products; a score is s * f2 (f2 > 0), and only masked tiles, where an unseen
     // page's scale may be anything, hold scores themselves.
-    float corr[kLive][2], f2[kLive][2][kSteps];
+    float corr[NT][2], f2[NT][2][kSteps];
     bool grew = false;
 #pragma unroll
-    for (int n = 0; n < kLive; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float top = -INFINITY;
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          f2[n][r][i] = fac[n][r] * ks[i];
-          if (kMask) {
+        for (int i = 0; i < kSteps; ++i) f2[n][r][i] = fac[n][r] * ks[i];
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               float& z = s[n][i][2 * u + r];
               z = key0 + 16 * i + key_at(u, gid) >= lim[n][r] ? -INFINITY : z * f2[n][r][i];
             }
+            f2[n][r][i] = 1.0f;
           }
-          const float top2 = fmaxf(s[n][i][r], s[n][i][2 + r]);
-          top = fmaxf(top, kMask ? top2 : top2 * f2[n][r][i]);
-        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) top = fmaxf(top, fmaxf(s[n][i][r], s[n][i][2 + r]) * f2[n][r][i]);
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -670,7 +743,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       v_ref = v_top;
       inv_ref = kPScale / v_top;
 #pragma unroll
-      for (int n = 0; n < kLive; ++n) {
+      for (int n = 0; n < NT; ++n) {
         l[n][0] *= corr[n][0];
         l[n][1] *= corr[n][1];
         const float c0 = corr[n][0] * rr, c1 = corr[n][1] * rr;
@@ -690,12 +763,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       }
     }
     // Weights as operands: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid
-    uint32_t pb[kLive][PP][kSteps][2];
+    uint32_t pb[NT][PP][kSteps][2];
     float vf[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) vf[i] = vs[i] * inv_ref;
 #pragma unroll
-    for (int n = 0; n < kLive; ++n) {
+    for (int n = 0; n < NT; ++n) {
       const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
@@ -704,11 +777,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
           float pv[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float z = s[n][i][2 * u + r];
-            const float w = ex2(kMask ? z - ref[r] : fmaf(z, f2[n][r][i], -ref[r]));
+            const float w = ex2(fmaf(s[n][i][2 * u + r], f2[n][r][i], -ref[r]));
             l[n][r] += w;
             pv[r] = w * vf[i];
-            if (kMask && z == -INFINITY) pv[r] = 0.0f;  // an unseen page's scale may be NaN
           }
           const uint32_t h = to_f16x2(pv[0], pv[1]);
           pb[n][0][i][u] = ptx::transpose8x8(h);
@@ -722,7 +793,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint32_t vw[4][D / 32];
-      bool odd = false;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         if (D == 128) {
@@ -731,57 +801,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         } else {
           const uint2 v = ptx::lds64(tile + i * 1024 + v_off[x]);
           vw[x][0] = v.x, vw[x][1] = v.y;
-        }
-        if (kMask) {
-          // what no row sees counts as zero: 0 * NaN would not vanish
-          const int key = key0 + 16 * i + key_at(x >> 1, 2 * tig + (x & 1));
-          if (key >= lim_max) {
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) vw[x][w] = 0u;
-          } else if (key >= lim_min) {
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) odd |= __vcmpeq4(vw[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
-          }
-        }
-      }
-      if (kMask && __any_sync(kFull, odd)) {
-        // NaN among values that only some of the rows see: those rows get NaN by a product of the
-        // places of the NaN with the rows' visibility, and the NaN are taken out of V.
-        uint32_t vis[kLive][2];
-#pragma unroll
-        for (int n = 0; n < kLive; ++n) {
-          const int l0 = __shfl_sync(kFull, lim[n][0], gid >> 1), l1 = __shfl_sync(kFull, lim[n][1], gid >> 1);
-          const int lm = (gid & 1) ? l1 : l0;  // of query row gid
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int k = key0 + 16 * i + key_at(u, 2 * tig);
-            vis[n][u] = (k < lm ? 0x3c00u : 0u) | (k + 1 < lm ? 0x3c000000u : 0u);
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          uint32_t at[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t nan = __vcmpeq4(vw[x][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            at[x] = nan & 0x38383838u;  // e4m3 one
-            vw[x][w] &= ~nan;
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t a = __byte_perm(at[0], at[1], half ? 0x7362 : 0x5140);
-            const uint32_t b = __byte_perm(at[2], at[3], half ? 0x7362 : 0x5140);
-            const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
-                                    kv::e4m3x2_to_f16x2(b >> 16)};
-#pragma unroll
-            for (int n = 0; n < kLive; ++n) {
-              float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              ptx::mma_f16(hit, av, vis[n][0], vis[n][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (hit[k] > 0.0f) acc[n][2 * w + half][k] = __int_as_float(0x7fffffff);
-            }
-          }
         }
       }
 #pragma unroll
@@ -793,21 +812,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
           const uint32_t av[4] = {kv::e4m3x2_to_f16x2(a), kv::e4m3x2_to_f16x2(a >> 16), kv::e4m3x2_to_f16x2(b),
                                   kv::e4m3x2_to_f16x2(b >> 16)};
 #pragma unroll
-          for (int n = 0; n < kLive; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int part = 0; part < PP; ++part)
-              ptx::mma_f16(acc[n][2 * w + half], av, pb[n][part][i][0], pb[n][part][i][1]);
+              product(n, acc[n][2 * w + half], av, pb[n][part][i][0], pb[n][part][i][1]);
         }
-    }
-  };
-
-  // The same for the tiles that the block has: sequences differ in their rows.
-  auto granule_live = [&](int st, auto mask_tag) {
-    if constexpr (NT == 1) {
-      granule(st, Int<1>{}, mask_tag);
-    } else {
-      if (live == 1) granule(st, Int<1>{}, mask_tag);
-      else granule(st, Int<NT>{}, mask_tag);
     }
   };
 
@@ -918,8 +927,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         break;
       }
       const int key0 = c.g * kKeys;
-      if (key0 + kKeys <= lim_min) granule_live(st, Int<0>{});
-      else if (key0 < lim_max) granule_live(st, Int<1>{});
+      if (key0 < lim_max) granule(st, key0 + kKeys > lim_min);
       __syncwarp();
       if (to_issue > 0) issue(st);
       else --in_flight;

@@ -154,6 +154,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same where `on`, which is uniform over the warp.
+__device__ __forceinline__ void mma_f16_if(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %10, 0;\n\t"
+      "@p mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n\t}"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(static_cast<int>(on)));
+}
 // Transposes an 8x8 matrix of 16-bit values whose row g is held by the lanes 4 g .. 4 g + 3, two each.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
