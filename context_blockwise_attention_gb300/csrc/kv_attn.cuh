@@ -1008,10 +1008,41 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   }
 }
 
-// Sums the partials of the items that several workers shared, and answers the rows that see nothing.
-// WPR warps per (row, query head), each going over every WPR-th partial.  What depends on the shapes
-// alone is worked out before the wait for the first kernel, while its last blocks still run.
+// Sum the partials of the items that several workers shared, and answer the rows that see nothing.  What
+// depends on the shapes alone is worked out before the wait for the first kernel, while its last blocks
+// still run.
 constexpr int kSumThreads = 256;
+
+// The partials of an output row: one of each worker from w0 on, the first in slot slot0.
+struct Parts {
+  int64_t w0;
+  int slot0, local;  // local: row of the item
+  int n;             // 0: the row sees nothing; -1: nothing to write here
+};
+template <int D, int RT>
+__device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, int64_t n_workers, int64_t id, int lane) {
+  Parts r{0, 0, 0, -1};
+  const int64_t W = plan[p.rows.n_seqs];
+  const int64_t row = id / p.hq;
+  const int h = static_cast<int>(id - row * p.hq);
+  const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+  const Seq seq = seq_of<D, RT>(p, b);
+  if (row < seq.r0 || row >= seq.r0 + seq.rows) return r;
+  r.n = 0;
+  if (seq.blocks == 0) return r;
+  const int head = h / p.group;
+  const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
+  const int block = rho / RT;
+  r.local = rho - block * RT;
+  const int64_t from = plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
+  r.w0 = worker_of(W, n_workers, from);
+  const int64_t w1 = worker_of(W, n_workers, from + seq.gpi - 1);
+  r.slot0 = share(W, n_workers, r.w0) < from ? 1 : 0;       // the later ones begin inside of the item
+  r.n = r.w0 == w1 ? -1 : static_cast<int>(w1 - r.w0) + 1;  // one: finished by its worker
+  return r;
+}
+
+// WPR warps for each (row, query head), each going over every WPR-th partial.
 template <int D, int RT, int WPR>
 __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
   constexpr int kN = D / 32, kPer = kSumThreads / 32 / WPR;  // rows of a block at a time
@@ -1023,37 +1054,16 @@ __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const _
   const int sub = warp % WPR;
   const int64_t outs = p.rows.n_rows * p.hq;
   make_plan<D, RT, kSumThreads>(p, plan, scratch);
-  const int64_t W = plan[p.rows.n_seqs], n = workers(W, most);
+  const int64_t n = workers(plan[p.rows.n_seqs], most);
   bool waited = false;
   for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kPer; id0 < outs; id0 += static_cast<int64_t>(gridDim.x) * kPer) {
     const int64_t id = id0 + warp / WPR;
-    const int64_t row = id / p.hq;
-    const int h = static_cast<int>(id - row * p.hq);
-    int local = 0, parts = -1;  // -1: nothing to write here
-    int64_t w0 = 0;
-    int slot0 = 0;
-    if (id < outs) {
-      const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
-      const Seq seq = seq_of<D, RT>(p, b);
-      if (row >= seq.r0 && row < seq.r0 + seq.rows) {
-        parts = 0;
-        if (seq.blocks > 0) {
-          const int head = h / p.group;
-          const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
-          const int block = rho / RT;
-          local = rho - block * RT;
-          const int64_t from =
-              plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
-          w0 = worker_of(W, n, from);
-          const int64_t w1 = worker_of(W, n, from + seq.gpi - 1);
-          slot0 = share(W, n, w0) < from ? 1 : 0;  // the later ones begin inside of the item
-          parts = w0 == w1 ? -1 : static_cast<int>(w1 - w0) + 1;  // one: finished by its worker
-        }
-      }
-    }
+    Parts r{0, 0, 0, -1};
+    if (id < outs) r = parts_of<D, RT>(p, plan, n, id, lane);
+    const int parts = r.n;
     if (!waited) ptx::wait_dependencies();
     waited = true;
-    auto place = [&](int i) { return ((w0 + i) * 2 + (i == 0 ? slot0 : 0)) * RT + local; };
+    auto place = [&](int i) { return ((r.w0 + i) * 2 + (i == 0 ? r.slot0 : 0)) * RT + r.local; };
     float top = -INFINITY, sum = 0.0f;
     float acc[kN];
 #pragma unroll
@@ -1137,6 +1147,94 @@ __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const _
   if (!waited) ptx::wait_dependencies();
 }
 
+// A block for each 32 columns of a (row, query head): eight lanes, four columns each, to a partial, so that 32
+// partials are summed side by side and 256 reads are on their way.  For one row of 1800 partials, as one long
+// sequence leaves them, a block of eight warps for a row's whole length took 27 us.
+template <int D, int RT>
+__global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_columns_kernel(const __grid_constant__ Params p, int64_t most) {
+  constexpr int kWarps = kSumThreads / 32, kSide = kSumThreads / 8, kSlices = D / 32;
+  extern __shared__ int64_t plan[];
+  __shared__ int64_t scratch[kWarps];
+  __shared__ float sh_m[kWarps], sh_l[kWarps];
+  __shared__ float4 sh_o[kWarps][8];
+  float* const weight = reinterpret_cast<float*>(plan + p.rows.n_seqs + 1);  // [most]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t ids = p.rows.n_rows * p.hq * kSlices;
+  make_plan<D, RT, kSumThreads>(p, plan, scratch);
+  const int64_t n = workers(plan[p.rows.n_seqs], most);
+  bool waited = false;
+  for (int64_t id = blockIdx.x; id < ids; id += gridDim.x) {
+    const int64_t out = id / kSlices;
+    const int col = static_cast<int>(id % kSlices) * 32;
+    const Parts r = parts_of<D, RT>(p, plan, n, out, lane);
+    if (!waited) ptx::wait_dependencies();
+    waited = true;
+    if (r.n < 0) continue;  // the same for the whole block
+    auto place = [&](int i) { return ((r.w0 + i) * 2 + (i == 0 ? r.slot0 : 0)) * RT + r.local; };
+    float top = -INFINITY;
+    for (int i = tid; i < r.n; i += kSumThreads) {
+      const float m = p.part_ml[place(i)].x;
+      weight[i] = m;
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (lane == 0) sh_m[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int i = tid; i < r.n; i += kSumThreads) {
+      const float wt = ex2(weight[i] - ref);
+      weight[i] = wt;
+      sum = fmaf(wt, p.part_ml[place(i)].y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) sh_l[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sh_l[w];
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float* const from = p.part_o + col + (tid & 7) * 4;
+    constexpr int kAhead = 8;
+    for (int i0 = tid >> 3; i0 < r.n; i0 += kSide * kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u * kSide < r.n) v[u] = *reinterpret_cast<const float4*>(from + place(i0 + u * kSide) * D);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u * kSide < r.n) {
+          const float wt = weight[i0 + u * kSide];
+          acc.x = fmaf(wt, v[u].x, acc.x), acc.y = fmaf(wt, v[u].y, acc.y);
+          acc.z = fmaf(wt, v[u].z, acc.z), acc.w = fmaf(wt, v[u].w, acc.w);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 8; o >>= 1) {
+      acc.x += __shfl_xor_sync(kFull, acc.x, o), acc.y += __shfl_xor_sync(kFull, acc.y, o);
+      acc.z += __shfl_xor_sync(kFull, acc.z, o), acc.w += __shfl_xor_sync(kFull, acc.w, o);
+    }
+    if (lane < 8) sh_o[warp][lane] = acc;
+    __syncthreads();
+    if (tid < 8) {
+      acc = sh_o[0][tid];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 x = sh_o[w][tid];
+        acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      store_row4(p, out * D + col + tid * 4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (col == 0 && tid == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+  }
+  if (!waited) ptx::wait_dependencies();  // as above
+}
+
 // The variant for a call: by the query rows that a sequence has on average.
 struct Plan {
   int nt, qp, pp;
@@ -1172,12 +1270,19 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
   // partials to a row; else one (2176 rows of 5 partials: 104 us the whole call, against 116 with eight).
   const int64_t workers = pl.grid * S::kWarps, parts = workers / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
   const bool wide = parts > 16 || outs <= 1024;
-  const int64_t blocks = wide ? outs : (outs + 7) / 8, resident = 4 * static_cast<int64_t>(num_sms);
-  cfg.dynamicSmemBytes = (p.rows.n_seqs + 1) * 8;
+  const int64_t resident = 4 * static_cast<int64_t>(num_sms);
+  // A block for 32 columns of a row where these are one wave and have many partials to read (1 x 120000 tokens,
+  // 5/1 heads: 28 us against 45; 1 x 8000, 32/8: 13.8 against 16.1; 4 x 30000: the same).  Two waves of them are
+  // slower (1 x 30000 with 32 rows, 32/8: 40 against 36).
+  const bool columns = outs * (D / 32) <= resident && parts > 32;
+  const int64_t blocks = columns ? outs * (D / 32) : wide ? outs : (outs + 7) / 8;
+  cfg.dynamicSmemBytes = (p.rows.n_seqs + 1) * 8 + (columns ? workers * 4 : 0);
   cfg.blockDim = dim3(kSumThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < resident ? blocks : resident));
-  e = wide ? cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 8>, p, workers)
-           : cudaLaunchKernelEx(&cfg, kv_attn_combine_kernel<D, S::kRows, 1>, p, workers);
+  const auto sum = columns ? kv_attn_combine_columns_kernel<D, S::kRows>
+                   : wide  ? kv_attn_combine_kernel<D, S::kRows, 8>
+                           : kv_attn_combine_kernel<D, S::kRows, 1>;
+  e = cudaLaunchKernelEx(&cfg, sum, p, workers);
   return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv_attn_combine_kernel launch");
 }
 
