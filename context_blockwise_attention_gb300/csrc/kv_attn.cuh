@@ -1020,12 +1020,10 @@ struct Parts {
   int n;             // 0: the row sees nothing; -1: nothing to write here
 };
 template <int D, int RT>
-__device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, int64_t n_workers, int64_t id, int lane) {
+__device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, int64_t n_workers, int64_t row, int h,
+                                          int b) {
   Parts r{0, 0, 0, -1};
   const int64_t W = plan[p.rows.n_seqs];
-  const int64_t row = id / p.hq;
-  const int h = static_cast<int>(id - row * p.hq);
-  const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
   const Seq seq = seq_of<D, RT>(p, b);
   if (row < seq.r0 || row >= seq.r0 + seq.rows) return r;
   r.n = 0;
@@ -1042,7 +1040,9 @@ __device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, 
   return r;
 }
 
-// WPR warps for each (row, query head), each going over every WPR-th partial.
+// WPR warps for each (row, query head), each going over every WPR-th partial.  Most rows of short items were
+// finished by their worker: a warp of its own looks 32 of its rows up side by side (58 x 32 items of up to 52
+// rows and one granule: 37 us the whole call, against 56 one row after the other).
 template <int D, int RT, int WPR>
 __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
   constexpr int kN = D / 32, kPer = kSumThreads / 32 / WPR;  // rows of a block at a time
@@ -1056,90 +1056,122 @@ __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const _
   make_plan<D, RT, kSumThreads>(p, plan, scratch);
   const int64_t n = workers(plan[p.rows.n_seqs], most);
   bool waited = false;
-  for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kPer; id0 < outs; id0 += static_cast<int64_t>(gridDim.x) * kPer) {
-    const int64_t id = id0 + warp / WPR;
-    Parts r{0, 0, 0, -1};
-    if (id < outs) r = parts_of<D, RT>(p, plan, n, id, lane);
-    const int parts = r.n;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kPer;
+  constexpr int kScan = WPR == 1 ? 32 : 1;
+  for (int64_t id0 = static_cast<int64_t>(blockIdx.x) * kPer + warp / WPR; id0 < outs; id0 += kScan * stride) {
+    Parts mine{0, 0, 0, -1};
+    unsigned todo;
+    if constexpr (WPR == 1) {
+      const int64_t my_id = id0 + lane * stride;
+      if (my_id < outs) {
+        const int64_t row = my_id / p.hq;
+        int b = 0, z = p.rows.n_seqs - 1;  // the last sequence that begins at or before the row
+        while (b < z) {
+          const int mid = (b + z + 1) >> 1;
+          if (kv::row_at(p.rows, mid) <= row) b = mid;
+          else z = mid - 1;
+        }
+        mine = parts_of<D, RT>(p, plan, n, row, static_cast<int>(my_id - row * p.hq), b);
+      }
+      todo = __ballot_sync(kFull, mine.n >= 0);
+    } else {
+      const int64_t row = id0 / p.hq;
+      const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+      mine = parts_of<D, RT>(p, plan, n, row, static_cast<int>(id0 - row * p.hq), b);
+      todo = mine.n >= 0 ? 1u : 0u;  // the same for the whole block
+    }
     if (!waited) ptx::wait_dependencies();
     waited = true;
-    auto place = [&](int i) { return ((r.w0 + i) * 2 + (i == 0 ? r.slot0 : 0)) * RT + r.local; };
-    float top = -INFINITY, sum = 0.0f;
-    float acc[kN];
+    while (todo != 0u) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1u;
+      const int64_t id = id0 + src * stride;
+      Parts r = mine;
+      if constexpr (WPR == 1) {
+        r.w0 = __shfl_sync(kFull, mine.w0, src);
+        r.slot0 = __shfl_sync(kFull, mine.slot0, src);
+        r.local = __shfl_sync(kFull, mine.local, src);
+        r.n = __shfl_sync(kFull, mine.n, src);
+      }
+      const int parts = r.n;
+      auto place = [&](int i) { return ((r.w0 + i) * 2 + (i == 0 ? r.slot0 : 0)) * RT + r.local; };
+      float top = -INFINITY, sum = 0.0f;
+      float acc[kN];
 #pragma unroll
-    for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-    for (int base = sub; base < parts; base += 32 * WPR) {
-      const int mine = base + lane * WPR;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (mine < parts) ml = p.part_ml[place(mine)];
-      float t = ml.x;
+      for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+      for (int base = sub; base < parts; base += 32 * WPR) {
+        const int mine = base + lane * WPR;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (mine < parts) ml = p.part_ml[place(mine)];
+        float t = ml.x;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
-      const float now = fmaxf(top, t);
-      const float ref = now == -INFINITY ? 0.0f : now;
-      const float old = ex2(top - ref);
-      const float wt = ex2(ml.x - ref);
-      float z = ml.y * wt;
+        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, o));
+        const float now = fmaxf(top, t);
+        const float ref = now == -INFINITY ? 0.0f : now;
+        const float old = ex2(top - ref);
+        const float wt = ex2(ml.x - ref);
+        float z = ml.y * wt;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-      sum = sum * old + z;
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+        sum = sum * old + z;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) acc[j] *= old;
-      top = now;
-      const int many = (parts - 1 - base) / WPR + 1;
-      const int count = many < 32 ? many : 32;
-      for (int i0 = 0; i0 < count; i0 += 4) {
-        float v[4][kN];
+        for (int j = 0; j < kN; ++j) acc[j] *= old;
+        top = now;
+        const int many = (parts - 1 - base) / WPR + 1;
+        const int count = many < 32 ? many : 32;
+        for (int i0 = 0; i0 < count; i0 += 4) {
+          float v[4][kN];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (i0 + u < count) {
-            const float* src = p.part_o + place(base + (i0 + u) * WPR) * D + lane * kN;
-            if constexpr (kN == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src);
-              v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][kN - 1] = x.w;
-            } else {
-              const float2 x = *reinterpret_cast<const float2*>(src);
-              v[u][0] = x.x, v[u][1] = x.y;
+          for (int u = 0; u < 4; ++u)
+            if (i0 + u < count) {
+              const float* src = p.part_o + place(base + (i0 + u) * WPR) * D + lane * kN;
+              if constexpr (kN == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(src);
+                v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][kN - 1] = x.w;
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                v[u][0] = x.x, v[u][1] = x.y;
+              }
+            }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float wi = __shfl_sync(kFull, wt, (i0 + u) & 31);
+            if (i0 + u < count) {
+#pragma unroll
+              for (int j = 0; j < kN; ++j) acc[j] = fmaf(wi, v[u][j], acc[j]);
             }
           }
+        }
+      }
+      if constexpr (WPR > 1) {
+        __syncthreads();  // the row before has been read
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float wi = __shfl_sync(kFull, wt, (i0 + u) & 31);
-          if (i0 + u < count) {
+        for (int j = 0; j < kN; ++j) sh_o[warp][lane * kN + j] = acc[j];
+        if (lane == 0) sh_ml[warp] = make_float2(top, sum);
+        __syncthreads();
+        if (warp == 0) {
+          float all = -INFINITY;
+          for (int w = 0; w < WPR; ++w) all = fmaxf(all, sh_ml[w].x);
+          const float ref = all == -INFINITY ? 0.0f : all;
+          sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kN; ++j) acc[j] = fmaf(wi, v[u][j], acc[j]);
+          for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+          for (int w = 0; w < WPR; ++w) {
+            const float wt = ex2(sh_ml[w].x - ref);
+            sum = fmaf(wt, sh_ml[w].y, sum);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) acc[j] = fmaf(wt, sh_o[w][lane * kN + j], acc[j]);
           }
+          top = all;
         }
       }
-    }
-    if constexpr (WPR > 1) {
-      __syncthreads();  // the row before has been read
+      if (sub == 0) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) sh_o[warp][lane * kN + j] = acc[j];
-      if (lane == 0) sh_ml[warp] = make_float2(top, sum);
-      __syncthreads();
-      if (warp == 0) {
-        float all = -INFINITY;
-        for (int w = 0; w < WPR; ++w) all = fmaxf(all, sh_ml[w].x);
-        const float ref = all == -INFINITY ? 0.0f : all;
-        sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-        for (int w = 0; w < WPR; ++w) {
-          const float wt = ex2(sh_ml[w].x - ref);
-          sum = fmaf(wt, sh_ml[w].y, sum);
-#pragma unroll
-          for (int j = 0; j < kN; ++j) acc[j] = fmaf(wt, sh_o[w][lane * kN + j], acc[j]);
-        }
-        top = all;
+        for (int j = 0; j < kN; ++j) acc[j] *= inv;
+        store_lane(p, id * D + lane * kN, acc);
+        if (lane == 0) p.lse[id] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
-    }
-    if (parts >= 0 && sub == 0) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int j = 0; j < kN; ++j) acc[j] *= inv;
-      store_lane(p, id * D + lane * kN, acc);
-      if (lane == 0) p.lse[id] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
   // A block without rows waits too: the kernel behind this one may begin once this grid is through,
@@ -1166,7 +1198,9 @@ __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_columns_kernel
   for (int64_t id = blockIdx.x; id < ids; id += gridDim.x) {
     const int64_t out = id / kSlices;
     const int col = static_cast<int>(id % kSlices) * 32;
-    const Parts r = parts_of<D, RT>(p, plan, n, out, lane);
+    const int64_t row = out / p.hq;
+    const int b = kv::find_seq(p.rows.n_seqs, row, lane, [&](int i) { return kv::row_at(p.rows, i); });
+    const Parts r = parts_of<D, RT>(p, plan, n, row, static_cast<int>(out - row * p.hq), b);
     if (!waited) ptx::wait_dependencies();
     waited = true;
     if (r.n < 0) continue;  // the same for the whole block
