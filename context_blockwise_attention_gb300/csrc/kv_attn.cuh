@@ -34,7 +34,8 @@
 // Precision.  A query row is scaled by a power of two to at most 2^15; as f16 a bf16 row is then
 // exact (over 2^28 of range), an fp32 row is split into a high and a low part, 22 bits.  P, times
 // 2^15, is one f16 part for a bf16 output (off by 2^-11 at most, against the output's 2^-8) and two parts
-// for an fp32 one.  Sums, maxima and the accumulators are fp32.
+// for an fp32 one; f16 ends at 2^-24, so a weight is off by 2^-40 of the largest page's scale besides, which
+// only columns show in which the heavy tokens hold zeros.  Sums, maxima and the accumulators are fp32.
 //
 // Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 86 us
 // for 471 MB, 5.5 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 149 us for 910 MB, 6.1 TB/s (copy:
