@@ -82,7 +82,7 @@ struct WriteParams {
   const void* x[2];  // k, v
   int32_t* status;
   uint32_t units;
-  int32_t heads;  // of a block of the tile kernel
+  int32_t heads, pages;  // of a block of the tile kernel
 };
 
 // One warp per (page, head, K or V): it goes over the page's new rows twice, first for the largest
@@ -196,9 +196,11 @@ __device__ __forceinline__ float top_of(const uint4& v, const float*) {
 // Prompts: the threads of a tile (page, head, K or V) hold its new rows in registers between the
 // largest magnitude and the conversion, so that they are read once.  A block takes as many heads of
 // one page at once as fit, and goes over p.heads of them, so that where the page lies is looked up
-// once.  Bound by memory: 2 or 4 bytes in and 1 out per number; 16-byte loads, all of a thread's in
-// flight at once: 64 numbers a thread, 32 in small pages (29 k tokens of 8 x 128 bf16, pages of 64, 178 MB:
-// 28.7 us, 6.2 TB/s, with 32 a thread 30.8; 32 k tokens, pages of 16: 34 us with 32, 36 with 64, 40 with 16).
+// once; where there are fewer heads than fit it takes p.pages pages (96 k and 196 k tokens of 1 x 64 bf16, pages of 16 and 32: 8.6 and
+// 18 us for 37 and 75 MB, with one page a block 39 and 44).  Bound by memory: 2 or 4 bytes in and 1 out per number;
+// 16-byte loads, all of a thread's in flight at once: 64 numbers a thread, 32 in small pages (29 k tokens of
+// 8 x 128 bf16, pages of 64, 178 MB: 28.7 us, 6.2 TB/s, with 32 a thread 30.8; 32 k tokens, pages of 16: 34 us with
+// 32, 36 with 64, 40 with 16).
 template <int D, int P>
 constexpr int kTileThreads = P >= 64 ? P * D / 64 : P * D / 32;
 template <int D, int P, class T>
@@ -211,17 +213,23 @@ __global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_co
   const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
   const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
   const int at = tid % kTT, row0 = at / kPerRow, col = at % kPerRow * kV;
+  const int nth = p.pages > 1 ? tid / kTT / hkv : 0;  // page of the block; the same for a whole warp
+  const uint32_t unit = blockIdx.x * p.pages + nth;
   ptx::wait_dependencies();
   PageSpan s;
-  if (!span_of(p.rows, p.c.n_pages, P, blockIdx.x, lane, s)) return;  // the same for the whole block
-  if (s.page < 0) {
-    if (tid == 0) kv::report(p.status, kv::kSitePage);
-    return;
+  bool some = nth < p.pages && unit < p.units && span_of(p.rows, p.c.n_pages, P, unit, lane, s);
+  if (some && s.page < 0) {
+    if (at == 0 && tid / kTT == nth * hkv) kv::report(p.status, kv::kSitePage);
+    some = false;
+  }
+  if (!some) {
+    if (p.pages == 1) return;  // the same for the whole block
+    s = PageSpan{0, 0, 0, 0};
   }
   int turn = 0;
   for (int h = h0; h < h1; h += kTiles, turn ^= 1) {
-    const int head = h + tid / kTT;
-    const bool mine = head < h1;
+    const int head = h + tid / kTT - nth * hkv;
+    const bool mine = some && head < h1;
     const T* x = static_cast<const T*>(p.x[which]) + (static_cast<int64_t>(s.row) * hkv + head) * D + col;
     const int64_t tile = static_cast<int64_t>(s.page) * hkv + head;
     uint8_t* out = static_cast<uint8_t*>(which ? p.c.v : p.c.k) + tile * P * D + col;
@@ -369,6 +377,104 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_kernel(const __
   }
 }
 
+// The same for up to four heads of a block, where a row alone does not keep enough loads in flight: a block
+// looks up where its rows' tokens live, a thread a row, and then goes over (row, head) pairs, kAhead of a
+// thread's in flight together.  60 k tokens of 1 / 2 / 3 / 4 x 128 to bf16: 8.1 / 13.2 / 22.4 / 33 us, against 21 /
+// 22.6 / 26.4 / 33 the other way; 31 k tokens of 8 x 128 35.1 against 33.6.
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kV = kVec<T>, kCols = D / kV, kPairs = kThreads / kCols, kAhead = 8;
+  __shared__ int seqs[2];
+  __shared__ int64_t place[kThreads];  // (page * hkv) * P + slot of a row, -1: none
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hkv = p.c.hkv, P = p.c.page_size, shift = 31 - __clz(P);
+  const int n_rows = static_cast<int>(p.rows.n_rows);
+  const int row0 = blockIdx.x * p.per_block;
+  const int row_end = n_rows - row0 < p.per_block ? n_rows : row0 + p.per_block;
+  const int which = blockIdx.y & 1, h0 = (blockIdx.y >> 1) * p.heads;
+  const int heads = hkv - h0 < p.heads ? hkv - h0 : p.heads;
+  const float inv_heads = 1.0f / static_cast<float>(heads);
+  const int col = tid % kCols * kV;
+  ptx::wait_dependencies();
+  if (warp < 2) {  // the sequences of the block's first and last row
+    const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
+                           [&](int i) { return kv::row_at(p.rows, i); });
+    if (lane == 0) seqs[warp] = b;
+  }
+  const uint8_t* const cache = static_cast<const uint8_t*>(which ? p.c.v : p.c.k) + col;
+  const float* const scales = which ? p.c.v_scale : p.c.k_scale;
+  T* const x_out = static_cast<T*>(p.x[which]) + col;
+  for (int base = row0; base < row_end; base += kThreads) {
+    const int n = row_end - base < kThreads ? row_end - base : kThreads;
+    __syncthreads();  // the places of the rows before have been read
+    if (tid < n) {
+      const int row = base + tid;
+      int b = seqs[0], z = seqs[1];
+      while (b < z) {  // the last one that begins at or before the row
+        const int mid = (b + z + 1) >> 1;
+        if (kv::row_at(p.rows, mid) <= row) b = mid;
+        else z = mid - 1;
+      }
+      const int r0 = static_cast<int>(kv::row_at(p.rows, b)), r1 = static_cast<int>(kv::row_at(p.rows, b + 1));
+      const int first = __ldg(p.rows.tokens + b);
+      int64_t at = -1;
+      if (row >= r0 && row < r1) {
+        const int64_t token = static_cast<int64_t>(first) + (row - r0);
+        const int64_t page = first < 0 ? -1 : kv::page_at(p.rows, p.c.n_pages, b, token >> shift);
+        if (page < 0) kv::report(p.status, kv::kSitePage);
+        else at = page * hkv * P + (token & (P - 1));
+      }
+      place[tid] = at;
+    }
+    __syncthreads();
+    const int pairs = n * heads;  // at most 2^20
+    for (int i0 = tid / kCols; i0 < pairs; i0 += kPairs * kAhead) {
+      uint32_t v[kAhead][kV / 4];
+      float f[kAhead];
+      int to[kAhead];  // row of the output's (row, head) pairs from (base, 0) on, -1: none
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int pair = i0 + i * kPairs;
+        to[i] = -1;
+        if (pair < pairs) {
+          const int r = static_cast<int>((static_cast<float>(pair) + 0.5f) * inv_heads);  // exact below 2^22
+          const int h = h0 + pair - r * heads;
+          const int64_t at = place[r];
+          if (at >= 0) {
+            to[i] = r * hkv + h;
+            const uint8_t* q = cache + (at + static_cast<int64_t>(h) * P) * D;
+            if constexpr (kV == 8) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(q));
+              v[i][0] = u.x, v[i][kV / 4 - 1] = u.y;
+            } else {
+              v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+            }
+            f[i] = __ldg(scales + (at >> shift) + h);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (to[i] >= 0) {
+          float x[kV];
+#pragma unroll
+          for (int j = 0; j < kV / 4; ++j) {
+            const float2 lo = kv::e4m3x2_to_float2(v[i][j]), hi = kv::e4m3x2_to_float2(v[i][j] >> 16);
+            x[4 * j] = lo.x * f[i], x[4 * j + 1] = lo.y * f[i];
+            x[4 * j + 2] = hi.x * f[i], x[4 * j + 3] = hi.y * f[i];
+          }
+          T* const o = x_out + (static_cast<int64_t>(base) * hkv + to[i]) * D;
+          if constexpr (kV == 8)
+            __stcs(reinterpret_cast<uint4*>(o), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                           pack_bf16x2(x[kV - 4], x[kV - 3]),
+                                                           pack_bf16x2(x[kV - 2], x[kV - 1])));
+          else
+            __stcs(reinterpret_cast<float4*>(o), make_float4(x[0], x[1], x[2], x[3]));
+        }
+    }
+  }
+}
+
 template <class K, class P>
 cp_status launch(K kernel, const P& p, int64_t bx, int64_t by, const char* what, cudaStream_t s) {
   if (bx > 0x7fffffff || by > 65535) {
@@ -399,8 +505,9 @@ cp_status write_tiles(WriteParams& p, int num_sms, cudaStream_t s) {
   constexpr int kTiles = kThreads / kTileThreads<D, P>;
   int32_t heads = heads_of(p.c.hkv, 2 * p.units, 8 * num_sms);
   p.heads = (heads + kTiles - 1) / kTiles * kTiles;
-  return launch(kv_write_tile_kernel<D, P, T>, p, p.units, 2 * ((p.c.hkv + p.heads - 1) / p.heads),
-                "kv_write_tile_kernel launch", s);
+  p.pages = p.c.hkv < kTiles ? kTiles / p.c.hkv : 1;
+  return launch(kv_write_tile_kernel<D, P, T>, p, (p.units + p.pages - 1) / p.pages,
+                2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_write_tile_kernel launch", s);
 }
 template <int D, class T>
 cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
@@ -433,7 +540,10 @@ cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
   p.per_block = static_cast<int32_t>(per < kRows ? kRows : per);
   const int64_t bx = (p.rows.n_rows + p.per_block - 1) / p.per_block;
   p.heads = heads_of(p.c.hkv, 2 * bx, 4 * num_sms);
-  return launch(kv_read_kernel<D, T>, p, bx, 2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_read_kernel launch", s);
+  if (p.heads > 4096) p.heads = 4096;  // of 256 rows: 2^20 pairs
+  const int64_t by = 2 * ((p.c.hkv + p.heads - 1) / p.heads);
+  return p.heads > 4 ? launch(kv_read_kernel<D, T>, p, bx, by, "kv_read_kernel launch", s)
+                     : launch(kv_read_few_kernel<D, T>, p, bx, by, "kv_read_few_kernel launch", s);
 }
 
 }  // namespace
@@ -441,7 +551,7 @@ cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
                           int32_t* status, int num_sms, cudaStream_t s) {
   const int64_t units = rows.n_rows / c.page_size + 2 * static_cast<int64_t>(rows.n_seqs);
-  WriteParams p{c, rows, {k, v}, status, static_cast<uint32_t>(units), 0};
+  WriteParams p{c, rows, {k, v}, status, static_cast<uint32_t>(units), 0, 1};
   if (c.d == 128) return bf16 ? write<128, __nv_bfloat16>(p, num_sms, s) : write<128, float>(p, num_sms, s);
   return bf16 ? write<64, __nv_bfloat16>(p, num_sms, s) : write<64, float>(p, num_sms, s);
 }
