@@ -511,13 +511,19 @@ cp_status write_tiles(WriteParams& p, int num_sms, cudaStream_t s) {
 }
 template <int D, class T>
 cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
-  // A block a tile pays where its threads have rows to hold: 64 sequences of 512 rows 34 against 60 us (pages of
-  // 64; of 16 34 against 41), of 128 rows 12 against 18 (pages of 16: 14 against 11), 512 sequences of 8 rows 23 to 32
-  // against 10; and where the tiles are few and a warp would take their rows one after the other: one sequence
-  // of 512 rows 2.3 against 8.5.
+  // Threads that hold a tile's rows pay where there are rows for them.  A warp a tile against them, us, bf16:
+  // 100 sequences, 8 x 128, pages of 128: 24 rows 6.7 / 11, 64 rows 14.4 / 13.8, 128 rows 26 / 19, 512 rows 90 / 53;
+  // pages of 64: 24 rows 7.3 / 9.0, 48 rows 11.6 / 10.8, 512 rows 81 / 53; of 32: 24 rows 6.4 / 7.7, 48 rows 11.6 /
+  // 9.8, 512 rows 60 / 57; of 16: 64 rows 10.5 / 11.1, 96 rows 13.1 / 12.5, 512 rows 61 / 58 (fp32, 40 sequences: 256
+  // rows 16.6 / 20, 384 rows 34 / 33); 64 sequences, 32 x 64, pages of 16: 4 rows 4.9 / 5.2, 8 rows 5.9 / 5.7, 512 rows
+  // 111 / 71.  They also pay where their blocks are few and a warp would take a tile's rows one after the other:
+  // 8 sequences, 8 x 128, pages of 128: 8 rows 3.0 / 3.2, 32 rows 5.3 / 3.4, 64 rows 9.9 / 3.5.
+  const int P = p.c.page_size;
   const int64_t tiles = static_cast<int64_t>(p.units) * p.c.hkv * 2, seqs = p.rows.n_seqs;
-  const bool long_rows = p.rows.n_rows >= seqs * (p.c.page_size < 64 ? 512 : p.c.page_size);
-  const bool few = p.rows.n_rows >= 8 * seqs && tiles <= 1500;
+  const int64_t blocks = tiles * P * D / (P >= 64 ? 64 : 32) / kThreads;
+  const int from = P == 128 ? 64 : P >= 32 ? 48 : D == 64 ? 8 : sizeof(T) == 2 ? 96 : 384;
+  const bool long_rows = p.rows.n_rows >= seqs * from;
+  const bool few = p.rows.n_rows >= 8 * seqs && blocks <= 2 * num_sms;
   if (!long_rows && !few) {
     const int64_t warps = tiles;
     return launch(kv_write_warp_kernel<D, T>, p, (warps + kThreads / 32 - 1) / (kThreads / 32), 1,
