@@ -30,16 +30,35 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
            static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
   r.grid = r.most < sms ? static_cast<int64_t>(r.most) : sms;
-  // Solo: no more items than SMs, and few granules to a warp by the page table's width: 4, or 16 where the
-  // items occupy most SMs (1 x 8 items of 1024 / 2048 tokens at D = 128: 9.6 / 14.0 us against 11.6 / 12.1
-  // split; 18 x 8 items of 2048 / 6144: 14.7 / 35.7 against 19.9 / 39.6).  One row a sequence, as far as can
-  // be told from their numbers, or few rows in all, since a block takes blocks of rows one after the other.
+  // Solo, by the page table's width in granules: as many blocks an item as the SMs hold clusters of (12 to 15 of
+  // 8 blocks, 36 of 4), where a block's warps have some granules each (32/8 heads, D = 128: 1 x 1000 / 4000
+  // tokens 9.4 / 20.6 us with one block, 8.5 / 10.0 with 8; 4 x 4000 21.1, 11.9 with 4; 8 x 4000 21.1, 15.8 with 2;
+  // 1 x 500 7.4, 8.4 with 8), as long as splitting is slower, which uses all SMs but has a second kernel: 1 x 4000
+  // tokens 10.0 us against 12.8, 4 x 4000 11.9 / 16.6, 4 x 8000 16.0 / 20.0, 8 x 4000 15.8 / 18.6, one KV head of
+  // 4000 9.5 / 9.6, of 8000 11.8 / 10.7; 18 x 8 items of 2048 / 6144 tokens, one block each, 14.7 / 35.7 against
+  // 19.9 / 39.6.  One row a sequence, as far as can be told from their numbers, or few rows in all, since the
+  // blocks take an item's blocks of rows one after the other.
   const int64_t width = (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096;
   const int64_t solo_items = seqs * d.cache.hkv;
-  r.solo = solo_items <= sms && width <= r.warps * (2 * solo_items > sms ? 16 : 4) &&
+  r.cluster = 1;
+  if (width > 2 * r.warps) {
+    if (solo_items * 8 <= sms * 5 / 8) r.cluster = 8;
+    else if (solo_items * 4 <= sms * 6 / 7) r.cluster = 4;
+    else if (solo_items * 2 <= sms * 6 / 7 && width > 3 * r.warps) r.cluster = 2;
+  }
+  const int64_t blocks = solo_items * r.cluster;
+  // Of clusters the more granules a warp the more of the SMs they take, and fewer for several blocks of rows,
+  // as the longest sequence can have and all have on average; a third less than equal lengths would bear, since
+  // splitting alone evens out different ones (28 x 0-7758 tokens, 4/2 heads, D = 64, 2 blocks an item: 18.8 us, split
+  // 15.4; 4 x 5027, 32/2 heads, D = 64, two blocks of rows: 15.0, split 12.9).
+  const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
+  const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
+  const bool narrow = r.cluster > 1 ? (d.cache.d == 128 ? 20 : 28) * width * turns <= r.warps * r.cluster * blocks
+                                    : width <= r.warps * (2 * blocks > sms ? 16 : 4);
+  r.solo = blocks <= sms && narrow &&
            (d.rows.n_rows <= seqs || d.rows.n_rows * group <= 4 * r.rows);
   if (r.solo) {
-    r.grid = solo_items;
+    r.grid = blocks;
     r.ml_off = r.o_off = r.aside_off = r.bytes = 0;
     return r;
   }
@@ -98,6 +117,7 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   const int64_t seqs = d.rows.n_seqs;
   const int64_t items = (seqs + d.rows.n_rows * p.group / pl.rows) * c.hkv;
   p.few = 128 * items;
+  p.cluster = pl.cluster;
   return c.d == 128 ? run_d<128>(p, pl, mk, mv, items, num_sms, s) : run_d<64>(p, pl, mk, mv, items, num_sms, s);
 }
 

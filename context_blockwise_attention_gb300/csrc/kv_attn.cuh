@@ -19,8 +19,9 @@
 // launched as a programmatic dependent, combines them in the order of the workers.  That kernel also
 // answers the rows of sequences without visible tokens, which are no items.
 //
-// Few short rows (SOLO): one block per (sequence, KV head), its warps share the granules, and the
-// partials meet in shared memory: one launch and no workspace.
+// Few short rows (SOLO): one block, or a cluster of up to 8, per (sequence, KV head); their warps share the
+// granules, and the partials meet in shared memory, a block's first and then the cluster's: one launch and no
+// workspace.
 //
 // Products.  mma.sync m16n8k16 with f16 operands: e4m3 -> f16 is exact and one instruction for two
 // values, and the 128-row tiles of tcgen05 would be mostly empty with 8 to 32 query rows.  Both
@@ -104,6 +105,7 @@ struct Params {
   int32_t* status;
   int64_t timeout_ns;
   int64_t few;     // workers that may have less than four numbers
+  int32_t cluster; // SOLO 2: blocks of an item, 2 to 8
   float* part_o;   // [workers][2][RT][D]
   float2* part_ml; // [workers][2][RT]: m (base 2), l
   float* aside;    // [workers][RT][D]: accumulators put aside
@@ -269,7 +271,8 @@ __device__ __forceinline__ void next_seq(const Params& p, Cursor& c, Seq& s) {
   c.blocks = s.blocks;
 }
 
-template <int D, int NT, int QP, int PP, bool SOLO>
+// SOLO: 0 split, 1 one block an item, 2 a cluster of p.cluster blocks (of its own: 2 to 7 % of the others' time).
+template <int D, int NT, int QP, int PP, int SOLO>
 __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     kv_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v) {
@@ -312,13 +315,18 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   int64_t left;  // numbers of the share from the cursor on
   bool inside;   // the share begins inside of an item
   const bool stalled = p.stall && blockIdx.x == 0 && warp == 0;  // test only
+  // SOLO: rank of the block among those of its item, and the warp and number of warps among all of them
+  const int cluster = SOLO == 2 ? p.cluster : 1;
+  const int rank = SOLO == 2 ? blockIdx.x % cluster : 0;
+  const int solo_warp = rank * S::kWarps + warp, solo_warps = cluster * S::kWarps;
   if constexpr (SOLO) {
-    c.b = blockIdx.x / p.hkv;
-    c.head = blockIdx.x - c.b * p.hkv;
+    const int item = blockIdx.x / cluster;
+    c.b = item / p.hkv;
+    c.head = item - c.b * p.hkv;
     seq = seq_of<D, RT>(p, c.b);
     if (seq.over && seq.rows > 0 && tid == 0) kv::report(p.status, kv::kSiteTokens);
     if (seq.blocks == 0) {  // nothing to see
-      for (int rho = warp; rho < seq.rows * p.group; rho += S::kWarps) {
+      for (int rho = solo_warp; rho < seq.rows * p.group; rho += solo_warps) {
         const int t = rho / p.group;
         const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
         const float zero[D / 32] = {};
@@ -331,8 +339,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     c.block = 0;
     c.gpi = seq.gpi;
     c.blocks = seq.blocks;
-    c.g = seq.gpi * warp / S::kWarps;
-    left = seq.gpi * (warp + 1) / S::kWarps - c.g;
+    c.g = seq.gpi * solo_warp / solo_warps;
+    left = seq.gpi * (solo_warp + 1) / solo_warps - c.g;
     inside = false;
   } else {
     make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
@@ -970,6 +978,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     __syncwarp();
     end_item(false, mine, reinterpret_cast<float2*>(mine + RT * D));
     __syncthreads();
+    auto finish = [&](int rho, float top, float sum, float (&x)[D / 32]) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] *= inv;
+      const int t = rho / p.group;
+      const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+      store_lane(p, out * D + lane * (D / 32), x);
+      if (lane == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    };
     for (int i = warp; i < RT; i += S::kWarps) {
       const int rho = row_q + i;
       if (rho >= seq.rows * p.group) break;
@@ -988,17 +1005,57 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) x[j] = fmaf(wt, from[j], x[j]);
       }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if constexpr (SOLO == 1) {
+        finish(rho, top, sum, x);
+      } else {  // the block's partial takes the place of its first warp's
+        __syncwarp();
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) x[j] *= inv;
-      const int t = rho / p.group;
-      const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
-      store_lane(p, out * D + lane * (D / 32), x);
-      if (lane == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        for (int j = 0; j < D / 32; ++j) reinterpret_cast<float*>(smem)[i * D + lane * (D / 32) + j] = x[j];
+        if (lane == 0) reinterpret_cast<float2*>(smem + RT * D * 4)[i] = make_float2(top, sum);
+      }
+    }
+    int stop = 0;
+    if constexpr (SOLO == 2) {
+      ptx::cluster_sync();
+      for (int i = rank + cluster * warp; i < RT; i += solo_warps) {
+        const int rho = row_q + i;
+        if (rho >= seq.rows * p.group) break;
+        float top = -INFINITY, sum = 0.0f;
+        if (lane < cluster) {
+          const uint32_t at = ptx::cluster_addr(base + RT * D * 4 + i * 8, lane);
+          top = ptx::ld_cluster(at);
+          sum = ptx::ld_cluster(at + 4);
+        }
+        const float mine = top;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        top = __shfl_sync(kFull, top, 0);
+        const float wt = ex2(mine - (top == -INFINITY ? 0.0f : top));
+        sum *= wt;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        sum = __shfl_sync(kFull, sum, 0);
+        float x[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < cluster; ++r) {
+          const float w = __shfl_sync(kFull, wt, r);
+          const uint32_t at = ptx::cluster_addr(base + (i * D + lane * (D / 32)) * 4, r);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) x[j] = fmaf(w, ptx::ld_cluster(at + 4 * j), x[j]);
+        }
+        finish(rho, top, sum, x);
+      }
+      // a wait that ran out in one block ends them all, since they read one another's memory
+      if (lane < cluster)
+        stop = __float_as_int(ptx::ld_cluster(ptx::cluster_addr(base + S::kCtlOff, lane)));
+      stop = __any_sync(kFull, stop != 0);
     }
     ptx::fence_proxy_async_smem();  // the next block's copies write where the partials were
-    __syncthreads();
-    if (++c.block == c.blocks || *abort_flag) break;
+    if constexpr (SOLO == 2) ptx::cluster_sync();
+    else __syncthreads();
+    if (++c.block == c.blocks || (SOLO == 2 ? stop != 0 : *abort_flag != 0)) break;
     f.block = c.block;
     f.g = c.g = g_first;
     left = to_issue = solo_left;
@@ -1282,7 +1339,8 @@ struct Plan {
   int nt, qp, pp;
   int rows;      // RT
   int warps;     // of a block
-  bool solo;     // one block per (sequence, KV head), no workspace
+  bool solo;     // one block or cluster of blocks per (sequence, KV head), no workspace
+  int cluster;
   double most;
   int64_t grid;
   int64_t ml_off, o_off, aside_off, bytes;
@@ -1293,15 +1351,20 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
   using S = Shape<D, NT, QP, PP>;
   static_assert(1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8 <= 232448, "shared memory of a block");
   const int smem = 1024 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
-  const auto kernel = pl.solo ? kv_attn_kernel<D, NT, QP, PP, true> : kv_attn_kernel<D, NT, QP, PP, false>;
+  const auto kernel = !pl.solo           ? kv_attn_kernel<D, NT, QP, PP, 0>
+                      : pl.cluster == 1 ? kv_attn_kernel<D, NT, QP, PP, 1>
+                                        : kv_attn_kernel<D, NT, QP, PP, 2>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel attribute");
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(pl.cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pl.solo && pl.cluster > 1 ? 2 : 1;
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(pl.grid));
   cfg.blockDim = dim3(S::kWarps * 32);

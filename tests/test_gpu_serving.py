@@ -274,9 +274,9 @@ ATTN = [  # rows, held, page, hq, hkv, d, in, out, stride of the shard or None (
 ]
 
 
-# a table as wide as the longest sequence needs, and a much wider one: short rows take one block a sequence and
-# head by the first, and are split by the second
-@pytest.mark.parametrize("wide", [0, 600])
+# a table as wide as the longest sequence needs, and much wider ones: short rows take one block a sequence and
+# head by the first, a cluster of blocks by some, and are split by the widest
+@pytest.mark.parametrize("wide", [0, 600, 2500])
 @pytest.mark.parametrize("rows,held,page,hq,hkv,d,din,dout,stride", ATTN)
 def test_attention(rows, held, page, hq, hkv, d, din, dout, stride, wide):
     pool = Pool(len(rows), held, page, hkv, d, 11)
@@ -290,7 +290,7 @@ def test_attention(rows, held, page, hq, hkv, d, din, dout, stride, wide):
     _check_attn(pool, pool.device(), q, rows, held, first, PosMap(base, stride or 1), dout, wide=wide)
 
 
-@pytest.mark.parametrize("wide", [0, 600])
+@pytest.mark.parametrize("wide", [0, 600, 2500])
 @pytest.mark.parametrize("dout", [BF16, F32])
 def test_attention_rows_that_see_little_or_nothing(dout, wide):
     rows, held = [6, 3, 2, 4], [50, 200, 0, 31]
@@ -339,7 +339,7 @@ def test_attention_ignores_nan_and_infinity_behind_a_row(g, d, page, dout):
     assert bool(o[1, 0].isnan().all())
 
 
-@pytest.mark.parametrize("wide", [0, 600])
+@pytest.mark.parametrize("wide", [0, 600, 2500])
 @pytest.mark.parametrize("d,page", [(64, 32), (128, 16)])
 @pytest.mark.parametrize("which,value", [(0, float("nan")), (0, float("inf")), (1, float("nan")), (1, float("inf"))])
 def test_attention_scale_that_is_not_finite_reaches_the_rows_that_see_its_page(which, value, d, page, wide):
@@ -433,6 +433,25 @@ def test_attention_one_long_sequence(held, page, hq, hkv, d, n, dout):
     pool.fill([held], 82)
     q = torch.randn((n, hq, d), generator=torch.Generator().manual_seed(83)).to(BF16)
     _check_attn(pool, pool.device(), q, [n], [held], [held - n], PosMap(0, 1), dout)
+
+
+@pytest.mark.parametrize("rows,held,page,hq,hkv,d,din,dout", [
+    ([1], [1200], 32, 4, 1, 128, BF16, BF16),
+    ([1, 1], [4000, 3], 64, 8, 2, 64, BF16, F32),
+    ([5, 1], [1500, 900], 16, 20, 5, 128, BF16, F32),       # an item of several blocks of rows
+    ([1, 0, 1], [2100, 50, 0], 128, 32, 8, 128, F32, F32),  # 24 items: four blocks each
+    ([1] * 7, [1100, 0, 900, 2000, 1, 33, 1500], 16, 16, 8, 128, BF16, BF16),  # 56 items: two
+    ([2, 1], [1700, 2300], 32, 8, 4, 64, F32, BF16),
+    ([1], [1700], 16, 80, 5, 64, F32, F32)])
+def test_attention_clusters(rows, held, page, hq, hkv, d, din, dout):
+    """Few rows over caches that are too long for one block an item and too short for a second kernel."""
+    pool = Pool(len(rows), held, page, hkv, d, 87)
+    pool.fill(held, 88)
+    q = torch.randn((sum(rows), hq, d), generator=torch.Generator().manual_seed(89)).to(din)
+    first = [m - n for n, m in zip(rows, held)]
+    assert cpa.kv_cache_attn_workspace(pool.device(), sum(rows), hq, len(rows), pool.table.shape[1], din, dout) == 0
+    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(0, 1), dout)
+    _check_attn(pool, pool.device(), q, rows, held, [f // 2 for f in first], PosMap(1, 2), dout)
 
 
 @pytest.mark.parametrize("d,page,dout", [(64, 16, BF16), (128, 32, F32)])
@@ -559,7 +578,7 @@ def test_attention_same_bits_on_streams_at_once_and_in_graphs():
     s.copy_(s0)
 
 
-@pytest.mark.parametrize("wide", [0, 500])
+@pytest.mark.parametrize("wide", [0, 500, 2500])
 def test_rows_before_the_first_and_behind_the_last_sequence(wide):
     """row_start may begin behind row 0: the rows before it belong to nobody, in all three calls."""
     rows, held, total = [2, 0, 1], [40, 9, 100], [42, 9, 101]
@@ -572,8 +591,8 @@ def test_rows_before_the_first_and_behind_the_last_sequence(wide):
     o = torch.full((8, 8, 64), 12345.0, device=DEV)
     lse = torch.full((8, 8), 12345.0, device=DEV)
     cpa.kv_cache_attn(q, cache, start, _i32(total), table, q_first=_i32(held), o=o, lse=lse)
-    want = cpa.kv_cache_attn(q[3:6].contiguous(), cache, start - 3, _i32(total), table, q_first=_i32(held))
-    assert torch.equal(o[3:6], want[0]) and torch.equal(lse[3:6], want[1])
+    want = cpa.kv_cache_attn(q.roll(-3, 0), cache, start - 3, _i32(total), table, q_first=_i32(held))  # the same shapes
+    assert torch.equal(o[3:6], want[0][:3]) and torch.equal(lse[3:6], want[1][:3])
     for x in (o, lse):
         assert bool((x[:3] == 12345.0).all()) and bool((x[6:] == 12345.0).all())
     k = torch.full((8, 2, 64), 12345.0, device=DEV)
@@ -633,7 +652,8 @@ def test_a_decoding_step_in_a_graph():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
-@pytest.mark.parametrize("width", [13, 400])  # a table of few pages: one block a sequence and head; of many: split
+# a table of few pages: one block a sequence and head; of more: a cluster of blocks; of many: split
+@pytest.mark.parametrize("width", [13, 100, 400, 2500])
 def test_attention_wait_runs_out(width):
     pool, cache, q, s, h, t = _serving_case(95, [1, 1], [400, 300])
     t = torch.cat([t, t.new_full((2, width - t.shape[1]), -1)], 1)
