@@ -38,11 +38,11 @@
 // for an fp32 one; f16 ends at 2^-24, so a weight is off by 2^-40 of the largest page's scale besides, which
 // only columns show in which the heavy tokens hold zeros.  Sums, maxima and the accumulators are fp32.
 //
-// Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 86 us
-// for 471 MB, 5.5 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 149 us for 910 MB, 6.1 TB/s (copy:
-// 6.8); 12 x 8192-16384 tokens with 8 / 16 / 32 / 128 query rows, D = 128: 66 / 81 / 123 / 408 us; one token
-// over 1000, 32/8, D = 128: 9.0 us.  What is left of the long calls is 6 us until the first data are
-// there for all, SMs that end up to a tenth later than others, and 4 us of the second kernel.
+// Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 86-88 us
+// for 471 MB, 5.4 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 147-149 us for 910 MB, 6.1 TB/s (copy:
+// 6.8); 16 x 2-6 rows over 1000-20000 tokens, 32/8, D = 128: 102 us; one token over 1000, 32/8, D = 128: 8.2 us; 4 x
+// 2000: 9.7 us.  What is left of the long calls is 6 us until the first data are there for all, SMs that end up
+// to a tenth later than others, and 4 us of the second kernel.
 #pragma once
 
 #include "internal.h"

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(cons
       place[tid] = at;
     }
     __syncthreads();
-    const int pairs = n * heads;  // at most 2^20
+    const int pairs = n * heads;
     for (int i0 = tid / kCols; i0 < pairs; i0 += kPairs * kAhead) {
       uint32_t v[kAhead][kV / 4];
       float f[kAhead];
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(cons
         const int pair = i0 + i * kPairs;
         to[i] = -1;
         if (pair < pairs) {
-          const int r = static_cast<int>((static_cast<float>(pair) + 0.5f) * inv_heads);  // exact below 2^22
+          const int r = static_cast<int>((static_cast<float>(pair) + 0.5f) * inv_heads);  // exact: below 2^22
           const int h = h0 + pair - r * heads;
           const int64_t at = place[r];
           if (at >= 0) {
@@ -546,7 +546,6 @@ cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
   p.per_block = static_cast<int32_t>(per < kRows ? kRows : per);
   const int64_t bx = (p.rows.n_rows + p.per_block - 1) / p.per_block;
   p.heads = heads_of(p.c.hkv, 2 * bx, 4 * num_sms);
-  if (p.heads > 4096) p.heads = 4096;  // of 256 rows: 2^20 pairs
   const int64_t by = 2 * ((p.c.hkv + p.heads - 1) / p.heads);
   return p.heads > 4 ? launch(kv_read_kernel<D, T>, p, bx, by, "kv_read_kernel launch", s)
                      : launch(kv_read_few_kernel<D, T>, p, bx, by, "kv_read_few_kernel launch", s);

@@ -536,8 +536,13 @@ def _serving_case(seed, rows, held, page=32, hq=8, hkv=2, d=64):
     return pool, pool.device(), q, _i32(_starts(rows)), _i32(held), _i32(pool.table)
 
 
-def test_attention_same_bits_on_streams_at_once_and_in_graphs():
-    cases = [_serving_case(70, [1, 2, 1], [900, 40, 333]), _serving_case(80, [4], [2000], page=128, hq=16, d=128)]
+@pytest.mark.parametrize("wide", [0, 60, 3000])  # one block an item, a cluster, split
+def test_attention_same_bits_on_streams_at_once_and_in_graphs(wide):
+    def widened(*case):
+        return (*case[:5], torch.cat([case[5], case[5].new_full((case[5].shape[0], wide), -1)], 1))
+
+    cases = [widened(*_serving_case(70, [1, 2, 1], [900, 40, 333])),
+             widened(*_serving_case(80, [4], [2000], page=128, hq=16, d=128))]
     alone = [cpa.kv_cache_attn(q, c, s, h, t) for _, c, q, s, h, t in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cases]
@@ -552,7 +557,7 @@ def test_attention_same_bits_on_streams_at_once_and_in_graphs():
         for got, want in ((r0, alone[0]), (r1, alone[1]), (raw, alone[1])):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     # a captured step replayed with other lengths, positions and pages
-    pool, cache, q, s, h, t = _serving_case(90, [1, 1, 1], [700, 64, 257], page=16)
+    pool, cache, q, s, h, t = widened(*_serving_case(90, [1, 1, 1], [700, 64, 257], page=16))
     h0, s0 = h.clone(), s.clone()
     first = _i32([699, 63, 256])
     o = torch.empty((3, 8, 64), device=DEV)
