@@ -20,16 +20,11 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   const int64_t per = (d.rows.n_rows + seqs - 1) / seqs * group;
   r.qp = d.in_dtype == CP_BF16 ? 1 : 2;
   r.pp = d.in_dtype == CP_BF16 && d.o_dtype == CP_BF16 ? 1 : 2;
-  // Two tiles of rows at once halve the copies and conversions, at 8 warps an SM (12 x 8192-16384 tokens, one
-  // against two tiles: D = 128, 16 rows 95 / 81 us, 32 rows 154 / 123; D = 64, 16 rows 49 / 61, 32 rows 78 / 79,
-  // 64 rows 140 / 124).
-  r.nt = per <= (d.cache.d == 128 ? 8 : 32) ? 1 : 2;
-  r.rows = r.nt * 8;
-  r.warps = r.nt * d.cache.d >= 256 || r.nt * r.qp >= 4 ? 8 : 12;
-  // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
-  r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
-           static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
-  r.grid = r.most < sms ? static_cast<int64_t>(r.most) : sms;
+  const auto tiles = [&](int nt) {
+    r.nt = nt;
+    r.rows = nt * 8;
+    r.warps = nt * d.cache.d >= 256 || nt * r.qp >= 4 ? 8 : 12;
+  };
   // Solo, by the page table's width in granules: as many blocks an item as the SMs hold clusters of (12 to 15 of
   // 8 blocks, 36 of 4), where a block's warps have some granules each (32/8 heads, D = 128: 1 x 1000 / 4000
   // tokens 9.4 / 20.6 us with one block, 8.5 / 10.0 with 8; 4 x 4000 21.1, 11.9 with 4; 8 x 4000 21.1, 15.8 with 2;
@@ -38,6 +33,7 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   // 4000 9.5 / 9.6, of 8000 11.8 / 10.7; 18 x 8 items of 2048 / 6144 tokens, one block each, 14.7 / 35.7 against
   // 19.9 / 39.6.  One row a sequence, as far as can be told from their numbers, or few rows in all, since the
   // blocks take an item's blocks of rows one after the other.
+  tiles(per <= 8 ? 1 : 2);
   const int64_t width = (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096;
   const int64_t solo_items = seqs * d.cache.hkv;
   r.cluster = 1;
@@ -60,8 +56,22 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   if (r.solo) {
     r.grid = blocks;
     r.ml_off = r.o_off = r.aside_off = r.bytes = 0;
+    r.most = 0;
     return r;
   }
+  // Two tiles of rows at once halve the copies and conversions, at 8 warps an SM and with half of the work in vain
+  // for items that end in the first.  One against two tiles, 12 x 8192-16384 tokens, us: D = 128, 8 KV heads (302 MB,
+  // more than the L2 cache keeps for the second block of rows), 16 rows 90 / 72, 24 rows 142 / 118, 32 rows 150 / 121;
+  // 4 KV heads, 16 rows 50 / 50, 24 rows 68 / 68, to fp32 74 / 84, 32 rows 79 / 72; different numbers of rows, 8 to
+  // 24 of 36 x 7334 tokens 33 / 35, 4 to 20 of 344 x 853 32 / 35; D = 64, 8 KV heads, 16 rows 47 / 52, 24 rows 64 / 73,
+  // 32 rows 79 / 76, to fp32 88 / 97, 64 rows 146 / 132.
+  const int64_t table = seqs * d.rows.max_pages, pages = table < d.cache.n_pages ? table : d.cache.n_pages;
+  const bool cached = pages * d.cache.hkv * d.cache.page_size * d.cache.d * 2 <= 160000000;
+  tiles(per <= (d.cache.d == 64 ? 32 : cached ? 24 : 8) ? 1 : 2);
+  // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
+  r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
+           static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
+  r.grid = r.most < sms ? static_cast<int64_t>(r.most) : sms;
   const int64_t slots = r.grid * r.warps * 2 * r.rows;
   r.ml_off = 0;
   r.o_off = (r.ml_off + slots * 8 + 255) / 256 * 256;
