@@ -7,7 +7,7 @@
 // give an angle in [-pi, pi).
 //
 // Bound by memory: every number is read and written once.  32768 tokens x 40 heads x 128 bf16 (671 MB):
-// 107 us, 6.3 TB/s; one thread a pair with its own cosine took 787.
+// 109 us, 6.2 TB/s; one thread a pair with its own cosine took 787.
 // A block takes a few tokens, makes their cosines and sines once in shared memory (a thread makes those
 // of one pair, and uses 8 for each 16 numbers), and turns all heads of all tensors with 16-byte
 // accesses; a thread's first loads are under way while the table is made.  Where the heads are few the table is
