@@ -271,7 +271,8 @@ __device__ __forceinline__ void next_seq(const Params& p, Cursor& c, Seq& s) {
   c.blocks = s.blocks;
 }
 
-// SOLO: 0 split, 1 one block an item, 2 a cluster of p.cluster blocks (of its own: 2 to 7 % of the others' time).
+// SOLO: 0 split, 1 one block an item, 2 a cluster of p.cluster blocks an item.  Three kernels, as the code of one
+// in another's cost it 2 to 7 %.
 template <int D, int NT, int QP, int PP, int SOLO>
 __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     kv_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_k,
@@ -1109,7 +1110,8 @@ __device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, 
 // finished by their worker: a warp of its own looks 32 of its rows up side by side (58 x 32 items of up to 52
 // rows and one granule: 37 us the whole call, against 56 one row after the other).
 template <int D, int RT, int WPR>
-__global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
+__global__ void __launch_bounds__(kSumThreads, 4)
+    kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
   constexpr int kN = D / 32, kPer = kSumThreads / 32 / WPR;  // rows of a block at a time
   extern __shared__ int64_t plan[];
   __shared__ int64_t scratch[kSumThreads / 32];
@@ -1248,7 +1250,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_kernel(const _
 // partials are summed side by side and 256 reads are on their way.  For one row of 1800 partials, as one long
 // sequence leaves them, a block of eight warps for a row's whole length took 27 us.
 template <int D, int RT>
-__global__ void __launch_bounds__(kSumThreads, 4) kv_attn_combine_columns_kernel(const __grid_constant__ Params p, int64_t most) {
+__global__ void __launch_bounds__(kSumThreads, 4)
+    kv_attn_combine_columns_kernel(const __grid_constant__ Params p, int64_t most) {
   constexpr int kWarps = kSumThreads / 32, kSide = kSumThreads / 8, kSlices = D / 32;
   extern __shared__ int64_t plan[];
   __shared__ int64_t scratch[kWarps];
@@ -1395,10 +1398,13 @@ template <int D>
 cp_status run_d(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
                 int num_sms, cudaStream_t s) {
   if (pl.pp == 1)
-    return pl.nt == 1 ? run<D, 1, 1, 1>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 1>(p, pl, mk, mv, items, num_sms, s);
+    return pl.nt == 1 ? run<D, 1, 1, 1>(p, pl, mk, mv, items, num_sms, s)
+                      : run<D, 2, 1, 1>(p, pl, mk, mv, items, num_sms, s);
   if (pl.qp == 1)
-    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 1, 2>(p, pl, mk, mv, items, num_sms, s);
-  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, num_sms, s) : run<D, 2, 2, 2>(p, pl, mk, mv, items, num_sms, s);
+    return pl.nt == 1 ? run<D, 1, 1, 2>(p, pl, mk, mv, items, num_sms, s)
+                      : run<D, 2, 1, 2>(p, pl, mk, mv, items, num_sms, s);
+  return pl.nt == 1 ? run<D, 1, 2, 2>(p, pl, mk, mv, items, num_sms, s)
+                    : run<D, 2, 2, 2>(p, pl, mk, mv, items, num_sms, s);
 }
 
 }  // namespace kvattn

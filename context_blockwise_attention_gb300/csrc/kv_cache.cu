@@ -196,11 +196,11 @@ __device__ __forceinline__ float top_of(const uint4& v, const float*) {
 // Prompts: the threads of a tile (page, head, K or V) hold its new rows in registers between the
 // largest magnitude and the conversion, so that they are read once.  A block takes as many heads of
 // one page at once as fit, and goes over p.heads of them, so that where the page lies is looked up
-// once; where there are fewer heads than fit it takes p.pages pages (96 k and 196 k tokens of 1 x 64 bf16, pages of 16 and 32: 8.6 and
-// 18 us for 37 and 75 MB, with one page a block 39 and 44).  Bound by memory: 2 or 4 bytes in and 1 out per number;
-// 16-byte loads, all of a thread's in flight at once: 64 numbers a thread, 32 in small pages (29 k tokens of
-// 8 x 128 bf16, pages of 64, 178 MB: 28.7 us, 6.2 TB/s, with 32 a thread 30.8; 32 k tokens, pages of 16: 34 us with
-// 32, 36 with 64, 40 with 16).
+// once; where there are fewer heads than fit it takes p.pages pages (96 k and 196 k tokens of 1 x 64 bf16, pages
+// of 16 and 32: 8.6 and 18 us for 37 and 75 MB, with one page a block 39 and 44).  Bound by memory: 2 or 4 bytes
+// in and 1 out per number; 16-byte loads, all of a thread's in flight at once: 64 numbers a thread, 32 in small
+// pages (29 k tokens of 8 x 128 bf16, pages of 64, 178 MB: 28.7 us, 6.2 TB/s, with 32 a thread 30.8; 32 k tokens,
+// pages of 16: 34 us with 32, 36 with 64, 40 with 16).
 template <int D, int P>
 constexpr int kTileThreads = P >= 64 ? P * D / 64 : P * D / 32;
 template <int D, int P, class T>
