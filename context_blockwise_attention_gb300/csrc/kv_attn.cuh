@@ -3,8 +3,8 @@
 //
 // Per (sequence, KV head) the g = hq / hkv query heads of the sequence's rows are one block of
 // query rows that share keys and values:
-//   s_ij = scale * ks(page of j) * (q_i . k8_j),  p_ij = 2^(s_ij log2 e - m_i),
-//   O_i = sum_j p_ij vs(page of j) v8_j / l_i,    LSE_i = ln 2 (m_i + log2 l_i),  l_i = sum_j p_ij.
+//   s_ij = log2 e * scale * ks(page of j) * (q_i . k8_j),  p_ij = 2^(s_ij - m_i),
+//   O_i = sum_j p_ij vs(page of j) v8_j / l_i,             LSE_i = ln 2 (m_i + log2 l_i),  l_i = sum_j p_ij.
 // Bound: every cached byte is read once for 2 g rows' worth of products per byte, so it is memory
 // bound for up to a few dozen rows; the design is about keeping loads in flight and splitting the
 // keys evenly, not about the tensor rate.
@@ -33,10 +33,15 @@
 // row, without bank conflicts under the 128-byte swizzle that the copies apply.
 //
 // Precision.  A query row is scaled by a power of two to at most 2^15; as f16 a bf16 row is then
-// exact (over 2^28 of range), an fp32 row is split into a high and a low part, 22 bits.  P, times
-// 2^15, is one f16 part for a bf16 output (off by 2^-11 at most, against the output's 2^-8) and two parts
-// for an fp32 one; f16 ends at 2^-24, so a weight is off by 2^-40 of the largest page's scale besides, which
-// only columns show in which the heavy tokens hold zeros.  Sums, maxima and the accumulators are fp32.
+// exact (over 2^28 of range), an fp32 row is split into a high and a low part, 22 bits.  An operand of P is a
+// contribution, p_ij vs, in one f16 part for a bf16 output (off by 2^-11 at most, against the output's 2^-8) and in
+// two for an fp32 one.  f16 ends at 2^-24, so the row's largest contribution is held at 2^15 to 2^16: m_i is
+//   max_j (s_ij + log2 vs(page of j)) - base,
+// a whole number, with one `base` for an item's pages, and p_ij vs 2^(15 - base) is the operand.  So a contribution
+// is off by 2^-40 of the row's largest besides, which only columns show in which the heavy tokens hold zeros; pages
+// whose scales differ by 2^40 lose nothing to one another; and what a row does not see has no part in its bits.  (With
+// the largest scale at 2^15 instead, a light or unseen token of a page 2^40 larger left nothing of the others.)  Sums,
+// maxima and the accumulators are fp32.
 //
 // Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 86-88 us
 // for 471 MB, 5.4 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 147-149 us for 910 MB, 6.1 TB/s (copy:
@@ -54,7 +59,11 @@ namespace cpattn {
 namespace kvattn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPScale = 32768.0f;  // largest P operand
+constexpr int kPExp = 15;            // P operands are below 2^(kPExp + kTop) = 65490 and f16's largest is 65504
+constexpr float kTop = 0.999f;       // largest s + log2 vs - base - m
+constexpr float kNear = 40.0f;       // largest |log2 vs - base| but for base = kFarBase
+constexpr int kFarBase = 40;
+constexpr float kNoBase = -10000.0f;
 constexpr int kSetup = 1;            // what an item costs besides its granules
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -506,13 +515,14 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   float fac[NT][2], m[NT][2], l[NT][2];
   int lim[NT][2];
   float acc[NT][kMt][4];
-  float v_ref = 1e-37f;  // largest V scale so far: P is held relative to it
-  float inv_ref = 0.0f;  // kPScale / v_ref
+  float b_off = kNoBase;  // -127 - base, a whole number
+  float b_unit = 0.0f;    // 2^(kPExp - base)
+  bool second = false;    // the granule at hand wants a second pass, see granule
   int lim_min = 0, lim_max = 0;
   int live = NT;         // tiles that have rows
   int row_q = 0;         // first query row (token row * group + head in group) of the block
   float* const aside = p.aside + worker * (RT * D);
-  float m_aside[NT][2], v_aside = 0.0f;  // what the values put aside refer to
+  float m_aside[NT][2] = {};  // what the values put aside refer to
   bool flushed = false;
   int since = 0;         // granules since then
   constexpr bool kHold = S::kHold;
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if (lim[n][r] < 0) lim[n][r] = lim_max;  // rows of nobody must not make the tile a masked one
-    v_ref = 1e-37f;
+    b_off = kNoBase;
     flushed = false;
     since = 0;
     if constexpr (kHold) {
@@ -650,6 +660,27 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     __syncwarp();
   };
 
+  // Another base.  A weight p_ij = 2^(s_ij - m_i) is as far from 1 as its page's scale from base, and fp32 holds
+  // 2^-126 to 2^127.  With base within 2^40 of all scales the heaviest weight is above 2^-41, far above what is lost.
+  // Otherwise base is kFarBase: a cache's scales are 2^-64 to 2^120, so the heaviest is between 2^-81 and 2^105
+  // whatever the scales are, and what is lost is below 2^-45 of it.
+  auto rebase = [&](int to) {
+    const float off = -127.0f - static_cast<float>(to);
+    if (b_off != kNoBase) {
+      const int by = static_cast<int>(b_off - off);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          m[n][r] -= static_cast<float>(by);
+          m_aside[n][r] -= static_cast<float>(by);
+          l[n][r] *= kv::pow2(by);
+        }
+    }
+    b_off = off;
+    b_unit = kv::pow2(kPExp - to);
+  };
+
   // One granule; masked: some of its keys are not seen by some row.  Masks and tiles without rows are uniform
   // branches and predicates, not variants: with four variants a warp's items of a few granules ran at the
   // speed of the instruction cache (62 x 16 items of some 3 granules, up to 60 rows, D = 64: 86 us, more than half
@@ -674,7 +705,42 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       // a value scale that is not finite comes in by the scores, which rows that do not see it leave out
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
-        if (!(vs[i] < INFINITY)) ks[i] = __int_as_float(0x7fffffff), vs[i] = 1e-37f;
+        if (!(fabsf(vs[i]) < INFINITY)) ks[i] = __int_as_float(0x7fffffff), vs[i] = 1.0f;
+      // steps that no row sees have no part in the choice of base (some row sees the first)
+#pragma unroll
+      for (int i = 1; i < kSteps; ++i)
+        if (key0 + 16 * i >= lim_max) vs[i] = vs[0];
+    }
+    // log2 of the steps' V scales, rounded up, less base
+    auto exponent = [](float x) { return static_cast<int>((__float_as_uint(x) + 0x7fffffu) & 0x7f800000u); };
+    float ve[kSteps];
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      ve[i] = fmaf(static_cast<float>(exponent(vs[i])), 0x1p-23f, b_off);
+      far |= fabsf(ve[i]) > kNear;
+    }
+    unsigned skip = 0u;  // steps that are left out
+    if (far) {
+      if (b_off == kNoBase) rebase(max((exponent(vs[0]) >> 23) - 127, -64));
+      unsigned away = 0u;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        away |= (fabsf(fmaf(static_cast<float>(exponent(vs[i])), 0x1p-23f, b_off)) > kNear ? 1u : 0u) << i;
+      // Where some rows do not see the far pages these are taken in a pass of their own, after the others, so that those
+      // rows keep their bits: no later key is one that they see.
+      if (b_off == -127.0f - kFarBase || away == 0u) {
+      } else if (masked && !second) {
+        skip = away;
+        second = true;
+      } else {
+        skip = second ? ~away : 0u;
+        second = false;
+        rebase(kFarBase);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        ve[i] = fmaxf(fmaf(static_cast<float>(exponent(vs[i])), 0x1p-23f, b_off), 63.0f + b_off);
     }
     // S^T: s[n][i][2 u + r] is key key_at(u, gid) of step i for query row 2 tig + r of tile n
     float s[NT][kSteps][4];
@@ -712,7 +778,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       }
     }
     // Maxima.  s keeps the products; a score is s * f2 (f2 > 0), and only masked tiles, where an unseen
-    // page's scale may be anything, hold scores themselves.
+    // page's scale may be anything, hold scores themselves.  m moves by whole numbers: rescaling is exact, and rare.
     float corr[NT][2], f2[NT][2][kSteps];
     bool grew = false;
 #pragma unroll
@@ -731,7 +797,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               float& z = s[n][i][2 * u + r];
-              z = key0 + 16 * i + key_at(u, gid) >= lim[n][r] ? -INFINITY : z * f2[n][r][i];
+              z = (skip >> i & 1u) || key0 + 16 * i + key_at(u, gid) >= lim[n][r] ? -INFINITY : z * f2[n][r][i];
             }
             f2[n][r][i] = 1.0f;
           }
@@ -742,28 +808,23 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
       for (int r = 0; r < 2; ++r) {
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) top = fmaxf(top, fmaxf(s[n][i][r], s[n][i][2 + r]) * f2[n][r][i]);
+        for (int i = 0; i < kSteps; ++i)
+          top = fmaxf(top, fmaf(fmaxf(s[n][i][r], s[n][i][2 + r]), f2[n][r][i], ve[i]));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-        const bool up = top > m[n][r];
+        const bool up = top - m[n][r] > kTop;  // false where both are -inf
         grew |= up;
-        const float now = up ? top : m[n][r];
-        corr[n][r] = now == -INFINITY ? 1.0f : ex2(m[n][r] - now);
+        const float now = up ? floorf(top + (1.0f - kTop)) : m[n][r];
+        corr[n][r] = up ? ex2(m[n][r] - now) : 1.0f;
         m[n][r] = now;
       }
-    float v_top = v_ref;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) v_top = fmaxf(v_top, vs[i]);
-    if (__any_sync(kFull, grew || v_top > v_ref)) {
-      const float rr = v_ref / v_top;
-      v_ref = v_top;
-      inv_ref = kPScale / v_top;
+    if (__any_sync(kFull, grew)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        l[n][0] *= corr[n][0];
-        l[n][1] *= corr[n][1];
-        const float c0 = corr[n][0] * rr, c1 = corr[n][1] * rr;
+        const float c0 = corr[n][0], c1 = corr[n][1];
+        l[n][0] *= c0;
+        l[n][1] *= c1;
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
           acc[n][j][0] *= c0;
@@ -783,7 +844,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     uint32_t pb[NT][PP][kSteps][2];
     float vf[kSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) vf[i] = vs[i] * inv_ref;
+    for (int i = 0; i < kSteps; ++i) vf[i] = vs[i] * b_unit;
+    if (skip != 0u) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (skip >> i & 1u) vf[i] = 0.0f;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
@@ -852,6 +918,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
   };
 
+  // Weight of what was put aside of a row.
+  auto keep_of = [&](int n, int r) { return flushed ? ex2(m_aside[n][r] - m[n][r]) : 0.0f; };
+
   // Puts the accumulators aside: adds them to the others and clears them.
   auto to_workspace = [&]() {
 #pragma unroll
@@ -859,7 +928,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float* const at = aside + (n * 8 + 2 * tig + r) * D + gid * kCols;
-        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
+        const float keep = keep_of(n, r);
 #pragma unroll
         for (int j = 0; j < kCols / 4; ++j) {
           float x[4];
@@ -871,7 +940,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
       for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
     }
-    v_aside = v_ref;
     flushed = true;
   };
   auto flush = [&]() {
@@ -890,10 +958,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   };
 
   // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial at
-  // part_o [RT][D], part_ml [RT].
+  // part_o [RT][D], part_ml [RT], with l between 1 and 2.
   auto end_item = [&](bool whole, float* part_o, float2* part_ml) {
     const int n_rows = seq.rows * p.group;
-    const float back = v_ref * (1.0f / kPScale);
+    const int base = static_cast<int>(-127.0f - b_off);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -905,8 +973,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         const int local = n * 8 + 2 * tig + r;
         const int rho = row_q + local;
         if (rho >= n_rows) continue;
-        const float keep = flushed ? ex2(m_aside[n][r] - m[n][r]) * (v_aside / v_ref) : 0.0f;
-        const float f = whole ? (sum == 0.0f ? 0.0f : back / sum) : back;
+        const float keep = keep_of(n, r);
+        const int up = min(max(static_cast<int>(__float_as_uint(sum) >> 23 & 255u) - 127, -100), 126);
+        const float norm = sum * kv::pow2(-up), ref = m[n][r] + static_cast<float>(up);
+        const float back = kv::pow2(min(max(base - kPExp - up, -126), 127));
+        const float f = whole ? (sum == 0.0f ? 0.0f : back / norm) : back;
         float* const part = part_o + local * D + gid * kCols;
         const int t = rho / p.group;
         const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
@@ -918,8 +989,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
           else *reinterpret_cast<float4*>(part + 4 * j) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
         }
         if (gid == 0) {
-          if (whole) p.lse[out] = sum == 0.0f ? -INFINITY : (m[n][r] + log2f(sum)) * kLn2;
-          else part_ml[local] = make_float2(m[n][r], sum);
+          if (whole) p.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(norm)) * kLn2;
+          else part_ml[local] = make_float2(sum == 0.0f ? -INFINITY : ref, norm);
         }
       }
   };
@@ -944,7 +1015,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         break;
       }
       const int key0 = c.g * kKeys;
-      if (key0 < lim_max) granule(st, key0 + kKeys > lim_min);
+      if (key0 < lim_max) {
+        granule(st, key0 + kKeys > lim_min);
+        if (second) continue;
+      }
       __syncwarp();
       if (to_issue > 0) issue(st);
       else --in_flight;

@@ -488,6 +488,10 @@ cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, voi
  *                    reports bad pages (cp_kv_rows)
  * A row that sees no token gets O = 0, LSE = -inf.  What unseen places hold (the rest of a page,
  * tokens behind a row's position), NaN among it, has no influence.
+ * Precision: sums and softmax statistics are fp32.  Queries are taken exactly (bf16) or to 22 bits (fp32), but no finer
+ * than 2^-38 of their row's largest element.  Weights are taken to 11 bits for a bf16 output and to 22 for an fp32 one;
+ * a token's weight times its page's V scale no finer than 2^-39 of the row's largest such product.  A weight below 2^-45
+ * of the row's largest may count as zero.
  * Rows of a sequence beyond a few dozen (long prompts) are answered, but cp_kv_cache_read followed
  * by cp_partial_attn is the faster way for them.
  * max_pages * page_size is at most 2e9, n_rows * hq below 2^31.

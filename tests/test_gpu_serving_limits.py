@@ -1,0 +1,127 @@
+"""The serving calls at the ends of what they accept: scales far apart, unseen contents, bad arrays,
+several host threads, and the kernels that small calls do not reach.  Against the float64 oracle,
+with the tolerances of the other serving tests unless one is derived here.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import helpers
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    helpers.ensure_built()
+
+import context_blockwise_attention_gb300 as cpa  # noqa: E402
+from test_gpu_serving import BF16, DEV, F32, Pool, _i32  # noqa: E402
+
+
+def _table(pool, path, q, rows):
+    """The page table of ``pool``, as wide as lets a call of ``rows`` rows of one sequence take ``path``: one block a KV
+    head; a cluster of blocks, which begins at more than two granules of 4096 / d tokens for each of a block's warps;
+    or the work split over all SMs, which alone needs a workspace."""
+    tiles = 1 if rows * q.shape[1] // pool.hkv <= 8 else 2
+    parts = 2 if q.dtype == F32 else 1
+    warps = 8 if tiles * pool.d >= 256 or tiles * parts >= 4 else 12
+    width = {"one": 0, "cluster": -(-(2 * warps + 1) * 4096 // (pool.d * pool.page)), "split": 2500}[path]
+    table = pool.table
+    if width > table.shape[1]:
+        table = np.concatenate([table, np.full((table.shape[0], width - table.shape[1]), -1)], 1)
+    for out in (BF16, F32):
+        need = cpa.kv_cache_attn_workspace(pool.device(), rows, q.shape[1], 1, table.shape[1], q.dtype, out)
+        assert (need > 0) == (path == "split")
+    return _i32(table)
+
+
+def _check_row(o, lse, q, k, v, v_scale, scale, dout, far=0.0):
+    """One row's output against softmax(scale k q) v.
+
+    As in the other tests, but for the last term of the tolerance: a contribution, weight times scale of the
+    page, is held as f16 with the row's largest at 2^15 to 2^16, and f16 has no step below 2^-24, so it is off by up to
+    2^-25 2^-15 = 2^-40 of the largest.  ``v_scale`` is the scale of each token's page; ``far`` is added to the
+    relative errors of the sums of weights."""
+    s = scale * (k @ q)
+    delta = float((2.0 ** -20 * scale * (np.abs(k) @ np.abs(q)) + 2.0 ** -22 * np.abs(s)).max())
+    p = np.exp(s - s.max())
+    z = p.sum()
+    ref, ref_l = p @ v / z, s.max() + np.log(z)
+    w = (2.0 ** -11 if dout == BF16 else 2.0 ** -21) + far
+    tol = p @ np.abs(v) / z * (2 * delta + w + s.size * 2.0 ** -27 + 2.0 ** -20)
+    tol = tol + 1.001 * 2.0 ** -40 * (p * v_scale).max() * (np.abs(v) / v_scale[:, None]).sum(0) / z
+    tol = tol + np.abs(ref) * (2.0 ** -8 if dout == BF16 else 2.0 ** -24) * 1.01 + 1e-30
+    err = np.abs(o.double().cpu().numpy() - ref)
+    assert np.all(err <= tol), (float((err / tol).max()), float(err.max()))
+    assert abs(float(lse) - ref_l) <= delta + s.size * 2.0 ** -24 + 2.0 ** -22 * abs(ref_l) + 2.0 ** -20 + far
+
+
+# ------------------------------------------------------------------ value scales
+@pytest.mark.parametrize("path,d,page,g", [
+    (path, *x) for path in ("one", "cluster", "split") for x in ((64, 16, 1), (64, 32, 3), (128, 16, 2), (128, 16, 5))
+] + [(path, *x) for path in ("one", "split") for x in ((64, 16, 6), (128, 16, 16))])
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_value_scales_of_unseen_pages_have_no_influence(dout, path, d, page, g):
+    """Two pages in one granule: the second, which only the last row sees, is up to 2^100 larger."""
+    held, rows = [page * 5 + 1], 3
+    pool = Pool(1, held, page, 1, d, 201)
+    pool.fill(held, 202)
+    q = torch.randn((rows, g, d), generator=torch.Generator().manual_seed(203)).to(BF16)
+    table = _table(pool, path, q, rows)
+    first = _i32([page * 5 - 2])  # positions page * 5 - 2, - 1 and page * 5: the last row sees the last page's one token
+    args = (_i32([0, rows]), _i32(held), table)
+    clean = cpa.kv_cache_attn(q.to(DEV), pool.device(), *args, q_first=first, o_dtype=dout)
+    last = pool.table[0, 5]
+    was = float(pool.scale[1][last, 0])
+    for up in (1, 6, 30, 45, 100):
+        pool.scale[1][last] = was * 2.0 ** up
+        o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), *args, q_first=first, o_dtype=dout)
+        assert torch.equal(o[:2], clean[0][:2]) and torch.equal(lse[:2], clean[1][:2]), up
+        k, v = pool.tokens_of(0, held[0])
+        scales = np.repeat(pool.scale[1][pool.table[0], 0].astype(np.float64), page)[:held[0]]
+        for i in range(rows):
+            n = page * 5 - 1 + i
+            for h in range(g):
+                _check_row(o[i, h], lse[i, h], q[i, h].double().numpy(), k[:n, 0], v[:n, 0], scales[:n], d ** -0.5, dout,
+                           0.0 if up < 10 else 2.0 ** -19 if up < 50 else 2.0 ** -18)
+
+
+# bits by which the far page's scores are below the others', exponents of the values of the ordinary and of the far pages
+APART = [(20, 0, 40), (60, 0, 40), (86, 0, 40), (10, 0, 100), (60, 0, 100), (110, 0, 100), (20, -55, 30), (70, -55, 60),
+         (100, -60, 105), (5, -60, 105), (3, 60, -40), (200, 0, 60)]
+
+
+@pytest.mark.parametrize("path", ["one", "cluster", "split"])
+@pytest.mark.parametrize("d,page,din", [(64, 16, BF16), (64, 128, F32), (128, 16, F32), (128, 64, BF16)])
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_value_scales_far_apart(dout, d, page, din, path):
+    """Light tokens in pages of far larger values, and heavy ones in pages of far smaller ones.
+
+    A weight's exponent holds the difference of the scales' exponents: up to 64, half a step of which is 2^-19, or up to
+    128 with 2^-18; times ln 2 the relative errors of the weight are below that."""
+    tokens, g = 5 * page, 5
+    rng = np.random.default_rng(211)
+    u = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    q = (u * (1 + rng.integers(0, 8, (2, g, d)) / 8)).astype(np.float64)  # a positive multiple of u, roughly
+    qt = torch.from_numpy(q).to(din)
+    for bits, low, high in APART:
+        pool = Pool(1, [tokens], page, 1, d, 212)
+        v = rng.standard_normal((tokens, 1, d))
+        k = np.zeros((tokens, 1, d))
+        far = np.zeros(tokens, bool)
+        far[page:2 * page] = far[4 * page:] = True
+        near = 0.5 * rng.standard_normal((tokens, d))
+        # q . u is about 1.44 d, so that a key of -a u has a score of about -1.44 a d / sqrt(d) nats
+        k[:, 0] = np.where(far[:, None], -bits * np.log(2.0) / (1.44 * d ** 0.5) * u, near)
+        v *= 2.0 ** np.where(far, high, low)[:, None, None]
+        for which, x in ((0, k), (1, v)):
+            oc.cache_write(pool.bytes[which], pool.scale[which], x, [0, tokens], [0], pool.table)
+        o, lse = cpa.kv_cache_attn(qt.to(DEV), pool.device(), _i32([0, 2]), _i32([tokens]),
+                                   _table(pool, path, qt, 2), o_dtype=dout)
+        kk, vv = pool.tokens_of(0, tokens)
+        scales = np.repeat(pool.scale[1][pool.table[0], 0].astype(np.float64), page)
+        for i in range(2):
+            for h in range(g):
+                _check_row(o[i, h], lse[i, h], qt[i, h].double().numpy(), kk[:, 0], vv[:, 0], scales, d ** -0.5, dout,
+                           2.0 ** -18 if abs(high - low) > 50 else 2.0 ** -19)
