@@ -918,8 +918,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
   };
 
-  // Weight of what was put aside of a row.
-  auto keep_of = [&](int n, int r) { return flushed ? ex2(m_aside[n][r] - m[n][r]) : 0.0f; };
+  // Weight of what was put aside of a row (zeros where it had seen nothing).
+  auto keep_of = [&](int n, int r) {
+    return flushed && m_aside[n][r] != -INFINITY ? ex2(m_aside[n][r] - m[n][r]) : 0.0f;
+  };
 
   // Puts the accumulators aside: adds them to the others and clears them.
   auto to_workspace = [&]() {

@@ -125,3 +125,31 @@ def test_value_scales_far_apart(dout, d, page, din, path):
             for h in range(g):
                 _check_row(o[i, h], lse[i, h], qt[i, h].double().numpy(), kk[:, 0], vv[:, 0], scales, d ** -0.5, dout,
                            2.0 ** -18 if abs(high - low) > 50 else 2.0 ** -19)
+
+
+@pytest.mark.parametrize("d,page,dout", [(128, 128, F32), (128, 64, BF16), (64, 128, F32)])
+def test_long_runs_of_weights_of_zero(d, page, dout):
+    """Scores of -inf (an infinite key scale against negative products) for longer than the sums are held before they
+    are put aside: they weigh nothing."""
+    pool = Pool(1, [2 * page], page, 1, d, 221)
+    rng = np.random.default_rng(222)
+    u = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    q = torch.from_numpy(u * (1 + rng.integers(0, 8, (2, 3, d)) / 8)).to(BF16)
+    k, v = rng.standard_normal((2 * page, 1, d)), rng.standard_normal((2 * page, 1, d))
+    k[:page] = -u
+    for which, x in ((0, k), (1, v)):
+        oc.cache_write(pool.bytes[which], pool.scale[which], x, [0, 2 * page], [0], pool.table)
+    bad, good = pool.table[0]
+    pool.scale[0][bad] = np.inf
+    run, repeats = 40 * 512 // page, 24  # runs of 20480 tokens; some hundred granules for each worker
+    table = np.tile(np.concatenate([np.full(run, bad), np.full(run, good)]), repeats * 10)[None]
+    o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), _i32([0, 2]), _i32([table.size * page]), _i32(table), o_dtype=dout)
+    pool.scale[0][bad] = 1.0
+    kk, vv = pool.tokens_of(0, 2 * page)
+    kk, vv = kk[page:, 0], vv[page:, 0]
+    scales = np.full(page, float(pool.scale[1][good, 0]))
+    for i in range(2):
+        for h in range(3):
+            # the tokens of the good page over and over: LSE grows by ln(repeats); 256 or 64 truncated sums of 2^-23
+            _check_row(o[i, h], float(lse[i, h]) - np.log(table.size / 2), q[i, h].double().numpy(), kk, vv, scales, d ** -0.5,
+                       dout, (256 if dout == BF16 else 64) * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -22 * 20)
