@@ -1428,12 +1428,14 @@ template <int D, int NT, int QP, int PP>
 cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUtensorMap& mv, int64_t items,
               int num_sms, cudaStream_t s) {
   using S = Shape<D, NT, QP, PP>;
-  static_assert(1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8 <= 232448, "shared memory of a block");
+  constexpr int most_smem = 1024 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8;
+  static_assert(most_smem <= 232448, "shared memory of a block");
   const int smem = 1024 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
   const auto kernel = !pl.solo           ? kv_attn_kernel<D, NT, QP, PP, 0>
                       : pl.cluster == 1 ? kv_attn_kernel<D, NT, QP, PP, 1>
                                         : kv_attn_kernel<D, NT, QP, PP, 2>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit is the function's, not the call's: always the same, for other host threads launch the kernel too.
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel attribute");
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2]{};

@@ -3,6 +3,8 @@ several host threads, and the kernels that small calls do not reach.  Against th
 with the tolerances of the other serving tests unless one is derived here.
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -153,3 +155,43 @@ def test_long_runs_of_weights_of_zero(d, page, dout):
             # the tokens of the good page over and over: LSE grows by ln(repeats); 256 or 64 truncated sums of 2^-23
             _check_row(o[i, h], float(lse[i, h]) - np.log(table.size / 2), q[i, h].double().numpy(), kk, vv, scales, d ** -0.5,
                        dout, (256 if dout == BF16 else 64) * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -22 * 20)
+
+
+# ------------------------------------------------------------------ calls at once
+def test_host_threads_with_one_and_with_many_sequences():
+    """Calls of one kernel from two host threads, whose blocks take different amounts of shared memory."""
+    errors, start = [], threading.Barrier(2)
+
+    def run(seqs):
+        try:
+            held = [40 + i % 3 for i in range(seqs)]
+            pool = Pool(seqs, held, 16, 1, 64, 231)
+            pool.fill(held[:1], 232)
+            for w in range(2):  # the same page for every sequence
+                pool.bytes[w][:] = pool.bytes[w][pool.table[0, 0]]
+                pool.scale[w][:] = pool.scale[w][pool.table[0, 0]]
+            cache = pool.device()
+            table = torch.cat([_i32(pool.table), _i32(np.full((seqs, 2500), -1))], 1)
+            q = torch.randn((seqs, 4, 64), generator=torch.Generator().manual_seed(233)).to(BF16).to(DEV)
+            args = (q, cache, _i32(range(seqs + 1)), _i32(held), table)
+            out = torch.empty((seqs, 4, 64), device=DEV), torch.empty((seqs, 4), device=DEV)
+            ws = torch.empty(max(1, cpa.kv_cache_attn_workspace(cache, seqs, 4, seqs, table.shape[1])), dtype=torch.uint8,
+                             device=DEV)
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            want = cpa.kv_cache_attn(*args, stream=stream)
+            stream.synchronize()
+            start.wait()
+            for _ in range(3000):
+                cpa.kv_cache_attn(*args, o=out[0], lse=out[1], workspace=ws, stream=stream)
+            stream.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+        except BaseException as e:  # noqa: B036 -- shown by the main thread
+            errors.append(e)
+            start.abort()
+    threads = [threading.Thread(target=run, args=(n,)) for n in (1, cpa.KV_MAX_SEQS)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
