@@ -3,6 +3,7 @@ several host threads, and the kernels that small calls do not reach.  Against th
 with the tolerances of the other serving tests unless one is derived here.
 """
 
+import ctypes
 import threading
 
 import numpy as np
@@ -18,6 +19,7 @@ if torch.cuda.is_available():
     helpers.ensure_built()
 
 import context_blockwise_attention_gb300 as cpa  # noqa: E402
+from context_blockwise_attention_gb300 import api  # noqa: E402
 from test_gpu_serving import BF16, DEV, F32, Pool, _i32  # noqa: E402
 
 
@@ -160,7 +162,7 @@ def test_long_runs_of_weights_of_zero(d, page, dout):
 # ------------------------------------------------------------------ calls at once
 def test_host_threads_with_one_and_with_many_sequences():
     """Calls of one kernel from two host threads, whose blocks take different amounts of shared memory."""
-    errors, start = [], threading.Barrier(2)
+    errors, start, call = [], threading.Barrier(2), cpa.load_library().cp_kv_cache_attn
 
     def run(seqs):
         try:
@@ -181,9 +183,18 @@ def test_host_threads_with_one_and_with_many_sequences():
             stream.wait_stream(torch.cuda.current_stream())
             want = cpa.kv_cache_attn(*args, stream=stream)
             stream.synchronize()
+            d = api._KvAttnDesc()  # the C call alone, so that most of a thread's time is spent in it
+            d.cache = api._KvCache(*(x.data_ptr() for x in cache), cache.k.shape[0], 16, 1, 64, 0)
+            d.rows = api._KvRows(args[2].data_ptr(), args[3].data_ptr(), table.data_ptr(), seqs, table.shape[1], seqs)
+            d.q, d.o, d.lse, d.workspace = (x.data_ptr() for x in (q, *out, ws))
+            d.workspace_bytes, d.in_dtype, d.o_dtype, d.hq = ws.numel(), api.CP_BF16, api.CP_F32, 4
+            d.kv_pos = api._PosMap(0, 1)
+            desc, raw = ctypes.byref(d), ctypes.c_void_p(stream.cuda_stream)
             start.wait()
-            for _ in range(3000):
-                cpa.kv_cache_attn(*args, o=out[0], lse=out[1], workspace=ws, stream=stream)
+            for i in range(20000):
+                assert call(desc, raw) == api.CP_OK, (seqs, i, cpa.load_library().cp_last_error())
+                if i % 200 == 0:
+                    stream.synchronize()
             stream.synchronize()
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
         except BaseException as e:  # noqa: B036 -- shown by the main thread
