@@ -125,7 +125,7 @@ struct Seq {
   int64_t r0;      // first row
   int64_t pos0;    // position of its first row
   int32_t rows;
-  int32_t tokens;  // cached tokens, as far as the page table reaches
+  int32_t tokens;  // cached tokens; of those behind the page table one, which has a bad page, stands for all
   int32_t keys;    // tokens that its last row sees
   int32_t gpi;     // granules of an item
   int32_t blocks;  // blocks of RT query rows; 0 where no row sees a token
@@ -150,7 +150,7 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   int64_t t = __ldg(p.rows.tokens + b);
   const int64_t room = static_cast<int64_t>(p.rows.max_pages) << p.page_log2;
   s.over = t > room;
-  if (s.over) t = room;
+  if (s.over) t = room + 1;
   s.tokens = t < 0 ? 0 : static_cast<int32_t>(t);
   s.pos0 = p.q_first != nullptr ? __ldg(p.q_first + b) : 0;
   s.keys = s.rows > 0 ? visible(p, s.tokens, s.pos0 + s.rows - 1) : 0;
@@ -393,7 +393,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   Cursor f = c;  // where the copies are
   int64_t to_issue = left;
   int f_keys = seq.keys;
-  int f_last = seq.over ? p.rows.max_pages - 1 : -1;  // a page that counts as bad
   int window = -32;        // lane i holds page window + i of sequence f.b
   int pages = -1;
 
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     if (static_cast<unsigned>(ord - window) >= 32u) {
       window = ord;
       const int64_t id = kv::page_at(p.rows, p.n_pages, f.b, ord + lane);
-      pages = id < 0 || ord + lane == f_last ? -1 : static_cast<int>(id);
+      pages = static_cast<int>(id);
     }
     return __shfl_sync(kFull, pages, ord - window);
   };
@@ -471,7 +470,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
           Seq s{};
           next_seq<D, RT>(p, f, s);
           f_keys = s.keys;
-          f_last = s.over ? p.rows.max_pages - 1 : -1;
           window = -32;
         }
       }

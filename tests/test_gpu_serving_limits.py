@@ -206,3 +206,39 @@ def test_host_threads_with_one_and_with_many_sequences():
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+# ------------------------------------------------------------------ counts and row starts that break the rules
+@pytest.mark.parametrize("path", ["one", "cluster", "split"])
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 128), (128, 32)])
+def test_more_tokens_than_the_table_has_pages_for(d, page, path):
+    """Rows that see tokens behind the table are NaN, those that end within it are as without the excess."""
+    pool = Pool(1, [6 * page], page, 1, d, 241)
+    pool.fill([6 * page], 242)
+    rows, g = 4, 2
+    q = torch.randn((rows, g, d), generator=torch.Generator().manual_seed(243)).to(BF16)
+    table = _table(pool, path, q, rows)
+    if path != "one":  # a full table: the same pages again
+        table = _i32(np.resize(pool.table, (1, table.shape[1])))
+    room = table.shape[1] * page
+    # two orders of the sums: twice each one's error, (2 delta + 2^-20 + n 2^-27) max |v| and delta + n 2^-24 + 2^-19,
+    # with delta = 2^-20 sum |q k| / sqrt(d) at most
+    k, v = pool.tokens_of(0, 6 * page)
+    delta = 2.0 ** -20 * np.abs(k[:, 0]).sum(1).max() * float(q.abs().max()) * d ** -0.5
+    tol = 2 * (2 * delta + 2.0 ** -20 + room * 2.0 ** -27) * np.abs(v).max()
+    tol_l = 2 * (delta + room * 2.0 ** -24 + 2.0 ** -19)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for last in (room - 3, room - 2, room - 1, room, room + 2):  # position of the last row
+        first = _i32([last - rows + 1])
+        args = (q.to(DEV), pool.device(), _i32([0, rows]))
+        want, want_l = cpa.kv_cache_attn(*args, _i32([room]), table, q_first=first)
+        for count in (room + 1, room + 1000, 2 ** 31 - 1):
+            status.zero_()
+            o, lse = cpa.kv_cache_attn(*args, _i32([count]), table, q_first=first, status=status)
+            assert status.item() & 0xFF == api.CP_ERR_INVALID_ARG
+            fine = max(0, min(rows, rows - (last - room + 1)))
+            if last < room:  # the same shares of the work
+                assert torch.equal(o[:fine], want[:fine]) and torch.equal(lse[:fine], want_l[:fine])
+            else:
+                assert bool(((o - want).abs()[:fine] <= tol).all()) and bool(((lse - want_l).abs()[:fine] <= tol_l).all())
+            assert bool(want.isfinite().all()) and bool(o[fine:].isnan().all()) and bool(lse[fine:].isnan().all())
