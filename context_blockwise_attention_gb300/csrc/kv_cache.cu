@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const __grid_co
   const int sub = static_cast<int>(w - unit * (2u * hkv));
   const int which = sub & 1, head = sub >> 1;
   ptx::wait_dependencies();
+  if (w == 0) kv::check_rows(p.rows, p.status, lane, 32);
   PageSpan s;
   if (!span_of(p.rows, p.c.n_pages, P, unit, lane, s)) return;
   if (s.page < 0) {
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_co
   const int nth = p.pages > 1 ? tid / kTT / hkv : 0;  // page of the block; the same for a whole warp
   const uint32_t unit = blockIdx.x * p.pages + nth;
   ptx::wait_dependencies();
+  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   PageSpan s;
   bool some = nth < p.pages && unit < p.units && span_of(p.rows, p.c.n_pages, P, unit, lane, s);
   if (some && s.page < 0) {
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_kernel(const __
   const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
   const int col = tid % kCols * kV;
   ptx::wait_dependencies();
+  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   if (warp < 2) {  // the sequences of the block's first and last row
     const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
                            [&](int i) { return kv::row_at(p.rows, i); });
@@ -396,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(cons
   const float inv_heads = 1.0f / static_cast<float>(heads);
   const int col = tid % kCols * kV;
   ptx::wait_dependencies();
+  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   if (warp < 2) {  // the sequences of the block's first and last row
     const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
                            [&](int i) { return kv::row_at(p.rows, i); });

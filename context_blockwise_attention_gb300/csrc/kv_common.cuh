@@ -11,7 +11,7 @@ namespace cpattn {
 namespace kv {
 
 // Sites of the status word of the cache kernels (bits 8 and up).
-enum Site { kSitePage = 32, kSiteTokens = 33, kSiteWait = 34 };
+enum Site { kSitePage = 32, kSiteTokens = 33, kSiteWait = 34, kSiteRows = 35 };
 
 __device__ __forceinline__ void report(int32_t* status, int site) {
   if (status != nullptr) atomicCAS(status, 0, CP_ERR_INVALID_ARG | (site << 8));
@@ -21,6 +21,16 @@ __device__ __forceinline__ void report(int32_t* status, int site) {
 __device__ __forceinline__ int64_t row_at(const cp_kv_rows& r, int i) {
   const int64_t x = __ldg(r.row_start + i);
   return x < 0 ? 0 : (x > r.n_rows ? r.n_rows : x);
+}
+
+// Reports row starts and counts that break the rules: by the first block of a kernel, thread `tid` of `threads`.
+__device__ __forceinline__ void check_rows(const cp_kv_rows& r, int32_t* status, int tid, int threads) {
+  if (status == nullptr) return;
+  for (int b = tid; b < r.n_seqs; b += threads) {
+    const int from = __ldg(r.row_start + b), to = __ldg(r.row_start + b + 1);
+    if (from < 0 || to < from || to > r.n_rows) report(status, kSiteRows);
+    else if (from < to && __ldg(r.tokens + b) < 0) report(status, kSiteTokens);
+  }
 }
 
 // Page of `ord`-th page of sequence b, or -1 where the table does not reach or names no page.

@@ -424,10 +424,12 @@ typedef struct {
  *   row_start   int32 [n_seqs + 1], non-decreasing, values in [0, n_rows]
  *   tokens      int32 [n_seqs], >= 0; its meaning is given at each call
  *   page_table  int32 [n_seqs, max_pages]; entries that hold no token of the call are not read
- * Contents that break these rules are not followed out of bounds: the kernels clamp row_start,
- * skip the entries of a sequence that need a page outside [0, n_pages) or behind max_pages (the
- * attention answers NaN for the rows that see such a page), and record
- * CP_ERR_INVALID_ARG | (site << 8) in *status where a status word is given.
+ * Contents that break these rules are not followed out of bounds: the kernels clamp row_start (a
+ * sequence whose rows would end before they begin has none), take a negative count for a sequence
+ * without tokens (its rows are neither written to the cache nor read from it), skip the entries of
+ * a sequence that need a page outside [0, n_pages) or behind max_pages (the attention answers NaN
+ * for the rows that see such a page), and record CP_ERR_INVALID_ARG | (site << 8) in *status where
+ * a status word is given.  The tokens of a sequence without rows are not looked at.
  */
 typedef struct {
   const int32_t* row_start;

@@ -242,3 +242,43 @@ def test_more_tokens_than_the_table_has_pages_for(d, page, path):
             else:
                 assert bool(((o - want).abs()[:fine] <= tol).all()) and bool(((lse - want_l).abs()[:fine] <= tol_l).all())
             assert bool(want.isfinite().all()) and bool(o[fine:].isnan().all()) and bool(lse[fine:].isnan().all())
+
+
+@pytest.mark.parametrize("seqs", [2, 300])
+@pytest.mark.parametrize("path", ["one", "split"])
+@pytest.mark.parametrize("long_rows", [False, True])  # both kernels that write
+def test_bad_row_starts_and_counts_are_reported(seqs, path, long_rows):
+    page, hkv, d, n = 16, 6, 64, 128 if long_rows else 2
+    held = [3 + i % 5 for i in range(seqs)]
+    pool = Pool(seqs, [h + n for h in held], page, hkv, d, 251)
+    pool.fill([min(20, h + n) for h in held], 252)
+    cache = pool.device()
+    wide = 0 if path == "one" else 1500
+    table = _i32(np.concatenate([pool.table, np.full((seqs, wide), -1)], 1))
+    rows = n * seqs
+    x = torch.randn((rows, hkv, d), generator=torch.Generator().manual_seed(253)).to(BF16).to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    starts = n * np.arange(seqs + 1)
+
+    def reported(start, counts):
+        out = []
+        for call in (lambda: cpa.kv_cache_write(cache, x, x, _i32(start), _i32(counts), table, status=status),
+                     lambda: cpa.kv_cache_read(cache, _i32(start), _i32(counts), table, rows, status=status),
+                     lambda: cpa.kv_cache_attn(x, cache, _i32(start), _i32(counts), table, status=status)):
+            status.zero_()
+            call()
+            out.append(status.item())
+        return [s & 0xFF for s in out]
+    fine, bad = [0] * 3, [api.CP_ERR_INVALID_ARG] * 3
+    assert reported(starts, held) == fine
+    for at, value in ((0, -1), (seqs, rows + 1), (1, rows + 7), (seqs // 2, -5), (seqs, 0)):
+        start = starts.copy()
+        start[at] = value
+        assert reported(start, held) == bad, (at, value)
+    for at in (0, seqs - 1):
+        counts = list(held)
+        counts[at] = -1
+        assert reported(starts, counts) == bad, at
+        start = starts.copy()  # without rows it does not matter
+        start[at + 1:] -= n
+        assert reported(start, counts) == fine, at
