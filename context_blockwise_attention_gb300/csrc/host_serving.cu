@@ -102,6 +102,9 @@ CP_API cp_status cp_kv_cache_write(const cp_kv_cache* cache, const cp_kv_rows* r
   cp_status st = validate_copy("cp_kv_cache_write", cache, rows, k, v, in_dtype, status);
   if (st != CP_OK) return st;
   if (rows->n_rows == 0 || rows->n_seqs == 0) return CP_OK;
+  // units of work (page, head, K or V) are numbered in 32 bits
+  if ((rows->n_rows / cache->page_size + 2 * static_cast<int64_t>(rows->n_seqs)) * cache->hkv > INT32_MAX)
+    CP_INVALID("cp_kv_cache_write: (n_rows / page_size + 2 n_seqs) * hkv must stay below 2^31");
   int sms = 0;
   if ((st = require_sm103(nullptr, &sms)) != CP_OK) return st;
   return launch_kv_write(*cache, *rows, k, v, in_dtype == CP_BF16, status, sms, stream);

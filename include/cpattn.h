@@ -451,6 +451,7 @@ typedef struct {
  * scale, NaN stays NaN, and neither counts for the scale.  Numbers above 1.9375 * 2^127 read back
  * as infinity.
  * Two sequences of one call, or two overlapping calls, must not write the same page.
+ * (n_rows / page_size + 2 n_seqs) * hkv is below 2^31.
  * Arguments: k, v device [n_rows, hkv, d] (in_dtype CP_F32 or CP_BF16), 16-byte aligned; status
  * device int32 or NULL (see cp_kv_rows; the caller zeroes it).
  * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.

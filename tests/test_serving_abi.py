@@ -181,3 +181,15 @@ def test_oracle_rotation_is_a_rotation():
     q, k = rng.standard_normal((1, 1, 32)), rng.standard_normal((1, 1, 32))
     s = [np.sum(oc.rotate(q, [[p + 7]], f, (16,)) * oc.rotate(k, [[p]], f, (16,))) for p in (0, 5, 1000)]
     assert np.allclose(s, s[0], atol=1e-9)
+
+
+def test_write_refuses_more_units_than_it_can_number():
+    """(page, head, K or V) in 32 bits: with 2^20 heads and 2048 sequences of a token each they were numbered twice over."""
+    fn = cpa.load_library().cp_kv_cache_write
+
+    def call(hkv, seqs, rows):
+        return fn(ctypes.byref(_cache(n_pages=64, page_size=16, hkv=hkv, d=64)),
+                  ctypes.byref(_rows(n_seqs=seqs, n_rows=rows)), 0x8000, 0x8000, api.CP_BF16, None, None)
+    assert call(1 << 20, 2048, 1) == BAD and cpa.load_library().cp_last_error()
+    assert call(1 << 19, 2048, 1) == BAD
+    assert call(1 << 20, 2048, 0) == api.CP_OK  # nothing to do
