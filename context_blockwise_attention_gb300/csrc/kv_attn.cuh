@@ -394,14 +394,16 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   Cursor f = c;  // where the copies are
   int64_t to_issue = left;
   int f_keys = seq.keys;
-  int window = -32;        // lane i holds page window + i of sequence f.b
+  int window = -32;        // lane i holds page window + i of sequence f.b, -1 behind its keys
   int pages = -1;
 
   auto page_of = [&](int ord) -> int {
     if (static_cast<unsigned>(ord - window) >= 32u) {
       window = ord;
-      const int64_t id = kv::page_at(p.rows, p.n_pages, f.b, ord + lane);
-      pages = static_cast<int>(id);
+      // entries that hold no token are the caller's to change at any time: they are not read
+      pages = -1;
+      if ((ord + lane) << p.page_log2 < f_keys)
+        pages = static_cast<int>(kv::page_at(p.rows, p.n_pages, f.b, ord + lane));
     }
     return __shfl_sync(kFull, pages, ord - window);
   };
