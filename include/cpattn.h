@@ -450,7 +450,8 @@ typedef struct {
  * same places again changes nothing.  Rounding is to nearest even; infinities become +-448 *
  * scale, NaN stays NaN, and neither counts for the scale.  Numbers above 1.9375 * 2^127 read back
  * as infinity.
- * Two sequences of one call, or two overlapping calls, must not write the same page.
+ * No page may be written twice at once: by two sequences of a call, by two entries of one sequence's
+ * table, or by two overlapping calls.
  * (n_rows / page_size + 2 n_seqs) * hkv is below 2^31.
  * Arguments: k, v device [n_rows, hkv, d] (in_dtype CP_F32 or CP_BF16), 16-byte aligned; status
  * device int32 or NULL (see cp_kv_rows; the caller zeroes it).
