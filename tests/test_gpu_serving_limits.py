@@ -19,7 +19,8 @@ if torch.cuda.is_available():
     helpers.ensure_built()
 
 import context_blockwise_attention_gb300 as cpa  # noqa: E402
-from context_blockwise_attention_gb300 import api  # noqa: E402
+import test_gpu_serving as serving  # noqa: E402
+from context_blockwise_attention_gb300 import PosMap, api  # noqa: E402
 from test_gpu_serving import BF16, DEV, F32, Pool, _i32  # noqa: E402
 
 
@@ -282,3 +283,76 @@ def test_bad_row_starts_and_counts_are_reported(seqs, path, long_rows):
         start = starts.copy()  # without rows it does not matter
         start[at + 1:] -= n
         assert reported(start, counts) == fine, at
+
+
+# ------------------------------------------------------------------ kernels that small calls do not reach
+def _spread(total, seqs, seed):
+    cuts = np.sort(np.random.default_rng(seed).integers(0, total + 1, seqs - 1))
+    return [int(x) for x in np.diff(np.concatenate([[0], cuts, [total]]))]
+
+
+@pytest.mark.parametrize("total,seqs,page,hkv,d,dtype", [
+    # several heads a block in turn, the last turn not full; more than eight heads of a row; sequences without rows
+    (3500, 70, 64, 11, 128, BF16),
+    (3500, 60, 32, 16, 64, F32),
+    (3510, 30, 16, 16, 128, BF16),
+    (3500, 35, 128, 8, 128, F32),
+    (5200, 3, 32, 5, 128, BF16),
+    (6000, 4, 128, 9, 64, BF16),
+])
+def test_prompts_of_many_rows_are_exact(total, seqs, page, hkv, d, dtype):
+    held = [(37 * b) % 150 for b in range(seqs)]
+    serving.test_write_and_read_are_exact(_spread(total, seqs, 261), held, page, hkv, d, dtype)
+
+
+VARIANTS = [  # path, rows of each sequence, tokens of each, hq, hkv, d, in, out
+    ("split", [7, 5], [700, 90], 8, 2, 128, F32, F32),
+    ("split", [30, 1], [260, 500], 4, 2, 128, F32, BF16),
+    ("one", [3, 3], [400, 77], 8, 2, 128, F32, F32),
+    ("cluster", [3], [700], 4, 1, 128, F32, F32),
+    ("cluster", [1, 1], [800, 660], 24, 2, 128, F32, BF16),
+    ("split", [2, 6], [700, 90], 8, 2, 64, F32, F32),
+    ("split", [20, 9], [400, 333], 2, 1, 64, F32, BF16),
+    ("one", [2, 1], [300, 1000], 8, 4, 64, F32, F32),
+    ("one", [1, 1, 1], [300, 0, 1000], 40, 4, 64, F32, F32),
+    ("split", [17, 9], [300, 700], 8, 2, 64, BF16, F32),
+    ("split", [17, 9], [300, 700], 8, 2, 64, BF16, BF16),
+    ("cluster", [3], [1650], 12, 3, 64, BF16, F32),
+    ("cluster", [1], [1700], 12, 3, 64, BF16, BF16),
+    ("cluster", [3], [1700], 15, 3, 64, BF16, BF16),
+    ("cluster", [2], [1100], 8, 1, 64, F32, F32),
+]
+
+
+@pytest.mark.parametrize("path,rows,held,hq,hkv,d,din,dout", VARIANTS)
+def test_attention_variants(path, rows, held, hq, hkv, d, din, dout):
+    """One and two tiles of query rows, one and two parts of queries and weights, each way of sharing the work."""
+    pool = Pool(len(rows), held, 16, hkv, d, 271)
+    pool.fill(held, 272)
+    q = torch.randn((sum(rows), hq, d), generator=torch.Generator().manual_seed(273)).to(din)
+    wide = 3000 if path == "split" else 0
+    need = cpa.kv_cache_attn_workspace(pool.device(), sum(rows), hq, len(rows), pool.table.shape[1] + wide, din, dout)
+    assert (need > 0) == (path == "split")
+    first = [m - n for n, m in zip(rows, held)]
+    serving._check_attn(pool, pool.device(), q, rows, held, first, PosMap(0, 1), dout, wide=wide)
+    serving._check_attn(pool, pool.device(), q, rows, held, None, PosMap(0, 1), dout, wide=wide)
+
+
+@pytest.mark.parametrize("d,g,din,dout", [(64, 20, BF16, F32), (64, 20, BF16, BF16), (64, 20, F32, F32), (128, 14, BF16, F32),
+                                          (128, 14, BF16, BF16), (128, 14, F32, F32)])
+def test_two_tiles_of_rows_put_their_sums_aside(d, g, din, dout):
+    """Millions of cached tokens, the same pages over and over, for more rows than one tile: as in the test of very
+    long rows, the sums hold at most A = 256 (bf16 outputs) or 64 truncated accumulations of 2^-23."""
+    once, repeats, page = 1024, 4096, 128
+    pool = Pool(1, [once], page, 1, d, 281)
+    pool.fill([once], 282, spread=1.0)
+    q = torch.randn((2, g, d), generator=torch.Generator().manual_seed(283)).to(din)
+    o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), _i32([0, 2]), _i32([once * repeats]),
+                               _i32(np.tile(pool.table, (1, repeats))), o_dtype=dout)
+    k, v = pool.tokens_of(0, once)
+    scales = np.repeat(pool.scale[1][pool.table[0], 0].astype(np.float64), page)
+    acc = (256 if dout == BF16 else 64) * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -22 * np.log(repeats)
+    for i in range(2):
+        for h in range(g):
+            _check_row(o[i, h], float(lse[i, h]) - np.log(repeats), q[i, h].double().numpy(), k[:, 0], v[:, 0], scales,
+                       d ** -0.5, dout, acc)
