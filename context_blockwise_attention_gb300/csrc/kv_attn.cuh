@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     }
     // Maxima.  s keeps the products; a score is s * f2 (f2 > 0), and only masked tiles, where an unseen
     // page's scale may be anything, hold scores themselves.  m moves by whole numbers: rescaling is exact, and rare.
-    float corr[NT][2], f2[NT][2][kSteps];
+    float down[NT][2], f2[NT][2][kSteps];
     bool grew = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -817,15 +817,18 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
         const bool up = top - m[n][r] > kTop;  // false where both are -inf
         grew |= up;
         const float now = up ? floorf(top + (1.0f - kTop)) : m[n][r];
-        corr[n][r] = up ? ex2(m[n][r] - now) : 1.0f;
+        down[n][r] = up ? m[n][r] - now : 0.0f;
         m[n][r] = now;
       }
     if (__any_sync(kFull, grew)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float c0 = corr[n][0], c1 = corr[n][1];
-        l[n][0] *= c0;
-        l[n][1] *= c1;
+        const float c0 = ex2(down[n][0]), c1 = ex2(down[n][1]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // in two steps: between scales far apart m moves by up to 184
+          const float half = floorf(0.5f * fmaxf(down[n][r], -300.0f));
+          l[n][r] = l[n][r] * ex2(half) * ex2(fmaxf(down[n][r], -300.0f) - half);
+        }
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
           acc[n][j][0] *= c0;

@@ -132,6 +132,36 @@ def test_value_scales_far_apart(dout, d, page, din, path):
                            2.0 ** -18 if abs(high - low) > 50 else 2.0 ** -19)
 
 
+@pytest.mark.parametrize("repeats", [1, 4000])
+@pytest.mark.parametrize("d,page,din", [(64, 64, BF16), (64, 128, F32), (128, 32, F32), (128, 64, BF16)])
+@pytest.mark.parametrize("dout", [BF16, F32])
+def test_value_scales_far_apart_in_turn(dout, d, page, din, repeats):
+    """Pages of the two kinds by turns, each a granule or more, so that a warp meets them one after the other: a few of
+    them with one block, and the same ones over and over, hundreds to a warp, with the work split."""
+    granule, g = 4096 // d, 5
+    tokens = 24 * granule
+    rng = np.random.default_rng(214)
+    u = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    qt = torch.from_numpy(u * (1 + rng.integers(0, 8, (1, g, d)) / 8)).to(din)
+    for bits, low, high in APART:
+        pool = Pool(1, [tokens], page, 1, d, 215)
+        far = np.arange(tokens) // page % 2 == 1
+        k = np.where(far[:, None], -bits * np.log(2.0) / (1.44 * d ** 0.5) * u, 0.5 * rng.standard_normal((tokens, d)))[:, None]
+        v = rng.standard_normal((tokens, 1, d)) * 2.0 ** np.where(far, high, low)[:, None, None]
+        for which, x in ((0, k), (1, v)):
+            oc.cache_write(pool.bytes[which], pool.scale[which], x, [0, tokens], [0], pool.table)
+        o, lse = cpa.kv_cache_attn(qt.to(DEV), pool.device(), _i32([0, 1]), _i32([tokens * repeats]),
+                                   _i32(np.tile(pool.table, (1, repeats))), o_dtype=dout)
+        kk, vv = pool.tokens_of(0, tokens)
+        scales = np.repeat(pool.scale[1][pool.table[0], 0].astype(np.float64), page)
+        more = 2.0 ** -18 if abs(high - low) > 50 else 2.0 ** -19
+        if repeats > 1:  # as in the test of very long rows
+            more += (256 if dout == BF16 else 64) * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -22 * np.log(repeats)
+        for h in range(g):
+            _check_row(o[0, h], float(lse[0, h]) - np.log(repeats), qt[0, h].double().numpy(), kk[:, 0], vv[:, 0], scales,
+                       d ** -0.5, dout, more)
+
+
 @pytest.mark.parametrize("d,page,dout", [(128, 128, F32), (128, 64, BF16), (64, 128, F32)])
 def test_long_runs_of_weights_of_zero(d, page, dout):
     """Scores of -inf (an infinite key scale against negative products) for longer than the sums are held before they
