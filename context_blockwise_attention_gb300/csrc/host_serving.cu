@@ -107,6 +107,7 @@ CP_API cp_status cp_kv_cache_write(const cp_kv_cache* cache, const cp_kv_rows* r
     CP_INVALID("cp_kv_cache_write: (n_rows / page_size + 2 n_seqs) * hkv must stay below 2^31");
   int sms = 0;
   if ((st = require_sm103(nullptr, &sms)) != CP_OK) return st;
+  if (status != nullptr && (st = launch_kv_check(*rows, status, stream)) != CP_OK) return st;
   return launch_kv_write(*cache, *rows, k, v, in_dtype == CP_BF16, status, sms, stream);
 }
 
@@ -118,6 +119,7 @@ CP_API cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* ro
   if (rows->n_rows == 0 || rows->n_seqs == 0) return CP_OK;
   int sms = 0;
   if ((st = require_sm103(nullptr, &sms)) != CP_OK) return st;
+  if (status != nullptr && (st = launch_kv_check(*rows, status, stream)) != CP_OK) return st;
   return launch_kv_read(*cache, *rows, k, v, out_dtype == CP_BF16, status, sms, stream);
 }
 
@@ -162,6 +164,7 @@ CP_API cp_status cp_kv_cache_attn(const cp_kv_attn_desc* desc, cudaStream_t stre
                static_cast<long long>(d.workspace_bytes), static_cast<long long>(need));
   const float scale = d.scale > 0.0f ? d.scale : 1.0f / sqrtf(static_cast<float>(d.cache.d));
   const int64_t timeout_ns = static_cast<int64_t>(d.wait_timeout_ms > 0 ? d.wait_timeout_ms : 2000) * 1000000LL;
+  if (d.status != nullptr && (st = launch_kv_check(d.rows, d.status, stream)) != CP_OK) return st;
   return launch_kv_attn(d, scale, timeout_ns, sms, stream);
 }
 

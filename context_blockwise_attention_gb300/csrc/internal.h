@@ -76,6 +76,7 @@ struct ReshardArgs {
 cp_status launch_reshard(const ReshardArgs& a, int num_sms, cudaStream_t s);
 
 // 8-bit cache (n_rows and n_seqs > 0).
+cp_status launch_kv_check(const cp_kv_rows& rows, int32_t* status, cudaStream_t s);
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
                           int32_t* status, int num_sms, cudaStream_t s);
 cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,

@@ -317,7 +317,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
     ptx::fence_proxy_async_smem();
   }
   ptx::wait_dependencies();  // launched early: what was in the stream before is complete from here on
-  if (blockIdx.x == 0) kv::check_rows(p.rows, p.status, tid, S::kWarps * 32);
   const int n_seqs = p.rows.n_seqs;
   const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs

@@ -76,6 +76,17 @@ __device__ __forceinline__ void requantise4(uint8_t* q, float ratio) {
       kv::to_e4m3x2(a.x * ratio, a.y * ratio) | (kv::to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }
 
+// Reports row starts and counts that break the rules.  A launch of its own, where there is a status word to report to:
+// as the first block's task in the writing kernels it cost calls without one up to 16 % (other code for the copies).
+__global__ void __launch_bounds__(kThreads) kv_check_rows_kernel(const __grid_constant__ cp_kv_rows r, int32_t* status) {
+  ptx::wait_dependencies();
+  for (int b = threadIdx.x; b < r.n_seqs; b += kThreads) {
+    const int from = __ldg(r.row_start + b), to = __ldg(r.row_start + b + 1);
+    if (from < 0 || to < from || to > r.n_rows) kv::report(status, kv::kSiteRows);
+    else if (from < to && __ldg(r.tokens + b) < 0) kv::report(status, kv::kSiteTokens);
+  }
+}
+
 struct WriteParams {
   cp_kv_cache c;
   cp_kv_rows rows;
@@ -98,7 +109,6 @@ __global__ void __launch_bounds__(kThreads) kv_write_warp_kernel(const __grid_co
   const int sub = static_cast<int>(w - unit * (2u * hkv));
   const int which = sub & 1, head = sub >> 1;
   ptx::wait_dependencies();
-  if (w == 0) kv::check_rows(p.rows, p.status, lane, 32);
   PageSpan s;
   if (!span_of(p.rows, p.c.n_pages, P, unit, lane, s)) return;
   if (s.page < 0) {
@@ -217,7 +227,6 @@ __global__ void __launch_bounds__(kThreads) kv_write_tile_kernel(const __grid_co
   const int nth = p.pages > 1 ? tid / kTT / hkv : 0;  // page of the block; the same for a whole warp
   const uint32_t unit = blockIdx.x * p.pages + nth;
   ptx::wait_dependencies();
-  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   PageSpan s;
   bool some = nth < p.pages && unit < p.units && span_of(p.rows, p.c.n_pages, P, unit, lane, s);
   if (some && s.page < 0) {
@@ -313,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_kernel(const __
   const int h1 = h0 + p.heads < hkv ? h0 + p.heads : hkv;
   const int col = tid % kCols * kV;
   ptx::wait_dependencies();
-  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   if (warp < 2) {  // the sequences of the block's first and last row
     const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
                            [&](int i) { return kv::row_at(p.rows, i); });
@@ -399,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(cons
   const float inv_heads = 1.0f / static_cast<float>(heads);
   const int col = tid % kCols * kV;
   ptx::wait_dependencies();
-  if (blockIdx.x == 0 && blockIdx.y == 0) kv::check_rows(p.rows, p.status, tid, kThreads);
   if (warp < 2) {  // the sequences of the block's first and last row
     const int b = find_seq(p.rows.n_seqs, warp == 0 ? row0 : row_end - 1, lane,
                            [&](int i) { return kv::row_at(p.rows, i); });
@@ -479,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, kReadBlocks) kv_read_few_kernel(cons
   }
 }
 
-template <class K, class P>
-cp_status launch(K kernel, const P& p, int64_t bx, int64_t by, const char* what, cudaStream_t s) {
+template <class K, class... P>
+cp_status launch(K kernel, int64_t bx, int64_t by, const char* what, cudaStream_t s, const P&... p) {
   if (bx > 0x7fffffff || by > 65535) {
     set_error("%s: too many rows or heads", what);
     return CP_ERR_INVALID_ARG;
@@ -494,7 +501,7 @@ cp_status launch(K kernel, const P& p, int64_t bx, int64_t by, const char* what,
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by));
   cfg.blockDim = dim3(kThreads);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p...);
   return e == cudaSuccess ? CP_OK : cuda_fail(e, what);
 }
 
@@ -510,8 +517,8 @@ cp_status write_tiles(WriteParams& p, int num_sms, cudaStream_t s) {
   int32_t heads = heads_of(p.c.hkv, 2 * p.units, 8 * num_sms);
   p.heads = (heads + kTiles - 1) / kTiles * kTiles;
   p.pages = p.c.hkv < kTiles ? kTiles / p.c.hkv : 1;
-  return launch(kv_write_tile_kernel<D, P, T>, p, (p.units + p.pages - 1) / p.pages,
-                2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_write_tile_kernel launch", s);
+  return launch(kv_write_tile_kernel<D, P, T>, (p.units + p.pages - 1) / p.pages,
+                2 * ((p.c.hkv + p.heads - 1) / p.heads), "kv_write_tile_kernel launch", s, p);
 }
 template <int D, class T>
 cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
@@ -530,8 +537,8 @@ cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
   const bool few = p.rows.n_rows >= 8 * seqs && blocks <= 2 * num_sms;
   if (!long_rows && !few) {
     const int64_t warps = tiles;
-    return launch(kv_write_warp_kernel<D, T>, p, (warps + kThreads / 32 - 1) / (kThreads / 32), 1,
-                  "kv_write_warp_kernel launch", s);
+    return launch(kv_write_warp_kernel<D, T>, (warps + kThreads / 32 - 1) / (kThreads / 32), 1,
+                  "kv_write_warp_kernel launch", s, p);
   }
   switch (p.c.page_size) {
     case 16: return write_tiles<D, 16, T>(p, num_sms, s);
@@ -551,11 +558,15 @@ cp_status read(ReadParams& p, int num_sms, cudaStream_t s) {
   const int64_t bx = (p.rows.n_rows + p.per_block - 1) / p.per_block;
   p.heads = heads_of(p.c.hkv, 2 * bx, 4 * num_sms);
   const int64_t by = 2 * ((p.c.hkv + p.heads - 1) / p.heads);
-  return p.heads > 4 ? launch(kv_read_kernel<D, T>, p, bx, by, "kv_read_kernel launch", s)
-                     : launch(kv_read_few_kernel<D, T>, p, bx, by, "kv_read_few_kernel launch", s);
+  return p.heads > 4 ? launch(kv_read_kernel<D, T>, bx, by, "kv_read_kernel launch", s, p)
+                     : launch(kv_read_few_kernel<D, T>, bx, by, "kv_read_few_kernel launch", s, p);
 }
 
 }  // namespace
+
+cp_status launch_kv_check(const cp_kv_rows& rows, int32_t* status, cudaStream_t s) {
+  return launch(kv_check_rows_kernel, 1, 1, "kv_check_rows_kernel launch", s, rows, status);
+}
 
 cp_status launch_kv_write(const cp_kv_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
                           int32_t* status, int num_sms, cudaStream_t s) {

@@ -23,16 +23,6 @@ __device__ __forceinline__ int64_t row_at(const cp_kv_rows& r, int i) {
   return x < 0 ? 0 : (x > r.n_rows ? r.n_rows : x);
 }
 
-// Reports row starts and counts that break the rules: by the first block of a kernel, thread `tid` of `threads`.
-__device__ __forceinline__ void check_rows(const cp_kv_rows& r, int32_t* status, int tid, int threads) {
-  if (status == nullptr) return;
-  for (int b = tid; b < r.n_seqs; b += threads) {
-    const int from = __ldg(r.row_start + b), to = __ldg(r.row_start + b + 1);
-    if (from < 0 || to < from || to > r.n_rows) report(status, kSiteRows);
-    else if (from < to && __ldg(r.tokens + b) < 0) report(status, kSiteTokens);
-  }
-}
-
 // Page of `ord`-th page of sequence b, or -1 where the table does not reach or names no page.
 __device__ __forceinline__ int64_t page_at(const cp_kv_rows& r, int64_t n_pages, int b, int64_t ord) {
   if (ord < 0 || ord >= r.max_pages) return -1;
