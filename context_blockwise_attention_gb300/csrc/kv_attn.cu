@@ -25,14 +25,16 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
     r.rows = nt * 8;
     r.warps = nt * d.cache.d >= 256 || nt * r.qp >= 4 ? 8 : 12;
   };
-  // Solo, by the page table's width in granules: as many blocks an item as the SMs hold clusters of (12 to 15 of
-  // 8 blocks, 36 of 4), where a block's warps have some granules each (32/8 heads, D = 128: 1 x 1000 / 4000
-  // tokens 9.4 / 20.6 us with one block, 8.5 / 10.0 with 8; 4 x 4000 21.1, 11.9 with 4; 8 x 4000 21.1, 15.8 with 2;
-  // 1 x 500 7.4, 8.4 with 8), as long as splitting is slower, which uses all SMs but has a second kernel: 1 x 4000
-  // tokens 10.0 us against 12.8, 4 x 4000 11.9 / 16.6, 4 x 8000 16.0 / 20.0, 8 x 4000 15.8 / 18.6, one KV head of
-  // 4000 9.5 / 9.6, of 8000 11.8 / 10.7; 18 x 8 items of 2048 / 6144 tokens, one block each, 14.7 / 35.7 against
-  // 19.9 / 39.6.  One row a sequence, as far as can be told from their numbers, or few rows in all, since the
-  // blocks take an item's blocks of rows one after the other.
+  // Solo, by the page table's width in granules, which bounds the tokens, the one thing about them that is known here:
+  // as many blocks an item as the SMs hold clusters of (12 to 15 of 8 blocks, 36 of 4), where a block's warps have some
+  // granules each (32/8 heads, D = 128, tables as wide as the sequences: 1 x 1000 / 4000 tokens 9.3 / 21.3 us with one
+  // block, 8.2 / 9.8 with 8; 4 x 4000 21.5, 11.7 with 4; 8 x 4000 21.6, 15.9 with 2; 1 x 500 7.2, 8.0 with 8), as long as
+  // splitting is slower, which uses all SMs but has a second kernel: 1 x 4000 tokens 9.8 us against 12.4, 4 x 4000
+  // 11.7 / 16.2, 4 x 8000 16.2 / 19.4, 8 x 4000 15.9 / 18.1, one KV head of 4000 9.4 / 9.0, of 8000 11.6 / 10.1; 18 x 8
+  // items of 2048 / 6144 tokens, one block each, 13.8 / 40.1 against 21.1 / 47.5.  One row a sequence, as far as can be
+  // told from their numbers, or few rows in all, since the blocks take an item's blocks of rows one after the other.
+  // What it costs is short sequences under a wide table: 1 x 1000 tokens with a table for 8192 8.0 us, for 16384 and more
+  // 11.3; 4 x 2000 9.3 and 14.1; 16 x 2000 with a table for 2000 14.3, for 8192 and more 19.4.
   tiles(per <= 8 ? 1 : 2);
   const int64_t width = (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096;
   const int64_t solo_items = seqs * d.cache.hkv;
@@ -45,8 +47,8 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   const int64_t blocks = solo_items * r.cluster;
   // Of clusters the more granules a warp the more of the SMs they take, and fewer for several blocks of rows,
   // as the longest sequence can have and all have on average; a third less than equal lengths would bear, since
-  // splitting alone evens out different ones (28 x 0-7758 tokens, 4/2 heads, D = 64, 2 blocks an item: 18.8 us, split
-  // 15.4; 4 x 5027, 32/2 heads, D = 64, two blocks of rows: 15.0, split 12.9).
+  // splitting alone evens out different ones (28 x 0-7758 tokens, 4/2 heads, D = 64, 2 blocks an item: 15.3 us, split
+  // 14.1; 4 x 5027, 32/2 heads, D = 64, two blocks of rows: 18.3, split 13.8).
   const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
   const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
   const bool narrow = r.cluster > 1 ? (d.cache.d == 128 ? 20 : 28) * width * turns <= r.warps * r.cluster * blocks
@@ -61,10 +63,14 @@ Plan plan_of(const cp_kv_attn_desc& d, int sms) {
   }
   // Two tiles of rows at once halve the copies and conversions, at 8 warps an SM and with half of the work in vain
   // for items that end in the first.  One against two tiles, 12 x 8192-16384 tokens, us: D = 128, 8 KV heads (302 MB,
-  // more than the L2 cache keeps for the second block of rows), 16 rows 90 / 72, 24 rows 142 / 118, 32 rows 150 / 121;
-  // 4 KV heads, 16 rows 50 / 50, 24 rows 68 / 68, to fp32 74 / 84, 32 rows 79 / 72; different numbers of rows, 8 to
-  // 24 of 36 x 7334 tokens 33 / 35, 4 to 20 of 344 x 853 32 / 35; D = 64, 8 KV heads, 16 rows 47 / 52, 24 rows 64 / 73,
-  // 32 rows 79 / 76, to fp32 88 / 97, 64 rows 146 / 132.
+  // more than the L2 cache keeps for the second block of rows), 16 rows 90 / 73, 24 rows 143 / 120, 32 rows 151 / 123;
+  // 4 KV heads, 16 rows 49 / 50, 24 rows 68 / 69, to fp32 74 / 84, 32 rows 80 / 72; D = 64, 8 KV heads, 16 rows
+  // 48.5 / 48.6, 24 rows 65 / 70, 32 rows 82 / 73, to fp32 91 / 88, 64 rows 153 / 127; 30 x 239-719 tokens, 1-3 rows of
+  // 128/32 heads, 36 / 51; 52 x 0-1534, 64/8, 24 / 31.
+  // Where the rule is wrong: 16 rows whose keys are 150 MB and fit the L2 by this border (9 x 8567 tokens, 128/8, D = 128:
+  // 54.7 / 48.8), 50 requests of some tokens with 1-4 rows of 128/16 heads (D = 64, to fp32 18.3 / 16.0), and calls of many
+  // rows over very few tokens, which two tiles answer slowly (1 x 8 tokens, 11 rows of 128/16 heads, D = 64: 8.0 / 15.5;
+  // 55 x 64-192, 1-15 rows of 64/8, D = 128: 36 / 49).
   const int64_t table = seqs * d.rows.max_pages, pages = table < d.cache.n_pages ? table : d.cache.n_pages;
   const bool cached = pages * d.cache.hkv * d.cache.page_size * d.cache.d * 2 <= 160000000;
   tiles(per <= (d.cache.d == 64 ? 32 : cached ? 24 : 8) ? 1 : 2);

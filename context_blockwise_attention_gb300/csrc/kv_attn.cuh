@@ -43,11 +43,11 @@
 // the largest scale at 2^15 instead, a light or unseen token of a page 2^40 larger left nothing of the others.)  Sums,
 // maxima and the accumulators are fp32.
 //
-// Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 86-88 us
-// for 471 MB, 5.4 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 147-149 us for 910 MB, 6.1 TB/s (copy:
-// 6.8); 16 x 2-6 rows over 1000-20000 tokens, 32/8, D = 128: 102 us; one token over 1000, 32/8, D = 128: 8.2 us; 4 x
-// 2000: 9.7 us.  What is left of the long calls is 6 us until the first data are there for all, SMs that end up
-// to a tenth later than others, and 4 us of the second kernel.
+// Measured (GB300, calls back to back in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16: 85-86 us
+// for 471 MB, 5.5 TB/s; 8 x 90000-131072, 64/8, D = 64, fp32 partials: 147-149 us for 910 MB, 6.1 TB/s (copy:
+// 6.8); 16 x 2-6 rows over 1000-20000 tokens, 32/8, D = 128: 104 us; one token over 1000, 32/8, D = 128: 8.2 us; 4 x
+// 2000: 9.3 us (tables for 8192 tokens at most).  What is left of the long calls is 6 us until the first data are there
+// for all, SMs that end up to a tenth later than others, and 4 us of the second kernel.
 #pragma once
 
 #include "internal.h"
@@ -166,8 +166,8 @@ __device__ __forceinline__ int64_t numbers(const Params& p, const Seq& s) {
 __device__ __forceinline__ int64_t share(int64_t W, int64_t n, int64_t w) { return W * w / n; }
 __device__ __forceinline__ int64_t worker_of(int64_t W, int64_t n, int64_t x) { return ((x + 1) * n - 1) / W; }
 // Of `most` workers those that get a share: where an item would have more than some 128 partials, workers
-// of at least four numbers (1 x 131072 / 40000 / 4096 tokens, 8/1, 4/2, 8/1 heads: 23.3 / 17.2 / 9.7 us; always as
-// many as there are: 29.3 / 19.8 / 9.7; always four numbers: 24.1 / 17.5 / 13.1).
+// of at least four numbers (1 x 131072 / 40000 / 4096 tokens, 8/1, 4/2, 8/1 heads: 22.7 / 16.7 / 9.1 us; always as
+// many as there are: 29.7 / 19.4 / 9.0; always four numbers: 22.8 / 16.7 / 12.8).
 __device__ __forceinline__ int64_t workers(const Params& p, int64_t W, int64_t most) {
   const int64_t few = W < p.few ? W : p.few, some = W / 4 > few ? W / 4 : few;
   return some < most ? some : most;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
   // One granule; masked: some of its keys are not seen by some row.  Masks and tiles without rows are uniform
   // branches and predicates, not variants: with four variants a warp's items of a few granules ran at the
   // speed of the instruction cache (62 x 16 items of some 3 granules, up to 60 rows, D = 64: 86 us, more than half
-  // of the stalls; now 55, and 16-row items of 8192 tokens 102 against 106).
+  // of the stalls; 55 with one path, and 16-row items of 8192 tokens 102 against 106).
   auto granule = [&](int st, bool masked) {
     const uint32_t tile = ring + st * S::kStage;
     const int key0 = c.g * kKeys;
@@ -1187,7 +1187,7 @@ __device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, 
 
 // WPR warps for each (row, query head), each going over every WPR-th partial.  Most rows of short items were
 // finished by their worker: a warp of its own looks 32 of its rows up side by side (58 x 32 items of up to 52
-// rows and one granule: 37 us the whole call, against 56 one row after the other).
+// rows and one granule: 36 us the whole call, against 56 one row after the other).
 template <int D, int RT, int WPR>
 __global__ void __launch_bounds__(kSumThreads, 4)
     kv_attn_combine_kernel(const __grid_constant__ Params p, int64_t most) {
@@ -1456,13 +1456,14 @@ cp_status run(const Params& p, const Plan& pl, const CUtensorMap& mk, const CUte
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p, mk, mv)) != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
   if (pl.solo) return CP_OK;
   // Eight warps an output row while there are few rows (320 rows of 8 partials: 8 us against 14), or many
-  // partials to a row; else one (2176 rows of 5 partials: 104 us the whole call, against 116 with eight).
+  // partials to a row; else one (2176 rows of 5 partials: 104 us the whole call, against 116 with eight; 45 x 0-103
+  // tokens, 1-4 rows of 128/32 heads 22 and 75).
   const int64_t workers = pl.grid * S::kWarps, parts = workers / (items < 1 ? 1 : items), outs = p.rows.n_rows * p.hq;
   const bool wide = parts > 16 || outs <= 1024;
   const int64_t resident = 4 * static_cast<int64_t>(num_sms);
   // A block for 32 columns of a row where these are one wave and have many partials to read (1 x 120000 tokens,
-  // 5/1 heads: 28 us against 45; 1 x 8000, 32/8: 13.8 against 16.1; 4 x 30000: the same).  Two waves of them are
-  // slower (1 x 30000 with 32 rows, 32/8: 40 against 36).
+  // 5/1 heads: 23 us against 31; 1 x 8000, 32/8, split: 13.6 against 14.3; 4 x 30000: the same).  Two waves of them are
+  // slower (1 x 30000 with 32 rows, 32/8: 39 against 36).
   const bool columns = outs * (D / 32) <= resident && parts > 32;
   const int64_t blocks = columns ? outs * (D / 32) : wide ? outs : (outs + 7) / 8;
   cfg.dynamicSmemBytes = (p.rows.n_seqs + 1) * 8 + (columns ? workers * 4 : 0);

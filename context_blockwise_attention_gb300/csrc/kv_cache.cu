@@ -526,9 +526,10 @@ cp_status write(WriteParams& p, int num_sms, cudaStream_t s) {
   // 100 sequences, 8 x 128, pages of 128: 24 rows 6.7 / 11, 64 rows 14.4 / 13.8, 128 rows 26 / 19, 512 rows 90 / 53;
   // pages of 64: 24 rows 7.3 / 9.0, 48 rows 11.6 / 10.8, 512 rows 81 / 53; of 32: 24 rows 6.4 / 7.7, 48 rows 11.6 /
   // 9.8, 512 rows 60 / 57; of 16: 64 rows 10.5 / 11.1, 96 rows 13.1 / 12.5, 512 rows 61 / 58 (fp32, 40 sequences: 256
-  // rows 16.6 / 20, 384 rows 34 / 33); 64 sequences, 32 x 64, pages of 16: 4 rows 4.9 / 5.2, 8 rows 5.9 / 5.7, 512 rows
-  // 111 / 71.  They also pay where their blocks are few and a warp would take a tile's rows one after the other:
-  // 8 sequences, 8 x 128, pages of 128: 8 rows 3.0 / 3.2, 32 rows 5.3 / 3.4, 64 rows 9.9 / 3.5.
+  // rows 16.6 / 20, 384 rows 34 / 33); 64 sequences, 32 x 64, pages of 16: 4 rows 4.5 / 4.9, 8 rows 5.6 / 5.5, 512 rows
+  // 110 / 71 (fp32: 8 rows 5.7 / 6.6, 16 rows 7.8 / 8.1, 32 rows 10.6 / 9.6, and with 8 heads 8 rows 3.3 / 3.2).  They
+  // also pay where their blocks are few and a warp would take a tile's rows one after the other: 8 sequences, 8 x 128,
+  // pages of 128: 8 rows 3.0 / 3.2, 32 rows 5.3 / 3.4, 64 rows 9.9 / 3.5.
   const int P = p.c.page_size;
   const int64_t tiles = static_cast<int64_t>(p.units) * p.c.hkv * 2, seqs = p.rows.n_seqs;
   const int64_t blocks = tiles * P * D / (P >= 64 ? 64 : 32) / kThreads;

@@ -1,8 +1,8 @@
 // Rotary positions with several axes (cp_rope_axes).
 //
 // The angle of pair i of a token is position * inv_freq[i].  The host turns inv_freq into a 64-bit
-// fraction of a turn, u = round(inv_freq / 2 pi * 2^64) mod 2^64; position * u modulo 2^64 is then
-// the fraction of a turn exactly, whatever the position, with three 32-bit integer products and no
+// fraction of a turn, u = inv_freq / 2 pi * 2^64 mod 2^64 less at most 2; position * u modulo 2^64 is then
+// the fraction of a turn to 2^-32, whatever the position, with three 32-bit integer products and no
 // fp64 arithmetic (which this part has little of).  Its upper 32 bits, read as a signed number,
 // give an angle in [-pi, pi).
 //

@@ -538,9 +538,9 @@ cp_status cp_kv_cache_attn_workspace(const cp_kv_attn_desc* desc, int64_t* bytes
  *   with (x_i, y_i) the elements (i, i + rot/2), or (2i, 2i + 1) where interleaved = 1.  Elements
  *   [rot, d) are copied.  inverse = 1 turns by -w: the inverse rotation, which is also the
  *   backward pass (the gradient of the inputs from that of the outputs).
- * Angles are reduced exactly: the kernel multiplies the position by round(inv_freq / 2 pi * 2^64)
- * modulo 2^64, so the fraction of a turn has no rounding that grows with the position (the angle
- * is off by less than 2e-7 for any int32 position).
+ * Angles are reduced in whole numbers: the kernel multiplies the position by inv_freq / 2 pi in units of
+ * 2^-64, cut off behind the unit, modulo one turn, so the angle is off by less than 2e-7 for any int32
+ * position.
  * Arguments:
  *   n_tensors   1..4
  *   in, out     host arrays [n_tensors] of device pointers, [tokens, heads[t], d], 16-byte
