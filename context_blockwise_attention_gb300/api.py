@@ -157,6 +157,15 @@ def load_library():
     lib.cp_kv_cache_attn.argtypes = [vp, vp]
     lib.cp_kv_cache_attn_workspace.restype = i32
     lib.cp_kv_cache_attn_workspace.argtypes = [vp, ctypes.POINTER(i64)]
+    for name in ("write", "read"):
+        f = getattr(lib, "cp_kv4_cache_" + name)
+        f.restype, f.argtypes = i32, [vp, vp, vp, vp, i32, vp, vp]
+    for name in ("attn", "weigh", "evict"):
+        f = getattr(lib, "cp_kv4_cache_" + name)
+        f.restype, f.argtypes = i32, [vp, vp]
+    for name in ("attn", "evict"):
+        f = getattr(lib, f"cp_kv4_cache_{name}_workspace")
+        f.restype, f.argtypes = i32, [vp, ctypes.POINTER(i64)]
     lib.cp_rope_axes.restype = i32
     lib.cp_rope_axes.argtypes = [i32, vp, vp, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, i32, vp]
     _lib = lib
@@ -841,6 +850,278 @@ def kv_cache_attn_workspace(cache, rows, hq, n_seqs, max_pages, dtype=torch.bflo
     with torch.cuda.device(index):
         return _attn_workspace(index, *_cache_fields(cache, index)[4:8], int(n_seqs), int(max_pages), int(rows), int(hq),
                                _code(dtype), _code(o_dtype))
+
+
+# ---------------------------------------------------------------- 4-bit KV cache
+class Kv4Cache(NamedTuple):
+    """A paged 4-bit cache: ``k``, ``v`` uint8 [pages, Hkv, page_size, D * 9 / 16], a token's e2m1 numbers
+    two to a byte and a scale byte for each 16 of them (the format is in include/cpattn.h)."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+
+def kv4_cache_empty(n_pages, page_size, hkv, d, device=None):
+    """Memory for a cache of ``n_pages`` pages; what it holds is undefined until it is written."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    shape = (n_pages, hkv, page_size, d * 9 // 16)
+    return Kv4Cache(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+_CACHE4 = struct.Struct("@2Pq4i")                                     # cp_kv4_cache
+_CACHE4_ROWS = struct.Struct("@2Pq4i3P2iq")                           # cp_kv4_cache, cp_kv_rows
+_KV4_ATTN = struct.Struct("@2Pq4i3P2iq4P3if2qPqP2i")                  # cp_kv4_attn_desc
+_KV4_WEIGH = struct.Struct("@2Pq4i3P2iq5P2i2f2qP2i")                  # cp_kv4_weigh_desc
+_KV4_EVICT = struct.Struct("@2Pq4i3P4i3PqP")                          # cp_kv4_evict_desc
+_CACHE4_BYTES = _CACHE4.size
+_U8 = torch.uint8
+_D_OF_ROW = {36: 64, 72: 128}
+
+
+def _cache4_fields(cache, index):
+    """The fields of cp_kv4_cache."""
+    k, v = cache
+    try:
+        fine = (k.dtype is _U8 and v.dtype is _U8 and k.get_device() == v.get_device() == index
+                and k.is_contiguous() and v.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for t, name in ((k, "k"), (v, "v")):
+            _ptr(t, "cache." + name, _U8, index)
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or shape[3] not in _D_OF_ROW:
+        _invalid("cache.k and cache.v must be [pages, Hkv, page_size, D * 9 / 16] for a D of 64 or 128")
+    n_pages, hkv, page_size, row = shape
+    return k.data_ptr(), v.data_ptr(), n_pages, page_size, hkv, _D_OF_ROW[row], 0
+
+
+def kv4_cache_write(cache, k, v, row_start, cached, page_table, status=None, stream=None):
+    """Stores new tokens in ``cache``: rows ``row_start[b] .. row_start[b + 1]`` of ``k``, ``v`` [rows, Hkv, D]
+    become the tokens ``cached[b], cached[b] + 1, ...`` of sequence b, whose page of tokens ``i * page_size ..`` is
+    ``page_table[b, i]``; int32 CUDA tensors as for ``kv_cache_write``.  Returns ``cache``."""
+    lib = load_library()
+    index = _index(k, "k")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv4_cache_write(cache, k, v, row_start, cached, page_table, status, stream)
+    dt = k.dtype
+    code = _code(dt)
+    pk, pv = _ptr(k, "k", dt, index), _ptr(v, "v", dt, index)
+    c = _cache4_fields(cache, index)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != c[4] or shape[2] != c[5]:
+        _invalid("k and v must be [rows, Hkv, D] with the cache's Hkv and D")
+    desc = _CACHE4_ROWS.pack(*c, *_rows_fields(row_start, cached, "cached", page_table, shape[0], index))
+    _check(lib.cp_kv4_cache_write(desc, desc[_CACHE4_BYTES:], pk, pv, code, _status_ptr(status, index),
+                                  _stream_of(stream, index)))
+    return cache
+
+
+def kv4_cache_read(cache, row_start, first, page_table, n_rows, dtype=torch.bfloat16, k=None, v=None, status=None,
+                   stream=None):
+    """Reads tokens back, exactly: rows ``row_start[b] .. row_start[b + 1]`` of the returned ``k``, ``v``
+    [n_rows, Hkv, D] hold the tokens ``first[b], first[b] + 1, ...`` of sequence b.  Rows of no sequence are left as
+    they were (undefined where this call allocates them)."""
+    lib = load_library()
+    index = _index(cache[0], "cache.k")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv4_cache_read(cache, row_start, first, page_table, n_rows, dtype, k, v, status, stream)
+    if isinstance(k, torch.Tensor):
+        dtype = k.dtype
+    code = _code(dtype)
+    c = _cache4_fields(cache, index)
+    shape = (n_rows, c[4], c[5])
+    desc = _CACHE4_ROWS.pack(*c, *_rows_fields(row_start, first, "first", page_table, n_rows, index))
+    dev = cache[0].device
+    k = _new(shape, dtype, dev, stream) if k is None else k
+    v = _new(shape, dtype, dev, stream) if v is None else v
+    pk, pv = _ptr(k, "k", dtype, index), _ptr(v, "v", dtype, index)
+    if k.shape != shape or v.shape != shape:
+        _invalid("k and v must be [n_rows, Hkv, D] with the cache's Hkv and D")
+    _check(lib.cp_kv4_cache_read(desc, desc[_CACHE4_BYTES:], pk, pv, code, _status_ptr(status, index),
+                                 _stream_of(stream, index)))
+    return k, v
+
+
+def kv4_cache_attn(q, cache, row_start, kv_lens, page_table, q_first=None, kv_pos=_POS0, scale=0.0, o=None,
+                   lse=None, o_dtype=None, workspace=None, flags=0, status=None, wait_timeout_ms=0, stream=None):
+    """(O, LSE) partial of each sequence's new rows ``q`` [rows, Hq, D] over its ``kv_lens[b]`` tokens in the 4-bit
+    ``cache``.  Arguments and results are ``kv_cache_attn``'s; ``workspace`` needs
+    ``kv4_cache_attn_workspace(...)`` bytes."""
+    lib = load_library()
+    index = _index(q, "q")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv4_cache_attn(q, cache, row_start, kv_lens, page_table, q_first, kv_pos, scale, o, lse, o_dtype,
+                                  workspace, flags, status, wait_timeout_ms, stream)
+    dt, dev = q.dtype, q.device
+    code = _code(dt)
+    pq = _ptr(q, "q", dt, index)
+    c = _cache4_fields(cache, index)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != c[5]:
+        _invalid("q must be [rows, Hq, D] with the cache's D")
+    rows, hq, _ = shape
+    r = _rows_fields(row_start, kv_lens, "kv_lens", page_table, rows, index)
+    first = _per_seq(q_first, "q_first", kv_lens, index)
+    if o is None:
+        o = _new(shape, o_dtype or torch.float32, dev, stream)
+    elif not isinstance(o, torch.Tensor) or o.shape != shape:
+        _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
+    if lse is None:
+        lse = _new(shape[:2], torch.float32, dev, stream)
+    elif not isinstance(lse, torch.Tensor) or lse.shape != shape[:2]:
+        _invalid("o must be [rows, Hq, D]; lse fp32 [rows, Hq]")
+    odt = o.dtype
+    ocode = _code(odt)
+    if workspace is None:
+        need = _attn4_workspace(index, *c[2:6], *r[3:], hq, code, ocode)
+        workspace = _new((need,), torch.uint8, dev, stream) if need else None
+    _check(lib.cp_kv4_cache_attn(
+        _KV4_ATTN.pack(*c, *r, pq, _ptr(o, "o", odt, index), _ptr(lse, "lse", torch.float32, index), first, code, ocode,
+                       hq, scale, kv_pos.base, kv_pos.stride, *_workspace_fields(workspace, index),
+                       _status_ptr(status, index), wait_timeout_ms, flags),
+        _stream_of(stream, index)))
+    return o, lse
+
+
+def _per_seq(t, name, like, index):
+    """The address of an optional int32 number for each sequence."""
+    if t is None:
+        return 0
+    ptr = _ptr(t, name, torch.int32, index)
+    if t.shape != like.shape:
+        _invalid(f"{name} must be [seqs]")
+    return ptr
+
+
+def _workspace_fields(workspace, index):
+    if workspace is None:
+        return 0, 0
+    return _ptr(workspace, "workspace", torch.uint8, index), workspace.numel()
+
+
+@functools.lru_cache(maxsize=256)
+def _attn4_workspace(index, n_pages, page_size, hkv, d, n_seqs, max_pages, n_rows, hq, code, ocode):
+    """Bytes of workspace by the shapes of a call; device ``index`` is the current one."""
+    some = 16  # the contents of the arrays do not matter here
+    need = ctypes.c_int64(0)
+    _check(load_library().cp_kv4_cache_attn_workspace(
+        _KV4_ATTN.pack(some, some, n_pages, page_size, hkv, d, 0, some, some, some, n_seqs, max_pages, n_rows,
+                       0, 0, 0, 0, code, ocode, hq, 0.0, 0, 1, 0, 0, 0, 0, 0), ctypes.byref(need)))
+    return need.value
+
+
+def kv4_cache_attn_workspace(cache, rows, hq, n_seqs, max_pages, dtype=torch.bfloat16, o_dtype=torch.float32):
+    """Bytes of workspace that ``kv4_cache_attn`` needs for ``rows`` rows of ``hq`` heads over ``n_seqs`` sequences
+    with ``max_pages`` table entries each."""
+    index = _index(cache[0], "cache.k")
+    with torch.cuda.device(index):
+        return _attn4_workspace(index, *_cache4_fields(cache, index)[2:6], int(n_seqs), int(max_pages), int(rows),
+                                int(hq), _code(dtype), _code(o_dtype))
+
+
+def _weight_ptr(weight, c, index):
+    ptr = _ptr(weight, "weight", torch.float32, index)
+    if weight.shape != (c[2], c[4], c[3]):
+        _invalid("weight must be fp32 [pages, Hkv, page_size]")
+    return ptr
+
+
+def kv4_cache_weigh(q, lse, cache, weight, row_start, kv_lens, page_table, known=None, q_first=None, kv_pos=_POS0,
+                    scale=0.0, decay=1.0, flags=0, status=None, wait_timeout_ms=0, stream=None):
+    """Adds the attention weight that each sequence's rows ``q`` [rows, Hq, D] give to its ``kv_lens[b]`` cached tokens
+    to ``weight`` (fp32 [pages, Hkv, page_size], laid out as the cache), which ``kv4_cache_evict`` goes by.
+
+    ``lse`` fp32 [rows, Hq] is the rows' final LSE, merged over the ranks.  ``known`` (int32 [seqs]): how many of the
+    tokens have gathered weight before; the others' memory need not be initialised.  Older weight is multiplied by
+    ``decay``.  ``q_first`` and ``kv_pos`` say which rows see a token, as for ``kv4_cache_attn``.  Sequences without
+    rows are left as they were.  Returns ``weight``.
+    """
+    lib = load_library()
+    index = _index(q, "q")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv4_cache_weigh(q, lse, cache, weight, row_start, kv_lens, page_table, known, q_first, kv_pos, scale,
+                                   decay, flags, status, wait_timeout_ms, stream)
+    dt = q.dtype
+    code = _code(dt)
+    pq = _ptr(q, "q", dt, index)
+    c = _cache4_fields(cache, index)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != c[5]:
+        _invalid("q must be [rows, Hq, D] with the cache's D")
+    rows, hq, _ = shape
+    plse = _ptr(lse, "lse", torch.float32, index)
+    if lse.shape != shape[:2]:
+        _invalid("lse must be fp32 [rows, Hq]")
+    _check(lib.cp_kv4_cache_weigh(
+        _KV4_WEIGH.pack(*c, *_rows_fields(row_start, kv_lens, "kv_lens", page_table, rows, index),
+                        _weight_ptr(weight, c, index), pq, plse, _per_seq(q_first, "q_first", kv_lens, index),
+                        _per_seq(known, "known", kv_lens, index), code, hq, scale, decay, kv_pos.base, kv_pos.stride,
+                        _status_ptr(status, index), wait_timeout_ms, flags),
+        _stream_of(stream, index)))
+    return weight
+
+
+def kv4_cache_evict(cache, weight, kv_lens, page_table, keep, recent=0, kept=None, new_lens=None, workspace=None,
+                    status=None, stream=None):
+    """Shortens every sequence of more than ``keep`` tokens to ``keep``, in place: its last ``recent`` tokens stay, and of
+    the others those with the largest ``weight`` (summed over the KV heads; of equal ones the earlier).
+
+    With z = keep - recent, tokens that stay below slot z keep their slots, the holes there are filled in order by those
+    that stay behind it, and the recent ones follow at z.  Returns ``kept`` int32 [seqs, keep], the slot that each
+    slot's token had (-1 behind the end), and ``new_lens`` int32 [seqs], which may be ``kv_lens`` itself.  Causal calls
+    that follow lower ``q_first[b]`` by ``kv_pos.stride`` for each token that sequence b lost.
+    """
+    lib = load_library()
+    index = _index(cache[0], "cache.k")
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return kv4_cache_evict(cache, weight, kv_lens, page_table, keep, recent, kept, new_lens, workspace, status,
+                                   stream)
+    c = _cache4_fields(cache, index)
+    plens, ptable = _ptr(kv_lens, "kv_lens", _I32, index), _ptr(page_table, "page_table", _I32, index)
+    table = page_table.shape
+    if len(table) != 2 or kv_lens.shape != (table[0],):
+        _invalid("kv_lens must be [seqs], page_table [seqs, pages]")
+    pweight = _weight_ptr(weight, c, index)
+    keep, recent = int(keep), int(recent)
+    if not 1 <= keep < 2 ** 31 or not 0 <= recent <= keep:
+        _invalid(f"keep {keep} must be positive and recent {recent} in [0, keep]")
+    dev = cache[0].device
+    kept = _new((table[0], keep), _I32, dev, stream) if kept is None else kept
+    new_lens = _new((table[0],), _I32, dev, stream) if new_lens is None else new_lens
+    pkept, pnew = _ptr(kept, "kept", _I32, index), _ptr(new_lens, "new_lens", _I32, index)
+    if kept.shape != (table[0], keep) or new_lens.shape != (table[0],):
+        _invalid("kept must be int32 [seqs, keep], new_lens int32 [seqs]")
+    if workspace is None:
+        need = _evict4_workspace(index, *c[2:6], table[0], table[1], keep)
+        workspace = _new((need,), torch.uint8, dev, stream) if need else None
+    _check(lib.cp_kv4_cache_evict(
+        _KV4_EVICT.pack(*c, pweight, plens, ptable, table[0], table[1], keep, recent, pkept, pnew,
+                        *_workspace_fields(workspace, index), _status_ptr(status, index)),
+        _stream_of(stream, index)))
+    return kept, new_lens
+
+
+@functools.lru_cache(maxsize=256)
+def _evict4_workspace(index, n_pages, page_size, hkv, d, n_seqs, max_pages, keep):
+    """Bytes of workspace by the shapes of a call; device ``index`` is the current one."""
+    some = 16  # the contents of the arrays do not matter here
+    need = ctypes.c_int64(0)
+    _check(load_library().cp_kv4_cache_evict_workspace(
+        _KV4_EVICT.pack(some, some, n_pages, page_size, hkv, d, 0, some, some, some, n_seqs, max_pages, keep, 0, some,
+                        some, 0, 0, 0), ctypes.byref(need)))
+    return need.value
+
+
+def kv4_cache_evict_workspace(cache, n_seqs, max_pages, keep):
+    """Bytes of workspace that ``kv4_cache_evict`` needs for ``n_seqs`` sequences with ``max_pages`` table entries."""
+    index = _index(cache[0], "cache.k")
+    with torch.cuda.device(index):
+        return _evict4_workspace(index, *_cache4_fields(cache, index)[2:6], int(n_seqs), int(max_pages), int(keep))
 
 
 # ---------------------------------------------------------------- rotary positions

@@ -84,6 +84,17 @@ cp_status launch_kv_read(const cp_kv_cache& c, const cp_kv_rows& rows, void* k, 
 int64_t kv_attn_workspace(const cp_kv_attn_desc& d, int num_sms);
 cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s);
 
+// 4-bit cache (n_rows, where there are rows, and n_seqs > 0).
+cp_status launch_kv4_write(const cp_kv4_cache& c, const cp_kv_rows& rows, const void* k, const void* v, bool bf16,
+                           int32_t* status, int num_sms, cudaStream_t s);
+cp_status launch_kv4_read(const cp_kv4_cache& c, const cp_kv_rows& rows, void* k, void* v, bool bf16, int32_t* status,
+                          int num_sms, cudaStream_t s);
+int64_t kv4_attn_workspace(const cp_kv4_attn_desc& d, int num_sms);
+cp_status launch_kv4_attn(const cp_kv4_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s);
+cp_status launch_kv4_weigh(const cp_kv4_weigh_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s);
+int64_t kv4_evict_workspace(const cp_kv4_evict_desc& d, int num_sms);
+cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t s);
+
 struct RopeArgs {
   int32_t n_tensors;
   const void* const* in;

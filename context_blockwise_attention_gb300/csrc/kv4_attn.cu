@@ -1,0 +1,106 @@
+// Attention over the paged 4-bit cache: the choice of the kernel variant, workspace and launch.
+#include "kv4_attn.cuh"
+
+namespace cpattn {
+
+using namespace kvattn;
+
+namespace kvattn {
+extern template cp_status run4_d<64>(const Params&, const Plan&, int64_t, int, cudaStream_t);
+extern template cp_status run4_d<128>(const Params&, const Plan&, int64_t, int, cudaStream_t);
+}  // namespace kvattn
+
+namespace {
+
+Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
+  Plan r;
+  const int64_t group = d.hq / d.cache.hkv, seqs = d.rows.n_seqs > 0 ? d.rows.n_seqs : 1;
+  const int64_t per = (d.rows.n_rows + seqs - 1) / seqs * group;
+  r.qp = d.in_dtype == CP_BF16 ? 1 : 2;
+  r.pp = d.in_dtype == CP_BF16 && d.o_dtype == CP_BF16 ? 1 : 2;
+  const auto tiles = [&](int nt) {
+    r.nt = nt;
+    r.rows = nt * 8;
+    r.warps = nt * d.cache.d >= 256 || nt * r.qp >= 4 ? 8 : 12;
+  };
+  // Solo, by the page table's width in granules, which bounds the tokens: as many blocks an item as the SMs hold
+  // clusters of, where a block's warps have some granules each.
+  tiles(per <= 8 ? 1 : 2);
+  const int64_t width = (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096;
+  const int64_t solo_items = seqs * d.cache.hkv;
+  r.cluster = 1;
+  if (width > 2 * r.warps) {
+    if (solo_items * 8 <= sms * 5 / 8) r.cluster = 8;
+    else if (solo_items * 4 <= sms * 6 / 7) r.cluster = 4;
+    else if (solo_items * 2 <= sms * 6 / 7 && width > 3 * r.warps) r.cluster = 2;
+  }
+  const int64_t blocks = solo_items * r.cluster;
+  const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
+  const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
+  const bool narrow = r.cluster > 1 ? (d.cache.d == 128 ? 20 : 28) * width * turns <= r.warps * r.cluster * blocks
+                                    : width <= r.warps * (2 * blocks > sms ? 16 : 4);
+  r.solo = blocks <= sms && narrow &&
+           (d.rows.n_rows <= seqs || d.rows.n_rows * group <= 4 * r.rows);
+  if (r.solo) {
+    r.grid = blocks;
+    r.ml_off = r.o_off = r.aside_off = r.bytes = 0;
+    r.most = 0;
+    return r;
+  }
+  tiles(per <= 8 ? 1 : 2);
+  // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
+  r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
+           static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
+  r.grid = r.most < sms ? static_cast<int64_t>(r.most) : sms;
+  const int64_t slots = r.grid * r.warps * 2 * r.rows;
+  r.ml_off = 0;
+  r.o_off = (r.ml_off + slots * 8 + 255) / 256 * 256;
+  r.aside_off = r.o_off + slots * d.cache.d * 4;
+  r.bytes = r.aside_off + slots / 2 * d.cache.d * 4;
+  return r;
+}
+
+}  // namespace
+
+int64_t kv4_attn_workspace(const cp_kv4_attn_desc& d, int num_sms) { return plan_of(d, num_sms).bytes; }
+
+cp_status launch_kv4_attn(const cp_kv4_attn_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s) {
+  const Plan pl = plan_of(d, num_sms);
+  if (pl.most > 1e12) {  // their products with a worker's number stay int64
+    set_error("cp_kv4_cache_attn: max_pages * page_size * hkv * n_seqs is too large for one call");
+    return CP_ERR_INVALID_ARG;
+  }
+  const cp_kv4_cache& c = d.cache;
+  uint8_t* const ws = static_cast<uint8_t*>(d.workspace);
+  Params p{};
+  p.tile[0] = static_cast<const uint8_t*>(c.k);
+  p.tile[1] = static_cast<const uint8_t*>(c.v);
+  p.rows = d.rows;
+  p.n_pages = c.n_pages;
+  p.q = d.q;
+  p.o = d.o;
+  p.lse = d.lse;
+  p.q_first = d.q_first;
+  p.hq = d.hq;
+  p.hkv = c.hkv;
+  p.group = d.hq / c.hkv;
+  p.page = c.page_size;
+  p.page_log2 = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  p.q_bf16 = d.in_dtype == CP_BF16;
+  p.o_bf16 = d.o_dtype == CP_BF16;
+  p.stall = (d.flags & CP_FLAG_TEST_STALL) != 0;
+  p.scale_log2 = scale * kLog2e;
+  p.kv_pos = d.kv_pos;
+  p.status = d.status;
+  p.timeout_ns = timeout_ns;
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + pl.o_off);
+  p.aside = reinterpret_cast<float*>(ws + pl.aside_off);
+  const int64_t seqs = d.rows.n_seqs;
+  const int64_t items = (seqs + d.rows.n_rows * p.group / pl.rows) * c.hkv;
+  p.few = 128 * items;
+  p.cluster = pl.cluster;
+  return c.d == 128 ? run4_d<128>(p, pl, items, num_sms, s) : run4_d<64>(p, pl, items, num_sms, s);
+}
+
+}  // namespace cpattn

@@ -1,0 +1,691 @@
+// Attention of a batch's new tokens over the paged 4-bit cache (cp_kv4_cache_attn): the kernels and their launches.
+// kv4_attn.cu chooses among them; kv4_attn_d64.cu and kv4_attn_d128.cu compile them.
+//
+// Per (sequence, KV head) the g = hq / hkv query heads of the sequence's rows are one block of query rows:
+//   s_ij = log2 e * scale * (q_i . k_j),  p_ij = 2^(s_ij - m_i),  O_i = sum_j p_ij v_j / l_i,
+//   LSE_i = ln 2 (m_i + log2 l_i),        l_i = sum_j p_ij,
+// k_j and v_j being e2m1 numbers times a scale for each 16 of them, which f16 holds exactly.
+//
+// The work is split as over the 8-bit cache (kv_split.cuh, kv_attn.cuh): granules of 4096 / D keys, equal shares of
+// consecutive ones for every warp, partials joined by a second kernel; or, for few short rows, a block or a cluster of
+// blocks an item.
+#pragma once
+
+#include "kv4_tile.cuh"
+
+namespace cpattn {
+namespace kvattn {
+
+constexpr int kPExp = 15;       // P operands are below 2^(kPExp + kTop) = 65490 and f16's largest is 65504
+constexpr float kTop = 0.999f;  // largest s - m
+
+// QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
+template <int D, int NT, int QP, int PP>
+struct Shape4 {
+  // More warps hide more latency; registers (O takes NT D / 4) bound their number.
+  static constexpr bool kHeavy = NT * D >= 256 || NT * QP >= 4;
+  static constexpr int kWarps = kHeavy ? 8 : 12;
+  static constexpr int kRows = NT * 8;  // RT
+  // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: the accumulators are added
+  // to others every kFlush granules, in registers where there are some left (kHold), else in the workspace.
+  static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
+  static constexpr int kFlush = PP == 1 ? 64 : kHold ? 4 : D == 128 ? 16 : 8;
+  static constexpr int kKeys = Granule<D>::kKeys;
+  static constexpr int kSteps = Granule<D>::kSteps;
+  static constexpr int kRow = Granule<D>::kRow;
+  static constexpr int kHalf = Granule<D>::kHalf;
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr bool kQSmem = D == 128 && NT * QP >= 4;  // query operands in shared memory
+  static constexpr int kStages = kHeavy && !kQSmem ? 5 : 3;
+  static constexpr int kQBytes = kQSmem ? NT * QP * (D / 16) * 256 : 0;
+  static constexpr int kWarpBytes = kStages * kStage + kQBytes;
+  // behind the warps' parts: barriers, control, plan
+  static constexpr int kBarOff = kWarps * kWarpBytes;  // [warp][stage] + stall
+  static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
+  static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;  // [warp] 8 bytes
+  static constexpr int kPlanOff = kScanOff + 16 * 8;
+};
+
+// SOLO: 0 split, 1 one block an item, 2 a cluster of p.cluster blocks an item.
+template <int D, int NT, int QP, int PP, int SOLO>
+__global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
+    kv4_attn_kernel(const __grid_constant__ Params p) {
+  using S = Shape4<D, NT, QP, PP>;
+  constexpr int RT = S::kRows;
+  constexpr int kMt = D / 16;  // 16-row tiles of O^T; also steps of 16 dimensions of S
+  constexpr int kCols = D / 8; // columns of O that a lane holds, for two query rows
+  constexpr int kSt = S::kStages, kSteps = S::kSteps, kKeys = S::kKeys;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  int64_t* const plan = reinterpret_cast<int64_t*>(smem + S::kPlanOff);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + S::kCtlOff);
+  const uint32_t base = ptx::smem_u32(smem);
+  const uint32_t ring = base + warp * S::kWarpBytes;
+  const uint32_t q_smem = ring + kSt * S::kStage;
+  const uint32_t bars = base + S::kBarOff + warp * kSt * 8;
+  const uint32_t stall_bar = base + S::kBarOff + S::kWarps * kSt * 8;
+
+  if (lane == 0) {
+    for (int i = 0; i < kSt; ++i) ptx::mbar_init(bars + i * 8, 1);
+    if (warp == 0) {
+      ptx::mbar_init(stall_bar, 1);
+      *abort_flag = 0;
+    }
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  ptx::wait_dependencies();  // launched early: what was in the stream before is complete from here on
+  const int n_seqs = p.rows.n_seqs;
+  const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
+  Cursor c;  // where the products are
+  Seq seq;
+  int64_t left;  // numbers of the share from the cursor on
+  bool inside;   // the share begins inside of an item
+  const bool stalled = p.stall && blockIdx.x == 0 && warp == 0;  // test only
+  // SOLO: rank of the block among those of its item, and the warp and number of warps among all of them
+  const int cluster = SOLO == 2 ? p.cluster : 1;
+  const int rank = SOLO == 2 ? blockIdx.x % cluster : 0;
+  const int solo_warp = rank * S::kWarps + warp, solo_warps = cluster * S::kWarps;
+  if constexpr (SOLO) {
+    const int item = blockIdx.x / cluster;
+    c.b = item / p.hkv;
+    c.head = item - c.b * p.hkv;
+    seq = seq_of<D, RT>(p, c.b);
+    if (seq.over && seq.rows > 0 && tid == 0) kv::report(p.status, kv::kSiteTokens);
+    if (seq.blocks == 0) {  // nothing to see
+      for (int rho = solo_warp; rho < seq.rows * p.group; rho += solo_warps) {
+        const int t = rho / p.group;
+        const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+        const float zero[D / 32] = {};
+        store_lane(p, out * D + lane * (D / 32), zero);
+        if (lane == 0) p.lse[out] = -INFINITY;
+      }
+      return;
+    }
+    __syncthreads();  // the abort flag is set up
+    c.block = 0;
+    c.gpi = seq.gpi;
+    c.blocks = seq.blocks;
+    c.g = seq.gpi * solo_warp / solo_warps;
+    left = seq.gpi * (solo_warp + 1) / solo_warps - c.g;
+    inside = false;
+  } else {
+    make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
+    ptx::launch_dependents();
+    if (stalled) {
+      sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+      return;
+    }
+    const int64_t W = plan[n_seqs];
+    const int64_t n_workers = workers(p, W, static_cast<int64_t>(gridDim.x) * S::kWarps);
+    if (worker >= n_workers) return;
+    const int64_t lo = share(W, n_workers, worker), hi = share(W, n_workers, worker + 1);
+    left = hi - lo;
+    int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (plan[mid] <= lo) a = mid;
+      else z = mid - 1;
+    }
+    c.b = a;
+    seq = seq_of<D, RT>(p, a);
+    const int64_t off = lo - plan[a];
+    const int64_t item = off / (seq.gpi + kSetup);
+    const int at = static_cast<int>(off - item * (seq.gpi + kSetup));
+    inside = at >= kSetup;
+    c.g = inside ? at - kSetup : 0;
+    if (!inside) left -= kSetup - at;
+    c.head = static_cast<int>(item / seq.blocks);
+    c.block = static_cast<int>(item - static_cast<int64_t>(c.head) * seq.blocks);
+    c.gpi = seq.gpi;
+    c.blocks = seq.blocks;
+    if (left <= 0) return;
+  }
+  bool ok = true;
+  if (stalled) {  // the block's other warps still meet it
+    ok = sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+    left = 0;
+  }
+  const int g_first = c.g, solo_left = static_cast<int>(left);  // of a block of rows, where SOLO
+  Feed<D, RT, 2> f{c, left, seq.keys, -32, -1};
+
+  // Starts the copies of the next granule into stage `st`.
+  auto issue = [&](int st) {
+    f.granule(p, lane, ring + st * S::kStage, bars + st * 8);
+    --f.left;
+    if (++f.c.g == f.c.gpi && f.left > kSetup) {
+      f.left -= kSetup;
+      f.c.g = 0;
+      if (++f.c.block == f.c.blocks) {
+        f.c.block = 0;
+        if (++f.c.head == p.hkv) {
+          Seq s{};
+          next_seq<D, RT>(p, f.c, s);
+          f.keys = s.keys;
+          f.window = -32;
+        }
+      }
+    } else if (f.c.g == f.c.gpi) {
+      f.left = 0;
+    }
+  };
+
+  uint32_t qf[S::kQSmem ? 1 : NT * QP][S::kQSmem ? 1 : kMt][2];
+  // of the lane's two query rows 2 tig, 2 tig + 1 in each tile
+  float fac[NT][2], m[NT][2], l[NT][2];
+  int lim[NT][2];
+  float acc[NT][kMt][4];
+  int lim_min = 0, lim_max = 0;
+  int live = NT;         // tiles that have rows
+  int row_q = 0;         // first query row (token row * group + head in group) of the block
+  float* const aside = p.aside + worker * (RT * D);
+  float m_aside[NT][2] = {};  // what the values put aside refer to
+  bool flushed = false;
+  int since = 0;         // granules since then
+  constexpr bool kHold = S::kHold;
+  float held[kHold ? kMt : 1][4];  // of the one tile
+
+  auto begin_item = [&]() {
+    row_q = c.block * RT;
+    const int n_rows = seq.rows * p.group;
+    live = min(NT, (n_rows - row_q + 7) / 8);
+    int lmin = 0x7fffffff, lmax = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // the lane's part of query row gid of the tile
+      const int rho = row_q + n * 8 + gid;
+      const bool live = rho < n_rows;
+      const int t = live ? rho / p.group : 0;
+      const int64_t at = ((seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group)) * D;
+      int lm = live ? visible(p, seq.tokens, seq.pos0 + t) : -1;
+      if (live) {
+        lmin = min(lmin, lm);
+        lmax = max(lmax, lm);
+      }
+      float f;
+      if constexpr (S::kQSmem) {
+        uint32_t x[QP][kMt][2];
+        f = query_operands<D, QP>(p, at, live, tig, x);
+#pragma unroll
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int j = 0; j < kMt; ++j)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_smem + (((n * QP + part) * kMt + j) * 32 + lane) * 8),
+                         "r"(x[part][j][0]), "r"(x[part][j][1])
+                         : "memory");
+      } else {
+        f = query_operands<D, QP>(p, at, live, tig, &qf[n * QP]);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);
+        lim[n][r] = __shfl_sync(kFull, lm, (2 * tig + r) * 4);
+        m[n][r] = -INFINITY;
+        l[n][r] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
+    lim_min = __reduce_min_sync(kFull, lmin);
+    lim_max = __reduce_max_sync(kFull, lmax);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (lim[n][r] < 0) lim[n][r] = lim_max;  // rows of nobody must not make the tile a masked one
+    flushed = false;
+    since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) held[j][0] = held[j][1] = held[j][2] = held[j][3] = 0.0f;
+    }
+  };
+
+  // Where some row of the block does not see all keys of the granule: values that no row sees count as zero, by
+  // their scales (0 * NaN would not vanish), and NaN among values that only some of the rows see go to those rows'
+  // accumulators and are taken out.
+  auto mask_values = [&](uint32_t tile) {
+    const int key0 = c.g * kKeys, first = max(lim_min - key0, 0);  // below kKeys
+    bool odd = false;
+#pragma unroll
+    for (int k = lane; k < kKeys; k += 32) {
+      const uint32_t at = tile + S::kHalf + k * S::kRow + D / 2;
+      uint32_t v[D / 64];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        if (key0 + k >= lim_max) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 4 * j), "r"(0) : "memory");
+        v[j] = lds32(at + 4 * j);
+        if (k >= first) odd |= __vcmpgeu4(v[j], 0xf8f8f8f8u) != 0u;
+      }
+    }
+    __syncwarp();
+    if (__any_sync(kFull, odd)) {
+#pragma unroll 1
+      for (int k = first; k < kKeys && key0 + k < lim_max; ++k) {
+        const uint32_t at = tile + S::kHalf + k * S::kRow + D / 2 + (D == 128 ? gid : gid >> 1);
+        const bool nan = lds8(at) >= 0xf8u;
+        __syncwarp();
+        if (nan) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (nan && key0 + k < lim[n][r]) {
+#pragma unroll
+              for (int j = 0; j < kMt; ++j) acc[n][j][r] = acc[n][j][2 + r] = __int_as_float(0x7fffffff);
+            }
+      }
+    }
+    ptx::fence_proxy_async_smem();  // before the next copies into the stage
+    __syncwarp();
+  };
+
+  // One granule; masked: some of its keys are not seen by some row.  Masks and tiles without rows are uniform
+  // branches and predicates, not variants: with four variants a warp's items of a few granules ran at the
+  // speed of the instruction cache (62 x 16 items of some 3 granules, up to 60 rows, D = 64: 86 us, more than half
+  // of the stalls; 55 with one path, and 16-row items of 8192 tokens 102 against 106).
+  auto granule = [&](int st, bool masked) {
+    const uint32_t tile = ring + st * S::kStage;
+    const int key0 = c.g * kKeys;
+    const bool both = NT == 1 || live > 1;
+    auto product = [&](int n, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+      if (n == 0) ptx::mma_f16(d, a, b0, b1);
+      else ptx::mma_f16_if(d, a, b0, b1, both);
+    };
+    if (masked) mask_values(tile);
+    // S^T: s[n][i][2 u + r] is key key_at(i, u, gid) for query row 2 tig + r of tile n
+    float s[NT][kSteps][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
+      key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4]) {
+#pragma unroll
+        for (int n = 0; n < NT * QP; ++n) {
+          if constexpr (S::kQSmem) {
+            const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
+            product(n / QP, s[n / QP][i], a, b.x, b.y);
+          } else {
+            product(n / QP, s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
+          }
+        }
+      });
+    }
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (key0 + key_at<D>(i, u, gid) >= lim[n][r]) s[n][i][2 * u + r] = -INFINITY;
+    }
+    // Maxima.  s keeps the products; a score is s * fac (fac > 0).  m moves by whole numbers: rescaling is exact, and rare.
+    float down[NT][2];
+    bool grew = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) top = fmaxf(top, fmaxf(s[n][i][r], s[n][i][2 + r]));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+        top *= fac[n][r];
+        const bool up = top - m[n][r] > kTop;  // false where both are -inf
+        grew |= up;
+        const float now = up ? floorf(top + (1.0f - kTop)) : m[n][r];
+        down[n][r] = up ? m[n][r] - now : 0.0f;
+        m[n][r] = now;
+      }
+    if (__any_sync(kFull, grew)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float c0 = ex2(down[n][0]), c1 = ex2(down[n][1]);
+        l[n][0] *= c0;
+        l[n][1] *= c1;
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) {
+          acc[n][j][0] *= c0;
+          acc[n][j][1] *= c1;
+          acc[n][j][2] *= c0;
+          acc[n][j][3] *= c1;
+          if constexpr (kHold) {
+            held[j][0] *= c0;
+            held[j][1] *= c1;
+            held[j][2] *= c0;
+            held[j][3] *= c1;
+          }
+        }
+      }
+    }
+    // Weights as operands, times 2^kPExp: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid
+    uint32_t pb[NT][PP][kSteps][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0] - kPExp, m[n][1] == -INFINITY ? 0.0f : m[n][1] - kPExp};
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float w[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            w[r] = ex2(fmaf(s[n][i][2 * u + r], fac[n][r], -ref[r]));
+            l[n][r] += w[r];
+          }
+          const uint32_t h = to_f16x2(w[0], w[1]);
+          pb[n][0][i][u] = ptx::transpose8x8(h);
+          if constexpr (PP == 2) {
+            const float2 back = from_f16x2(h);
+            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(w[0] - back.x, w[1] - back.y));
+          }
+        }
+    }
+    // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      value_operands<D>(tile, i, gid, tig, [&](int w, const uint32_t (&a)[4]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int part = 0; part < PP; ++part) product(n, acc[n][w], a, pb[n][part][i][0], pb[n][part][i][1]);
+      });
+  };
+
+  // Columns 4 j .. 4 j + 3 of the lane's part of query row 2 tig + r of tile n: the accumulators, with
+  // what was put aside (`from`) at weight `keep`.
+  auto four = [&](int n, int r, int j, const float* from, float keep, float (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = acc[n][2 * j + (e >> 1)][2 * (e & 1) + r];
+      if constexpr (kHold) x[e] += held[2 * j + (e >> 1)][2 * (e & 1) + r];
+    }
+    if (flushed) {
+      const float4 y = *reinterpret_cast<const float4*>(from + 4 * j);
+      x[0] = fmaf(y.x, keep, x[0]), x[1] = fmaf(y.y, keep, x[1]);
+      x[2] = fmaf(y.z, keep, x[2]), x[3] = fmaf(y.w, keep, x[3]);
+    }
+  };
+
+  // Weight of what was put aside of a row (zeros where it had seen nothing).
+  auto keep_of = [&](int n, int r) {
+    return flushed && m_aside[n][r] != -INFINITY ? ex2(m_aside[n][r] - m[n][r]) : 0.0f;
+  };
+
+  // Puts the accumulators aside: adds them to the others and clears them.
+  auto to_workspace = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float* const at = aside + (n * 8 + 2 * tig + r) * D + gid * kCols;
+        const float keep = keep_of(n, r);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, at, keep, x);
+          *reinterpret_cast<float4*>(at + 4 * j) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        m_aside[n][r] = m[n][r];
+      }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) acc[n][j][0] = acc[n][j][1] = acc[n][j][2] = acc[n][j][3] = 0.0f;
+    }
+    flushed = true;
+  };
+  auto flush = [&]() {
+    since = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int j = 0; j < kMt; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          held[j][e] += acc[0][j][e];
+          acc[0][j][e] = 0.0f;
+        }
+    } else {
+      to_workspace();
+    }
+  };
+
+  // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial at
+  // part_o [RT][D], part_ml [RT], with l between 1 and 2.
+  auto end_item = [&](bool whole, float* part_o, float2* part_ml) {
+    const int n_rows = seq.rows * p.group;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[n][r];
+        sum += __shfl_xor_sync(kFull, sum, 4);
+        sum += __shfl_xor_sync(kFull, sum, 8);
+        sum += __shfl_xor_sync(kFull, sum, 16);
+        const int local = n * 8 + 2 * tig + r;
+        const int rho = row_q + local;
+        if (rho >= n_rows) continue;
+        const float keep = keep_of(n, r);
+        const int up = min(max(static_cast<int>(__float_as_uint(sum) >> 23 & 255u) - 127, -100), 126);
+        const float norm = sum * kv::pow2(-up), ref = m[n][r] + static_cast<float>(up - kPExp);
+        const float back = kv::pow2(-up);
+        const float f = whole ? (sum == 0.0f ? 0.0f : back / norm) : back;
+        float* const part = part_o + local * D + gid * kCols;
+        const int t = rho / p.group;
+        const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          float x[4];
+          four(n, r, j, aside + local * D + gid * kCols, keep, x);
+          if (whole) store_row4(p, out * D + gid * kCols + 4 * j, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+          else *reinterpret_cast<float4*>(part + 4 * j) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        }
+        if (gid == 0) {
+          if (whole) p.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(norm)) * kLn2;
+          else part_ml[local] = make_float2(sum == 0.0f ? -INFINITY : ref, norm);
+        }
+      }
+  };
+
+  // A stage is mostly there already: the clock that bounds the wait is read only where it is not.
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+  };
+  int st = 0, in_flight = 0;
+  uint32_t parity = 0;
+  bool from_start = c.g == 0;  // the item at hand is ours from its first granule on
+  while (true) {  // once; for each block of rows where SOLO
+    for (int i = 0; i < kSt; ++i)
+      if (f.left > 0) {
+        issue(st + i < kSt ? st + i : st + i - kSt);
+        ++in_flight;
+      }
+    begin_item();
+    while (left > 0) {
+      if (!wait(bars + st * 8, parity)) {
+        ok = false;
+        break;
+      }
+      const int key0 = c.g * kKeys;
+      if (key0 < lim_max) {
+        granule(st, key0 + kKeys > lim_min);
+      }
+      __syncwarp();
+      if (f.left > 0) issue(st);
+      else --in_flight;
+      if (++st == kSt) {
+        st = 0;
+        parity ^= 1u;
+      }
+      --left;
+      ++c.g;
+      if (c.g == c.gpi || left == 0) {
+        if (SOLO) break;
+        const int64_t slot = worker * 2 + (inside ? 0 : 1);
+        end_item(from_start && c.g == c.gpi, p.part_o + slot * (RT * D), p.part_ml + slot * RT);
+        left -= kSetup;  // of the next item
+        if (left <= 0) break;
+        c.g = 0;
+        from_start = true;
+        inside = false;
+        if (++c.block == c.blocks) {
+          c.block = 0;
+          if (++c.head == p.hkv) next_seq<D, RT>(p, c, seq);
+        }
+        begin_item();
+      } else if (++since == S::kFlush && (kHold || !SOLO)) {  // 16 granules need no more
+        flush();
+      }
+    }
+    if (!SOLO) break;
+    // The warps' partials meet where their stages were; a warp of no granules leaves an empty one.
+    static_assert(S::kStages * S::kStage >= RT * (D * 4 + 8), "a warp's partial fits its stages");
+    float* const mine = reinterpret_cast<float*>(smem + warp * S::kWarpBytes);
+    __syncwarp();
+    end_item(false, mine, reinterpret_cast<float2*>(mine + RT * D));
+    __syncthreads();
+    auto finish = [&](int rho, float top, float sum, float (&x)[D / 32]) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] *= inv;
+      const int t = rho / p.group;
+      const int64_t out = (seq.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+      store_lane(p, out * D + lane * (D / 32), x);
+      if (lane == 0) p.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    };
+    for (int i = warp; i < RT; i += S::kWarps) {
+      const int rho = row_q + i;
+      if (rho >= seq.rows * p.group) break;
+      float top = -INFINITY;
+      for (int w = 0; w < S::kWarps; ++w)
+        top = fmaxf(top, reinterpret_cast<const float2*>(smem + w * S::kWarpBytes + RT * D * 4)[i].x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, x[D / 32];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] = 0.0f;
+      for (int w = 0; w < S::kWarps; ++w) {
+        const float2 ml = reinterpret_cast<const float2*>(smem + w * S::kWarpBytes + RT * D * 4)[i];
+        const float wt = ex2(ml.x - ref);
+        sum = fmaf(wt, ml.y, sum);
+        const float* const from = reinterpret_cast<const float*>(smem + w * S::kWarpBytes) + i * D + lane * (D / 32);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = fmaf(wt, from[j], x[j]);
+      }
+      if constexpr (SOLO == 1) {
+        finish(rho, top, sum, x);
+      } else {  // the block's partial takes the place of its first warp's
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) reinterpret_cast<float*>(smem)[i * D + lane * (D / 32) + j] = x[j];
+        if (lane == 0) reinterpret_cast<float2*>(smem + RT * D * 4)[i] = make_float2(top, sum);
+      }
+    }
+    int stop = 0;
+    if constexpr (SOLO == 2) {
+      ptx::cluster_sync();
+      for (int i = rank + cluster * warp; i < RT; i += solo_warps) {
+        const int rho = row_q + i;
+        if (rho >= seq.rows * p.group) break;
+        float top = -INFINITY, sum = 0.0f;
+        if (lane < cluster) {
+          const uint32_t at = ptx::cluster_addr(base + RT * D * 4 + i * 8, lane);
+          top = ptx::ld_cluster(at);
+          sum = ptx::ld_cluster(at + 4);
+        }
+        const float mine = top;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        top = __shfl_sync(kFull, top, 0);
+        const float wt = ex2(mine - (top == -INFINITY ? 0.0f : top));
+        sum *= wt;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        sum = __shfl_sync(kFull, sum, 0);
+        float x[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < cluster; ++r) {
+          const float w = __shfl_sync(kFull, wt, r);
+          const uint32_t at = ptx::cluster_addr(base + (i * D + lane * (D / 32)) * 4, r);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) x[j] = fmaf(w, ptx::ld_cluster(at + 4 * j), x[j]);
+        }
+        finish(rho, top, sum, x);
+      }
+      // a wait that ran out in one block ends them all, since they read one another's memory
+      if (lane < cluster)
+        stop = __float_as_int(ptx::ld_cluster(ptx::cluster_addr(base + S::kCtlOff, lane)));
+      stop = __any_sync(kFull, stop != 0);
+    }
+    ptx::fence_proxy_async_smem();  // the next block's copies write where the partials were
+    if constexpr (SOLO == 2) ptx::cluster_sync();
+    else __syncthreads();
+    if (++c.block == c.blocks || (SOLO == 2 ? stop != 0 : *abort_flag != 0)) break;
+    f.c.block = c.block;
+    f.c.g = c.g = g_first;
+    left = f.left = solo_left;
+  }
+  if (!ok) {
+    // copies in flight must not outlive the block: those of this granule and, where there was more to
+    // copy, of the next
+    for (int i = 0; i < in_flight; ++i) {
+      sync::wait_drain(bars + st * 8, parity, p.timeout_ns);
+      if (++st == kSt) {
+        st = 0;
+        parity ^= 1u;
+      }
+    }
+  }
+}
+
+template <int D, int NT, int QP, int PP>
+cp_status run4(const Params& p, const Plan& pl, int64_t items, int num_sms, cudaStream_t s) {
+  using S = Shape4<D, NT, QP, PP>;
+  constexpr int most_smem = 128 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8;
+  static_assert(most_smem <= 232448, "shared memory of a block");
+  const int smem = 128 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
+  const auto kernel = !pl.solo           ? kv4_attn_kernel<D, NT, QP, PP, 0>
+                      : pl.cluster == 1 ? kv4_attn_kernel<D, NT, QP, PP, 1>
+                                        : kv4_attn_kernel<D, NT, QP, PP, 2>;
+  // The limit is the function's, not the call's: always the same, for other host threads launch the kernel too.
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_attn_kernel attribute");
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(pl.cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pl.solo && pl.cluster > 1 ? 2 : 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid));
+  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return cuda_fail(e, "kv4_attn_kernel launch");
+  if (pl.solo) return CP_OK;
+  return launch_sum<D, S::kRows>(p, pl.grid * S::kWarps, items, num_sms, s);
+}
+
+template <int D>
+cp_status run4_d(const Params& p, const Plan& pl, int64_t items, int num_sms, cudaStream_t s) {
+  if (pl.pp == 1)
+    return pl.nt == 1 ? run4<D, 1, 1, 1>(p, pl, items, num_sms, s)
+                      : run4<D, 2, 1, 1>(p, pl, items, num_sms, s);
+  if (pl.qp == 1)
+    return pl.nt == 1 ? run4<D, 1, 1, 2>(p, pl, items, num_sms, s)
+                      : run4<D, 2, 1, 2>(p, pl, items, num_sms, s);
+  return pl.nt == 1 ? run4<D, 1, 2, 2>(p, pl, items, num_sms, s)
+                    : run4<D, 2, 2, 2>(p, pl, items, num_sms, s);
+}
+
+}  // namespace kvattn
+}  // namespace cpattn

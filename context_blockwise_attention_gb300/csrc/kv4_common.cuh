@@ -1,0 +1,65 @@
+// The row format of the 4-bit cache: d e2m1 numbers, the even elements in the low nibbles, then d / 16
+// scale bytes, one for each 16 numbers.
+//
+// A scale byte is the upper half of an f16 number without its sign: five exponent bits (bias 15), three
+// fraction bits; it becomes a half by a shift.  Scales reach from 2^-17 to 10240, so e2m1 (two significant
+// bits, at most 6) times scale (four) is exact in f16, below 2^16 and a multiple of 2^-18, and in bf16.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace cpattn {
+namespace kv4 {
+
+template <int D>
+constexpr int kRow = D / 2 + D / 16;  // bytes of a row: 72 or 36
+
+constexpr uint32_t kNaN = 255;         // scale byte of a group with a number that is not finite
+constexpr uint32_t kMostScale = 0xe2;  // 10240: 6 times the next one is beyond f16
+
+// The byte of the scale nearest to amax / 6 (ties to even).  The quotient is never rounded onto a tie of the scales:
+// six times a tie is exact in fp32, and the next number of fp32 is 2/3 of a step of the quotient away or more.
+__device__ __forceinline__ uint32_t scale_code(float amax) {
+  const float x = __fdiv_rn(amax, 6.0f);
+  uint32_t code;
+  if (x < 0x1p-14f) {
+    code = static_cast<uint32_t>(__float2int_rn(x * 0x1p17f));
+  } else {
+    uint32_t u = __float_as_uint(x);
+    u += 0x7ffffu + ((u >> 20) & 1u);
+    code = (u >> 20) - ((127u - 15u) << 3);
+  }
+  return code < kMostScale ? code : kMostScale;
+}
+__device__ __forceinline__ float scale_of(uint32_t code) {
+  float f;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(static_cast<uint16_t>(code << 7)));
+  return f;
+}
+
+// Two fp32 to two e2m1 numbers (first in the low nibble): round to nearest even, at most 6.
+__device__ __forceinline__ uint32_t to_e2m1x2(float a, float b) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The eight e2m1 numbers of a word as f16 pairs, exact: byte i's low nibble is the low half of h[i].
+__device__ __forceinline__ void to_f16x2(uint32_t word, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(word));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Scale bytes as halves: byte `at` (0 or 1) of `bytes` in both, and of two words below 256 one in each.
+__device__ __forceinline__ uint32_t scale_twice(uint32_t bytes, int at) {
+  return __byte_perm(bytes, 0u, at == 0 ? 0x0404 : 0x1414) >> 1;
+}
+__device__ __forceinline__ uint32_t scale_pair(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x4101) >> 1; }
+
+}  // namespace kv4
+}  // namespace cpattn

@@ -1,0 +1,372 @@
+// The attention weight that the tokens of the paged 4-bit cache gather (cp_kv4_cache_weigh).
+//
+//   weight_j := decay weight_j + sum over the rows i that see j and the query heads of the KV head of
+//               2^(log2 e (scale (q_i . k_j) - LSE_i)),
+// with the rows' final LSE, so that the weights of all ranks' tokens are parts of one softmax.  Given the LSE there is
+// no running maximum and nothing to join: every key is on its own.  Bound: keys and weights are read once and weights
+// written once; values are not touched.
+//
+// The unit of work is a granule (4096 / D tokens of one sequence and head) with all of the sequence's rows, so each
+// weight has one writer and its sum one order.  Granules are numbered sequence after sequence, each head beginning with
+// kSetup numbers more, and every warp has an equal share of consecutive ones.  A share's part of a head is gone over
+// once for each block of RT query rows; the keys come by a ring of copies as for attention, the old weights with them.
+#include "kv4_tile.cuh"
+
+namespace cpattn {
+namespace kvattn {
+
+namespace {
+
+struct WeighParams {
+  Params p;  // q, lse (read), rows, tile[0], ...
+  float* weight;
+  const int32_t* known;
+  float decay;
+};
+
+template <int D, int NT, int QP>
+struct WeighShape {
+  using G = Granule<D>;
+  static constexpr bool kHeavy = NT * QP * D >= 512;  // query operands take NT QP D / 8 registers
+  static constexpr int kWarps = kHeavy ? 8 : 16;
+  static constexpr int kRows = NT * 8;  // RT
+  static constexpr int kStages = kHeavy ? 6 : 4;
+  static constexpr int kOldOff = G::kHalf;                  // old weights of the granule
+  static constexpr int kPageOff = kOldOff + G::kKeys * 4;   // pages of its parts
+  static constexpr int kStage = kPageOff + 16;
+  static constexpr int kBarOff = kWarps * kStages * kStage;
+  static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
+  static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;
+  static constexpr int kPlanOff = kScanOff + 16 * 8;
+};
+
+struct WeighSeq {
+  int64_t r0, pos0;
+  int32_t rows, tokens, known, gpi, blocks;
+  bool over;
+};
+template <int D, int RT>
+__device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& w, int b) {
+  const Params& p = w.p;
+  WeighSeq s;
+  s.r0 = kv::row_at(p.rows, b);
+  const int64_t r1 = kv::row_at(p.rows, b + 1);
+  s.rows = r1 > s.r0 ? static_cast<int32_t>(r1 - s.r0) : 0;
+  const int64_t t = __ldg(p.rows.tokens + b), room = static_cast<int64_t>(p.rows.max_pages) << p.page_log2;
+  s.over = t > room;
+  s.tokens = t < 0 ? 0 : static_cast<int32_t>(t < room ? t : room);
+  s.known = w.known != nullptr ? __ldg(w.known + b) : s.tokens;
+  s.pos0 = p.q_first != nullptr ? __ldg(p.q_first + b) : 0;
+  s.gpi = s.rows > 0 ? (s.tokens + kKeysOf<D> - 1) / kKeysOf<D> : 0;
+  s.blocks = s.rows > 0 ? (s.rows * p.group + RT - 1) / RT : 0;
+  return s;
+}
+
+// A walk over a share: for each sequence and head the granules g0 .. g1 - 1, once for each block of rows.
+template <int D, int RT>
+struct Walk {
+  int b, head, block, g, g0, g1;
+  int64_t left;  // numbers of the share behind this part
+  WeighSeq s;
+
+  // Takes the part that begins with granule g0 out of `left` numbers that begin there.
+  __device__ __forceinline__ void enter(int from) {
+    block = 0;
+    g = g0 = from;
+    g1 = static_cast<int>(s.gpi - from < left ? s.gpi : from + left);
+    left -= g1 - g0;
+  }
+  // To the next granule; false at the end of the share.
+  __device__ __forceinline__ bool next(const WeighParams& w) {
+    if (++g < g1) return true;
+    if (++block < s.blocks) {
+      g = g0;
+      return true;
+    }
+    left -= kSetup;
+    if (left <= 0) return false;
+    if (++head == w.p.hkv) {
+      head = 0;
+      do {
+        if (++b >= w.p.rows.n_seqs) return false;
+        s = weigh_seq<D, RT>(w, b);
+      } while (s.gpi == 0);
+    }
+    enter(0);
+    return true;
+  }
+};
+
+template <int D, int NT, int QP>
+__global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
+    kv4_weigh_kernel(const __grid_constant__ WeighParams w) {
+  using S = WeighShape<D, NT, QP>;
+  using G = Granule<D>;
+  constexpr int RT = S::kRows, kMt = D / 16, kSt = S::kStages, kSteps = G::kSteps, kKeys = G::kKeys;
+  const Params& p = w.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  int64_t* const plan = reinterpret_cast<int64_t*>(smem + S::kPlanOff);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + S::kCtlOff);
+  const uint32_t base = ptx::smem_u32(smem);
+  const uint32_t ring = base + warp * kSt * S::kStage;
+  const uint32_t bars = base + S::kBarOff + warp * kSt * 8;
+  const uint32_t stall_bar = base + S::kBarOff + S::kWarps * kSt * 8;
+  if (lane == 0) {
+    for (int i = 0; i < kSt; ++i) ptx::mbar_init(bars + i * 8, 1);
+    if (warp == 0) {
+      ptx::mbar_init(stall_bar, 1);
+      *abort_flag = 0;
+    }
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  ptx::wait_dependencies();
+  const int n_seqs = p.rows.n_seqs;
+  const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  make_plan_of<S::kWarps * 32>(n_seqs, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff), [&](int b) {
+    const WeighSeq s = weigh_seq<D, RT>(w, b);
+    if (s.over && s.rows > 0 && blockIdx.x == 0) kv::report(p.status, kv::kSiteTokens);
+    return s.gpi > 0 ? static_cast<int64_t>(p.hkv) * (s.gpi + kSetup) : 0;
+  });
+  if (p.stall && blockIdx.x == 0 && warp == 0) {  // test only
+    sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+    return;
+  }
+  const int64_t W = plan[n_seqs];
+  const int64_t most = static_cast<int64_t>(gridDim.x) * S::kWarps, n_workers = W < most ? W : most;
+  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
+  if (worker >= n_workers) return;
+  const int64_t lo = share(W, n_workers, worker);
+  Walk<D, RT> c;
+  {
+    int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (plan[mid] <= lo) a = mid;
+      else z = mid - 1;
+    }
+    c.b = a;
+    c.s = weigh_seq<D, RT>(w, a);
+    const int64_t off = lo - plan[a];
+    c.head = static_cast<int>(off / (c.s.gpi + kSetup));
+    const int at = static_cast<int>(off - static_cast<int64_t>(c.head) * (c.s.gpi + kSetup));
+    c.left = share(W, n_workers, worker + 1) - lo;
+    if (at < kSetup) c.left -= kSetup - at;
+    if (c.left <= 0) return;
+    c.enter(at < kSetup ? 0 : at - kSetup);
+  }
+  Walk<D, RT> f = c;  // where the copies are
+  bool more = true;   // to copy
+  Feed<D, RT, 1> feed{{f.b, f.head, 0, f.g, 0, 0}, 0, f.s.tokens, -32, -1};
+
+  auto issue = [&](int st) {
+    const uint32_t dst = ring + st * S::kStage, bar = bars + st * 8;
+    if (feed.c.b != f.b) {
+      feed.c.b = f.b;
+      feed.keys = f.s.tokens;
+      feed.window = -32;
+    }
+    feed.c.head = f.head;
+    feed.c.g = f.g;
+    // old weights of the first block of rows; pages for the way back
+    const int key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, kKeys), part = min(p.page, kKeys);
+    uint32_t tx = 0;
+    for (int k = 0, i = 0; k < wanted; k += part, ++i) {
+      const int page = feed.page_of(p, lane, (key0 + k) >> p.page_log2);
+      if (lane == 0)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + S::kPageOff + 4 * i), "r"(page) : "memory");
+      if (page >= 0 && f.block == 0) {
+        const uint32_t bytes = ((min(wanted - k, part) + 3) & ~3) * 4;
+        tx += bytes;
+        if (lane == 0) {
+          const int64_t at = static_cast<int64_t>(page * p.hkv + f.head) * p.page + ((key0 + k) & (p.page - 1));
+          ptx::bulk_load(dst + S::kOldOff + 4 * k, w.weight + at, bytes, bar);
+        }
+      }
+    }
+    feed.granule(p, lane, dst, bar, tx);
+    more = f.next(w);
+  };
+
+  uint32_t qf[NT * QP][kMt][2];
+  float fac[NT][2], lse2[NT][2];  // of the lane's two query rows 2 tig, 2 tig + 1 in each tile
+  int lim[NT][2];
+  int lim_min = 0;
+  auto begin_block = [&]() {
+    const int row_q = c.block * RT, n_rows = c.s.rows * p.group;
+    int lmin = 0x7fffffff;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int rho = row_q + n * 8 + gid;  // the lane's part of query row gid of the tile
+      const bool live = rho < n_rows;
+      const int t = live ? rho / p.group : 0;
+      const int64_t out = (c.s.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
+      const int lm = live ? visible(p, c.s.tokens, c.s.pos0 + t) : 0;
+      // a row whose LSE is not finite has no weights to give
+      const float lse = live ? __ldg(p.lse + out) : INFINITY;
+      const float l2 = fabsf(lse) < INFINITY ? lse * kLog2e : INFINITY;
+      if (live) lmin = min(lmin, lm);
+      const float f = query_operands<D, QP>(p, out * D, live, tig, &qf[n * QP]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);
+        lim[n][r] = __shfl_sync(kFull, lm, (2 * tig + r) * 4);
+        lse2[n][r] = __shfl_sync(kFull, l2, (2 * tig + r) * 4);
+      }
+    }
+    lim_min = __reduce_min_sync(kFull, lmin);
+  };
+
+  auto granule = [&](int st) {
+    const uint32_t tile = ring + st * S::kStage;
+    const int key0 = c.g * kKeys;
+    const bool masked = key0 + kKeys > lim_min;
+    float sum[2 * kSteps];  // key key_at(i, u, gid)
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4]) {
+#pragma unroll
+        for (int n = 0; n < NT * QP; ++n) ptx::mma_f16(s[n / QP], a, qf[n][j][0], qf[n][j][1]);
+      });
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float e = ex2(fmaf(s[n][2 * u + r], fac[n][r], -lse2[n][r]));
+            x += masked && key0 + key_at<D>(i, u, gid) >= lim[n][r] ? 0.0f : e;
+          }
+        x += __shfl_xor_sync(kFull, x, 1);
+        x += __shfl_xor_sync(kFull, x, 2);
+        sum[2 * i + u] = x;
+      }
+    }
+    // lane (gid, tig) writes the keys of sums tig and, at D = 64, tig + 4
+#pragma unroll
+    for (int q = 0; q < kSteps / 2; ++q) {
+      const float x = tig == 0 ? sum[4 * q] : tig == 1 ? sum[4 * q + 1] : tig == 2 ? sum[4 * q + 2] : sum[4 * q + 3];
+      const int k = key_at<D>(2 * q + (tig >> 1), tig & 1, gid), key = key0 + k;
+      if (key >= c.s.tokens) continue;
+      const int page = static_cast<int>(lds32(tile + S::kPageOff + (p.page >= kKeys ? 0 : 4 * (k >> p.page_log2))));
+      if (page < 0) continue;
+      float* const at = w.weight + static_cast<int64_t>(page * p.hkv + c.head) * p.page + (key & (p.page - 1));
+      float old = 0.0f;
+      if (c.block > 0) old = *at;  // what this lane wrote
+      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(tile + S::kOldOff + 4 * k));
+      *at = old + x;
+    }
+  };
+
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+  };
+  int st = 0, in_flight = 0;
+  uint32_t parity = 0;
+  for (int i = 0; i < kSt; ++i)
+    if (more) {
+      issue(i);
+      ++in_flight;
+    }
+  begin_block();
+  while (in_flight > 0) {
+    if (!wait(bars + st * 8, parity)) break;
+    granule(st);
+    __syncwarp();
+    if (more) issue(st);
+    else --in_flight;
+    if (++st == kSt) {
+      st = 0;
+      parity ^= 1u;
+    }
+    const int block = c.block, head = c.head, b = c.b;
+    if (c.next(w) && (c.block != block || c.head != head || c.b != b)) begin_block();
+  }
+  for (int i = 0; i < in_flight; ++i) {  // after a wait that ran out: copies in flight must not outlive the block
+    sync::wait_drain(bars + st * 8, parity, p.timeout_ns);
+    if (++st == kSt) {
+      st = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
+template <int D, int NT, int QP>
+cp_status run_weigh(const WeighParams& w, int num_sms, cudaStream_t s) {
+  using S = WeighShape<D, NT, QP>;
+  constexpr int most_smem = 128 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8;
+  static_assert(most_smem <= 232448, "shared memory of a block");
+  const auto kernel = kv4_weigh_kernel<D, NT, QP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_weigh_kernel attribute");
+  const Params& p = w.p;
+  const double most = (static_cast<double>(p.rows.max_pages) * p.page / kKeysOf<D> + 1 + kSetup) * p.hkv * p.rows.n_seqs;
+  if (most > 1e12) {
+    set_error("cp_kv4_cache_weigh: max_pages * page_size * hkv * n_seqs is too large for one call");
+    return CP_ERR_INVALID_ARG;
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(most < num_sms ? most : num_sms));
+  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.dynamicSmemBytes = 128 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
+  e = cudaLaunchKernelEx(&cfg, kernel, w);
+  return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv4_weigh_kernel launch");
+}
+
+template <int D>
+cp_status run_weigh_d(const WeighParams& w, int nt, int num_sms, cudaStream_t s) {
+  if (w.p.q_bf16)
+    return nt == 1   ? run_weigh<D, 1, 1>(w, num_sms, s)
+           : nt == 2 ? run_weigh<D, 2, 1>(w, num_sms, s)
+                     : run_weigh<D, 4, 1>(w, num_sms, s);
+  return nt == 1 ? run_weigh<D, 1, 2>(w, num_sms, s) : run_weigh<D, 2, 2>(w, num_sms, s);
+}
+
+}  // namespace
+}  // namespace kvattn
+
+cp_status launch_kv4_weigh(const cp_kv4_weigh_desc& d, float scale, int64_t timeout_ns, int num_sms, cudaStream_t s) {
+  using namespace kvattn;
+  const cp_kv4_cache& c = d.cache;
+  WeighParams w{};
+  Params& p = w.p;
+  p.tile[0] = static_cast<const uint8_t*>(c.k);
+  p.rows = d.rows;
+  p.n_pages = c.n_pages;
+  p.q = d.q;
+  p.lse = const_cast<float*>(d.lse);
+  p.q_first = d.q_first;
+  p.hq = d.hq;
+  p.hkv = c.hkv;
+  p.group = d.hq / c.hkv;
+  p.page = c.page_size;
+  p.page_log2 = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  p.q_bf16 = d.in_dtype == CP_BF16;
+  p.stall = (d.flags & CP_FLAG_TEST_STALL) != 0;
+  p.scale_log2 = scale * kLog2e;
+  p.kv_pos = d.kv_pos;
+  p.status = d.status;
+  p.timeout_ns = timeout_ns;
+  w.weight = d.weight;
+  w.known = d.known;
+  w.decay = d.decay;
+  // the fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries)
+  const int64_t per = (d.rows.n_rows + d.rows.n_seqs - 1) / d.rows.n_seqs * p.group;
+  const int nt = per <= 8 ? 1 : per <= 16 || !p.q_bf16 ? 2 : 4;
+  return c.d == 128 ? run_weigh_d<128>(w, nt, num_sms, s) : run_weigh_d<64>(w, nt, num_sms, s);
+}
+
+}  // namespace cpattn

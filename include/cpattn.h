@@ -528,6 +528,161 @@ cp_status cp_kv_cache_attn(const cp_kv_attn_desc* desc, cudaStream_t stream);
 cp_status cp_kv_cache_attn_workspace(const cp_kv_attn_desc* desc, int64_t* bytes_out);
 
 /*
+ * ---------------------------------------------------------------- 4-bit KV cache
+ * The same cache in a little over half of the bytes, with tokens that can leave it.  One page and head is page_size rows
+ * of d * 9 / 16 bytes:
+ *   numbers  e2m1 (sign, two exponent bits of bias 1, one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the
+ *            even element in the low nibble
+ *   scales   a byte for each 16 numbers: five exponent bits (bias 15), three fraction bits, no sign, that is the
+ *            upper bits of a half; the cached number is e2m1 * scale, exact in bf16 and in f16
+ * A group's scale is the number of that format nearest to a sixth of its largest magnitude (ties to even), from 2^-17 to
+ * 10240, or 0 (the group then reads back as zeros): magnitudes above 61440 become 61440.  Numbers are rounded to
+ * nearest even, to 6 times the scale at most.  A group that holds an infinity or NaN gets the byte 255 and codes of 0 and
+ * reads back as NaN.  No other bytes above 226 are written, and none may be there.
+ * Every token is on its own: writing one changes no other, and rows can be moved as they are.
+ * Pages, rows and tables are as for the 8-bit cache (cp_kv_rows).
+ */
+typedef struct {
+  void* k; /* device [n_pages, hkv, page_size, d * 9 / 16] bytes, 16-byte aligned */
+  void* v;
+  int64_t n_pages;
+  int32_t page_size; /* 16, 32, 64 or 128 */
+  int32_t hkv;       /* at most 65536 */
+  int32_t d;         /* 64 or 128 */
+  int32_t reserved;
+} cp_kv4_cache;
+
+/*
+ * cp_kv4_cache_write -- stores new tokens: rows->tokens[b] is the number of tokens that sequence b already has, and its
+ * rows become the tokens tokens[b], tokens[b] + 1, ...  Rows whose page is bad (cp_kv_rows) are not stored.  No place may
+ * be written twice at once.
+ * Arguments: k, v device [n_rows, hkv, d] (in_dtype CP_F32 or CP_BF16), 16-byte aligned; status device int32 or NULL
+ * (see cp_kv_rows; the caller zeroes it).
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.
+ */
+cp_status cp_kv4_cache_write(const cp_kv4_cache* cache, const cp_kv_rows* rows, const void* k, const void* v,
+                             int32_t in_dtype, int32_t* status, cudaStream_t stream);
+
+/*
+ * cp_kv4_cache_read -- the way back, as cp_kv_cache_read: exact in both out_dtypes.  Rows whose page is bad are left as
+ * they were.
+ */
+cp_status cp_kv4_cache_read(const cp_kv4_cache* cache, const cp_kv_rows* rows, void* k, void* v, int32_t out_dtype,
+                            int32_t* status, cudaStream_t stream);
+
+/*
+ * cp_kv4_cache_attn -- attention of each sequence's new tokens over its cached ones as an (O, LSE) partial.  Arguments,
+ * results, limits and errors are cp_kv_cache_attn's (cp_kv_attn_desc).
+ * A token with a NaN key makes the rows that see it NaN; a NaN value does so in its group of 16 columns.
+ * Precision: sums and softmax statistics are fp32.  Queries are taken exactly (bf16) or to 22 bits (fp32), but no finer
+ * than 2^-38 of their row's largest element.  Weights are taken to 11 bits for a bf16 output and to 22 for an fp32 one, but
+ * no finer than 2^-40 of the row's largest.
+ */
+typedef struct {
+  cp_kv4_cache cache;
+  cp_kv_rows rows;
+  const void* q;
+  void* o;
+  float* lse;
+  const int32_t* q_first;
+  int32_t in_dtype;
+  int32_t o_dtype;
+  int32_t hq;
+  float scale;
+  cp_posmap kv_pos;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;
+  int32_t wait_timeout_ms;
+  int32_t flags;
+} cp_kv4_attn_desc;
+
+cp_status cp_kv4_cache_attn(const cp_kv4_attn_desc* desc, cudaStream_t stream);
+
+/* Bytes of workspace for a cp_kv4_cache_attn call; reads the shapes and dtypes of desc only. */
+cp_status cp_kv4_cache_attn_workspace(const cp_kv4_attn_desc* desc, int64_t* bytes_out);
+
+/*
+ * cp_kv4_cache_weigh -- the attention weight that cached tokens gather, for cp_kv4_cache_evict: for each sequence b that
+ * has rows in the call, each of its first rows->tokens[b] tokens j and each KV head,
+ *   weight := (j < known[b] ? decay * weight : 0) + sum of exp(scale * (q . k_j) - lse)
+ * over the rows that see the token (q_first and kv_pos as for the attention) and the KV head's query heads.
+ *   weight   device fp32 [n_pages, hkv, page_size]: laid out as the cache, 16-byte aligned
+ *   q, lse   device [n_rows, hq, d] (in_dtype), 16-byte aligned; fp32 [n_rows, hq]: the rows' final LSE, merged over the
+ *            ranks, so that the weights of all ranks' tokens add up to 1 for each row and query head.  A row and head
+ *            whose lse is not finite gives nothing.
+ *   known    device int32 [n_seqs] or NULL: how many of the tokens have gathered weight already; the memory of the others
+ *            need not be initialised.  NULL: all.  With decay 0 no old weight is looked at.
+ *   decay    in [0, 1]
+ *   status, wait_timeout_ms, flags  as for the attention
+ * The weights of other tokens and of sequences without rows stay as they are.  A key that is NaN gets NaN.  Tokens on a
+ * bad page are left out.  Every weight has one writer and one order of its sum, which depends on the shapes alone.  No page
+ * may belong to two sequences of a call.
+ * Limits and errors are the attention's; max_pages * page_size * hkv * n_seqs is below 1e13.
+ */
+typedef struct {
+  cp_kv4_cache cache; /* v is not looked at */
+  cp_kv_rows rows;
+  float* weight;
+  const void* q;
+  const float* lse;
+  const int32_t* q_first;
+  const int32_t* known;
+  int32_t in_dtype;
+  int32_t hq;
+  float scale;
+  float decay;
+  cp_posmap kv_pos;
+  int32_t* status;
+  int32_t wait_timeout_ms;
+  int32_t flags;
+} cp_kv4_weigh_desc;
+
+cp_status cp_kv4_cache_weigh(const cp_kv4_weigh_desc* desc, cudaStream_t stream);
+
+/*
+ * cp_kv4_cache_evict -- shortens every sequence of more than `keep` tokens to `keep`: its last `recent` tokens stay, and of
+ * the others the z = keep - recent whose weight, summed over the KV heads, is largest (of equal ones the earlier; NaN is
+ * below everything).  Rows of K and V and their weights move: of the slots below z those whose token stays are as they
+ * were, the others receive, in order, the tokens that stay from slot z on; the recent tokens follow from slot z on in
+ * their order.  What slots from `keep` on hold then belongs to no token.
+ *   tokens      device int32 [n_seqs]: tokens of each sequence
+ *   page_table  device int32 [n_seqs, max_pages]; no page may belong to two sequences or stand twice in a table
+ *   kept        device int32 [n_seqs, keep], written: the slot that each slot's token had, -1 behind the sequence's end
+ *   new_tokens  device int32 [n_seqs], written: tokens of each sequence afterwards; may be `tokens` itself
+ *   workspace   device memory, 16-byte aligned, of at least cp_kv4_cache_evict_workspace bytes; it need not be initialised
+ *               and holds nothing afterwards.  Calls that may overlap need one each.
+ *   status      device int32 or NULL: CP_ERR_INVALID_ARG | (site << 8) where a sequence has a negative count (taken for 0),
+ *               more tokens than its table has pages for, or a page outside [0, n_pages).  The latter two are left as they
+ *               are, with `kept` naming their first slots.
+ * Since keys are stored rotated, where a token stands does not matter to later rows that see all of the cache.  Causal rows
+ * are right as long as every evicted sequence's q_first[b] is lowered by kv_pos.stride for each token that it lost and no
+ * row stands before a token that was not among the recent ones.
+ * 1 <= keep, n_seqs * keep below 2^31, 0 <= recent <= keep, max_pages * page_size at most 2e9.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA.
+ */
+typedef struct {
+  cp_kv4_cache cache;
+  float* weight;
+  const int32_t* tokens;
+  const int32_t* page_table;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t keep;
+  int32_t recent;
+  int32_t* kept;
+  int32_t* new_tokens;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;
+} cp_kv4_evict_desc;
+
+cp_status cp_kv4_cache_evict(const cp_kv4_evict_desc* desc, cudaStream_t stream);
+
+/* Bytes of workspace for a cp_kv4_cache_evict call; reads the shapes of desc only. */
+cp_status cp_kv4_cache_evict_workspace(const cp_kv4_evict_desc* desc, int64_t* bytes_out);
+
+/*
  * ---------------------------------------------------------------- rotary positions
  * cp_rope_axes -- rotary position embedding with one to four position axes (text, or time, height
  * and width of a video token), of up to four tensors of the same tokens (queries and keys) in one
