@@ -16,8 +16,9 @@
 namespace cpattn {
 namespace kvattn {
 
-constexpr int kPExp = 15;       // P operands are below 2^(kPExp + kTop) = 65490 and f16's largest is 65504
-constexpr float kTop = 0.999f;  // largest s - m
+constexpr int kPExp = 12;       // P operands are at most 2^(kPExp + kSlack) = 32768 and f16's largest is 65504
+constexpr float kPUnit = 4096.0f;  // 2^kPExp
+constexpr float kSlack = 3.0f;  // largest s - m
 
 // QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
 template <int D, int NT, int QP, int PP>
@@ -34,16 +35,17 @@ struct Shape4 {
   static constexpr int kSteps = Granule<D>::kSteps;
   static constexpr int kRow = Granule<D>::kRow;
   static constexpr int kHalf = Granule<D>::kHalf;
-  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStage = 2 * Granule<D>::kPair;  // keys, values
   static constexpr bool kQSmem = D == 128 && NT * QP >= 4;  // query operands in shared memory
-  static constexpr int kStages = kHeavy && !kQSmem ? 5 : 3;
+  static constexpr int kStages = kHeavy && !kQSmem ? 3 : 2;
   static constexpr int kQBytes = kQSmem ? NT * QP * (D / 16) * 256 : 0;
   static constexpr int kWarpBytes = kStages * kStage + kQBytes;
-  // behind the warps' parts: barriers, control, plan
+  // behind the warps' parts: barriers, control.  The plan is looked at before the first copies and lies where they go.
   static constexpr int kBarOff = kWarps * kWarpBytes;  // [warp][stage] + stall
   static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
   static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;  // [warp] 8 bytes
-  static constexpr int kPlanOff = kScanOff + 16 * 8;
+  static constexpr int kBytes = kScanOff + 16 * 8;
+  static_assert(kBarOff >= (CP_KV_MAX_SEQS + 1) * 8, "the plan fits the rings");
 };
 
 // SOLO: 0 split, 1 one block an item, 2 a cluster of p.cluster blocks an item.
@@ -59,7 +61,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
-  int64_t* const plan = reinterpret_cast<int64_t*>(smem + S::kPlanOff);
+  int64_t* const plan = reinterpret_cast<int64_t*>(smem);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + S::kCtlOff);
   const uint32_t base = ptx::smem_u32(smem);
   const uint32_t ring = base + warp * S::kWarpBytes;
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
   Cursor c;  // where the products are
   Seq seq;
-  int64_t left;  // numbers of the share from the cursor on
+  int left;      // numbers of the share from the cursor on; at most 1e12 / (8 * 152) where the grid is full
   bool inside;   // the share begins inside of an item
   const bool stalled = p.stall && blockIdx.x == 0 && warp == 0;  // test only
   // SOLO: rank of the block among those of its item, and the warp and number of warps among all of them
@@ -115,33 +117,36 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   } else {
     make_plan<D, RT, S::kWarps * 32>(p, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff));
     ptx::launch_dependents();
-    if (stalled) {
-      sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
-      return;
-    }
     const int64_t W = plan[n_seqs];
     const int64_t n_workers = workers(p, W, static_cast<int64_t>(gridDim.x) * S::kWarps);
-    if (worker >= n_workers) return;
-    const int64_t lo = share(W, n_workers, worker), hi = share(W, n_workers, worker + 1);
-    left = hi - lo;
-    int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
-    while (a < z) {
-      const int mid = (a + z + 1) >> 1;
-      if (plan[mid] <= lo) a = mid;
-      else z = mid - 1;
+    const bool idle = worker >= n_workers || stalled;
+    left = 0;
+    inside = false;
+    if (!idle) {
+      const int64_t lo = share(W, n_workers, worker), hi = share(W, n_workers, worker + 1);
+      left = static_cast<int>(hi - lo);
+      int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
+      while (a < z) {
+        const int mid = (a + z + 1) >> 1;
+        if (plan[mid] <= lo) a = mid;
+        else z = mid - 1;
+      }
+      c.b = a;
+      seq = seq_of<D, RT>(p, a);
+      const int64_t off = lo - plan[a];
+      const int64_t item = off / (seq.gpi + kSetup);
+      const int at = static_cast<int>(off - item * (seq.gpi + kSetup));
+      inside = at >= kSetup;
+      c.g = inside ? at - kSetup : 0;
+      if (!inside) left -= kSetup - at;
+      c.head = static_cast<int>(item / seq.blocks);
+      c.block = static_cast<int>(item - static_cast<int64_t>(c.head) * seq.blocks);
+      c.gpi = seq.gpi;
+      c.blocks = seq.blocks;
     }
-    c.b = a;
-    seq = seq_of<D, RT>(p, a);
-    const int64_t off = lo - plan[a];
-    const int64_t item = off / (seq.gpi + kSetup);
-    const int at = static_cast<int>(off - item * (seq.gpi + kSetup));
-    inside = at >= kSetup;
-    c.g = inside ? at - kSetup : 0;
-    if (!inside) left -= kSetup - at;
-    c.head = static_cast<int>(item / seq.blocks);
-    c.block = static_cast<int>(item - static_cast<int64_t>(c.head) * seq.blocks);
-    c.gpi = seq.gpi;
-    c.blocks = seq.blocks;
+    ptx::fence_proxy_async_smem();
+    __syncthreads();  // the plan has been read: the copies may begin
+    if (stalled) sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
     if (left <= 0) return;
   }
   bool ok = true;
@@ -149,27 +154,33 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     ok = sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
     left = 0;
   }
-  const int g_first = c.g, solo_left = static_cast<int>(left);  // of a block of rows, where SOLO
-  Feed<D, RT, 2> f{c, left, seq.keys, -32, -1};
+  const int g_first = c.g, solo_left = left;  // of a block of rows, where SOLO
+  Cursor f = c;         // where the copies are
+  int to_issue = left;
+  Feed<D, 2> feed{c.b, c.head, seq.keys, -32, -1};
 
-  // Starts the copies of the next granule into stage `st`.
+  // Starts the copies of the next granules into stage `st`.
   auto issue = [&](int st) {
-    f.granule(p, lane, ring + st * S::kStage, bars + st * 8);
-    --f.left;
-    if (++f.c.g == f.c.gpi && f.left > kSetup) {
-      f.left -= kSetup;
-      f.c.g = 0;
-      if (++f.c.block == f.c.blocks) {
-        f.c.block = 0;
-        if (++f.c.head == p.hkv) {
-          Seq s{};
-          next_seq<D, RT>(p, f.c, s);
-          f.keys = s.keys;
-          f.window = -32;
+    const int n = together(f.g, min(f.gpi, f.g + to_issue));
+    feed.stage(p, lane, f.g, n, ring + st * S::kStage, bars + st * 8);
+    to_issue -= n;
+    f.g += n;
+    if (f.g == f.gpi) {
+      to_issue -= kSetup;
+      if (to_issue > 0) {
+        f.g = 0;
+        if (++f.block == f.blocks) {
+          f.block = 0;
+          if (++f.head == p.hkv) {
+            Seq s{};
+            next_seq<D, RT>(p, f, s);
+            feed.b = f.b;
+            feed.keys = s.keys;
+            feed.window = -32;
+          }
+          feed.head = f.head;
         }
       }
-    } else if (f.c.g == f.c.gpi) {
-      f.left = 0;
     }
   };
 
@@ -247,12 +258,12 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   // Where some row of the block does not see all keys of the granule: values that no row sees count as zero, by
   // their scales (0 * NaN would not vanish), and NaN among values that only some of the rows see go to those rows'
   // accumulators and are taken out.
-  auto mask_values = [&](uint32_t tile) {
-    const int key0 = c.g * kKeys, first = max(lim_min - key0, 0);  // below kKeys
+  auto mask_values = [&](uint32_t tile, int key0) {
+    const int first = max(lim_min - key0, 0);  // below kKeys
     bool odd = false;
 #pragma unroll
     for (int k = lane; k < kKeys; k += 32) {
-      const uint32_t at = tile + S::kHalf + k * S::kRow + D / 2;
+      const uint32_t at = tile + k * S::kRow + D / 2;
       uint32_t v[D / 64];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     if (__any_sync(kFull, odd)) {
 #pragma unroll 1
       for (int k = first; k < kKeys && key0 + k < lim_max; ++k) {
-        const uint32_t at = tile + S::kHalf + k * S::kRow + D / 2 + (D == 128 ? gid : gid >> 1);
+        const uint32_t at = tile + k * S::kRow + D / 2 + (D == 128 ? gid : gid >> 1);
         const bool nan = lds8(at) >= 0xf8u;
         __syncwarp();
         if (nan) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
@@ -287,29 +298,31 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   // branches and predicates, not variants: with four variants a warp's items of a few granules ran at the
   // speed of the instruction cache (62 x 16 items of some 3 granules, up to 60 rows, D = 64: 86 us, more than half
   // of the stalls; 55 with one path, and 16-row items of 8192 tokens 102 against 106).
-  auto granule = [&](int st, bool masked) {
-    const uint32_t tile = ring + st * S::kStage;
-    const int key0 = c.g * kKeys;
+  auto granule = [&](uint32_t tile, int key0) {
+    const bool masked = key0 + kKeys > lim_min;
+    const uint32_t values = tile + Granule<D>::kPair;
     const bool both = NT == 1 || live > 1;
     auto product = [&](int n, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
       if (n == 0) ptx::mma_f16(d, a, b0, b1);
       else ptx::mma_f16_if(d, a, b0, b1, both);
     };
-    if (masked) mask_values(tile);
+    if (masked) mask_values(values, key0);
     // S^T: s[n][i][2 u + r] is key key_at(i, u, gid) for query row 2 tig + r of tile n
     float s[NT][kSteps][4];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < kSteps; i += 2) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.0f;
-      key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4]) {
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][i][e] = s[n][i + 1][e] = 0.0f;
+      key_operands<D>(tile, i, gid, tig, [&](int step, int j, const uint32_t (&a)[4]) {
 #pragma unroll
         for (int n = 0; n < NT * QP; ++n) {
           if constexpr (S::kQSmem) {
             const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
-            product(n / QP, s[n / QP][i], a, b.x, b.y);
+            product(n / QP, s[n / QP][step], a, b.x, b.y);
           } else {
-            product(n / QP, s[n / QP][i], a, qf[n][j][0], qf[n][j][1]);
+            product(n / QP, s[n / QP][step], a, qf[n][j][0], qf[n][j][1]);
           }
         }
       });
@@ -325,52 +338,56 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
             for (int u = 0; u < 2; ++u)
               if (key0 + key_at<D>(i, u, gid) >= lim[n][r]) s[n][i][2 * u + r] = -INFINITY;
     }
-    // Maxima.  s keeps the products; a score is s * fac (fac > 0).  m moves by whole numbers: rescaling is exact, and rare.
-    float down[NT][2];
+    // Maxima.  s keeps the products; a score is s * fac (fac > 0).  m is a whole number, so rescaling is exact, and it
+    // moves only where a score is more than kSlack above it: mostly a comparison by every lane on its own is enough.
     bool grew = false;
+    float top[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float top = -INFINITY;
+        top[n][r] = fmaxf(s[n][0][r], s[n][0][2 + r]);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) top = fmaxf(top, fmaxf(s[n][i][r], s[n][i][2 + r]));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-        top *= fac[n][r];
-        const bool up = top - m[n][r] > kTop;  // false where both are -inf
-        grew |= up;
-        const float now = up ? floorf(top + (1.0f - kTop)) : m[n][r];
-        down[n][r] = up ? m[n][r] - now : 0.0f;
-        m[n][r] = now;
+        for (int i = 1; i < kSteps; ++i) top[n][r] = fmaxf(top[n][r], fmaxf(s[n][i][r], s[n][i][2 + r]));
+        top[n][r] *= fac[n][r];
+        grew |= top[n][r] > m[n][r] + kSlack;  // false where both are -inf
       }
     if (__any_sync(kFull, grew)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float c0 = ex2(down[n][0]), c1 = ex2(down[n][1]);
-        l[n][0] *= c0;
-        l[n][1] *= c1;
+        float c[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x = top[n][r];
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+          const float now = x > m[n][r] + kSlack ? floorf(x) : m[n][r];
+          c[r] = now > m[n][r] ? ex2(m[n][r] - now) : 1.0f;
+          m[n][r] = now;
+          l[n][r] *= c[r];
+        }
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
-          acc[n][j][0] *= c0;
-          acc[n][j][1] *= c1;
-          acc[n][j][2] *= c0;
-          acc[n][j][3] *= c1;
+          acc[n][j][0] *= c[0];
+          acc[n][j][1] *= c[1];
+          acc[n][j][2] *= c[0];
+          acc[n][j][3] *= c[1];
           if constexpr (kHold) {
-            held[j][0] *= c0;
-            held[j][1] *= c1;
-            held[j][2] *= c0;
-            held[j][3] *= c1;
+            held[j][0] *= c[0];
+            held[j][1] *= c[1];
+            held[j][2] *= c[0];
+            held[j][3] *= c[1];
           }
         }
       }
     }
-    // Weights as operands, times 2^kPExp: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid
+    // Weights as operands, times 2^kPExp: pb[n][part][i][u], keys 2 tig, 2 tig + 1 of group u for query row gid.  The power
+    // of two is not part of the exponent's argument, whose rounding would be that of a number of 12.
     uint32_t pb[NT][PP][kSteps][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0] - kPExp, m[n][1] == -INFINITY ? 0.0f : m[n][1] - kPExp};
+      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -381,18 +398,20 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
             w[r] = ex2(fmaf(s[n][i][2 * u + r], fac[n][r], -ref[r]));
             l[n][r] += w[r];
           }
-          const uint32_t h = to_f16x2(w[0], w[1]);
+          float a, b;
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(w[0], w[1]), ptx::f2_pack(kPUnit, kPUnit)), a, b);
+          const uint32_t h = to_f16x2(a, b);
           pb[n][0][i][u] = ptx::transpose8x8(h);
           if constexpr (PP == 2) {
             const float2 back = from_f16x2(h);
-            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(w[0] - back.x, w[1] - back.y));
+            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(a - back.x, b - back.y));
           }
         }
     }
     // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      value_operands<D>(tile, i, gid, tig, [&](int w, const uint32_t (&a)[4]) {
+      value_operands<D>(values, i, gid, tig, [&](int w, const uint32_t (&a)[4]) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -473,8 +492,8 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         if (rho >= n_rows) continue;
         const float keep = keep_of(n, r);
         const int up = min(max(static_cast<int>(__float_as_uint(sum) >> 23 & 255u) - 127, -100), 126);
-        const float norm = sum * kv::pow2(-up), ref = m[n][r] + static_cast<float>(up - kPExp);
-        const float back = kv::pow2(-up);
+        const float norm = sum * kv::pow2(-up), ref = m[n][r] + static_cast<float>(up);
+        const float back = kv::pow2(-kPExp - up);
         const float f = whole ? (sum == 0.0f ? 0.0f : back / norm) : back;
         float* const part = part_o + local * D + gid * kCols;
         const int t = rho / p.group;
@@ -502,7 +521,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   bool from_start = c.g == 0;  // the item at hand is ours from its first granule on
   while (true) {  // once; for each block of rows where SOLO
     for (int i = 0; i < kSt; ++i)
-      if (f.left > 0) {
+      if (to_issue > 0) {
         issue(st + i < kSt ? st + i : st + i - kSt);
         ++in_flight;
       }
@@ -512,19 +531,21 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         ok = false;
         break;
       }
-      const int key0 = c.g * kKeys;
-      if (key0 < lim_max) {
-        granule(st, key0 + kKeys > lim_min);
+      const int n = together(c.g, min(c.gpi, c.g + left));
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int key0 = (c.g + i) * kKeys;
+        if (key0 < lim_max) granule(ring + st * S::kStage + i * S::kHalf, key0);
       }
       __syncwarp();
-      if (f.left > 0) issue(st);
+      if (to_issue > 0) issue(st);
       else --in_flight;
       if (++st == kSt) {
         st = 0;
         parity ^= 1u;
       }
-      --left;
-      ++c.g;
+      left -= n;
+      c.g += n;
       if (c.g == c.gpi || left == 0) {
         if (SOLO) break;
         const int64_t slot = worker * 2 + (inside ? 0 : 1);
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
           if (++c.head == p.hkv) next_seq<D, RT>(p, c, seq);
         }
         begin_item();
-      } else if (++since == S::kFlush && (kHold || !SOLO)) {  // 16 granules need no more
+      } else if ((since += n) >= S::kFlush && (kHold || !SOLO)) {  // 16 granules need no more
         flush();
       }
     }
@@ -628,9 +649,9 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     if constexpr (SOLO == 2) ptx::cluster_sync();
     else __syncthreads();
     if (++c.block == c.blocks || (SOLO == 2 ? stop != 0 : *abort_flag != 0)) break;
-    f.c.block = c.block;
-    f.c.g = c.g = g_first;
-    left = f.left = solo_left;
+    f.block = c.block;
+    f.g = c.g = g_first;
+    left = to_issue = solo_left;
   }
   if (!ok) {
     // copies in flight must not outlive the block: those of this granule and, where there was more to
@@ -648,14 +669,13 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
 template <int D, int NT, int QP, int PP>
 cp_status run4(const Params& p, const Plan& pl, int64_t items, int num_sms, cudaStream_t s) {
   using S = Shape4<D, NT, QP, PP>;
-  constexpr int most_smem = 128 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8;
-  static_assert(most_smem <= 232448, "shared memory of a block");
-  const int smem = 128 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
+  constexpr int smem = 128 + S::kBytes;
+  static_assert(smem <= 232448, "shared memory of a block");
   const auto kernel = !pl.solo           ? kv4_attn_kernel<D, NT, QP, PP, 0>
                       : pl.cluster == 1 ? kv4_attn_kernel<D, NT, QP, PP, 1>
                                         : kv4_attn_kernel<D, NT, QP, PP, 2>;
   // The limit is the function's, not the call's: always the same, for other host threads launch the kernel too.
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_attn_kernel attribute");
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2]{};

@@ -22,8 +22,11 @@ struct Granule {
   static constexpr int kSteps = kKeys / 16;  // steps of 16 keys
   static constexpr int kRow = kv4::kRow<D>;
   static constexpr int kHalf = kKeys * kRow;  // bytes of K (or V): 2304
-  static constexpr int kMt = D / 16;
+  static constexpr int kPair = 2 * kHalf;     // K (or V) of a stage, which holds one granule or two
 };
+// How many granules from g on go through the ring together, of those up to `end`: two from an even one on, which lie in one
+// page or in whole pages.  One wait and one set of copies for two: the rings' upkeep was a quarter of the instructions.
+__device__ __forceinline__ int together(int g, int end) { return (g & 1) == 0 && g + 1 < end ? 2 : 1; }
 
 // Key of row c of group u (the operand's rows 8 u .. 8 u + 7) in step i.
 template <int D>
@@ -48,43 +51,53 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
-// The operands of K in step i of the granule at `tile`: use(j, a) for each 16 dimensions.  Lane (gid, tig) holds
-// dimensions D / 4 * tig .. + D / 4 - 1 of rows gid of both groups, four of them in each operand.
+// The operands of K in steps i0 and i0 + 1 of the granule at `tile`: use(i, j, a) for each 16 dimensions, the two steps
+// in turn, so that neighbouring products do not wait for one another.  Lane (gid, tig) holds dimensions D / 4 * tig ..
+// + D / 4 - 1 of rows gid of both groups, four of them in each operand.
 template <int D, class F>
-__device__ __forceinline__ void key_operands(uint32_t tile, int i, int gid, int tig, F&& use) {
+__device__ __forceinline__ void key_operands(uint32_t tile, int i0, int gid, int tig, F&& use) {
   using G = Granule<D>;
-  uint32_t word[2][D / 32], scale[2];
+  uint32_t word[2][2][D / 32], scale[2][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint32_t row = tile + key_at<D>(i, u, gid) * G::kRow;
-    if constexpr (D == 128) {
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint2 v = ptx::lds64(row + 16 * tig + 8 * q);
-        word[u][2 * q] = v.x, word[u][2 * q + 1] = v.y;
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t row = tile + key_at<D>(i0 + i, u, gid) * G::kRow;
+      if constexpr (D == 128) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint2 v = ptx::lds64(row + 16 * tig + 8 * q);
+          word[i][u][2 * q] = v.x, word[i][u][2 * q + 1] = v.y;
+        }
+        scale[i][u] = lds16(row + 64 + 2 * tig);
+      } else {
+        word[i][u][0] = lds32(row + 8 * tig), word[i][u][1] = lds32(row + 8 * tig + 4);
+        scale[i][u] = lds8(row + 32 + tig);
       }
-      scale[u] = lds16(row + 64 + 2 * tig);
-    } else {
-      word[u][0] = lds32(row + 8 * tig), word[u][1] = lds32(row + 8 * tig + 4);
-      scale[u] = lds8(row + 32 + tig);
     }
-  }
 #pragma unroll
   for (int q = 0; q < D / 32; ++q) {
-    const uint32_t s0 = kv4::scale_twice(scale[0], q >> 1), s1 = kv4::scale_twice(scale[1], q >> 1);
-    uint32_t x[4], y[4];
-    kv4::to_f16x2(word[0][q], x);
-    kv4::to_f16x2(word[1][q], y);
+    uint32_t x[2][2][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t a[4] = {kv4::mul_f16x2(x[2 * h], s0), kv4::mul_f16x2(y[2 * h], s1),
-                             kv4::mul_f16x2(x[2 * h + 1], s0), kv4::mul_f16x2(y[2 * h + 1], s1)};
-      use(2 * q + h, a);
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t s = kv4::scale_twice(scale[i][u], q >> 1);
+        kv4::to_f16x2(word[i][u][q], x[i][u]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) x[i][u][h] = kv4::mul_f16x2(x[i][u][h], s);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a[4] = {x[i][0][2 * h], x[i][1][2 * h], x[i][0][2 * h + 1], x[i][1][2 * h + 1]};
+        use(i0 + i, 2 * q + h, a);
+      }
   }
 }
 
-// The operands of V^T in step i: use(w, a) for each tile w of 16 columns of O, whose rows gid and gid + 8 are columns
+// The operands of V^T in step i of the values at `tile`: use(w, a) for each tile w of 16 columns of O, whose rows gid and gid + 8 are columns
 // D / 8 * gid + 2 w and + 1.  Nibbles of two keys are put side by side before they become halves.
 template <int D, class F>
 __device__ __forceinline__ void value_operands(uint32_t tile, int i, int gid, int tig, F&& use) {
@@ -94,7 +107,7 @@ __device__ __forceinline__ void value_operands(uint32_t tile, int i, int gid, in
     uint32_t byte[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const uint32_t row = tile + G::kHalf + key_at<D>(i, x >> 1, 2 * tig + (x & 1)) * G::kRow;
+      const uint32_t row = tile + key_at<D>(i, x >> 1, 2 * tig + (x & 1)) * G::kRow;
       if constexpr (D == 128) {
         const uint2 v = ptx::lds64(row + 8 * gid);
         word[x][0] = v.x, word[x][D / 64 - 1] = v.y;
@@ -163,13 +176,11 @@ __device__ __forceinline__ float query_operands(const Params& p, int64_t at, boo
 }
 
 // Where a warp's copies are: the granules of its share, in order, into the stages of its ring.  TENSORS: K, or K and V.
-template <int D, int RT, int TENSORS>
+template <int D, int TENSORS>
 struct Feed {
   using G = Granule<D>;
-  static constexpr int kStage = TENSORS * G::kHalf;
-  Cursor c;
-  int64_t left;  // numbers to copy
-  int keys;      // tokens of sequence c.b that are wanted
+  int b, head;  // sequence and KV head
+  int keys;     // tokens of the sequence that are wanted
   int window, pages;  // lane i holds page window + i of the sequence, -1 behind its keys
 
   __device__ __forceinline__ int page_of(const Params& p, int lane, int ord) {
@@ -178,44 +189,50 @@ struct Feed {
       // entries that hold no token are the caller's to change at any time: they are not read
       pages = -1;
       if ((static_cast<int64_t>(ord) + lane) << p.page_log2 < keys)
-        pages = static_cast<int>(kv::page_at(p.rows, p.n_pages, c.b, ord + lane));
+        pages = static_cast<int>(kv::page_at(p.rows, p.n_pages, b, ord + lane));
     }
     return __shfl_sync(kFull, pages, ord - window);
   }
+  // Stands in for tokens that have no page: keys that are NaN, which reach the rows that see them, and values of 0.
+  __device__ __forceinline__ void stand_in(const Params& p, int lane, uint32_t dst, int rows) {
+    for (int i = lane; i < rows * G::kRow / 4; i += 32) {
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * i), "r"(0xffffffffu) : "memory");
+      if (TENSORS == 2) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + G::kPair + 4 * i), "r"(0u) : "memory");
+    }
+    ptx::fence_proxy_async_smem();  // before the next copies into the stage
+    __syncwarp();
+    if (lane == 0) kv::report(p.status, kv::kSitePage);
+  }
+  // One lane's: copies `rows` rows, up to a whole group of 4, which is a multiple of 16 bytes and does not leave the page.
+  __device__ __forceinline__ uint32_t copy(const Params& p, int page, int slot, int rows, uint32_t dst, uint32_t bar) {
+    const uint32_t bytes = ((rows + 3) & ~3) * G::kRow;
+    const int64_t at = static_cast<int64_t>((page * p.hkv + head) * p.page + slot) * G::kRow;  // rows: below 2^31
+    ptx::bulk_load(dst, p.tile[0] + at, bytes, bar);
+    if (TENSORS == 2) ptx::bulk_load(dst + G::kPair, p.tile[1] + at, bytes, bar);
+    return TENSORS * bytes;
+  }
 
-  // Starts the copies of the next granule's rows to `dst`, as far as there are tokens; they arrive at `bar`.  What has no
-  // page gets keys that are NaN, which reach the rows that see them, and values of 0.  tx: bytes of other copies to `bar`.
-  __device__ __forceinline__ void granule(const Params& p, int lane, uint32_t dst, uint32_t bar, uint32_t tx = 0) {
-    const int key0 = c.g * G::kKeys;
-    const int wanted = min(keys - key0, G::kKeys);
-    const int part = min(p.page, G::kKeys);  // tokens of one page
-    bool bad = false;
-#pragma unroll 1
-    for (int k = 0; k < wanted; k += part) {
-      const int page = page_of(p, lane, (key0 + k) >> p.page_log2);
-      if (page >= 0) {
-        // whole groups of 4 rows, multiples of 16 bytes; they do not leave the page
-        const uint32_t bytes = ((min(wanted - k, part) + 3) & ~3) * G::kRow;
-        tx += TENSORS * bytes;
-        if (lane < TENSORS) {
-          const int64_t row = static_cast<int64_t>(page * p.hkv + c.head) * p.page + ((key0 + k) & (p.page - 1));
-          ptx::bulk_load(dst + lane * G::kHalf + k * G::kRow, p.tile[lane] + row * G::kRow, bytes, bar);
-        }
-      } else {
-        bad = true;
-        for (int i = lane; i < part * G::kRow / 4; i += 32) {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + k * G::kRow + 4 * i), "r"(0xffffffffu) : "memory");
-          if (TENSORS == 2)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + G::kHalf + k * G::kRow + 4 * i), "r"(0u) : "memory");
-        }
+  // Starts the copies of n granules from g on to `dst`, as far as there are tokens; they arrive at `bar`, whose phase ends
+  // with this call's arrival and the bytes of the copies.  tx: bytes of other copies to `bar`.
+  __device__ __forceinline__ void stage(const Params& p, int lane, int g, int n, uint32_t dst, uint32_t bar, uint32_t tx = 0) {
+    const int key0 = g * G::kKeys;
+    const int wanted = min(keys - key0, n * G::kKeys);
+    if (p.page >= n * G::kKeys) {
+      const int page = page_of(p, lane, key0 >> p.page_log2);
+      if (page < 0) stand_in(p, lane, dst, n * G::kKeys);
+      if (lane == 0) {
+        if (page >= 0) tx += copy(p, page, key0 & (p.page - 1), wanted, dst, bar);
+        ptx::mbar_arrive_expect_tx(bar, tx);
       }
+      return;
     }
-    if (bad) {
-      ptx::fence_proxy_async_smem();  // before the next copies into the stage
-      __syncwarp();
-      if (lane == 0) kv::report(p.status, kv::kSitePage);
+#pragma unroll 1
+    for (int k = 0; k < wanted; k += p.page) {
+      const int page = page_of(p, lane, (key0 + k) >> p.page_log2);
+      if (page < 0) stand_in(p, lane, dst + k * G::kRow, p.page);
+      else if (lane == 0) tx += copy(p, page, 0, min(wanted - k, p.page), dst + k * G::kRow, bar);
     }
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, tx);  // the phase cannot end before
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, tx);
   }
 };
 

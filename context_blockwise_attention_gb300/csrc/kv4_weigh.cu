@@ -27,17 +27,19 @@ struct WeighParams {
 template <int D, int NT, int QP>
 struct WeighShape {
   using G = Granule<D>;
-  static constexpr bool kHeavy = NT * QP * D >= 512;  // query operands take NT QP D / 8 registers
-  static constexpr int kWarps = kHeavy ? 8 : 16;
+  static constexpr bool kHeavy = NT * QP * D >= 256;  // query operands take NT QP D / 8 registers
+  static constexpr int kWarps = kHeavy ? 8 : 12;
   static constexpr int kRows = NT * 8;  // RT
-  static constexpr int kStages = kHeavy ? 6 : 4;
-  static constexpr int kOldOff = G::kHalf;                  // old weights of the granule
-  static constexpr int kPageOff = kOldOff + G::kKeys * 4;   // pages of its parts
-  static constexpr int kStage = kPageOff + 16;
+  static constexpr int kStages = kHeavy ? 4 : 3;
+  static constexpr int kOldOff = G::kPair;                      // old weights of the granules
+  static constexpr int kPageOff = kOldOff + 2 * G::kKeys * 4;   // pages of their parts, 8 at most
+  static constexpr int kStage = kPageOff + 32;
+  // The plan is looked at before the first copies and lies where they go.
   static constexpr int kBarOff = kWarps * kStages * kStage;
   static constexpr int kCtlOff = kBarOff + (kWarps * kStages + 1) * 8;
   static constexpr int kScanOff = (kCtlOff + 8 + 15) / 16 * 16;
-  static constexpr int kPlanOff = kScanOff + 16 * 8;
+  static constexpr int kBytes = kScanOff + 16 * 8;
+  static_assert(kBarOff >= (CP_KV_MAX_SEQS + 1) * 8, "the plan fits the rings");
 };
 
 struct WeighSeq {
@@ -66,19 +68,21 @@ __device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& w, int b) {
 template <int D, int RT>
 struct Walk {
   int b, head, block, g, g0, g1;
-  int64_t left;  // numbers of the share behind this part
+  int left;  // numbers of the share behind this part
   WeighSeq s;
 
   // Takes the part that begins with granule g0 out of `left` numbers that begin there.
   __device__ __forceinline__ void enter(int from) {
     block = 0;
     g = g0 = from;
-    g1 = static_cast<int>(s.gpi - from < left ? s.gpi : from + left);
+    g1 = s.gpi - from < left ? s.gpi : from + left;
     left -= g1 - g0;
   }
-  // To the next granule; false at the end of the share.
+  __device__ __forceinline__ int step() const { return together(g, g1); }
+  // Past the granules of a step; false at the end of the share.
   __device__ __forceinline__ bool next(const WeighParams& w) {
-    if (++g < g1) return true;
+    g += step();
+    if (g < g1) return true;
     if (++block < s.blocks) {
       g = g0;
       return true;
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
-  int64_t* const plan = reinterpret_cast<int64_t*>(smem + S::kPlanOff);
+  int64_t* const plan = reinterpret_cast<int64_t*>(smem);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + S::kCtlOff);
   const uint32_t base = ptx::smem_u32(smem);
   const uint32_t ring = base + warp * kSt * S::kStage;
@@ -131,17 +135,15 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     if (s.over && s.rows > 0 && blockIdx.x == 0) kv::report(p.status, kv::kSiteTokens);
     return s.gpi > 0 ? static_cast<int64_t>(p.hkv) * (s.gpi + kSetup) : 0;
   });
-  if (p.stall && blockIdx.x == 0 && warp == 0) {  // test only
-    sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
-    return;
-  }
+  const bool stalled = p.stall && blockIdx.x == 0 && warp == 0;  // test only
   const int64_t W = plan[n_seqs];
   const int64_t most = static_cast<int64_t>(gridDim.x) * S::kWarps, n_workers = W < most ? W : most;
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
-  if (worker >= n_workers) return;
-  const int64_t lo = share(W, n_workers, worker);
   Walk<D, RT> c;
-  {
+  c.left = 0;
+  bool idle = worker >= n_workers || stalled;
+  if (!idle) {
+    const int64_t lo = share(W, n_workers, worker);
     int a = 0, z = n_seqs - 1;  // the last sequence whose numbers begin at or before lo
     while (a < z) {
       const int mid = (a + z + 1) >> 1;
@@ -153,41 +155,44 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     const int64_t off = lo - plan[a];
     c.head = static_cast<int>(off / (c.s.gpi + kSetup));
     const int at = static_cast<int>(off - static_cast<int64_t>(c.head) * (c.s.gpi + kSetup));
-    c.left = share(W, n_workers, worker + 1) - lo;
+    c.left = static_cast<int>(share(W, n_workers, worker + 1) - lo);
     if (at < kSetup) c.left -= kSetup - at;
-    if (c.left <= 0) return;
-    c.enter(at < kSetup ? 0 : at - kSetup);
+    idle = c.left <= 0;
+    if (!idle) c.enter(at < kSetup ? 0 : at - kSetup);
   }
+  ptx::fence_proxy_async_smem();
+  __syncthreads();  // the plan has been read: the copies may begin
+  if (stalled) sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
+  if (idle) return;
   Walk<D, RT> f = c;  // where the copies are
   bool more = true;   // to copy
-  Feed<D, RT, 1> feed{{f.b, f.head, 0, f.g, 0, 0}, 0, f.s.tokens, -32, -1};
+  Feed<D, 1> feed{f.b, f.head, f.s.tokens, -32, -1};
 
   auto issue = [&](int st) {
     const uint32_t dst = ring + st * S::kStage, bar = bars + st * 8;
-    if (feed.c.b != f.b) {
-      feed.c.b = f.b;
+    if (feed.b != f.b) {
+      feed.b = f.b;
       feed.keys = f.s.tokens;
       feed.window = -32;
     }
-    feed.c.head = f.head;
-    feed.c.g = f.g;
+    feed.head = f.head;
     // old weights of the first block of rows; pages for the way back
-    const int key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, kKeys), part = min(p.page, kKeys);
+    const int n = f.step(), key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, n * kKeys), part = min(p.page, n * kKeys);
     uint32_t tx = 0;
+#pragma unroll 1
     for (int k = 0, i = 0; k < wanted; k += part, ++i) {
       const int page = feed.page_of(p, lane, (key0 + k) >> p.page_log2);
-      if (lane == 0)
+      if (lane == 0) {
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + S::kPageOff + 4 * i), "r"(page) : "memory");
-      if (page >= 0 && f.block == 0) {
-        const uint32_t bytes = ((min(wanted - k, part) + 3) & ~3) * 4;
-        tx += bytes;
-        if (lane == 0) {
-          const int64_t at = static_cast<int64_t>(page * p.hkv + f.head) * p.page + ((key0 + k) & (p.page - 1));
+        if (page >= 0 && f.block == 0) {
+          const uint32_t bytes = ((min(wanted - k, part) + 3) & ~3) * 4;
+          tx += bytes;
+          const int64_t at = (page * p.hkv + f.head) * p.page + ((key0 + k) & (p.page - 1));
           ptx::bulk_load(dst + S::kOldOff + 4 * k, w.weight + at, bytes, bar);
         }
       }
     }
-    feed.granule(p, lane, dst, bar, tx);
+    feed.stage(p, lane, f.g, n, dst, bar, tx);
     more = f.next(w);
   };
 
@@ -220,34 +225,40 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     lim_min = __reduce_min_sync(kFull, lmin);
   };
 
-  auto granule = [&](int st) {
-    const uint32_t tile = ring + st * S::kStage;
-    const int key0 = c.g * kKeys;
+  // Granule i of a stage.
+  auto granule = [&](uint32_t stage, int i, int n_here) {
+    const uint32_t tile = stage + i * G::kHalf;
+    const int key0 = (c.g + i) * kKeys;
+    const int part_log2 = p.page >= n_here * kKeys ? 31 : p.page_log2;  // the stage's tokens of one page
     const bool masked = key0 + kKeys > lim_min;
     float sum[2 * kSteps];  // key key_at(i, u, gid)
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      float s[NT][4];
+    for (int step0 = 0; step0 < kSteps; step0 += 2) {
+      float s[NT][2][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-      key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4]) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT * QP; ++n) ptx::mma_f16(s[n / QP], a, qf[n][j][0], qf[n][j][1]);
+        for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.0f;
+      key_operands<D>(tile, step0, gid, tig, [&](int step, int j, const uint32_t (&a)[4]) {
+#pragma unroll
+        for (int n = 0; n < NT * QP; ++n) ptx::mma_f16(s[n / QP][step & 1], a, qf[n][j][0], qf[n][j][1]);
       });
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float x = 0.0f;
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < 2; ++u) {
+          float x = 0.0f;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float e = ex2(fmaf(s[n][2 * u + r], fac[n][r], -lse2[n][r]));
-            x += masked && key0 + key_at<D>(i, u, gid) >= lim[n][r] ? 0.0f : e;
-          }
-        x += __shfl_xor_sync(kFull, x, 1);
-        x += __shfl_xor_sync(kFull, x, 2);
-        sum[2 * i + u] = x;
-      }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float e = ex2(fmaf(s[n][half][2 * u + r], fac[n][r], -lse2[n][r]));
+              x += masked && key0 + key_at<D>(step0 + half, u, gid) >= lim[n][r] ? 0.0f : e;
+            }
+          x += __shfl_xor_sync(kFull, x, 1);
+          x += __shfl_xor_sync(kFull, x, 2);
+          sum[2 * (step0 + half) + u] = x;
+        }
     }
     // lane (gid, tig) writes the keys of sums tig and, at D = 64, tig + 4
 #pragma unroll
@@ -255,18 +266,21 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       const float x = tig == 0 ? sum[4 * q] : tig == 1 ? sum[4 * q + 1] : tig == 2 ? sum[4 * q + 2] : sum[4 * q + 3];
       const int k = key_at<D>(2 * q + (tig >> 1), tig & 1, gid), key = key0 + k;
       if (key >= c.s.tokens) continue;
-      const int page = static_cast<int>(lds32(tile + S::kPageOff + (p.page >= kKeys ? 0 : 4 * (k >> p.page_log2))));
+      const int in_stage = i * kKeys + k;
+      const int page = static_cast<int>(lds32(stage + S::kPageOff + 4 * (in_stage >> part_log2)));
       if (page < 0) continue;
-      float* const at = w.weight + static_cast<int64_t>(page * p.hkv + c.head) * p.page + (key & (p.page - 1));
+      float* const at = w.weight + ((page * p.hkv + c.head) * p.page + (key & (p.page - 1)));
       float old = 0.0f;
       if (c.block > 0) old = *at;  // what this lane wrote
-      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(tile + S::kOldOff + 4 * k));
+      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(stage + S::kOldOff + 4 * in_stage));
       *at = old + x;
     }
   };
 
   auto wait = [&](uint32_t bar, uint32_t par) {
-    return __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+    const bool ok = __all_sync(kFull, ptx::mbar_try_wait(bar, par)) || sync::wait_warp(bar, par, ctl, kv::kSiteWait);
+    __syncwarp();  // the stage's pages, which a lane wrote
+    return ok;
   };
   int st = 0, in_flight = 0;
   uint32_t parity = 0;
@@ -278,7 +292,9 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   begin_block();
   while (in_flight > 0) {
     if (!wait(bars + st * 8, parity)) break;
-    granule(st);
+    const int n = c.step();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) granule(ring + st * S::kStage, i, n);
     __syncwarp();
     if (more) issue(st);
     else --in_flight;
@@ -301,10 +317,10 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
 template <int D, int NT, int QP>
 cp_status run_weigh(const WeighParams& w, int num_sms, cudaStream_t s) {
   using S = WeighShape<D, NT, QP>;
-  constexpr int most_smem = 128 + S::kPlanOff + (CP_KV_MAX_SEQS + 1) * 8;
-  static_assert(most_smem <= 232448, "shared memory of a block");
+  constexpr int smem = 128 + S::kBytes;
+  static_assert(smem <= 232448, "shared memory of a block");
   const auto kernel = kv4_weigh_kernel<D, NT, QP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_weigh_kernel attribute");
   const Params& p = w.p;
   const double most = (static_cast<double>(p.rows.max_pages) * p.page / kKeysOf<D> + 1 + kSetup) * p.hkv * p.rows.n_seqs;
@@ -321,7 +337,7 @@ cp_status run_weigh(const WeighParams& w, int num_sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(most < num_sms ? most : num_sms));
   cfg.blockDim = dim3(S::kWarps * 32);
-  cfg.dynamicSmemBytes = 128 + S::kPlanOff + (p.rows.n_seqs + 1) * 8;
+  cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, kernel, w);
   return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv4_weigh_kernel launch");
 }

@@ -576,7 +576,7 @@ cp_status cp_kv4_cache_read(const cp_kv4_cache* cache, const cp_kv_rows* rows, v
  * A token with a NaN key makes the rows that see it NaN; a NaN value does so in its group of 16 columns.
  * Precision: sums and softmax statistics are fp32.  Queries are taken exactly (bf16) or to 22 bits (fp32), but no finer
  * than 2^-38 of their row's largest element.  Weights are taken to 11 bits for a bf16 output and to 22 for an fp32 one, but
- * no finer than 2^-40 of the row's largest.
+ * no finer than 2^-37 of the row's largest.
  */
 typedef struct {
   cp_kv4_cache cache;

@@ -8,8 +8,8 @@ Tolerances are per element and follow from the arithmetic:
   argument) plus 2^-22 |s|; weights have 22 bits for an fp32 output and 11 for a bf16 one, ex2 2^-22; sums over n keys
   add n / 16 accumulations of 2^-23.  So with delta the largest score error of a row,
   |dO| <= (sum_j p_j |v_j|) (2 delta + w + n 2^-27 + 2^-20), w = 2^-21 or 2^-11, plus half a step of the output type, and
-  |dLSE| <= delta + n 2^-24 + 2^-22 |LSE| + 2^-20.  A weight is held as f16, the largest of a row above 2^14 and steps
-  of 2^-24 at least, so it is off by up to 2^-25 2^-14 = 2^-39 of the largest besides: 2^-39 sum_j |v_j| / z.
+  |dLSE| <= delta + n 2^-24 + 2^-22 |LSE| + 2^-20.  A weight is held as f16, the largest of a row at 2^12 or more and
+  steps of 2^-24 at least, so it is off by up to 2^-25 2^-12 = 2^-37 of the largest besides: 2^-37 sum_j |v_j| / z.
 * gathered weight: exp(s - LSE) is off by delta + 2^-22 (|s| + |LSE|) + 2^-22 of itself (the fp32 LSE given is taken as
   it is), the sum of n of them by n + 2 roundings of 2^-24.  The old weight is added to the sum over a block of 8 query
   rows or more, and what comes out is the old weight of the next block: with g query heads to a KV head a sequence's rows
@@ -254,7 +254,7 @@ def _check_rows(pool, q, rows, held, q_first, kv_pos, got_o, got_l, o_dtype, sca
                 ref, ref_l = (p @ vh) / z, top + np.log(z)
                 delta = float((2.0 ** -20 * sc * (np.abs(kh) @ np.abs(x)) + 2.0 ** -22 * np.abs(s)).max())
                 w = 2.0 ** -11 if o_dtype == BF16 else 2.0 ** -21
-                tol = (p @ np.abs(vh)) / z * (2 * delta + w + n * 2.0 ** -27 + 2.0 ** -20) + 2.0 ** -39 * np.abs(vh).sum(0) / z
+                tol = (p @ np.abs(vh)) / z * (2 * delta + w + n * 2.0 ** -27 + 2.0 ** -20) + 2.0 ** -37 * np.abs(vh).sum(0) / z
                 tol = tol + np.abs(ref) * (2.0 ** -8 if o_dtype == BF16 else 2.0 ** -24) * 1.01 + 1e-30
                 err = np.abs(go - ref)
                 assert np.all(err <= tol), (b, i, h, float((err / tol).max()), float(err.max()))
