@@ -10,9 +10,9 @@
 // is kept in shared memory (in the workspace where it does not fit); the z-th largest is found by its bits, 11, 11 and 10
 // at a time, from histograms that the blocks add up through distributed shared memory; of equal tokens the first stay.
 // The weights are read once; the rest is latency, of some ten barriers of a cluster.
-// Second kernel, blocks for each (sequence, head): the fills, whose sources and holes do not overlap, then the recent rows,
-// which move towards the front by n - keep: a batch is read before it is written, and the batches in order.  They may
-// overwrite slots that fills come from, so they are the task of the block of a (sequence, head) that ends last.
+// Second kernel, a warp a token: the fills, whose sources and holes do not overlap.  Third kernel, a block for each
+// (sequence, head): the recent rows, which move towards the front by n - keep and may overwrite slots that fills came
+// from; a batch is read before it is written, and the batches in order.
 #include <type_traits>
 
 #include "internal.h"
@@ -23,10 +23,11 @@ namespace cpattn {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMostInSmem = 40960;  // tokens of a block
-constexpr int kMoveThreads = 256;
+constexpr int kAtOnce = 4;          // tokens of a thread whose weights are on their way together
+constexpr int kFillThreads = 256, kRecentThreads = 512;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Sequence {  // what the first kernel tells the second
@@ -43,35 +44,36 @@ struct EvictParams {
   int32_t* new_tokens;
   int32_t* status;
   Sequence* seqs;      // workspace: [n_seqs]
-  int32_t* done;       // [n_seqs, hkv]: blocks of the second kernel that have made their fills
   int32_t* holes;      // [n_seqs, keep]
   uint32_t* store;     // [n_seqs, cluster] of room + 3 room / 32 words, where shared memory is too small; else null
   int32_t cluster, room;  // room: tokens of a block, a multiple of 32
-  int32_t splits;      // blocks of a (sequence, head) in the second kernel
+  int32_t per_seq;     // blocks of a sequence in the second kernel
 };
 
 __device__ __forceinline__ int page_of(const EvictParams& p, int b, int token) {
   return __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (token >> p.page_log2));
 }
-// Row of a token among the cache's rows for head 0.
-__device__ __forceinline__ int64_t row_of(const EvictParams& p, int b, int token) {
-  return (static_cast<int64_t>(page_of(p, b, token)) * p.c.hkv << p.page_log2) + (token & ((1 << p.page_log2) - 1));
+// Row of a token among the cache's rows for head 0, which are below 2^31.
+__device__ __forceinline__ int row_in(const EvictParams& p, int page, int token) {
+  return (page * p.c.hkv << p.page_log2) + (token & ((1 << p.page_log2) - 1));
+}
+__device__ __forceinline__ int row_of(const EvictParams& p, int b, int token) {
+  return row_in(p, page_of(p, b, token), token);
 }
 
-// The sum of a token's weights over the heads, rounded once: the rounding errors of the additions are summed apart
-// (Knuth's two-sum), so that the order of the heads does not decide between tokens.
-__device__ __forceinline__ float weight_of(const EvictParams& p, int64_t row) {
-  const float* w = p.weight + row;
+// A sum that is rounded once: the rounding errors of the additions are summed apart (Knuth's two-sum), so that the order
+// of the heads does not decide between tokens.
+struct Sum {
   float s = 0.0f, err = 0.0f;
-#pragma unroll 8
-  for (int h = 0; h < p.c.hkv; ++h) {
-    const float x = w[static_cast<int64_t>(h) << p.page_log2];
+  __device__ __forceinline__ void add(float x) {
     const float t = __fadd_rn(s, x), y = __fsub_rn(t, s);
     err = __fadd_rn(err, __fadd_rn(__fsub_rn(s, __fsub_rn(t, y)), __fsub_rn(x, y)));
     s = t;
   }
-  return fabsf(s) < INFINITY && fabsf(err) < INFINITY ? __fadd_rn(s, err) : s;
-}
+  __device__ __forceinline__ float value() const {
+    return fabsf(s) < INFINITY && fabsf(err) < INFINITY ? __fadd_rn(s, err) : s;
+  }
+};
 // Whole numbers in the order of the weights; NaN is below all of them.
 __device__ __forceinline__ uint32_t order_of(float w) {
   if (w != w) return 0u;
@@ -91,14 +93,10 @@ __device__ __forceinline__ int scan(int x, int* scratch, int& all) {
   __syncthreads();  // scratch has been read
   if (lane == 31) scratch[warp] = in;
   __syncthreads();
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scratch[w];
-    all += scratch[w];
-  }
-  return before + in - x;
+  static_assert(kWarps == 32, "a lane reads a warp's sum");
+  const int of = scratch[lane];
+  all = __reduce_add_sync(kFull, of);
+  return static_cast<int>(__reduce_add_sync(kFull, lane < warp ? of : 0)) + in - x;
 }
 
 __device__ __forceinline__ int ld_cluster_int(uint32_t addr) { return __float_as_int(ptx::ld_cluster(addr)); }
@@ -133,8 +131,6 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
       p.seqs[b] = Sequence{n, 0, 0, 0};
     }
   };
-  for (int i = rank * kThreads + tid; i < p.c.hkv; i += cluster * kThreads)
-    p.done[static_cast<int64_t>(b) * p.c.hkv + i] = 0;
   if (rank == 0 && tid == 0 && (held < 0 || over)) kv::report(p.status, kv::kSiteTokens);
   if (n <= p.keep || over) {  // the same for the whole cluster
     leave();
@@ -148,33 +144,57 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
   int* const hole_rank = reinterpret_cast<int*>(stay + p.room / 32);
   int* const mover_rank = hole_rank + p.room / 32;
 
-  // Pages of all tokens, the recent ones too, have to be there before anything is read or changed.
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  // Pages of all tokens, the recent ones too, have to be there before anything is changed.
   int bad = 0;
-  const int pages = (n + (1 << p.page_log2) - 1) >> p.page_log2;
-  for (int i = rank * kThreads + tid; i < pages; i += cluster * kThreads) {
-    const int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + i);
+  for (int i = old + rank * kThreads + tid; i < n; i += cluster * kThreads) {
+    const int page = page_of(p, b, i);
     bad |= page < 0 || page >= p.c.n_pages;
+  }
+  for (int base = tid; base < mine; base += kAtOnce * kThreads) {
+    int row[kAtOnce];
+    Sum sum[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int i = base + j * kThreads;
+      row[j] = -1;
+      if (i < mine) {
+        const int page = page_of(p, b, from + i);
+        if (page < 0 || page >= p.c.n_pages) bad = 1;
+        else row[j] = row_in(p, page, from + i);
+      }
+    }
+#pragma unroll 4
+    for (int h = 0; h < p.c.hkv; ++h) {
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (row[j] >= 0) sum[j].add(p.weight[row[j] + (h << p.page_log2)]);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int i = base + j * kThreads;
+      if (i < mine) {
+        const uint32_t k = order_of(sum[j].value());
+        key[i] = k;
+        atomicAdd(&hist[0][k >> 21], 1);
+      }
+    }
   }
   bad = __syncthreads_or(bad);
   if (tid == 0) counts[0] = bad;
-  meet();
+  meet();  // the first histograms are there too
   if (cluster > 1) {
-    bad = 0;
     for (int r = 0; r < cluster; ++r) bad |= ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(&counts[0]), r));
-    ptx::cluster_sync();  // a block that ends now may be asked no more
+    bad = __syncthreads_or(bad);
   }
   if (bad) {
+    if (cluster > 1) ptx::cluster_sync();  // a block that has ended can be asked no more
     if (rank == 0 && tid == 0) kv::report(p.status, kv::kSitePage);
     leave();
     return;
   }
 
-  for (int i = tid; i < mine; i += kThreads) {
-    const uint32_t k = order_of(weight_of(p, row_of(p, b, from + i)));
-    key[i] = k;
-    atomicAdd(&hist[0][k >> 21], 1);
-  }
   // The z-th largest: bits found so far, and how many of the tokens that begin with them stay.
   uint32_t bits = 0;
   int want = z, ties_before = 0;
@@ -189,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
           if (k >> (pass == 1 ? 21 : 10) == above) atomicAdd(&hist[pass][k >> shift & (bins - 1)], 1);
         }
       }
-      meet();
+      if (pass > 0) meet();
       constexpr int kPer = kBins / kThreads;
       int count[kPer], sum = 0;
       const int per = bins / kThreads;
@@ -295,99 +315,113 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
 
 // Rows move in nine pieces, of 8 bytes at D = 128 and 4 at D = 64.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(const __grid_constant__ EvictParams p) {
-  using Piece = typename std::conditional<D == 128, uint2, uint32_t>::type;
-  constexpr int kUnits = 19;   // of a token: K, V, weight
-  constexpr int kAhead = 8;    // of a thread
-  __shared__ int last;
+using Piece = typename std::conditional<D == 128, uint2, uint32_t>::type;
+
+// A warp a token: lanes 0 to 8 move pieces of K, 9 to 17 of V, lane 18 the weight, of kHeads heads at a time.
+template <int D>
+__global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kHeads = 8;
   ptx::wait_dependencies();
-  const int split = blockIdx.x % p.splits;
-  const int64_t item = blockIdx.x / p.splits;
-  const int b = static_cast<int>(item / p.c.hkv), head = static_cast<int>(item - static_cast<int64_t>(b) * p.c.hkv);
-  const Sequence s = p.seqs[b];
-  const int tid = threadIdx.x;
-  if (s.recent == 0 && s.fills == 0) return;
-  const int64_t head_rows = static_cast<int64_t>(head) << p.page_log2;
+  const int b = blockIdx.x / p.per_seq, lane = threadIdx.x & 31;
+  const int first = (blockIdx.x % p.per_seq) * (kFillThreads / 32) + (threadIdx.x >> 5);
+  const int fills = __ldg(&p.seqs[b].fills);
   const int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
   const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
-  // Moves `rows` tokens, the i-th from source(i) to target(i), in batches; `ordered`: a batch is read before it is written.
-  const auto move = [&](int first, int step, int rows, bool ordered, auto target, auto source) {
-    const int64_t units = static_cast<int64_t>(rows) * kUnits;
-    for (int64_t base = static_cast<int64_t>(first) * kMoveThreads * kAhead; base < units;
-         base += static_cast<int64_t>(step) * kMoveThreads * kAhead) {
-      Piece x[kAhead];
-      void* to[kAhead];
+  uint8_t* const base = lane < 18 ? static_cast<uint8_t*>(lane < 9 ? p.c.k : p.c.v) +
+                                        (lane < 9 ? lane : lane - 9) * static_cast<int>(sizeof(Piece<D>))
+                                  : reinterpret_cast<uint8_t*>(p.weight);
+  const int64_t stride = lane < 18 ? kv4::kRow<D> : 4;
+  for (int i = first; i < fills; i += p.per_seq * (kFillThreads / 32)) {
+    const int t = __ldg(list + i);
+    const int to = row_of(p, b, t), from = row_of(p, b, __ldg(kept + t));
+    if (lane > 18) continue;
+    for (int h = 0; h < p.c.hkv; h += kHeads) {
+      Piece<D> x[kHeads];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int64_t unit = base + j * kMoveThreads + tid;
-        to[j] = nullptr;
-        if (unit < units) {
-          const int i = static_cast<int>(unit / kUnits), e = static_cast<int>(unit - static_cast<int64_t>(i) * kUnits);
-          const int t = target(i);
-          const int64_t at = row_of(p, b, t) + head_rows, src = row_of(p, b, source(i, t)) + head_rows;
-          if (e < 18) {
-            uint8_t* const rows8 = static_cast<uint8_t*>(e < 9 ? p.c.k : p.c.v);
-            const int piece = (e < 9 ? e : e - 9) * static_cast<int>(sizeof(Piece));
-            x[j] = *reinterpret_cast<const Piece*>(rows8 + src * kv4::kRow<D> + piece);
-            to[j] = rows8 + at * kv4::kRow<D> + piece;
-          } else {
-            *reinterpret_cast<float*>(&x[j]) = p.weight[src];
-            to[j] = p.weight + at;
-          }
+      for (int j = 0; j < kHeads; ++j)
+        if (h + j < p.c.hkv) {
+          const uint8_t* const at = base + (from + ((h + j) << p.page_log2)) * stride;
+          if (lane < 18) x[j] = *reinterpret_cast<const Piece<D>*>(at);
+          else *reinterpret_cast<uint32_t*>(&x[j]) = *reinterpret_cast<const uint32_t*>(at);
         }
-      }
-      if (ordered) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int64_t unit = base + j * kMoveThreads + tid;
-        if (to[j] != nullptr) {
-          if (unit % kUnits < 18) *static_cast<Piece*>(to[j]) = x[j];
-          else *static_cast<float*>(to[j]) = *reinterpret_cast<const float*>(&x[j]);
+      for (int j = 0; j < kHeads; ++j)
+        if (h + j < p.c.hkv) {
+          uint8_t* const at = base + (to + ((h + j) << p.page_log2)) * stride;
+          if (lane < 18) *reinterpret_cast<Piece<D>*>(at) = x[j];
+          else *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(&x[j]);
+        }
+    }
+  }
+}
+
+// The recent tokens of a (sequence, head): unit u is piece u % 19 of token u / 19.  Batch after batch, each read before it
+// is written: a target is never the source of a later batch, since targets are in front of their sources.
+template <int D>
+__global__ void __launch_bounds__(kRecentThreads) kv4_recent_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kUnits = 19, kAhead = 8;
+  ptx::wait_dependencies();
+  const int b = blockIdx.x / p.c.hkv, head = blockIdx.x % p.c.hkv;
+  const Sequence s = p.seqs[b];
+  const int head_row = head << p.page_log2, by = s.n - p.keep;
+  const int64_t units = static_cast<int64_t>(s.recent) * kUnits;
+  for (int64_t base = threadIdx.x; base - threadIdx.x < units; base += kRecentThreads * kAhead) {
+    Piece<D> x[kAhead];
+    uint8_t* to[kAhead];
+    bool weight[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t unit = base + j * kRecentThreads;
+      to[j] = nullptr;
+      weight[j] = false;
+      if (unit < units) {
+        const int i = static_cast<int>(unit / kUnits), e = static_cast<int>(unit - static_cast<int64_t>(i) * kUnits);
+        const int64_t at = row_of(p, b, s.z + i) + head_row, from = row_of(p, b, s.z + i + by) + head_row;
+        weight[j] = e == 18;
+        if (weight[j]) {
+          to[j] = reinterpret_cast<uint8_t*>(p.weight + at);
+          *reinterpret_cast<float*>(&x[j]) = p.weight[from];
+        } else {
+          uint8_t* const rows = static_cast<uint8_t*>(e < 9 ? p.c.k : p.c.v) + (e < 9 ? e : e - 9) * sizeof(Piece<D>);
+          to[j] = rows + at * kv4::kRow<D>;
+          x[j] = *reinterpret_cast<const Piece<D>*>(rows + from * kv4::kRow<D>);
         }
       }
     }
-  };
-  move(split, p.splits, s.fills, false, [&](int i) { return __ldg(list + i); },
-       [&](int, int t) { return __ldg(kept + t); });
-  if (s.recent == 0) return;
-  if (p.splits > 1) {
-    __threadfence();
     __syncthreads();
-    if (tid == 0) last = atomicAdd(p.done + item, 1) == p.splits - 1 ? 1 : 0;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-  } else {
-    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (to[j] != nullptr) {
+        if (weight[j]) *reinterpret_cast<float*>(to[j]) = *reinterpret_cast<const float*>(&x[j]);
+        else *reinterpret_cast<Piece<D>*>(to[j]) = x[j];
+      }
   }
-  const int by = s.n - p.keep;
-  move(0, 1, s.recent, true, [&](int i) { return s.z + i; }, [&](int, int t) { return t + by; });
 }
 
 struct Layout {
-  int cluster, room, splits;
-  int64_t done_off, holes_off, store_off, bytes;
+  int cluster, room, per_seq;
+  int64_t holes_off, store_off, bytes;
   int smem;
 };
-// Blocks of a sequence: enough that one has 4096 tokens or fewer, as the page table's width tells, while the SMs hold
+// Blocks of a sequence: enough that one has 2048 tokens or fewer, as the page table's width tells, while the SMs hold
 // them all.
 Layout layout_of(const cp_kv4_evict_desc& d, int sms) {
   Layout r;
   const int64_t most = static_cast<int64_t>(d.max_pages) * d.cache.page_size, seqs = d.n_seqs > 0 ? d.n_seqs : 1;
   r.cluster = 1;
-  while (r.cluster < 8 && most > 4096 * static_cast<int64_t>(r.cluster) &&
+  while (r.cluster < 8 && most > 2048 * static_cast<int64_t>(r.cluster) &&
          (seqs * r.cluster * 2 <= sms || most > kMostInSmem * static_cast<int64_t>(r.cluster)))
     r.cluster *= 2;
   r.room = static_cast<int>(((most + r.cluster - 1) / r.cluster + 31) / 32 * 32);
   const bool fits = r.room <= kMostInSmem;
   const int64_t words = r.room + static_cast<int64_t>(r.room) / 32 * 3;
   r.smem = fits ? static_cast<int>(words * 4) : 0;
-  const int64_t items = seqs * d.cache.hkv;
-  r.splits = static_cast<int>(items >= 4 * sms ? 1 : (4 * sms + items - 1) / items);
-  const int64_t turns = (static_cast<int64_t>(d.keep) * 19 + kMoveThreads * 8 - 1) / (kMoveThreads * 8);
-  if (r.splits > turns) r.splits = turns > 0 ? static_cast<int>(turns) : 1;
-  r.done_off = (seqs * static_cast<int64_t>(sizeof(Sequence)) + 255) / 256 * 256;
-  r.holes_off = r.done_off + (items * 4 + 255) / 256 * 256;
+  // a warp for each fill, of which there are as many as tokens that stay from slot z on, up to 16 blocks an SM
+  int64_t fills = most - d.keep < d.keep - d.recent ? most - d.keep : d.keep - d.recent;
+  if (fills < 1) fills = 1;
+  const int64_t per = kFillThreads / 32, share = (16 * static_cast<int64_t>(sms) + seqs - 1) / seqs;
+  r.per_seq = static_cast<int>((fills + per - 1) / per < share ? (fills + per - 1) / per : share);
+  r.holes_off = (seqs * static_cast<int64_t>(sizeof(Sequence)) + 255) / 256 * 256;
   r.store_off = r.holes_off + (seqs * d.keep * 4 + 255) / 256 * 256;
   r.bytes = r.store_off + (fits ? 0 : seqs * r.cluster * words * 4);
   return r;
@@ -414,12 +448,11 @@ cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t
   p.new_tokens = d.new_tokens;
   p.status = d.status;
   p.seqs = reinterpret_cast<Sequence*>(ws);
-  p.done = reinterpret_cast<int32_t*>(ws + l.done_off);
   p.holes = reinterpret_cast<int32_t*>(ws + l.holes_off);
   p.store = l.smem == 0 ? reinterpret_cast<uint32_t*>(ws + l.store_off) : nullptr;
   p.cluster = l.cluster;
   p.room = l.room;
-  p.splits = l.splits;
+  p.per_seq = l.per_seq;
   constexpr int most_smem = (kMostInSmem + kMostInSmem / 32 * 3) * 4;
   // The limit is the function's, not the call's: always the same, for other host threads launch the kernel too.
   cudaError_t e = cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
@@ -438,12 +471,22 @@ cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(l.smem);
   if ((e = cudaLaunchKernelEx(&cfg, kv4_select_kernel, p)) != cudaSuccess) return cuda_fail(e, "kv4_select_kernel launch");
+  if (static_cast<int64_t>(d.max_pages) * d.cache.page_size <= d.keep) return CP_OK;  // nothing can be too long
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(d.n_seqs) * d.cache.hkv * l.splits));
-  cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, p);
-  return e == cudaSuccess ? CP_OK : cuda_fail(e, "kv4_move_kernel launch");
+  if (d.keep > d.recent) {
+    cfg.gridDim = dim3(static_cast<unsigned>(d.n_seqs * l.per_seq));
+    cfg.blockDim = dim3(kFillThreads);
+    e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_fill_kernel<128> : kv4_fill_kernel<64>, p);
+    if (e != cudaSuccess) return cuda_fail(e, "kv4_fill_kernel launch");
+  }
+  if (d.recent > 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(d.n_seqs * d.cache.hkv));
+    cfg.blockDim = dim3(kRecentThreads);
+    e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_recent_kernel<128> : kv4_recent_kernel<64>, p);
+    if (e != cudaSuccess) return cuda_fail(e, "kv4_recent_kernel launch");
+  }
+  return CP_OK;
 }
 
 }  // namespace cpattn

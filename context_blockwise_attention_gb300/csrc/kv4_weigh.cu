@@ -6,7 +6,7 @@
 // no running maximum and nothing to join: every key is on its own.  Bound: keys and weights are read once and weights
 // written once; values are not touched.
 //
-// The unit of work is a granule (4096 / D tokens of one sequence and head) with all of the sequence's rows, so each
+// The unit of work is a granule (8192 / D tokens of one sequence and head) with all of the sequence's rows, so each
 // weight has one writer and its sum one order.  Granules are numbered sequence after sequence, each head beginning with
 // kSetup numbers more, and every warp has an equal share of consecutive ones.  A share's part of a head is gone over
 // once for each block of RT query rows; the keys come by a ring of copies as for attention, the old weights with them.
@@ -26,13 +26,13 @@ struct WeighParams {
 
 template <int D, int NT, int QP>
 struct WeighShape {
-  using G = Granule<D>;
-  static constexpr bool kHeavy = NT * QP * D >= 256;  // query operands take NT QP D / 8 registers
-  static constexpr int kWarps = kHeavy ? 8 : 12;
+  static constexpr int kKeys = 8192 / D;  // of a granule
+  static constexpr int kQ = NT * QP * D / 8;    // registers of query operands
+  static constexpr int kWarps = kQ <= 16 ? 16 : kQ <= 32 ? 12 : 8;
   static constexpr int kRows = NT * 8;  // RT
-  static constexpr int kStages = kHeavy ? 4 : 3;
-  static constexpr int kOldOff = G::kPair;                      // old weights of the granules
-  static constexpr int kPageOff = kOldOff + 2 * G::kKeys * 4;   // pages of their parts, 8 at most
+  static constexpr int kStages = kWarps == 16 ? 2 : kWarps == 12 ? 3 : 4;
+  static constexpr int kOldOff = kKeys * kv4::kRow<D>;  // old weights of the granule
+  static constexpr int kPageOff = kOldOff + kKeys * 4;   // pages of its parts, 8 at most
   static constexpr int kStage = kPageOff + 32;
   // The plan is looked at before the first copies and lies where they go.
   static constexpr int kBarOff = kWarps * kStages * kStage;
@@ -47,7 +47,7 @@ struct WeighSeq {
   int32_t rows, tokens, known, gpi, blocks;
   bool over;
 };
-template <int D, int RT>
+template <int KEYS, int RT>
 __device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& w, int b) {
   const Params& p = w.p;
   WeighSeq s;
@@ -59,13 +59,13 @@ __device__ __forceinline__ WeighSeq weigh_seq(const WeighParams& w, int b) {
   s.tokens = t < 0 ? 0 : static_cast<int32_t>(t < room ? t : room);
   s.known = w.known != nullptr ? __ldg(w.known + b) : s.tokens;
   s.pos0 = p.q_first != nullptr ? __ldg(p.q_first + b) : 0;
-  s.gpi = s.rows > 0 ? (s.tokens + kKeysOf<D> - 1) / kKeysOf<D> : 0;
+  s.gpi = s.rows > 0 ? (s.tokens + KEYS - 1) / KEYS : 0;
   s.blocks = s.rows > 0 ? (s.rows * p.group + RT - 1) / RT : 0;
   return s;
 }
 
 // A walk over a share: for each sequence and head the granules g0 .. g1 - 1, once for each block of rows.
-template <int D, int RT>
+template <int KEYS, int RT>
 struct Walk {
   int b, head, block, g, g0, g1;
   int left;  // numbers of the share behind this part
@@ -78,11 +78,9 @@ struct Walk {
     g1 = s.gpi - from < left ? s.gpi : from + left;
     left -= g1 - g0;
   }
-  __device__ __forceinline__ int step() const { return together(g, g1); }
-  // Past the granules of a step; false at the end of the share.
+  // To the next granule; false at the end of the share.
   __device__ __forceinline__ bool next(const WeighParams& w) {
-    g += step();
-    if (g < g1) return true;
+    if (++g < g1) return true;
     if (++block < s.blocks) {
       g = g0;
       return true;
@@ -93,7 +91,7 @@ struct Walk {
       head = 0;
       do {
         if (++b >= w.p.rows.n_seqs) return false;
-        s = weigh_seq<D, RT>(w, b);
+        s = weigh_seq<KEYS, RT>(w, b);
       } while (s.gpi == 0);
     }
     enter(0);
@@ -105,8 +103,7 @@ template <int D, int NT, int QP>
 __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     kv4_weigh_kernel(const __grid_constant__ WeighParams w) {
   using S = WeighShape<D, NT, QP>;
-  using G = Granule<D>;
-  constexpr int RT = S::kRows, kMt = D / 16, kSt = S::kStages, kSteps = G::kSteps, kKeys = G::kKeys;
+  constexpr int RT = S::kRows, kMt = D / 16, kSt = S::kStages, kKeys = S::kKeys, kSteps = kKeys / 16;
   const Params& p = w.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((128u - (ptx::smem_u32(smem_raw) & 127u)) & 127u);
@@ -131,7 +128,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   const int n_seqs = p.rows.n_seqs;
   const sync::Ctl ctl{abort_flag, p.status, p.timeout_ns};
   make_plan_of<S::kWarps * 32>(n_seqs, plan, reinterpret_cast<int64_t*>(smem + S::kScanOff), [&](int b) {
-    const WeighSeq s = weigh_seq<D, RT>(w, b);
+    const WeighSeq s = weigh_seq<S::kKeys, RT>(w, b);
     if (s.over && s.rows > 0 && blockIdx.x == 0) kv::report(p.status, kv::kSiteTokens);
     return s.gpi > 0 ? static_cast<int64_t>(p.hkv) * (s.gpi + kSetup) : 0;
   });
@@ -139,7 +136,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   const int64_t W = plan[n_seqs];
   const int64_t most = static_cast<int64_t>(gridDim.x) * S::kWarps, n_workers = W < most ? W : most;
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;  // neighbours on different SMs
-  Walk<D, RT> c;
+  Walk<S::kKeys, RT> c;
   c.left = 0;
   bool idle = worker >= n_workers || stalled;
   if (!idle) {
@@ -151,7 +148,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       else z = mid - 1;
     }
     c.b = a;
-    c.s = weigh_seq<D, RT>(w, a);
+    c.s = weigh_seq<S::kKeys, RT>(w, a);
     const int64_t off = lo - plan[a];
     c.head = static_cast<int>(off / (c.s.gpi + kSetup));
     const int at = static_cast<int>(off - static_cast<int64_t>(c.head) * (c.s.gpi + kSetup));
@@ -164,7 +161,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   __syncthreads();  // the plan has been read: the copies may begin
   if (stalled) sync::wait_warp(stall_bar, 0, ctl, kv::kSiteWait);
   if (idle) return;
-  Walk<D, RT> f = c;  // where the copies are
+  Walk<S::kKeys, RT> f = c;  // where the copies are
   bool more = true;   // to copy
   Feed<D, 1> feed{f.b, f.head, f.s.tokens, -32, -1};
 
@@ -177,7 +174,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     }
     feed.head = f.head;
     // old weights of the first block of rows; pages for the way back
-    const int n = f.step(), key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, n * kKeys), part = min(p.page, n * kKeys);
+    const int key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, kKeys), part = min(p.page, kKeys);
     uint32_t tx = 0;
 #pragma unroll 1
     for (int k = 0, i = 0; k < wanted; k += part, ++i) {
@@ -192,7 +189,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
         }
       }
     }
-    feed.stage(p, lane, f.g, n, dst, bar, tx);
+    feed.stage(p, lane, 2 * f.g, 2, dst, bar, tx);  // two of the attention's granules
     more = f.next(w);
   };
 
@@ -225,11 +222,9 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     lim_min = __reduce_min_sync(kFull, lmin);
   };
 
-  // Granule i of a stage.
-  auto granule = [&](uint32_t stage, int i, int n_here) {
-    const uint32_t tile = stage + i * G::kHalf;
-    const int key0 = (c.g + i) * kKeys;
-    const int part_log2 = p.page >= n_here * kKeys ? 31 : p.page_log2;  // the stage's tokens of one page
+  auto granule = [&](uint32_t tile) {
+    const int key0 = c.g * kKeys;
+    const int part_log2 = p.page >= kKeys ? 31 : p.page_log2;  // the granule's tokens of one page
     const bool masked = key0 + kKeys > lim_min;
     float sum[2 * kSteps];  // key key_at(i, u, gid)
 #pragma unroll
@@ -260,19 +255,18 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
           sum[2 * (step0 + half) + u] = x;
         }
     }
-    // lane (gid, tig) writes the keys of sums tig and, at D = 64, tig + 4
+    // lane (gid, tig) writes the keys of sums tig, tig + 4, ...
 #pragma unroll
     for (int q = 0; q < kSteps / 2; ++q) {
       const float x = tig == 0 ? sum[4 * q] : tig == 1 ? sum[4 * q + 1] : tig == 2 ? sum[4 * q + 2] : sum[4 * q + 3];
       const int k = key_at<D>(2 * q + (tig >> 1), tig & 1, gid), key = key0 + k;
       if (key >= c.s.tokens) continue;
-      const int in_stage = i * kKeys + k;
-      const int page = static_cast<int>(lds32(stage + S::kPageOff + 4 * (in_stage >> part_log2)));
+      const int page = static_cast<int>(lds32(tile + S::kPageOff + 4 * (k >> part_log2)));
       if (page < 0) continue;
       float* const at = w.weight + ((page * p.hkv + c.head) * p.page + (key & (p.page - 1)));
       float old = 0.0f;
       if (c.block > 0) old = *at;  // what this lane wrote
-      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(stage + S::kOldOff + 4 * in_stage));
+      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(tile + S::kOldOff + 4 * k));
       *at = old + x;
     }
   };
@@ -292,9 +286,7 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   begin_block();
   while (in_flight > 0) {
     if (!wait(bars + st * 8, parity)) break;
-    const int n = c.step();
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) granule(ring + st * S::kStage, i, n);
+    granule(ring + st * S::kStage);
     __syncwarp();
     if (more) issue(st);
     else --in_flight;
@@ -323,7 +315,7 @@ cp_status run_weigh(const WeighParams& w, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_weigh_kernel attribute");
   const Params& p = w.p;
-  const double most = (static_cast<double>(p.rows.max_pages) * p.page / kKeysOf<D> + 1 + kSetup) * p.hkv * p.rows.n_seqs;
+  const double most = (static_cast<double>(p.rows.max_pages) * p.page / S::kKeys + 1 + kSetup) * p.hkv * p.rows.n_seqs;
   if (most > 1e12) {
     set_error("cp_kv4_cache_weigh: max_pages * page_size * hkv * n_seqs is too large for one call");
     return CP_ERR_INVALID_ARG;
@@ -348,6 +340,8 @@ cp_status run_weigh_d(const WeighParams& w, int nt, int num_sms, cudaStream_t s)
     return nt == 1   ? run_weigh<D, 1, 1>(w, num_sms, s)
            : nt == 2 ? run_weigh<D, 2, 1>(w, num_sms, s)
                      : run_weigh<D, 4, 1>(w, num_sms, s);
+  if constexpr (D == 64)
+    if (nt == 4) return run_weigh<D, 4, 2>(w, num_sms, s);
   return nt == 1 ? run_weigh<D, 1, 2>(w, num_sms, s) : run_weigh<D, 2, 2>(w, num_sms, s);
 }
 
@@ -379,9 +373,9 @@ cp_status launch_kv4_weigh(const cp_kv4_weigh_desc& d, float scale, int64_t time
   w.weight = d.weight;
   w.known = d.known;
   w.decay = d.decay;
-  // the fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries)
+  // the fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries at D = 128)
   const int64_t per = (d.rows.n_rows + d.rows.n_seqs - 1) / d.rows.n_seqs * p.group;
-  const int nt = per <= 8 ? 1 : per <= 16 || !p.q_bf16 ? 2 : 4;
+  const int nt = per <= 8 ? 1 : per <= 16 || (!p.q_bf16 && c.d == 128) ? 2 : 4;
   return c.d == 128 ? run_weigh_d<128>(w, nt, num_sms, s) : run_weigh_d<64>(w, nt, num_sms, s);
 }
 
