@@ -27,6 +27,7 @@ constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMostInSmem = 40960;  // tokens of a block
 constexpr int kAtOnce = 4;          // tokens of a thread whose weights are on their way together
+constexpr int kMostCluster = 8;
 constexpr int kFillThreads = 256, kRecentThreads = 512;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -99,7 +100,15 @@ __device__ __forceinline__ int scan(int x, int* scratch, int& all) {
   return static_cast<int>(__reduce_add_sync(kFull, lane < warp ? of : 0)) + in - x;
 }
 
-__device__ __forceinline__ int ld_cluster_int(uint32_t addr) { return __float_as_int(ptx::ld_cluster(addr)); }
+// What `x` is in all blocks of the cluster: the loads are on their way together.
+__device__ __forceinline__ void ld_all(const int* x, int cluster, int (&of)[kMostCluster]) {
+  const uint32_t at = ptx::smem_u32(x);
+#pragma unroll
+  for (int r = 0; r < kMostCluster; ++r) {
+    of[r] = 0;
+    if (r < cluster) of[r] = __float_as_int(ptx::ld_cluster(ptx::cluster_addr(at, r)));
+  }
+}
 
 // Bit k of a word of tokens: the first `count` of them.
 __device__ __forceinline__ uint32_t first_bits(int count) {
@@ -119,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
     else __syncthreads();
   };
   ptx::wait_dependencies();
+  ptx::launch_dependents();
   const int held = __ldg(p.tokens + b);
   const int n = held < 0 ? 0 : held;
   const bool over = n > static_cast<int64_t>(p.max_pages) << p.page_log2;
@@ -145,13 +155,10 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
   int* const mover_rank = hole_rank + p.room / 32;
 
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  if (tid == 0) counts[0] = 0;
   __syncthreads();
   // Pages of all tokens, the recent ones too, have to be there before anything is changed.
   int bad = 0;
-  for (int i = old + rank * kThreads + tid; i < n; i += cluster * kThreads) {
-    const int page = page_of(p, b, i);
-    bad |= page < 0 || page >= p.c.n_pages;
-  }
   for (int base = tid; base < mine; base += kAtOnce * kThreads) {
     int row[kAtOnce];
     Sum sum[kAtOnce];
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
         else row[j] = row_in(p, page, from + i);
       }
     }
-#pragma unroll 4
+#pragma unroll 8
     for (int h = 0; h < p.c.hkv; ++h) {
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
@@ -181,12 +188,18 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
       }
     }
   }
-  bad = __syncthreads_or(bad);
-  if (tid == 0) counts[0] = bad;
+  for (int i = old + rank * kThreads + tid; i < n; i += cluster * kThreads) {
+    const int page = page_of(p, b, i);
+    bad |= page < 0 || page >= p.c.n_pages;
+  }
+  if (bad) counts[0] = 1;
   meet();  // the first histograms are there too
+  bad = counts[0];
+  int of[kMostCluster];
   if (cluster > 1) {
-    for (int r = 0; r < cluster; ++r) bad |= ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(&counts[0]), r));
-    bad = __syncthreads_or(bad);
+    ld_all(&counts[0], cluster, of);
+#pragma unroll
+    for (int r = 0; r < kMostCluster; ++r) bad |= of[r];
   }
   if (bad) {
     if (cluster > 1) ptx::cluster_sync();  // a block that has ended can be asked no more
@@ -219,7 +232,9 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
         if (j < per) {
           int* const at = &hist[pass][bins - 1 - (tid * per + j)];
           if (cluster > 1) {
-            for (int r = 0; r < cluster; ++r) count[j] += ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(at), r));
+            ld_all(at, cluster, of);
+#pragma unroll
+            for (int r = 0; r < kMostCluster; ++r) count[j] += of[r];
           } else {
             count[j] = *at;
           }
@@ -241,23 +256,27 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
       __syncthreads();
     }
     // equal tokens of the blocks before
-    for (int r = 0; r < rank; ++r)
-      ties_before += ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(&hist[2][bits & 1023u]), r));
+    if (cluster > 1) {
+      ld_all(&hist[2][bits & 1023u], rank, of);
+#pragma unroll
+      for (int r = 0; r < kMostCluster; ++r) ties_before += of[r];
+    }
   }
 
   // What stays, 32 tokens a word; the first `want` of the tokens that equal the z-th largest.
+  if (z > 0)
+    for (int w = warp; w < words; w += kWarps) {
+      const int i = 32 * w + lane;
+      const uint32_t k = i < mine ? key[i] : 0u;
+      const uint32_t more = __ballot_sync(kFull, i < mine && k > bits), same = __ballot_sync(kFull, i < mine && k == bits);
+      if (lane == 0) stay[w] = more, hole_rank[w] = static_cast<int>(same);
+    }
+  __syncthreads();
   int holes = 0, movers = 0, ties = ties_before;
   for (int base = 0; base < words; base += kThreads) {
     const int w = base + tid;
     uint32_t more = 0, same = 0;
-    if (w < words && z > 0)
-      for (int j = 0; j < 32; ++j) {
-        const int k = (j + lane) & 31;  // another bank for each lane
-        if (32 * w + k >= mine) continue;
-        const uint32_t x = key[32 * w + k];
-        more |= (x > bits ? 1u : 0u) << k;
-        same |= (x == bits ? 1u : 0u) << k;
-      }
+    if (w < words && z > 0) more = stay[w], same = static_cast<uint32_t>(hole_rank[w]);
     int all;
     int left = want - (ties + scan(__popc(same), scratch, all));
     ties += all;
@@ -283,13 +302,14 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
   int holes_before = 0, movers_before = 0, fills = holes;
   if (cluster > 1) {
     fills = 0;
-    for (int r = 0; r < cluster; ++r) {
-      const int h = ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(&counts[1]), r));
-      if (r < rank) {
-        holes_before += h;
-        movers_before += ld_cluster_int(ptx::cluster_addr(ptx::smem_u32(&counts[2]), r));
-      }
-      fills += h;
+    int of_movers[kMostCluster];
+    ld_all(&counts[1], cluster, of);
+    ld_all(&counts[2], rank, of_movers);
+#pragma unroll
+    for (int r = 0; r < kMostCluster; ++r) {
+      if (r < rank) holes_before += of[r];
+      movers_before += of_movers[r];
+      fills += of[r];
     }
   }
   int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
@@ -322,6 +342,7 @@ template <int D>
 __global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kHeads = 8;
   ptx::wait_dependencies();
+  ptx::launch_dependents();
   const int b = blockIdx.x / p.per_seq, lane = threadIdx.x & 31;
   const int first = (blockIdx.x % p.per_seq) * (kFillThreads / 32) + (threadIdx.x >> 5);
   const int fills = __ldg(&p.seqs[b].fills);
@@ -358,8 +379,8 @@ __global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_con
 // The recent tokens of a (sequence, head): unit u is piece u % 19 of token u / 19.  Batch after batch, each read before it
 // is written: a target is never the source of a later batch, since targets are in front of their sources.
 template <int D>
-__global__ void __launch_bounds__(kRecentThreads) kv4_recent_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int kUnits = 19, kAhead = 8;
+__global__ void __launch_bounds__(kRecentThreads, 2) kv4_recent_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kUnits = 19, kAhead = 4;
   ptx::wait_dependencies();
   const int b = blockIdx.x / p.c.hkv, head = blockIdx.x % p.c.hkv;
   const Sequence s = p.seqs[b];
@@ -403,13 +424,13 @@ struct Layout {
   int64_t holes_off, store_off, bytes;
   int smem;
 };
-// Blocks of a sequence: enough that one has 2048 tokens or fewer, as the page table's width tells, while the SMs hold
-// them all.
+// Blocks of a sequence: enough that one has two rounds of weights to read, as the page table's width tells, while the SMs
+// hold them all: a cluster's barriers cost as much as a round.
 Layout layout_of(const cp_kv4_evict_desc& d, int sms) {
   Layout r;
   const int64_t most = static_cast<int64_t>(d.max_pages) * d.cache.page_size, seqs = d.n_seqs > 0 ? d.n_seqs : 1;
   r.cluster = 1;
-  while (r.cluster < 8 && most > 2048 * static_cast<int64_t>(r.cluster) &&
+  while (r.cluster < kMostCluster && most > 8192 * static_cast<int64_t>(r.cluster) &&
          (seqs * r.cluster * 2 <= sms || most > kMostInSmem * static_cast<int64_t>(r.cluster)))
     r.cluster *= 2;
   r.room = static_cast<int>(((most + r.cluster - 1) / r.cluster + 31) / 32 * 32);
