@@ -1,10 +1,14 @@
 // Writing tokens into the paged 4-bit cache and reading them back (cp_kv4_cache_write / _read).
 //
 // Every group of 16 numbers is on its own: its scale, its codes, 9 bytes.  So the unit of work is a group of a
-// (row of the call, head), a thread's: 16 numbers in or out with 16-byte accesses, 8 bytes of codes, and the scale
-// bytes of a row put together by its lanes.  Memory bound: a number costs its own size and 9/16 of a byte.
+// (row of the call, head), a thread's: 16 numbers in or out with 16-byte accesses, 8 bytes of codes and a scale byte.
+// Memory bound: a number costs its own size and 9/16 of a byte.
 // A block takes kRows rows of the call: it looks their pages up once, side by side, and goes over the rows of one
 // head after the other, so that neighbouring lanes write (or read) consecutive rows of a page.
+// Measured (GB300, 29 k tokens of 8 heads, D = 128, bf16, 152 MB each way): writing 31 us, reading 30 (floor 22.5 each).
+// One group of a thread at a time is best: two took 33 and 33 us, four and eight 32 and 37, since more registers leave
+// fewer warps; so were half a group a thread for reading (whole lines of stores, 34) and smaller or larger blocks (59 us for
+// both kernels in turn, 60 to 63 with 16 or 64 rows or more blocks to an SM).
 #include "internal.h"
 #include "kv4_common.cuh"
 #include "ptx.cuh"
@@ -112,58 +116,42 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const __grid_consta
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.parts) * kRows;
   const int part = static_cast<int>(blockIdx.x % p.parts);
   look_up(p, row0, part == 0, s);
-  const int hkv = p.c.hkv, lane = threadIdx.x & 31;
-  const int all = 2 * hkv * kRows * kGroups, end = min(all, (part + 1) * p.per);
-#pragma unroll 2
-  for (int i = part * p.per + threadIdx.x; i < end; i += kThreads) {  // whole warps: kRows * kGroups >= 32
+  const int hkv = p.c.hkv;
+  const int end = min(2 * hkv * kRows * kGroups, (part + 1) * p.per);
+  for (int i = part * p.per + threadIdx.x; i < end; i += kThreads) {
     const Item<D> it(i, hkv);
     const int32_t at = s.at[it.row];
-    uint32_t code = 0;
-    uint2 packed = make_uint2(0u, 0u);
-    uint8_t* out = nullptr;
-    if (at >= 0) {
-      const T* x = static_cast<const T*>(p.x[it.which]) + ((row0 + it.row) * hkv + it.head) * D + it.group * 16;
-      out = static_cast<uint8_t*>(it.which ? p.c.v : p.c.k) +
-            (at + static_cast<int64_t>(it.head) * p.c.page_size) * kv4::kRow<D>;
-      uint32_t w[kWords];
-      load16(x, w);
-      const uint32_t top = magnitude_bits(w);
-      code = top < 0x7f800000u ? kv4::scale_code(__uint_as_float(top)) : kv4::kNaN;
-      if (code != 0u && code != kv4::kNaN) {
-        // x / scale by two products, as x times the reciprocal in two parts (Brisebarre and Muller's multiplication by
-        // a constant of twice the precision): off by 2^-47 before its one rounding, so numbers that are a tie of e2m1
-        // times the scale stay ties and no others become one.  fp32's quotient would be the same and take longer.
-        const float scale = kv4::scale_of(code);
-        const float hi = __frcp_rn(scale), lo = __fmaf_rn(-scale, hi, 1.0f) * hi;
-        uint32_t c[8];
+    if (at < 0) continue;
+    uint32_t w[kWords];
+    load16(static_cast<const T*>(p.x[it.which]) + ((row0 + it.row) * hkv + it.head) * D + it.group * 16, w);
+    const uint32_t top = magnitude_bits(w);
+    uint32_t code = kv4::kNaN;
+    uint32_t packed[2] = {0u, 0u};
+    if (top < 0x7f800000u) {
+      code = kv4::scale_code(__uint_as_float(top));
+      float hi, lo;
+      kv4::reciprocal(kv4::scale_of(code), hi, lo);
+      const uint64_t hi2 = ptx::f2_pack(hi, hi), lo2 = ptx::f2_pack(lo, lo);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = number(w, 2 * j), b = number(w, 2 * j + 1);
-          c[j] = kv4::to_e2m1x2(__fmaf_rn(a, hi, a * lo), __fmaf_rn(b, hi, b * lo));
+      for (int q = 0; q < 2; ++q) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t two = ptx::f2_pack(number(w, 8 * q + 2 * j), number(w, 8 * q + 2 * j + 1));
+          ptx::f2_unpack(ptx::f2_fma(two, hi2, ptx::f2_mul(two, lo2)), x[2 * j], x[2 * j + 1]);  // as kv4::times
         }
-        packed.x = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-        packed.y = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+        packed[q] = code != 0u ? kv4::to_e2m1x8(x) : 0u;
       }
     }
-    // the row's scale bytes, by its lanes
-    uint32_t bytes[2];
-    bytes[0] = it.group < 4 ? code << (8 * it.group) : 0u;
-    bytes[1] = it.group >= 4 ? code << (8 * (it.group - 4)) : 0u;
-#pragma unroll
-    for (int o = 1; o < kGroups; o <<= 1) {
-      bytes[0] |= __shfl_xor_sync(0xffffffffu, bytes[0], o);
-      if (D == 128) bytes[1] |= __shfl_xor_sync(0xffffffffu, bytes[1], o);
+    uint8_t* const out = static_cast<uint8_t*>(it.which ? p.c.v : p.c.k) +
+                         (at + static_cast<int64_t>(it.head) * p.c.page_size) * kv4::kRow<D>;
+    if constexpr (D == 128) {  // rows begin at multiples of 8 bytes
+      *reinterpret_cast<uint2*>(out + it.group * 8) = make_uint2(packed[0], packed[1]);
+    } else {
+      reinterpret_cast<uint32_t*>(out)[it.group * 2] = packed[0];
+      reinterpret_cast<uint32_t*>(out)[it.group * 2 + 1] = packed[1];
     }
-    if (at >= 0) {
-      if constexpr (D == 128) {  // rows begin at multiples of 8 bytes
-        *reinterpret_cast<uint2*>(out + it.group * 8) = packed;
-        if (it.group == 0) *reinterpret_cast<uint2*>(out + 64) = make_uint2(bytes[0], bytes[1]);
-      } else {
-        reinterpret_cast<uint32_t*>(out)[it.group * 2] = packed.x;
-        reinterpret_cast<uint32_t*>(out)[it.group * 2 + 1] = packed.y;
-        if (it.group == 0) reinterpret_cast<uint32_t*>(out)[8] = bytes[0];
-      }
-    }
+    out[D / 2 + it.group] = static_cast<uint8_t>(code);
   }
 }
 
@@ -187,14 +175,13 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
   const int part = static_cast<int>(blockIdx.x % p.parts);
   look_up(p, row0, part == 0, s);
   const int hkv = p.c.hkv;
-  const int all = 2 * hkv * kRows * kGroups, end = min(all, (part + 1) * p.per);
-#pragma unroll 4
+  const int end = min(2 * hkv * kRows * kGroups, (part + 1) * p.per);
   for (int i = part * p.per + threadIdx.x; i < end; i += kThreads) {
     const Item<D> it(i, hkv);
     const int32_t at = s.at[it.row];
     if (at < 0) continue;
-    const uint8_t* in = static_cast<const uint8_t*>(it.which ? p.c.v : p.c.k) +
-                        (at + static_cast<int64_t>(it.head) * p.c.page_size) * kv4::kRow<D>;
+    const uint8_t* const in = static_cast<const uint8_t*>(it.which ? p.c.v : p.c.k) +
+                              (at + static_cast<int64_t>(it.head) * p.c.page_size) * kv4::kRow<D>;
     uint32_t word[2];
     if constexpr (D == 128) {
       const uint2 v = __ldg(reinterpret_cast<const uint2*>(in + it.group * 8));
@@ -204,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
       word[1] = __ldg(reinterpret_cast<const uint32_t*>(in) + it.group * 2 + 1);
     }
     const uint32_t scale = kv4::scale_twice(__ldg(in + D / 2 + it.group), 0);
-    T* out = static_cast<T*>(p.x[it.which]) + ((row0 + it.row) * hkv + it.head) * D + it.group * 16;
+    T* const out = static_cast<T*>(p.x[it.which]) + ((row0 + it.row) * hkv + it.head) * D + it.group * 16;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       uint32_t h[4];
@@ -227,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
 // Blocks of rows are cut by heads until the SMs have some four blocks each.
 void cut(CopyParams& p, int num_sms, int64_t& blocks) {
   const int64_t groups = (p.rows.n_rows + kRows - 1) / kRows;
-  const int all = 2 * p.c.hkv * kRows * p.c.d / 16;  // at most 2^31 / 16 * 32 / ... : checked on the host
+  const int all = 2 * p.c.hkv * kRows * (p.c.d / 16);  // at most 2^25
   const int most = (all + kThreads - 1) / kThreads;
   int64_t parts = (4 * static_cast<int64_t>(num_sms) + groups - 1) / groups;
   if (parts > most) parts = most;

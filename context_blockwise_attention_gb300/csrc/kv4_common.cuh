@@ -17,18 +17,19 @@ constexpr int kRow = D / 2 + D / 16;  // bytes of a row: 72 or 36
 constexpr uint32_t kNaN = 255;         // scale byte of a group with a number that is not finite
 constexpr uint32_t kMostScale = 0xe2;  // 10240: 6 times the next one is beyond f16
 
-// The byte of the scale nearest to amax / 6 (ties to even).  The quotient is never rounded onto a tie of the scales:
-// six times a tie is exact in fp32, and the next number of fp32 is 2/3 of a step of the quotient away or more.
+// x times a constant c given in two parts, hi = c rounded (or nearly) and lo = c - hi: off by 2^-47 before its one
+// rounding (Brisebarre and Muller's multiplication by a constant of twice the precision).  So x / 6 and x / scale, taken
+// by the reciprocals, are never rounded onto a tie of the next step but where they are one: numbers that are a divisor
+// times a tie are exact in fp32, and the next number of fp32 is at least 0.53 of a step of the quotient away.
+__device__ __forceinline__ float times(float x, float hi, float lo) { return __fmaf_rn(x, hi, __fmul_rn(x, lo)); }
+
+// The byte of the scale nearest to amax / 6 (ties to even).
 __device__ __forceinline__ uint32_t scale_code(float amax) {
-  const float x = __fdiv_rn(amax, 6.0f);
-  uint32_t code;
-  if (x < 0x1p-14f) {
-    code = static_cast<uint32_t>(__float2int_rn(x * 0x1p17f));
-  } else {
-    uint32_t u = __float_as_uint(x);
-    u += 0x7ffffu + ((u >> 20) & 1u);
-    code = (u >> 20) - ((127u - 15u) << 3);
-  }
+  const float x = times(amax, 0x1.555556p-3f, -0x1.555556p-28f);
+  const uint32_t small = static_cast<uint32_t>(__float2int_rn(x * 0x1p17f));
+  uint32_t u = __float_as_uint(x);
+  u += 0x7ffffu + ((u >> 20) & 1u);
+  const uint32_t code = x < 0x1p-14f ? small : (u >> 20) - ((127u - 15u) << 3);
   return code < kMostScale ? code : kMostScale;
 }
 __device__ __forceinline__ float scale_of(uint32_t code) {
@@ -37,10 +38,19 @@ __device__ __forceinline__ float scale_of(uint32_t code) {
   return f;
 }
 
-// Two fp32 to two e2m1 numbers (first in the low nibble): round to nearest even, at most 6.
-__device__ __forceinline__ uint32_t to_e2m1x2(float a, float b) {
+// The reciprocal of a scale in two parts.
+__device__ __forceinline__ void reciprocal(float scale, float& hi, float& lo) {
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(scale));
+  lo = __fmul_rn(__fmaf_rn(-scale, hi, 1.0f), hi);
+}
+
+// Eight fp32 to a word of e2m1 numbers, the first in the lowest nibble: round to nearest even, at most 6.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 // The eight e2m1 numbers of a word as f16 pairs, exact: byte i's low nibble is the low half of h[i].
