@@ -34,6 +34,9 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
     else if (solo_items * 4 <= sms * 6 / 7) r.cluster = 4;
     else if (solo_items * 2 <= sms * 6 / 7 && width > 3 * r.warps) r.cluster = 2;
   }
+#ifdef FORCE_NT
+  tiles(FORCE_NT);
+#endif
   const int64_t blocks = solo_items * r.cluster;
   const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
   const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
@@ -48,6 +51,9 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
     return r;
   }
   tiles(per <= 8 ? 1 : 2);
+#ifdef FORCE_NT
+  tiles(FORCE_NT);
+#endif
   // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
   r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
            static_cast<double>(seqs + d.rows.n_rows * group / r.rows);

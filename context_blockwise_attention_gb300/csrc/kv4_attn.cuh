@@ -36,8 +36,8 @@ struct Shape4 {
   static constexpr int kRow = Granule<D>::kRow;
   static constexpr int kHalf = Granule<D>::kHalf;
   static constexpr int kStage = 2 * Granule<D>::kPair;  // keys, values
-  static constexpr bool kQSmem = D == 128 && NT * QP >= 4;  // query operands in shared memory
-  static constexpr int kStages = kHeavy && !kQSmem ? 3 : 2;
+  static constexpr bool kQSmem = D == 128 && NT >= 2;  // query operands in shared memory
+  static constexpr int kStages = kWarps == 8 && !kQSmem ? 3 : 2;
   static constexpr int kQBytes = kQSmem ? NT * QP * (D / 16) * 256 : 0;
   static constexpr int kWarpBytes = kStages * kStage + kQBytes;
   // behind the warps' parts: barriers, control.  The plan is looked at before the first copies and lies where they go.
@@ -301,10 +301,9 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   auto granule = [&](uint32_t tile, int key0) {
     const bool masked = key0 + kKeys > lim_min;
     const uint32_t values = tile + Granule<D>::kPair;
-    const bool both = NT == 1 || live > 1;
     auto product = [&](int n, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
       if (n == 0) ptx::mma_f16(d, a, b0, b1);
-      else ptx::mma_f16_if(d, a, b0, b1, both);
+      else ptx::mma_f16_if(d, a, b0, b1, live > n);
     };
     if (masked) mask_values(values, key0);
     // S^T: s[n][i][2 u + r] is key key_at(i, u, gid) for query row 2 tig + r of tile n
@@ -697,14 +696,13 @@ cp_status run4(const Params& p, const Plan& pl, int64_t items, int num_sms, cuda
 
 template <int D>
 cp_status run4_d(const Params& p, const Plan& pl, int64_t items, int num_sms, cudaStream_t s) {
+  if constexpr (D == 128)
+    if (pl.nt == 3) return run4<D, 3, 1, 1>(p, pl, items, num_sms, s);
   if (pl.pp == 1)
-    return pl.nt == 1 ? run4<D, 1, 1, 1>(p, pl, items, num_sms, s)
-                      : run4<D, 2, 1, 1>(p, pl, items, num_sms, s);
+    return pl.nt == 1 ? run4<D, 1, 1, 1>(p, pl, items, num_sms, s) : run4<D, 2, 1, 1>(p, pl, items, num_sms, s);
   if (pl.qp == 1)
-    return pl.nt == 1 ? run4<D, 1, 1, 2>(p, pl, items, num_sms, s)
-                      : run4<D, 2, 1, 2>(p, pl, items, num_sms, s);
-  return pl.nt == 1 ? run4<D, 1, 2, 2>(p, pl, items, num_sms, s)
-                    : run4<D, 2, 2, 2>(p, pl, items, num_sms, s);
+    return pl.nt == 1 ? run4<D, 1, 1, 2>(p, pl, items, num_sms, s) : run4<D, 2, 1, 2>(p, pl, items, num_sms, s);
+  return pl.nt == 1 ? run4<D, 1, 2, 2>(p, pl, items, num_sms, s) : run4<D, 2, 2, 2>(p, pl, items, num_sms, s);
 }
 
 }  // namespace kvattn

@@ -183,15 +183,15 @@ struct Feed {
   int keys;     // tokens of the sequence that are wanted
   int window, pages;  // lane i holds page window + i of the sequence, -1 behind its keys
 
-  __device__ __forceinline__ int page_of(const Params& p, int lane, int ord) {
-    if (static_cast<unsigned>(ord - window) >= 32u) {
+  // Makes the window hold the pages ord .. ord + n - 1; n is at most 8.
+  __device__ __forceinline__ void look(const Params& p, int lane, int ord, int n) {
+    if (static_cast<unsigned>(ord - window) + n > 32u) {
       window = ord;
       // entries that hold no token are the caller's to change at any time: they are not read
       pages = -1;
       if ((static_cast<int64_t>(ord) + lane) << p.page_log2 < keys)
         pages = static_cast<int>(kv::page_at(p.rows, p.n_pages, b, ord + lane));
     }
-    return __shfl_sync(kFull, pages, ord - window);
   }
   // Stands in for tokens that have no page: keys that are NaN, which reach the rows that see them, and values of 0.
   __device__ __forceinline__ void stand_in(const Params& p, int lane, uint32_t dst, int rows) {
@@ -213,26 +213,44 @@ struct Feed {
   }
 
   // Starts the copies of n granules from g on to `dst`, as far as there are tokens; they arrive at `bar`, whose phase ends
-  // with this call's arrival and the bytes of the copies.  tx: bytes of other copies to `bar`.
-  __device__ __forceinline__ void stage(const Params& p, int lane, int g, int n, uint32_t dst, uint32_t bar, uint32_t tx = 0) {
+  // with this call's arrival and the bytes of the copies.  more(i, page, slot, rows) is called by one lane for each page's
+  // part i, and answers with the bytes of its own copies to `bar`; page is -1 where there is none.
+  template <class F>
+  __device__ __forceinline__ void stage(const Params& p, int lane, int g, int n, uint32_t dst, uint32_t bar, F&& more) {
     const int key0 = g * G::kKeys;
     const int wanted = min(keys - key0, n * G::kKeys);
+    const int ord = key0 >> p.page_log2;
     if (p.page >= n * G::kKeys) {
-      const int page = page_of(p, lane, key0 >> p.page_log2);
+      look(p, lane, ord, 1);
+      const int page = __shfl_sync(kFull, pages, ord - window);
       if (page < 0) stand_in(p, lane, dst, n * G::kKeys);
       if (lane == 0) {
-        if (page >= 0) tx += copy(p, page, key0 & (p.page - 1), wanted, dst, bar);
+        const int slot = key0 & (p.page - 1);
+        uint32_t tx = more(0, page, slot, wanted);
+        if (page >= 0) tx += copy(p, page, slot, wanted, dst, bar);
         ptx::mbar_arrive_expect_tx(bar, tx);
       }
       return;
     }
-#pragma unroll 1
-    for (int k = 0; k < wanted; k += p.page) {
-      const int page = page_of(p, lane, (key0 + k) >> p.page_log2);
-      if (page < 0) stand_in(p, lane, dst + k * G::kRow, p.page);
-      else if (lane == 0) tx += copy(p, page, 0, min(wanted - k, p.page), dst + k * G::kRow, bar);
+    // several pages: the lane that holds a page copies its part
+    const int parts = (wanted + p.page - 1) >> p.page_log2;
+    look(p, lane, ord, parts);
+    const int i = lane - (ord - window);
+    const bool mine = static_cast<unsigned>(i) < static_cast<unsigned>(parts);
+    uint32_t tx = 0;
+    if (mine) {
+      const int rows = min(wanted - (i << p.page_log2), p.page);
+      tx = more(i, pages, 0, rows);
+      if (pages >= 0) tx += copy(p, pages, 0, rows, dst + (i << p.page_log2) * G::kRow, bar);
     }
+    tx = __reduce_add_sync(kFull, tx);
+    unsigned bad = __ballot_sync(kFull, mine && pages < 0) >> (ord - window);
+    for (; bad != 0u; bad &= bad - 1u)
+      stand_in(p, lane, dst + ((__ffs(bad) - 1) << p.page_log2) * G::kRow, p.page);
     if (lane == 0) ptx::mbar_arrive_expect_tx(bar, tx);
+  }
+  __device__ __forceinline__ void stage(const Params& p, int lane, int g, int n, uint32_t dst, uint32_t bar) {
+    stage(p, lane, g, n, dst, bar, [](int, int, int, int) { return 0u; });
   }
 };
 

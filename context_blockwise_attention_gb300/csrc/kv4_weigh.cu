@@ -173,23 +173,15 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       feed.window = -32;
     }
     feed.head = f.head;
-    // old weights of the first block of rows; pages for the way back
-    const int key0 = f.g * kKeys, wanted = min(f.s.tokens - key0, kKeys), part = min(p.page, kKeys);
-    uint32_t tx = 0;
-#pragma unroll 1
-    for (int k = 0, i = 0; k < wanted; k += part, ++i) {
-      const int page = feed.page_of(p, lane, (key0 + k) >> p.page_log2);
-      if (lane == 0) {
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + S::kPageOff + 4 * i), "r"(page) : "memory");
-        if (page >= 0 && f.block == 0) {
-          const uint32_t bytes = ((min(wanted - k, part) + 3) & ~3) * 4;
-          tx += bytes;
-          const int64_t at = (page * p.hkv + f.head) * p.page + ((key0 + k) & (p.page - 1));
-          ptx::bulk_load(dst + S::kOldOff + 4 * k, w.weight + at, bytes, bar);
-        }
-      }
-    }
-    feed.stage(p, lane, 2 * f.g, 2, dst, bar, tx);  // two of the attention's granules
+    // Two of the attention's granules; pages for the way back, and old weights for the first block of rows.
+    feed.stage(p, lane, 2 * f.g, 2, dst, bar, [&](int i, int page, int slot, int rows) {
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + S::kPageOff + 4 * i), "r"(page) : "memory");
+      if (page < 0 || f.block > 0) return 0u;
+      const uint32_t bytes = ((rows + 3) & ~3) * 4;
+      const int64_t at = (page * p.hkv + f.head) * p.page + slot;
+      ptx::bulk_load(dst + S::kOldOff + 4 * (i << p.page_log2), w.weight + at, bytes, bar);
+      return bytes;
+    });
     more = f.next(w);
   };
 

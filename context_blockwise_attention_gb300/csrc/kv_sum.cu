@@ -305,6 +305,7 @@ CP_SUM(64, 8);
 CP_SUM(64, 16);
 CP_SUM(128, 8);
 CP_SUM(128, 16);
+CP_SUM(128, 24);
 #undef CP_SUM
 
 }  // namespace kvattn
