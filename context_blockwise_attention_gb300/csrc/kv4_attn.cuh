@@ -314,16 +314,20 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][i][e] = s[n][i + 1][e] = 0.0f;
-      key_operands<D>(tile, i, gid, tig, [&](int step, int j, const uint32_t (&a)[4]) {
+      key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
 #pragma unroll
-        for (int n = 0; n < NT * QP; ++n) {
-          if constexpr (S::kQSmem) {
-            const uint2 b = ptx::lds64(q_smem + ((n * kMt + j) * 32 + lane) * 8);
-            product(n / QP, s[n / QP][step], a, b.x, b.y);
-          } else {
-            product(n / QP, s[n / QP][step], a, qf[n][j][0], qf[n][j][1]);
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (S::kQSmem) {
+              const uint2 q = ptx::lds64(q_smem + (((n * QP + part) * kMt + j) * 32 + lane) * 8);
+              product(n, s[n][i], a, q.x, q.y);
+              product(n, s[n][i + 1], b, q.x, q.y);
+            } else {
+              product(n, s[n][i], a, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+              product(n, s[n][i + 1], b, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+            }
           }
-        }
       });
     }
     if (masked) {
@@ -410,11 +414,13 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      value_operands<D>(values, i, gid, tig, [&](int w, const uint32_t (&a)[4]) {
+      value_operands<D>(values, i, gid, tig, [&](int w, const uint32_t (&a)[4][4]) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int part = 0; part < PP; ++part)
 #pragma unroll
-          for (int part = 0; part < PP; ++part) product(n, acc[n][w], a, pb[n][part][i][0], pb[n][part][i][1]);
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) product(n, acc[n][w + j], a[j], pb[n][part][i][0], pb[n][part][i][1]);
       });
   };
 

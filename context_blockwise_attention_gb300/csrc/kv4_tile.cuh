@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
-// The operands of K in steps i0 and i0 + 1 of the granule at `tile`: use(i, j, a) for each 16 dimensions, the two steps
-// in turn, so that neighbouring products do not wait for one another.  Lane (gid, tig) holds dimensions D / 4 * tig ..
-// + D / 4 - 1 of rows gid of both groups, four of them in each operand.
+// The operands of K in steps i0 and i0 + 1 of the granule at `tile`: use(j, a, b) for each 16 dimensions, a of the one
+// step and b of the other, so that neighbouring products need not wait for one another.  Lane (gid, tig) holds dimensions
+// D / 4 * tig .. + D / 4 - 1 of rows gid of both groups, four of them in each operand.
 template <int D, class F>
 __device__ __forceinline__ void key_operands(uint32_t tile, int i0, int gid, int tig, F&& use) {
   using G = Granule<D>;
@@ -88,17 +88,17 @@ __device__ __forceinline__ void key_operands(uint32_t tile, int i0, int gid, int
         for (int h = 0; h < 4; ++h) x[i][u][h] = kv4::mul_f16x2(x[i][u][h], s);
       }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t a[4] = {x[i][0][2 * h], x[i][1][2 * h], x[i][0][2 * h + 1], x[i][1][2 * h + 1]};
-        use(i0 + i, 2 * q + h, a);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a[4] = {x[0][0][2 * h], x[0][1][2 * h], x[0][0][2 * h + 1], x[0][1][2 * h + 1]};
+      const uint32_t b[4] = {x[1][0][2 * h], x[1][1][2 * h], x[1][0][2 * h + 1], x[1][1][2 * h + 1]};
+      use(2 * q + h, a, b);
+    }
   }
 }
 
-// The operands of V^T in step i of the values at `tile`: use(w, a) for each tile w of 16 columns of O, whose rows gid and gid + 8 are columns
-// D / 8 * gid + 2 w and + 1.  Nibbles of two keys are put side by side before they become halves.
+// The operands of V^T in step i of the values at `tile`: use(w, a) for four tiles w .. w + 3 of 16 columns of O; rows gid
+// and gid + 8 of tile w are columns D / 8 * gid + 2 w and + 1.  Nibbles of two keys are put side by side before they
+// become halves.
 template <int D, class F>
 __device__ __forceinline__ void value_operands(uint32_t tile, int i, int gid, int tig, F&& use) {
   using G = Granule<D>;
@@ -130,12 +130,13 @@ __device__ __forceinline__ void value_operands(uint32_t tile, int i, int gid, in
       kv4::to_f16x2((a & kLow) | ((b << 4) & ~kLow), h[x][0]);
       kv4::to_f16x2(((a >> 4) & kLow) | (b & ~kLow), h[x][1]);
     }
+    uint32_t a[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a[4] = {kv4::mul_f16x2(h[0][0][j], scale[0]), kv4::mul_f16x2(h[0][1][j], scale[0]),
-                             kv4::mul_f16x2(h[1][0][j], scale[1]), kv4::mul_f16x2(h[1][1][j], scale[1])};
-      use(4 * q + j, a);
+      a[j][0] = kv4::mul_f16x2(h[0][0][j], scale[0]), a[j][1] = kv4::mul_f16x2(h[0][1][j], scale[0]);
+      a[j][2] = kv4::mul_f16x2(h[1][0][j], scale[1]), a[j][3] = kv4::mul_f16x2(h[1][1][j], scale[1]);
     }
+    use(4 * q, a);
   }
 }
 

@@ -226,9 +226,14 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.0f;
-      key_operands<D>(tile, step0, gid, tig, [&](int step, int j, const uint32_t (&a)[4]) {
+      key_operands<D>(tile, step0, gid, tig, [&](int j, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
 #pragma unroll
-        for (int n = 0; n < NT * QP; ++n) ptx::mma_f16(s[n / QP][step & 1], a, qf[n][j][0], qf[n][j][1]);
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            ptx::mma_f16(s[n][0], a, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+            ptx::mma_f16(s[n][1], b, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+          }
       });
 #pragma unroll
       for (int half = 0; half < 2; ++half)
