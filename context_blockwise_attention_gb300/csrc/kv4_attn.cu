@@ -34,9 +34,6 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
     else if (solo_items * 4 <= sms * 6 / 7) r.cluster = 4;
     else if (solo_items * 2 <= sms * 6 / 7 && width > 3 * r.warps) r.cluster = 2;
   }
-#ifdef FORCE_NT
-  tiles(FORCE_NT);
-#endif
   const int64_t blocks = solo_items * r.cluster;
   const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
   const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
@@ -50,10 +47,23 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
     r.most = 0;
     return r;
   }
-  tiles(per <= 8 ? 1 : 2);
-#ifdef FORCE_NT
-  tiles(FORCE_NT);
-#endif
+  // Tiles of rows at once: two share the conversion of the keys, which costs more than a tile's products, but leave 8 warps
+  // an SM instead of 12 at D = 128, and half of the work is in vain for items that end in the first.  Measured over
+  // 16 x 2000-16000 tokens, 8 KV heads, bf16, one / two tiles (three), us:
+  //   D = 128, equal rows  8: 45 / 55 (64); 12: 66 / 62 (70); 16: 67 / 63 (71); 24: 91 / 95 (80); 32: 116 / 99 (121);
+  //            48: 168 / 143 (131); 64: 215 / 181 (182); 96: 315 / 260 (237)
+  //            of 8-16 rows 54 / 61, of 8-24 64 / 69 (77), of 16-32 82 / 76, of 16-48 102 / 93 (98)
+  //   D = 64,  equal rows  8: 32 / 36; 12: 43 / 39; 16: 44 / 39; 24: 58 / 56; 32: 72 / 59; of 8-16 36 / 37, of 8-24 42 / 41
+  // So one tile up to 8 rows; three where that saves a third of the passes; and one again for mixed numbers of rows up
+  // to 16 (12 at D = 64), as a total that the sequences do not divide shows, while the L2 cache hands the keys to the
+  // second block of rows.
+  const int64_t mean = (d.rows.n_rows * group + seqs - 1) / seqs;
+  const bool mixed = d.rows.n_rows % seqs != 0;
+  const int64_t table = seqs * d.rows.max_pages, pages = table < d.cache.n_pages ? table : d.cache.n_pages;
+  const bool cached = pages * d.cache.hkv * d.cache.page_size * d.cache.d * 9 / 8 <= 160000000;
+  if (mixed && cached && r.pp == 1) tiles(mean <= (d.cache.d == 64 ? 12 : 16) ? 1 : 2);
+  else if (r.pp == 1 && d.cache.d == 128 && !mixed && 4 * ((mean + 23) / 24) < 3 * ((mean + 15) / 16)) tiles(3);
+  else tiles(mean <= 8 ? 1 : 2);
   // numbers at most, in fp64: the page table's width times the heads may pass 64 bits
   r.most = (static_cast<double>(d.rows.max_pages) * d.cache.page_size * d.cache.d / 4096 + 1 + kSetup) * d.cache.hkv *
            static_cast<double>(seqs + d.rows.n_rows * group / r.rows);
