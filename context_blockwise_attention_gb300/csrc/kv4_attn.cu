@@ -23,8 +23,16 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
     r.rows = nt * 8;
     r.warps = nt * d.cache.d >= 256 || nt * r.qp >= 4 ? 8 : 12;
   };
-  // Solo, by the page table's width in granules, which bounds the tokens: as many blocks an item as the SMs hold
-  // clusters of, where a block's warps have some granules each.
+  // Solo, by the page table's width in granules, which bounds the tokens, the one thing about them that is known here: as
+  // many blocks an item as the SMs hold clusters of, where a block's warps have some granules each, as long as splitting,
+  // which uses all SMs but has a second kernel, is slower.  Equal sequences, 1, 2, 4, 8 blocks an item / split, us:
+  //   D = 128  4 x 8 items (sequences x KV heads) of 1000 tokens 8.7, 9.1, 8.3, - / 12.9; 4000: 20, 15, 11.5, - / 16; 8000:
+  //            34, 22, 15.5, - / 19; 8 x 8 of 8000: 35, 25, -, - / 27; 16 x 8 of 4000: 23 / 28
+  //            1 item of 1000 9.3, 9.4, 8.4, 8.8 / 9.0; 4000: 20, 15, 11.4, 10.6 / 9.7; 4 items of 8000: 33, 22, 16, 12.2 / 14.5
+  //   D = 64   4 x 8 of 1000 6.8, 7.3, 7.3, - / 11.7; 8000: 20, 15, 10.9, - / 15; 8 x 8 of 8000: 20, 15, -, - / 17
+  //            1 item of 2000 8.4, 8.3, 7.2, 7.4 / 8.3; 8000: 20, 15, 10.4, 9.1 / 8.8; 4 items of 8000: 20, 15, 10.5, 9.1 / 12.1
+  // One row a sequence, as far as can be told from their numbers, or few rows in all, since the blocks take an item's
+  // blocks of rows one after the other.  What it costs is short sequences under a wide table, which are split.
   tiles(per <= 8 ? 1 : 2);
   const int64_t width = (static_cast<int64_t>(d.rows.max_pages) * d.cache.page_size * d.cache.d + 4095) / 4096;
   const int64_t solo_items = seqs * d.cache.hkv;
@@ -37,7 +45,7 @@ Plan plan_of(const cp_kv4_attn_desc& d, int sms) {
   const int64_t blocks = solo_items * r.cluster;
   const int64_t most_rows = d.rows.n_rows > seqs ? d.rows.n_rows - seqs + 1 : 1;
   const int64_t turns = ((most_rows * group + r.rows - 1) / r.rows) * ((per + r.rows - 1) / r.rows);
-  const bool narrow = r.cluster > 1 ? (d.cache.d == 128 ? 20 : 28) * width * turns <= r.warps * r.cluster * blocks
+  const bool narrow = r.cluster > 1 ? 12 * width * turns <= r.warps * r.cluster * blocks
                                     : width <= r.warps * (2 * blocks > sms ? 16 : 4);
   r.solo = blocks <= sms && narrow &&
            (d.rows.n_rows <= seqs || d.rows.n_rows * group <= 4 * r.rows);

@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     const bool masked = key0 + kKeys > lim_min;
     const uint32_t values = tile + Granule<D>::kPair;
     auto product = [&](int n, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-      if (n == 0) ptx::mma_f16(d, a, b0, b1);
+      // tiles without rows are left out where that is cheaper than asking (D = 64: 1 to 4 %; at D = 128 asking costs 2 %)
+      if (n == 0 || D == 128) ptx::mma_f16(d, a, b0, b1);
       else ptx::mma_f16_if(d, a, b0, b1, live > n);
     };
     if (masked) mask_values(values, key0);
