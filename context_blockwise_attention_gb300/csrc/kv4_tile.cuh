@@ -186,7 +186,7 @@ struct Feed {
 
   // Makes the window hold the pages ord .. ord + n - 1; n is at most 8.
   __device__ __forceinline__ void look(const Params& p, int lane, int ord, int n) {
-    if (static_cast<unsigned>(ord - window) + n > 32u) {
+    if (ord < window || ord + n > window + 32) {
       window = ord;
       // entries that hold no token are the caller's to change at any time: they are not read
       pages = -1;

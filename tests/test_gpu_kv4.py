@@ -438,6 +438,20 @@ def test_attention_shapes(rows, held, page, hq, hkv, d, din, dout):
     _check_attn(pool, pool.device(), q, rows, held, [m - n for n, m in zip(rows, held)], PosMap(0, 1), dout)
 
 
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shares_that_begin_inside_an_item_and_go_on_with_the_next_head(d, page):
+    """Small pages, some items to a warp: it looks up pages from the middle of one head on and then those of another."""
+    held = [130 + (37 * i) % 200 for i in range(40)]
+    rows = [1] * 40
+    pool = Pool(40, held, page, 32, d, 84)
+    pool.fill(held, 85)
+    q = torch.randn((40, 32, d), generator=torch.Generator().manual_seed(86)).to(BF16)
+    first = [m - 1 for m in held]
+    _check_attn(pool, pool.device(), q, rows, held, first, PosMap(0, 1), F32, wide=2500)
+    _check_weigh(pool, q, rows, held, first, PosMap(0, 1), None, 1.0, 87, wide=2500)
+
+
 @pytest.mark.parametrize("wide", [0, 3000])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_bad_pages_answer_nan_and_report(d, wide):
