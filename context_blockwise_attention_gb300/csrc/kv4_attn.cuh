@@ -6,9 +6,30 @@
 //   LSE_i = ln 2 (m_i + log2 l_i),        l_i = sum_j p_ij,
 // k_j and v_j being e2m1 numbers times a scale for each 16 of them, which f16 holds exactly.
 //
-// The work is split as over the 8-bit cache (kv_split.cuh, kv_attn.cuh): granules of 4096 / D keys, equal shares of
-// consecutive ones for every warp, partials joined by a second kernel; or, for few short rows, a block or a cluster of
-// blocks an item.
+// Work split.  As over the 8-bit cache (kv_split.cuh, kv_attn.cuh): granules of 4096 / D keys, equal shares of
+// consecutive ones for every warp, which copies ahead into a ring of its own; partials joined by a second kernel
+// (kv_sum.cu).  For few short rows (SOLO) a block or a cluster of blocks an item.  Two granules share a stage of the ring,
+// its wait and its copies: the upkeep of single ones was a quarter of the instructions (83 -> 74 us on the batch below).
+//
+// Products.  mma.sync m16n8k16 with f16 operands, transposed, S^T = K Q^T and O^T = V^T P^T, so that 8 query rows fill an
+// operand.  e2m1 becomes f16 by one instruction for two numbers and is multiplied by its scale in pairs, which is exact
+// (kv4_common.cuh): 2 + 2 instructions for 4 numbers of K and as many, and a half more to put two keys' nibbles side by
+// side, of V.  The 4-bit and 8-bit tensor products take no operands of these scales and precision: queries and weights
+// would have to be rounded to 4 or 8 bits.
+//
+// Precision.  A query row is scaled by a power of two to at most 2^15; as f16 a bf16 row is then exact (over 2^28 of range),
+// an fp32 row is split into a high and a low part, 22 bits.  Weights are held relative to a whole number m_i that is at
+// most kSlack below the row's largest score, times 2^12: one f16 part for a bf16 output (off by 2^-11 at most, against the
+// output's 2^-8), two for an fp32 one.  f16 ends at 2^-24, so a weight is off by 2^-37 of the row's largest besides.
+// Sums, maxima and the accumulators are fp32.
+//
+// Bound.  Each cached byte is used for twice as many products as in the 8-bit cache, and conversions and scales are half
+// of some 580 instructions for a granule and tile of rows: the SMs issue at 55 % of their rate and the ALU pipe is busy for
+// 47 % of the time, beside memory at two thirds of its rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8
+// heads, D = 128, bf16: 73.5 us for 328 MB, 4.5 TB/s (the 8-bit cache: 86); copies alone, without products, 65; the first
+// data are there after 8 us, and SMs end up to a tenth later than others.  8 x 90000-131072, 64/8, D = 64, fp32 partials:
+// 114 us for 513 MB, 4.5 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 100 us; one token over 1000: 8 us.
+// Slower: K and V in slots of their own with 16 warps (73, 118 and 122 us: they spill or hold less in flight).
 #pragma once
 
 #include "kv4_tile.cuh"
@@ -16,14 +37,15 @@
 namespace cpattn {
 namespace kvattn {
 
-constexpr int kPExp = 12;       // P operands are at most 2^(kPExp + kSlack) = 32768 and f16's largest is 65504
+constexpr int kPExp = 12;          // P operands are at most 2^(kPExp + kSlack) = 32768 and f16's largest is 65504
 constexpr float kPUnit = 4096.0f;  // 2^kPExp
-constexpr float kSlack = 3.0f;  // largest s - m
+constexpr float kSlack = 3.0f;     // largest s - m
 
 // QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
 template <int D, int NT, int QP, int PP>
 struct Shape4 {
-  // More warps hide more latency; registers (O takes NT D / 4) bound their number.
+  // More warps hide more latency; registers (O takes NT D / 4) bound their number (10 warps of two tiles spill: 122 us where
+  // 8 take 110).
   static constexpr bool kHeavy = NT * D >= 256 || NT * QP >= 4;
   static constexpr int kWarps = kHeavy ? 8 : 12;
   static constexpr int kRows = NT * 8;  // RT
@@ -307,14 +329,19 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
       else ptx::mma_f16_if(d, a, b0, b1, live > n);
     };
     if (masked) mask_values(values, key0);
-    // S^T: s[n][i][2 u + r] is key key_at(i, u, gid) for query row 2 tig + r of tile n
+    // S^T: s[n][i][2 u + r] is key key_at(i, u, gid) for query row 2 tig + r of tile n.  The low parts of fp32 queries are
+    // summed on their own: as part of the larger sums each of their truncated additions would cost as much as one of those
+    // (7 x 0-8191 tokens, 32/32, D = 128: 1.8e-6 relative to the exact outputs, 1.4e-6 so, in the same time).
     float s[NT][kSteps][4];
 #pragma unroll
     for (int i = 0; i < kSteps; i += 2) {
+      float z[QP][NT][2][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int part = 0; part < QP; ++part)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][i][e] = s[n][i + 1][e] = 0.0f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[part][n][0][e] = z[part][n][1][e] = 0.0f;
       key_operands<D>(tile, i, gid, tig, [&](int j, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
 #pragma unroll
         for (int part = 0; part < QP; ++part)
@@ -322,14 +349,20 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
           for (int n = 0; n < NT; ++n) {
             if constexpr (S::kQSmem) {
               const uint2 q = ptx::lds64(q_smem + (((n * QP + part) * kMt + j) * 32 + lane) * 8);
-              product(n, s[n][i], a, q.x, q.y);
-              product(n, s[n][i + 1], b, q.x, q.y);
+              product(n, z[part][n][0], a, q.x, q.y);
+              product(n, z[part][n][1], b, q.x, q.y);
             } else {
-              product(n, s[n][i], a, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
-              product(n, s[n][i + 1], b, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+              product(n, z[part][n][0], a, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
+              product(n, z[part][n][1], b, qf[n * QP + part][j][0], qf[n * QP + part][j][1]);
             }
           }
       });
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][i + h][e] = QP == 2 ? z[0][n][h][e] + z[QP - 1][n][h][e] : z[0][n][h][e];
     }
     if (masked) {
 #pragma unroll

@@ -10,6 +10,13 @@
 // weight has one writer and its sum one order.  Granules are numbered sequence after sequence, each head beginning with
 // kSetup numbers more, and every warp has an equal share of consecutive ones.  A share's part of a head is gone over
 // once for each block of RT query rows; the keys come by a ring of copies as for attention, the old weights with them.
+//
+// Bound by instructions: a granule's conversions, products and exponentials are some 370 instructions for 64 keys at
+// D = 128, issued at 57 % of the SMs' rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16:
+// 42 us for 173 MB, 4.1 TB/s (granules of half the size and 12 warps 49); 4 x 1-4 rows over 30000-65536, 64/8, D = 64,
+// fp32: 53 us, of which the tensor cores are busy for 42 % (32 query rows of two f16 parts).  Shares by the cost of a
+// sequence's rows were slower (84: a granule's time depends little on its tiles), as were predicates around tiles
+// without rows (60).
 #include "kv4_tile.cuh"
 
 namespace cpattn {
@@ -26,13 +33,13 @@ struct WeighParams {
 
 template <int D, int NT, int QP>
 struct WeighShape {
-  static constexpr int kKeys = 8192 / D;  // of a granule
-  static constexpr int kQ = NT * QP * D / 8;    // registers of query operands
+  static constexpr int kKeys = 8192 / D;      // of a granule
+  static constexpr int kQ = NT * QP * D / 8;  // registers of query operands
   static constexpr int kWarps = kQ <= 16 ? 16 : kQ <= 32 ? 12 : 8;
   static constexpr int kRows = NT * 8;  // RT
   static constexpr int kStages = kWarps == 16 ? 2 : kWarps == 12 ? 3 : 4;
   static constexpr int kOldOff = kKeys * kv4::kRow<D>;  // old weights of the granule
-  static constexpr int kPageOff = kOldOff + kKeys * 4;   // pages of its parts, 8 at most
+  static constexpr int kPageOff = kOldOff + kKeys * 4;  // pages of its parts, 8 at most
   static constexpr int kStage = kPageOff + 32;
   // The plan is looked at before the first copies and lies where they go.
   static constexpr int kBarOff = kWarps * kStages * kStage;
@@ -370,7 +377,9 @@ cp_status launch_kv4_weigh(const cp_kv4_weigh_desc& d, float scale, int64_t time
   w.weight = d.weight;
   w.known = d.known;
   w.decay = d.decay;
-  // the fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries at D = 128)
+  // The fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries at D = 128), since every
+  // pass converts the keys again.  4 x 30000-65536 tokens, 64/8 heads, one / two / four tiles, us: D = 64, fp32, 8 rows
+  // 25 / 34 / -, 16: 43 / 35 / -, 24: 61 / 64 / 54, 32: 78 / 65 / 54; D = 128, bf16, 8: 32 / 40 / -, 32: 105 / 81 / 62.
   const int64_t per = (d.rows.n_rows + d.rows.n_seqs - 1) / d.rows.n_seqs * p.group;
   const int nt = per <= 8 ? 1 : per <= 16 || (!p.q_bf16 && c.d == 128) ? 2 : 4;
   return c.d == 128 ? run_weigh_d<128>(w, nt, num_sms, s) : run_weigh_d<64>(w, nt, num_sms, s);
