@@ -11,12 +11,13 @@
 // at a time, from histograms that the blocks add up through distributed shared memory; of equal tokens the first stay.
 // The weights are read once; the rest is latency, of some ten barriers: of 11 us for 4224 tokens and one block 5 until the
 // sums are there, 3 for the three histograms, 2 for the marks; of 18 us for 65536 tokens and 8 blocks the histograms take 4.
-// Second kernel, a warp a token: the fills, whose sources and holes do not overlap.  Third kernel, a block for each
-// (sequence, head): the recent rows, which move towards the front by n - keep and may overwrite slots that fills came
-// from; a batch is read before it is written, and the batches in order.
-// Measured (GB300, in a graph, with 4 us for copying the weights first): 64 x 4000-4224 tokens to 4096, 8 heads, D = 128: 28 us
-// (floor 2.7, latency of three kernels); 8 x 20000-65536 to 4096, D = 64: 53 us (floor 6.6; filling takes 20, for rows of 36
-// bytes cost the 64 or 96 of the sectors that they touch).
+// Second kernel: some blocks take the recent tokens of a (sequence, head), which move towards the front by n - keep and
+// may overwrite slots that fills came from, in batches that are read before they are written; a warp a token the other
+// fills, whose sources and holes do not overlap with anything.  A kernel for each of the two took 2 and 3 us more on the
+// cases below, keys and values in the same blocks 1 and 3 us more.
+// Measured (GB300, in a graph, with 4 us for copying the weights first): 64 x 4000-4224 tokens to 4096, 8 heads, D = 128:
+// 26.5 us (floor 2.7; latency of two kernels); 8 x 20000-65536 to 4096, D = 64: 47.5 us (floor 6.6; filling takes 20, for
+// rows of 36 bytes cost the 64 or 96 of the sectors that they touch).
 #include <type_traits>
 
 #include "internal.h"
@@ -32,7 +33,7 @@ constexpr int kBins = 2048;
 constexpr int kMostInSmem = 40960;  // tokens of a block
 constexpr int kAtOnce = 4;          // tokens of a thread whose weights are on their way together
 constexpr int kMostCluster = 8;
-constexpr int kFillThreads = 256, kRecentThreads = 512;
+constexpr int kMoveThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Sequence {  // what the first kernel tells the second
@@ -52,7 +53,8 @@ struct EvictParams {
   int32_t* holes;      // [n_seqs, keep]
   uint32_t* store;     // [n_seqs, cluster] of room + 3 room / 32 words, where shared memory is too small; else null
   int32_t cluster, room;  // room: tokens of a block, a multiple of 32
-  int32_t per_seq;     // blocks of a sequence in the second kernel
+  int32_t ordered;     // blocks of the second kernel that move recent tokens
+  int32_t per_seq;     // blocks of a sequence that move fills
 };
 
 __device__ __forceinline__ int page_of(const EvictParams& p, int b, int token) {
@@ -352,14 +354,63 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
 template <int D>
 using Piece = typename std::conditional<D == 128, uint2, uint32_t>::type;
 
-// A warp a token: lanes 0 to 8 move pieces of K, 9 to 17 of V, lane 18 the weight, of kHeads heads at a time.
+// The recent tokens of a (sequence, head), their keys or their values and weights, and in front of them the fills that come
+// from slots which they overwrite: those are among the first fills, as these are in the order of their sources.  A thread
+// takes piece t % 10 of token t / 10.  Batch after batch, each read before it is written: a target is never the source of
+// a later batch, since the recent ones' are in front of their sources and the fills' in front of z.
 template <int D>
-__global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_constant__ EvictParams p) {
+__device__ __forceinline__ void move_in_order(const EvictParams& p, int b, int head, bool values) {
+  constexpr int kTokens = kMoveThreads / 10, kAhead = 4;
+  const Sequence s = p.seqs[b];
+  if (s.recent == 0) return;
+  const int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
+  const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
+  const int fills = min(s.fills, s.recent), by = s.n - p.keep, mine = threadIdx.x / 10, e = threadIdx.x % 10;
+  const bool weight = e == 9;
+  uint8_t* const base = weight ? reinterpret_cast<uint8_t*>(p.weight)
+                               : static_cast<uint8_t*>(values ? p.c.v : p.c.k) + e * static_cast<int>(sizeof(Piece<D>));
+  const int64_t stride = weight ? 4 : kv4::kRow<D>, tokens = static_cast<int64_t>(fills) + s.recent;
+  for (int64_t first = 0; first < tokens; first += kTokens * kAhead) {
+    Piece<D> x[kAhead];
+    uint8_t* to[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t i = first + j * kTokens + mine;
+      to[j] = nullptr;
+      if (i < tokens && mine < kTokens && (values || !weight)) {
+        const int slot = i < fills ? __ldg(list + i) : s.z + static_cast<int>(i - fills);
+        const int source = i < fills ? __ldg(kept + slot) : slot + by;
+        if (i < fills && source >= p.keep) continue;  // another block's
+        to[j] = base + (row_of(p, b, slot) + (head << p.page_log2)) * stride;
+        const uint8_t* const from = base + (row_of(p, b, source) + (head << p.page_log2)) * stride;
+        if (weight) *reinterpret_cast<uint32_t*>(&x[j]) = *reinterpret_cast<const uint32_t*>(from);
+        else x[j] = *reinterpret_cast<const Piece<D>*>(from);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (to[j] != nullptr) {
+        if (weight) *reinterpret_cast<uint32_t*>(to[j]) = *reinterpret_cast<const uint32_t*>(&x[j]);
+        else *reinterpret_cast<Piece<D>*>(to[j]) = x[j];
+      }
+  }
+}
+
+// The first blocks take the recent tokens of a (sequence, head) each, the others the fills that come from behind them, a
+// warp a token: lanes 0 to 8 move pieces of K, 9 to 17 of V, lane 18 the weight, of kHeads heads at a time.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads, 4) kv4_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kHeads = 8;
   ptx::wait_dependencies();
   ptx::launch_dependents();
-  const int b = blockIdx.x / p.per_seq, lane = threadIdx.x & 31;
-  const int first = (blockIdx.x % p.per_seq) * (kFillThreads / 32) + (threadIdx.x >> 5);
+  const int block = static_cast<int>(blockIdx.x) - p.ordered, lane = threadIdx.x & 31;
+  if (block < 0) {
+    const int pair = blockIdx.x >> 1;
+    move_in_order<D>(p, pair / p.c.hkv, pair % p.c.hkv, blockIdx.x & 1);
+    return;
+  }
+  const int b = block / p.per_seq, first = (block % p.per_seq) * (kMoveThreads / 32) + (threadIdx.x >> 5);
   const int fills = __ldg(&p.seqs[b].fills);
   const int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
   const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
@@ -367,9 +418,10 @@ __global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_con
                                         (lane < 9 ? lane : lane - 9) * static_cast<int>(sizeof(Piece<D>))
                                   : reinterpret_cast<uint8_t*>(p.weight);
   const int64_t stride = lane < 18 ? kv4::kRow<D> : 4;
-  for (int i = first; i < fills; i += p.per_seq * (kFillThreads / 32)) {
-    const int t = __ldg(list + i);
-    const int to = row_of(p, b, t), from = row_of(p, b, __ldg(kept + t));
+  for (int i = first; i < fills; i += p.per_seq * (kMoveThreads / 32)) {
+    const int t = __ldg(list + i), source = __ldg(kept + t);
+    if (source < p.keep) continue;
+    const int to = row_of(p, b, t), from = row_of(p, b, source);
     if (lane > 18) continue;
     for (int h = 0; h < p.c.hkv; h += kHeads) {
       Piece<D> x[kHeads];
@@ -391,49 +443,6 @@ __global__ void __launch_bounds__(kFillThreads) kv4_fill_kernel(const __grid_con
   }
 }
 
-// The recent tokens of a (sequence, head): unit u is piece u % 19 of token u / 19.  Batch after batch, each read before it
-// is written: a target is never the source of a later batch, since targets are in front of their sources.
-template <int D>
-__global__ void __launch_bounds__(kRecentThreads, 2) kv4_recent_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int kUnits = 19, kAhead = 4;
-  ptx::wait_dependencies();
-  const int b = blockIdx.x / p.c.hkv, head = blockIdx.x % p.c.hkv;
-  const Sequence s = p.seqs[b];
-  const int head_row = head << p.page_log2, by = s.n - p.keep;
-  const int64_t units = static_cast<int64_t>(s.recent) * kUnits;
-  for (int64_t base = threadIdx.x; base - threadIdx.x < units; base += kRecentThreads * kAhead) {
-    Piece<D> x[kAhead];
-    uint8_t* to[kAhead];
-    bool weight[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int64_t unit = base + j * kRecentThreads;
-      to[j] = nullptr;
-      weight[j] = false;
-      if (unit < units) {
-        const int i = static_cast<int>(unit / kUnits), e = static_cast<int>(unit - static_cast<int64_t>(i) * kUnits);
-        const int64_t at = row_of(p, b, s.z + i) + head_row, from = row_of(p, b, s.z + i + by) + head_row;
-        weight[j] = e == 18;
-        if (weight[j]) {
-          to[j] = reinterpret_cast<uint8_t*>(p.weight + at);
-          *reinterpret_cast<float*>(&x[j]) = p.weight[from];
-        } else {
-          uint8_t* const rows = static_cast<uint8_t*>(e < 9 ? p.c.k : p.c.v) + (e < 9 ? e : e - 9) * sizeof(Piece<D>);
-          to[j] = rows + at * kv4::kRow<D>;
-          x[j] = *reinterpret_cast<const Piece<D>*>(rows + from * kv4::kRow<D>);
-        }
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (to[j] != nullptr) {
-        if (weight[j]) *reinterpret_cast<float*>(to[j]) = *reinterpret_cast<const float*>(&x[j]);
-        else *reinterpret_cast<Piece<D>*>(to[j]) = x[j];
-      }
-  }
-}
-
 struct Layout {
   int cluster, room, per_seq;
   int64_t holes_off, store_off, bytes;
@@ -452,10 +461,10 @@ Layout layout_of(const cp_kv4_evict_desc& d, int sms) {
   const bool fits = r.room <= kMostInSmem;
   const int64_t words = r.room + static_cast<int64_t>(r.room) / 32 * 3;
   r.smem = fits ? static_cast<int>(words * 4) : 0;
-  // a warp for each fill, of which there are as many as tokens that stay from slot z on, up to 16 blocks an SM
+  // a warp for each fill, of which there are as many as tokens that stay from slot z on, up to 8 blocks an SM
   int64_t fills = most - d.keep < d.keep - d.recent ? most - d.keep : d.keep - d.recent;
   if (fills < 1) fills = 1;
-  const int64_t per = kFillThreads / 32, share = (16 * static_cast<int64_t>(sms) + seqs - 1) / seqs;
+  const int64_t per = kMoveThreads / 32, share = (8 * static_cast<int64_t>(sms) + seqs - 1) / seqs;
   r.per_seq = static_cast<int>((fills + per - 1) / per < share ? (fills + per - 1) / per : share);
   r.holes_off = (seqs * static_cast<int64_t>(sizeof(Sequence)) + 255) / 256 * 256;
   r.store_off = r.holes_off + (seqs * d.keep * 4 + 255) / 256 * 256;
@@ -488,6 +497,7 @@ cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t
   p.store = l.smem == 0 ? reinterpret_cast<uint32_t*>(ws + l.store_off) : nullptr;
   p.cluster = l.cluster;
   p.room = l.room;
+  p.ordered = d.recent > 0 ? d.n_seqs * d.cache.hkv * 2 : 0;
   p.per_seq = l.per_seq;
   constexpr int most_smem = (kMostInSmem + kMostInSmem / 32 * 3) * 4;
   // The limit is the function's, not the call's: always the same, for other host threads launch the kernel too.
@@ -510,18 +520,10 @@ cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t
   if (static_cast<int64_t>(d.max_pages) * d.cache.page_size <= d.keep) return CP_OK;  // nothing can be too long
   cfg.numAttrs = 1;
   cfg.dynamicSmemBytes = 0;
-  if (d.keep > d.recent) {
-    cfg.gridDim = dim3(static_cast<unsigned>(d.n_seqs * l.per_seq));
-    cfg.blockDim = dim3(kFillThreads);
-    e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_fill_kernel<128> : kv4_fill_kernel<64>, p);
-    if (e != cudaSuccess) return cuda_fail(e, "kv4_fill_kernel launch");
-  }
-  if (d.recent > 0) {
-    cfg.gridDim = dim3(static_cast<unsigned>(d.n_seqs * d.cache.hkv));
-    cfg.blockDim = dim3(kRecentThreads);
-    e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_recent_kernel<128> : kv4_recent_kernel<64>, p);
-    if (e != cudaSuccess) return cuda_fail(e, "kv4_recent_kernel launch");
-  }
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ordered + (d.keep > d.recent ? d.n_seqs * l.per_seq : 0)));
+  cfg.blockDim = dim3(kMoveThreads);
+  e = cudaLaunchKernelEx(&cfg, d.cache.d == 128 ? kv4_move_kernel<128> : kv4_move_kernel<64>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_move_kernel launch");
   return CP_OK;
 }
 
