@@ -9,7 +9,7 @@
 // Work split.  As over the 8-bit cache (kv_split.cuh, kv_attn.cuh): granules of 4096 / D keys, equal shares of
 // consecutive ones for every warp, which copies ahead into a ring of its own; partials joined by a second kernel
 // (kv_sum.cu).  For few short rows (SOLO) a block or a cluster of blocks an item.  Two granules share a stage of the ring,
-// its wait and its copies: the upkeep of single ones was a quarter of the instructions (83 -> 74 us on the batch below).
+// its wait and its copies: the upkeep of single ones was a quarter of the instructions (83 -> 74 us on the batch below, as it was then).
 //
 // Products.  mma.sync m16n8k16 with f16 operands, transposed, S^T = K Q^T and O^T = V^T P^T, so that 8 query rows fill an
 // operand.  e2m1 becomes f16 by one instruction for two numbers and is multiplied by its scale in pairs, which is exact
@@ -37,6 +37,10 @@
 namespace cpattn {
 namespace kvattn {
 
+// What an item costs besides its granules: its end and the next one's begin take a warp 3 to 5 us, a granule of the two
+// long cases below 1.3.  At 1 the warps with many short items ended last, 8 us behind the others; 1 / 2 / 3 / 4, us: the
+// batch 73.7 / 69.5 / 69.5 / 69.6, 16 x 2-6 rows 99.6 / 100.2 / 97.0 / 96.0, 26 other calls in the mean 13.9 at each.
+constexpr int kSetup = 3;
 constexpr int kPExp = 12;          // P operands are at most 2^(kPExp + kSlack) = 32768 and f16's largest is 65504
 constexpr float kPUnit = 4096.0f;  // 2^kPExp
 constexpr float kSlack = 3.0f;     // largest s - m

@@ -24,6 +24,8 @@ namespace kvattn {
 
 namespace {
 
+constexpr int kSetup = 1;  // what a head costs besides its granules (2, 3 and 4 are no faster)
+
 struct WeighParams {
   Params p;  // q, lse (read), rows, tile[0], ...
   float* weight;

@@ -132,6 +132,7 @@ cp_status launch_kv_attn(const cp_kv_attn_desc& d, float scale, int64_t timeout_
   p.aside = reinterpret_cast<float*>(ws + pl.aside_off);
   const int64_t seqs = d.rows.n_seqs;
   const int64_t items = (seqs + d.rows.n_rows * p.group / pl.rows) * c.hkv;
+  p.setup = kSetup;
   p.few = 128 * items;
   p.cluster = pl.cluster;
   return c.d == 128 ? run_d<128>(p, pl, mk, mv, items, num_sms, s) : run_d<64>(p, pl, mk, mv, items, num_sms, s);

@@ -56,6 +56,7 @@
 namespace cpattn {
 namespace kvattn {
 
+constexpr int kSetup = 1;            // what an item costs besides its granules
 constexpr int kPExp = 15;            // P operands are below 2^(kPExp + kTop) = 65490 and f16's largest is 65504
 constexpr float kTop = 0.999f;       // largest s + log2 vs - base - m
 constexpr float kNear = 40.0f;       // largest |log2 vs - base| but for base = kFarBase

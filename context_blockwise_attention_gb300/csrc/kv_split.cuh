@@ -11,7 +11,6 @@ namespace cpattn {
 namespace kvattn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kSetup = 1;            // what an item costs besides its granules
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int D>
@@ -33,6 +32,7 @@ struct Params {
   int32_t* status;
   int64_t timeout_ns;
   int64_t few;     // workers that may have less than four numbers
+  int32_t setup;   // what an item costs besides its granules, in granules
   int32_t cluster; // SOLO 2: blocks of an item, 2 to 8
   float* part_o;   // [workers][2][RT][D]
   float2* part_ml; // [workers][2][RT]: m (base 2), l
@@ -78,7 +78,7 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   return s;
 }
 __device__ __forceinline__ int64_t numbers(const Params& p, const Seq& s) {
-  return static_cast<int64_t>(s.blocks) * p.hkv * (s.gpi + kSetup);
+  return static_cast<int64_t>(s.blocks) * p.hkv * (s.gpi + p.setup);
 }
 
 // Shares of W numbers among n workers: worker w has [share(w), share(w + 1)).

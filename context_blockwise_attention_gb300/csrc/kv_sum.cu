@@ -30,7 +30,7 @@ __device__ __forceinline__ Parts parts_of(const Params& p, const int64_t* plan, 
   const int rho = static_cast<int>(row - seq.r0) * p.group + (h - head * p.group);
   const int block = rho / RT;
   r.local = rho - block * RT;
-  const int64_t from = plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + kSetup) + kSetup;
+  const int64_t from = plan[b] + (static_cast<int64_t>(head) * seq.blocks + block) * (seq.gpi + p.setup) + p.setup;
   r.w0 = worker_of(W, n_workers, from);
   const int64_t w1 = worker_of(W, n_workers, from + seq.gpi - 1);
   r.slot0 = share(W, n_workers, r.w0) < from ? 1 : 0;       // the later ones begin inside of the item
