@@ -6,17 +6,20 @@
 // no running maximum and nothing to join: every key is on its own.  Bound: keys and weights are read once and weights
 // written once; values are not touched.
 //
-// The unit of work is a granule (8192 / D tokens of one sequence and head) with all of the sequence's rows, so each
-// weight has one writer and its sum one order.  Granules are numbered sequence after sequence, each head beginning with
-// kSetup numbers more, and every warp has an equal share of consecutive ones.  A share's part of a head is gone over
-// once for each block of RT query rows; the keys come by a ring of copies as for attention, the old weights with them.
+// The unit of work is a granule (4096 / D tokens of one sequence and head) with all of the sequence's rows, so each
+// weight has one writer and its sum one order; two share a stage of the ring, its wait and its copies.  Granules are
+// numbered sequence after sequence, each head beginning with kSetup numbers more, and every warp has an equal share of
+// consecutive ones.  A share's part of a head is gone over once for each block of RT query rows; the keys come by a ring
+// of copies as for attention, the old weights with them.
 //
-// Bound by instructions: a granule's conversions, products and exponentials are some 370 instructions for 64 keys at
-// D = 128, issued at 57 % of the SMs' rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128, bf16:
-// 42 us for 173 MB, 4.1 TB/s (granules of half the size and 12 warps 49); 4 x 1-4 rows over 30000-65536, 64/8, D = 64,
-// fp32: 53 us, of which the tensor cores are busy for 42 % (32 query rows of two f16 parts).  Shares by the cost of a
-// sequence's rows were slower (84: a granule's time depends little on its tiles), as were predicates around tiles
-// without rows (60).
+// Bound by instructions: the conversions, products and exponentials of two granules are some 370 instructions for 64 keys
+// at D = 128, issued at 57 % of the SMs' rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128,
+// bf16: 41.5 us for 173 MB, 4.2 TB/s (12 warps 49); 4 x 1-4 rows over 30000-65536, 64/8, D = 64, fp32: 49.5 us, of which the
+// tensor cores are busy for 45 % (32 query rows of two f16 parts).  With shares of whole stages it took 54, some warps
+// having 9 and some 10 of them (14 calls of many kinds 9 % more in the mean; 16 rows of 4 at D = 128, bf16, 59 against
+// 62).  Shares by the cost of a sequence's rows were slower (84: a granule's time depends little on its tiles), as were
+// predicates around tiles without rows (60); queries in shared memory and 12 warps gained 3 to 8 % for fp32 and lost 25 %
+// for bf16 at D = 128.
 #include "kv4_tile.cuh"
 
 namespace cpattn {
@@ -24,7 +27,8 @@ namespace kvattn {
 
 namespace {
 
-constexpr int kSetup = 1;  // what a head costs besides its granules (2, 3 and 4 are no faster)
+// What a head costs besides its granules, in granules (1 / 2 / 4: the batch above 41.9 / 41.5 / 41.4 us).
+constexpr int kSetup = 2;
 
 struct WeighParams {
   Params p;  // q, lse (read), rows, tile[0], ...
@@ -35,13 +39,13 @@ struct WeighParams {
 
 template <int D, int NT, int QP>
 struct WeighShape {
-  static constexpr int kKeys = 8192 / D;      // of a granule
+  static constexpr int kKeys = Granule<D>::kKeys;
   static constexpr int kQ = NT * QP * D / 8;  // registers of query operands
   static constexpr int kWarps = kQ <= 16 ? 16 : kQ <= 32 ? 12 : 8;
   static constexpr int kRows = NT * 8;  // RT
   static constexpr int kStages = kWarps == 16 ? 2 : kWarps == 12 ? 3 : 4;
-  static constexpr int kOldOff = kKeys * kv4::kRow<D>;  // old weights of the granule
-  static constexpr int kPageOff = kOldOff + kKeys * 4;  // pages of its parts, 8 at most
+  static constexpr int kOldOff = Granule<D>::kPair;         // old weights of the stage's keys
+  static constexpr int kPageOff = kOldOff + 2 * kKeys * 4;  // pages of their parts, 8 at most
   static constexpr int kStage = kPageOff + 32;
   // The plan is looked at before the first copies and lies where they go.
   static constexpr int kBarOff = kWarps * kStages * kStage;
@@ -87,9 +91,12 @@ struct Walk {
     g1 = s.gpi - from < left ? s.gpi : from + left;
     left -= g1 - g0;
   }
-  // To the next granule; false at the end of the share.
+  // How many granules go through the ring together.
+  __device__ __forceinline__ int step() const { return together(g, g1); }
+  // To the granules behind these; false at the end of the share.
   __device__ __forceinline__ bool next(const WeighParams& w) {
-    if (++g < g1) return true;
+    g += step();
+    if (g < g1) return true;
     if (++block < s.blocks) {
       g = g0;
       return true;
@@ -182,8 +189,8 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       feed.window = -32;
     }
     feed.head = f.head;
-    // Two of the attention's granules; pages for the way back, and old weights for the first block of rows.
-    feed.stage(p, lane, 2 * f.g, 2, dst, bar, [&](int i, int page, int slot, int rows) {
+    // Pages too, for the way back, and old weights for the first block of rows.
+    feed.stage(p, lane, f.g, f.step(), dst, bar, [&](int i, int page, int slot, int rows) {
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + S::kPageOff + 4 * i), "r"(page) : "memory");
       if (page < 0 || f.block > 0) return 0u;
       const uint32_t bytes = ((rows + 3) & ~3) * 4;
@@ -223,9 +230,9 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
     lim_min = __reduce_min_sync(kFull, lmin);
   };
 
-  auto granule = [&](uint32_t tile) {
-    const int key0 = c.g * kKeys;
-    const int part_log2 = p.page >= kKeys ? 31 : p.page_log2;  // the granule's tokens of one page
+  auto granule = [&](uint32_t stage, int i, int part_log2) {
+    const uint32_t tile = stage + i * Granule<D>::kHalf;
+    const int key0 = (c.g + i) * kKeys;
     const bool masked = key0 + kKeys > lim_min;
     float sum[2 * kSteps];  // key key_at(i, u, gid)
 #pragma unroll
@@ -267,12 +274,13 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       const float x = tig == 0 ? sum[4 * q] : tig == 1 ? sum[4 * q + 1] : tig == 2 ? sum[4 * q + 2] : sum[4 * q + 3];
       const int k = key_at<D>(2 * q + (tig >> 1), tig & 1, gid), key = key0 + k;
       if (key >= c.s.tokens) continue;
-      const int page = static_cast<int>(lds32(tile + S::kPageOff + 4 * (k >> part_log2)));
+      const int page = static_cast<int>(lds32(stage + S::kPageOff + 4 * (i * kKeys + k >> part_log2)));
       if (page < 0) continue;
       float* const at = w.weight + ((page * p.hkv + c.head) * p.page + (key & (p.page - 1)));
       float old = 0.0f;
       if (c.block > 0) old = *at;  // what this lane wrote
-      else if (key < c.s.known && w.decay != 0.0f) old = w.decay * __uint_as_float(lds32(tile + S::kOldOff + 4 * k));
+      else if (key < c.s.known && w.decay != 0.0f)
+        old = w.decay * __uint_as_float(lds32(stage + S::kOldOff + 4 * (i * kKeys + k)));
       *at = old + x;
     }
   };
@@ -292,7 +300,9 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
   begin_block();
   while (in_flight > 0) {
     if (!wait(bars + st * 8, parity)) break;
-    granule(ring + st * S::kStage);
+    const int n = c.step(), part_log2 = p.page >= n * kKeys ? 31 : p.page_log2;  // the stage's tokens of one page
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) granule(ring + st * S::kStage, i, part_log2);
     __syncwarp();
     if (more) issue(st);
     else --in_flight;
@@ -381,7 +391,8 @@ cp_status launch_kv4_weigh(const cp_kv4_weigh_desc& d, float scale, int64_t time
   w.decay = d.decay;
   // The fewest tiles of 8 rows that hold a sequence's rows on average, 4 at most (2 of fp32 queries at D = 128), since every
   // pass converts the keys again.  4 x 30000-65536 tokens, 64/8 heads, one / two / four tiles, us: D = 64, fp32, 8 rows
-  // 25 / 34 / -, 16: 43 / 35 / -, 24: 61 / 64 / 54, 32: 78 / 65 / 54; D = 128, bf16, 8: 32 / 40 / -, 32: 105 / 81 / 62.
+  // 23 / 30 / 47, 16: 41 / 30 / 47, 24: 58 / 56 / 48, 32: 75 / 57 / 48; D = 128, bf16, 8: 30 / 39 / 58, 16: 56 / 40 / 59,
+  // 24: 79 / 78 / 60, 32: 104 / 80 / 61.
   const int64_t per = (d.rows.n_rows + d.rows.n_seqs - 1) / d.rows.n_seqs * p.group;
   const int nt = per <= 8 ? 1 : per <= 16 || (!p.q_bf16 && c.d == 128) ? 2 : 4;
   return c.d == 128 ? run_weigh_d<128>(w, nt, num_sms, s) : run_weigh_d<64>(w, nt, num_sms, s);
