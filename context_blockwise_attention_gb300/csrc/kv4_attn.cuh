@@ -26,7 +26,7 @@
 // Bound.  Each cached byte is used for twice as many products as in the 8-bit cache, and conversions and scales are half
 // of some 580 instructions for a granule and tile of rows: the SMs issue at 57 % of their rate and the ALU pipe is busy for
 // 49 % of the time, beside memory at two thirds of its rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8
-// heads, D = 128, bf16: 69.5 us for 328 MB, 4.7 TB/s (the 8-bit cache: 86): copies begin at 4 us, the first data are there
+// heads, D = 128, bf16: 69 us for 328 MB, 4.7 TB/s (the 8-bit cache: 86): copies begin at 4 us, the first data are there
 // at 8, the warps end at 53 to 64 and the second kernel at 68; 6 TB/s between.  8 x 90000-131072, 64/8, D = 64, fp32
 // partials: 114 us for 513 MB, 4.5 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 97 us; one token over 1000: 8 us.
 // Slower: K and V in slots of their own with 16 warps (73, 118 and 122 us: they spill or hold less in flight).
@@ -54,9 +54,11 @@ struct Shape4 {
   static constexpr int kWarps = kHeavy ? 8 : 12;
   static constexpr int kRows = NT * 8;  // RT
   // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: the accumulators are added
-  // to others every kFlush granules, in registers where there are some left (kHold), else in the workspace.
+  // to others every kFlush granules, in registers where there are some left (kHold), else in the workspace.  Every 2 or 4
+  // with kHold, on the 8 long sequences above: 4.2e-7 to 7.0e-7 or 5.5e-7 to 7.5e-7 relative to the exact outputs, and
+  // 0.3 us between them.
   static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
-  static constexpr int kFlush = PP == 1 ? 64 : kHold ? 4 : D == 128 ? 16 : 8;
+  static constexpr int kFlush = PP == 1 ? 64 : kHold ? 2 : D == 128 ? 16 : 8;
   static constexpr int kKeys = Granule<D>::kKeys;
   static constexpr int kSteps = Granule<D>::kSteps;
   static constexpr int kRow = Granule<D>::kRow;
@@ -428,26 +430,29 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
     uint32_t pb[NT][PP][kSteps][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+      // two rows at a time
+      const uint64_t ref = ptx::f2_pack(m[n][0] == -INFINITY ? 0.0f : -m[n][0], m[n][1] == -INFINITY ? 0.0f : -m[n][1]);
+      const uint64_t both = ptx::f2_pack(fac[n][0], fac[n][1]), unit = ptx::f2_pack(kPUnit, kPUnit);
+      uint64_t sum = ptx::f2_pack(l[n][0], l[n][1]);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           float w[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            w[r] = ex2(fmaf(s[n][i][2 * u + r], fac[n][r], -ref[r]));
-            l[n][r] += w[r];
-          }
+          ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[n][i][2 * u], s[n][i][2 * u + 1]), both, ref), w[0], w[1]);
+          const uint64_t w2 = ptx::f2_pack(ex2(w[0]), ex2(w[1])), x2 = ptx::f2_mul(w2, unit);
+          sum = ptx::f2_add(sum, w2);
           float a, b;
-          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(w[0], w[1]), ptx::f2_pack(kPUnit, kPUnit)), a, b);
+          ptx::f2_unpack(x2, a, b);
           const uint32_t h = to_f16x2(a, b);
           pb[n][0][i][u] = ptx::transpose8x8(h);
           if constexpr (PP == 2) {
             const float2 back = from_f16x2(h);
-            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(a - back.x, b - back.y));
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(back.x, back.y), ptx::f2_pack(-1.0f, -1.0f), x2), a, b);
+            pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(a, b));
           }
         }
+      ptx::f2_unpack(sum, l[n][0], l[n][1]);
     }
     // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll
