@@ -13,9 +13,9 @@
 // of copies as for attention, the old weights with them.
 //
 // Bound by instructions: the conversions, products and exponentials of two granules are some 370 instructions for 64 keys
-// at D = 128, issued at 57 % of the SMs' rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128,
+// at D = 128, issued at 60 % of the SMs' rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8 heads, D = 128,
 // bf16: 41.5 us for 173 MB, 4.2 TB/s (12 warps 49); 4 x 1-4 rows over 30000-65536, 64/8, D = 64, fp32: 49.5 us, of which the
-// tensor cores are busy for 45 % (32 query rows of two f16 parts).  With shares of whole stages it took 54, some warps
+// tensor cores are busy for 42 % (32 query rows of two f16 parts).  With shares of whole stages it took 54, some warps
 // having 9 and some 10 of them (14 calls of many kinds 9 % more in the mean; 16 rows of 4 at D = 128, bf16, 59 against
 // 62).  Shares by the cost of a sequence's rows were slower (84: a granule's time depends little on its tiles), as were
 // predicates around tiles without rows (60); queries in shared memory and 12 warps gained 3 to 8 % for fp32 and lost 25 %
