@@ -215,11 +215,13 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       const int t = live ? rho / p.group : 0;
       const int64_t out = (c.s.r0 + t) * p.hq + c.head * p.group + (rho - t * p.group);
       const int lm = live ? visible(p, c.s.tokens, c.s.pos0 + t) : 0;
-      // a row whose LSE is not finite has no weights to give
+      // A row whose LSE is not finite has no weights to give: 2^(0 - inf) with zeros for its operands, since its query, which
+      // the LSE mostly comes from, need not be finite.
       const float lse = live ? __ldg(p.lse + out) : INFINITY;
-      const float l2 = fabsf(lse) < INFINITY ? lse * kLog2e : INFINITY;
+      const bool gives = fabsf(lse) < INFINITY;
+      const float l2 = gives ? lse * kLog2e : INFINITY;
       if (live) lmin = min(lmin, lm);
-      const float f = query_operands<D, QP>(p, out * D, live, tig, &qf[n * QP]);
+      const float f = query_operands<D, QP>(p, out * D, gives, tig, &qf[n * QP]);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);

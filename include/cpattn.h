@@ -610,7 +610,7 @@ cp_status cp_kv4_cache_attn_workspace(const cp_kv4_attn_desc* desc, int64_t* byt
  *   weight   device fp32 [n_pages, hkv, page_size]: laid out as the cache, 16-byte aligned
  *   q, lse   device [n_rows, hq, d] (in_dtype), 16-byte aligned; fp32 [n_rows, hq]: the rows' final LSE, merged over the
  *            ranks, so that the weights of all ranks' tokens add up to 1 for each row and query head.  A row and head
- *            whose lse is not finite gives nothing.
+ *            whose lse is not finite gives nothing, whatever its query holds.
  *   known    device int32 [n_seqs] or NULL: how many of the tokens have gathered weight already; the memory of the others
  *            need not be initialised.  NULL: all.  With decay 0 no old weight is looked at.
  *   decay    in [0, 1]
