@@ -44,6 +44,18 @@ constexpr int kSetup = 3;
 constexpr int kPExp = 12;          // P operands are at most 2^(kPExp + kSlack) = 32768 and f16's largest is 65504
 constexpr float kPUnit = 4096.0f;  // 2^kPExp
 constexpr float kSlack = 3.0f;     // largest s - m
+// m goes by scores that are rounded to fp32 and weights by fma(product, factor, -m), which is not: they differ by 2^-4 at most
+// where |m| is below kLarge, but by 8 from 2^27 on.  So from kLarge on m is set 2 to 4 fp32 steps below the score, the exponent
+// stays at or above 0 for the largest, and ends at kMost, below which f16 holds the weight: scores of a large magnitude that
+// are some steps of fp32 apart, which is less than they are off, count as equal.  (Ending the exponents costs 1 % of the batch
+// below and 0 to 1 % of the other calls; a path of their own for such rows, with rounded scores, 2 to 4 %.)
+constexpr float kLarge = 1048576.0f;
+constexpr float kMost = 3.9f;
+__device__ __forceinline__ float at_most(float x, float most) {  // NaN stays
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+  return y;
+}
 
 // QP, PP: f16 parts of a query element and of a weight.  NT: tiles of 8 query rows.
 template <int D, int NT, int QP, int PP>
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
             for (int u = 0; u < 2; ++u)
               if (key0 + key_at<D>(i, u, gid) >= lim[n][r]) s[n][i][2 * u + r] = -INFINITY;
     }
-    // Maxima.  s keeps the products; a score is s * fac (fac > 0).  m is a whole number, so rescaling is exact, and it
+    // Maxima.  s and top keep the products; a score is s * fac (fac > 0).  m is a whole number, so rescaling is exact, and it
     // moves only where a score is more than kSlack above it: mostly a comparison by every lane on its own is enough.
     bool grew = false;
     float top[NT][2];
@@ -392,8 +404,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         top[n][r] = fmaxf(s[n][0][r], s[n][0][2 + r]);
 #pragma unroll
         for (int i = 1; i < kSteps; ++i) top[n][r] = fmaxf(top[n][r], fmaxf(s[n][i][r], s[n][i][2 + r]));
-        top[n][r] *= fac[n][r];
-        grew |= top[n][r] > m[n][r] + kSlack;  // false where both are -inf
+        grew |= fmaf(top[n][r], fac[n][r], -m[n][r]) > kSlack;  // false where both are -inf
       }
     if (__any_sync(kFull, grew)) {
 #pragma unroll
@@ -401,11 +412,12 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         float c[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x = top[n][r];
+          float x = top[n][r] * fac[n][r];
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          const float now = x > m[n][r] + kSlack ? floorf(x) : m[n][r];
+          const float low = fabsf(x) >= kLarge ? fmaf(fabsf(x), -0x1p-22f, x) : x;
+          const float now = x > m[n][r] + kSlack ? fmaxf(floorf(low), m[n][r]) : m[n][r];
           c[r] = now > m[n][r] ? ex2(m[n][r] - now) : 1.0f;
           m[n][r] = now;
           l[n][r] *= c[r];
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         for (int u = 0; u < 2; ++u) {
           float w[2];
           ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[n][i][2 * u], s[n][i][2 * u + 1]), both, ref), w[0], w[1]);
-          const uint64_t w2 = ptx::f2_pack(ex2(w[0]), ex2(w[1])), x2 = ptx::f2_mul(w2, unit);
+          const uint64_t w2 = ptx::f2_pack(ex2(at_most(w[0], kMost)), ex2(at_most(w[1], kMost))), x2 = ptx::f2_mul(w2, unit);
           sum = ptx::f2_add(sum, w2);
           float a, b;
           ptx::f2_unpack(x2, a, b);
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
   };
 
   // Leaves the rows of an item: the answer where the item was this worker's alone, else a partial at
-  // part_o [RT][D], part_ml [RT], with l between 1 and 2.
+  // part_o [RT][D], part_ml [RT], with l between 1 and 2 where |m| is below kLarge.
   auto end_item = [&](bool whole, float* part_o, float2* part_ml) {
     const int n_rows = seq.rows * p.group;
 #pragma unroll
@@ -539,7 +551,9 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         const int rho = row_q + local;
         if (rho >= n_rows) continue;
         const float keep = keep_of(n, r);
-        const int up = min(max(static_cast<int>(__float_as_uint(sum) >> 23 & 255u) - 127, -100), 126);
+        // the exponent of l goes to m, but for an m that might not hold it
+        const int up =
+            fabsf(m[n][r]) >= kLarge ? 0 : min(max(static_cast<int>(__float_as_uint(sum) >> 23 & 255u) - 127, -100), 126);
         const float norm = sum * kv::pow2(-up), ref = m[n][r] + static_cast<float>(up);
         const float back = kv::pow2(-kPExp - up);
         const float f = whole ? (sum == 0.0f ? 0.0f : back / norm) : back;

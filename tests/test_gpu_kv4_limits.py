@@ -2,10 +2,12 @@
 other tests unless one is derived here.
 """
 
+import numpy as np
 import pytest
 import torch
 
 import helpers
+from oracle import cache4 as o4
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +41,86 @@ def test_rows_whose_query_is_not_finite_give_no_weight(d, page, hq, dtype):
     assert torch.equal(lse.isfinite().cpu(), ~spoilt) and torch.equal(lse.cpu()[~spoilt], clean.cpu()[~spoilt])
     kv4._check_weigh(pool, q, rows, held, first, PosMap(0, 1), None, 1.0, 204)
     kv4._check_weigh(pool, q, rows, held, first, PosMap(0, 1), [190, 0, 33], 0.5, 205)
+
+
+@pytest.mark.parametrize("wide,at_once", [(2500, 24), (0, 2), (600, 2)])  # split; one block; a cluster of blocks
+@pytest.mark.parametrize("d,page,g,din,dout", [(64, 64, 4, BF16, BF16), (64, 16, 8, F32, F32), (64, 128, 12, BF16, F32),
+                                               (128, 32, 4, F32, F32), (128, 64, 16, BF16, BF16), (128, 128, 8, BF16, F32),
+                                               (128, 64, 20, BF16, BF16)])
+def test_scores_of_any_size(d, page, g, din, dout, wide, at_once):
+    """Rows whose largest score, from 2^10 to 2^98, is that of all tokens with one key, beside which the others vanish; and
+    rows of the opposite sign, whose largest is that of the tokens with the key's opposite.  Equal keys have equal scores,
+    so the answer is the mean of these tokens' values, off by what rounds weights and sums: w + n 2^-27 + 2^-20 of the mean
+    magnitude (as for other calls, without the scores' errors), and the output's half step.  LSE is the score, within its own
+    error, plus ln n."""
+    held, hkv, rows = 700, 2, 24
+    pool = Pool(1, [held], page, hkv, d, 211)
+    rng = np.random.default_rng(212)
+    key = rng.choice([-1.0, 1.0], (1, hkv, d)) * rng.uniform(0.5, 1, (1, hkv, d)) * 2.0 ** 13
+    kind = rng.choice([1.0, 1.0, -1.0, 0.0, 0.5], held)
+    o4.cache_write(pool.rows[0], kind[:, None, None] * key, [0, held], [0], pool.table)
+    o4.cache_write(pool.rows[1], rng.standard_normal((held, hkv, d)), [0, held], [0], pool.table)
+    x = torch.from_numpy(np.repeat(np.sign(key), g, 1) * np.abs(rng.standard_normal((rows // 2, hkv * g, d)))).to(F32)
+    x = x * torch.exp2(torch.arange(rows // 2) * 8.0 - 4.0)[:, None, None]
+    q = torch.stack((x, -3 * x), 1).reshape(rows, hkv * g, d).to(din)
+    table = _i32(np.concatenate([pool.table, np.full((1, wide), -1)], 1))
+    cache = pool.device()
+    got = [cpa.kv4_cache_attn(q[i:i + at_once].to(DEV), cache, _i32([0, at_once]), _i32([held]), table, o_dtype=dout)
+           for i in range(0, rows, at_once)]
+    o, lse = (torch.cat(t).double().cpu().numpy() for t in zip(*got))
+    k, v = pool.tokens_of(0, held)
+    for i in range(rows):
+        top = kind == (-1.0 if i % 2 else 1.0)
+        n = int(top.sum())
+        for h in range(hkv * g):
+            qd = q[i, h].double().numpy()
+            s = (k[:, h // g] @ qd) * d ** -0.5
+            assert s[top].min() - np.max(s[~top]) > 200  # the others' weights are below any rounding
+            vh = v[top, h // g]
+            ref, mean = vh.mean(0), np.abs(vh).mean(0)
+            w = 2.0 ** -11 if dout == BF16 else 2.0 ** -21
+            tol = mean * (w + n * 2.0 ** -27 + 2.0 ** -20 + 2.0 ** -37)
+            tol = tol + np.abs(ref) * (2.0 ** -8 if dout == BF16 else 2.0 ** -24) * 1.01
+            err = np.abs(o[i, h] - ref)
+            assert np.all(err <= tol), (i, h, s.max(), float((err / tol).max()))
+            a = np.abs(k[top, h // g][0]) @ np.abs(qd) * d ** -0.5
+            assert abs(lse[i, h] - (s.max() + np.log(n))) <= 2.0 ** -20 * a + 2.0 ** -22 * abs(s.max()) + n * 2.0 ** -24 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("wide,at_once", [(2500, 20), (0, 2), (600, 2)])
+@pytest.mark.parametrize("d,page,din,dout", [(64, 64, BF16, BF16), (64, 16, F32, F32), (128, 32, BF16, F32), (128, 128, F32, F32)])
+def test_large_scores_next_to_one_another(d, page, din, dout, wide, at_once):
+    """Large scores that differ in their last steps of fp32, in any order.  Each is off by delta, and from 2^20 on those
+    within 5 steps (2^-20 of the score) count as equal, so what is known of a row is that it is a mean of the values of tokens
+    whose score is the largest but for that, and LSE that score plus the logarithm of at most their number."""
+    held, rows = 900, 20
+    pool = Pool(1, [held], page, 1, d, 241)
+    rng = np.random.default_rng(242)
+    key = rng.choice([-1.0, 1.0], (1, 1, d)) * 2.0 ** 13 * np.repeat([6.0, 4.0, 3.0, 2.0], d // 4)
+    k = np.repeat(key, held, 0)
+    small = rng.integers(0, d, held)  # one element of a token is a step smaller, most steps alike in the sum
+    k[np.arange(held), 0, small] *= rng.choice([1.0, 0.75], held)
+    o4.cache_write(pool.rows[0], k, [0, held], [0], pool.table)
+    o4.cache_write(pool.rows[1], rng.standard_normal((held, 1, d)), [0, held], [0], pool.table)
+    x = np.repeat(np.sign(key), 4, 1) * 2.0 ** rng.uniform(-16, 0, (rows, 4, d))
+    x[:, :, :d // 2] = np.sign(key)[:, :, :d // 2]
+    x = x * 2.0 ** np.arange(-2, rows - 2)[:, None, None] * rng.choice([-1.0, 1.0], (rows, 1, 1))
+    q = torch.from_numpy(x).to(din)
+    table = _i32(np.concatenate([pool.table, np.full((1, wide), -1)], 1))
+    cache = pool.device()
+    got = [cpa.kv4_cache_attn(q[i:i + at_once].to(DEV), cache, _i32([0, at_once]), _i32([held]), table, o_dtype=dout)
+           for i in range(0, rows, at_once)]
+    o, lse = (torch.cat(t).double().cpu().numpy() for t in zip(*got))
+    k, v = (t[:, 0] for t in pool.tokens_of(0, held))
+    for i in range(rows):
+        for h in range(4):
+            qd = q[i, h].double().numpy()
+            s = (k @ qd) * d ** -0.5
+            top = s.max()
+            delta = float((2.0 ** -20 * d ** -0.5 * (np.abs(k) @ np.abs(qd)) + 2.0 ** -22 * np.abs(s)).max())
+            among = v[s >= top - 2 * delta - 2.0 ** -20 * abs(top) - 40]
+            # weights and sums: 2^-11 or 2^-21, 900 2^-27 and 2^-20; the output's half step
+            tol = np.abs(among).max(0) * (2.0 ** -7 if dout == BF16 else 2.0 ** -16)
+            assert np.all(o[i, h] >= among.min(0) - tol) and np.all(o[i, h] <= among.max(0) + tol), (i, h, top)
+            off = delta + 2.0 ** -20 * abs(top) + 2.0 ** -20
+            assert top - off <= lse[i, h] <= top + off + np.log(len(s)), (i, h, top, lse[i, h])
