@@ -104,7 +104,8 @@ cp_status validate_call(const char* who, const cp_posmap& kv_pos, float scale, i
   if (kv_pos.stride < 1) CP_INVALID("%s: position strides must be >= 1", who);
   if (kv_pos.base < 0) CP_INVALID("%s: positions must be >= 0", who);
   if (kv_pos.stride > 2000000000 || kv_pos.base > 2000000000) CP_INVALID("%s: global positions exceed 2e9", who);
-  if (!(scale >= 0.0f) || isinf(scale)) CP_INVALID("%s: scale must be finite and >= 0", who);
+  // the kernels take scores in base 2
+  if (!(scale >= 0.0f) || isinf(scale * 1.4426950408889634f)) CP_INVALID("%s: scale must be >= 0 and at most 2e38", who);
   if (flags & ~CP_FLAG_TEST_STALL) CP_INVALID("%s: unknown flag bits 0x%x", who, flags);
   if (wait_timeout_ms < 0) CP_INVALID("%s: wait_timeout_ms must be >= 0", who);
   if (!aligned(status, 4) || !aligned(q_first, 4)) CP_INVALID("%s: status and q_first must be 4-byte aligned", who);

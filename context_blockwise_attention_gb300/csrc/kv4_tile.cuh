@@ -173,7 +173,9 @@ __device__ __forceinline__ float query_operands(const Params& p, int64_t at, boo
         qf[QP - 1][j][h] = to_f16x2(a - back.x, b - back.y);
       }
     }
-  return p.scale_log2 * kv::pow2(e - 14);
+  // Kept above 0 and finite: else a masked product, -inf, or one of zeros would become NaN.  Where it is less than 2^-126 all
+  // scores, of products below 2^39, are as good as 0.
+  return fminf(fmaxf(p.scale_log2 * kv::pow2(e - 14), 0x1p-126f), 3.402823466e38f);
 }
 
 // Where a warp's copies are: the granules of its share, in order, into the stages of its ring.  TENSORS: K, or K and V.

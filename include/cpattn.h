@@ -484,7 +484,7 @@ cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, voi
  *                    rank's shard map, the same for all sequences; only differences matter, so a
  *                    caller whose shards start elsewhere for each sequence shifts q_first[b])
  *   q, o, lse        device [n_rows, hq, d] (in_dtype), [n_rows, hq, d] (o_dtype), fp32 [n_rows, hq]
- *   scale            softmax scale; 0 means 1/sqrt(d)
+ *   scale            softmax scale, at most 2e38; 0 means 1/sqrt(d)
  *   workspace        device memory, 16-byte aligned, of at least cp_kv_cache_attn_workspace bytes;
  *                    it need not be initialised and holds nothing afterwards.  Calls that may
  *                    overlap need one each.

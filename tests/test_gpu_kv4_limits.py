@@ -124,3 +124,40 @@ def test_large_scores_next_to_one_another(d, page, din, dout, wide, at_once):
             assert np.all(o[i, h] >= among.min(0) - tol) and np.all(o[i, h] <= among.max(0) + tol), (i, h, top)
             off = delta + 2.0 ** -20 * abs(top) + 2.0 ** -20
             assert top - off <= lse[i, h] <= top + off + np.log(len(s)), (i, h, top, lse[i, h])
+
+
+@pytest.mark.parametrize("scale,power", [(1e-12, None), (1e-38, -60), (1e-45, 0), (1e30, 20), (2e38, -140), (2e38, 100)])
+@pytest.mark.parametrize("wide,d", [(0, 64), (0, 128), (2500, 64), (2500, 128)])
+def test_softmax_scales_of_any_size(wide, d, scale, power):
+    """Rows whose factor from products to scores leaves fp32's range: of zeros (power None) or small queries with a tiny
+    scale, all of whose weights are equal, tokens that a row does not see among the others in a granule; and of a huge scale,
+    where keys are zeros, so that scores are zeros all the same."""
+    held, rows = 77, 4
+    pool = Pool(1, [held], 32, 1, d, 221)
+    rng = np.random.default_rng(222)
+    if scale < 1:
+        o4.cache_write(pool.rows[0], rng.standard_normal((held, 1, d)), [0, held], [0], pool.table)
+    else:
+        o4.cache_write(pool.rows[0], np.zeros((held, 1, d)), [0, held], [0], pool.table)
+    o4.cache_write(pool.rows[1], rng.standard_normal((held, 1, d)), [0, held], [0], pool.table)
+    q = torch.randn((rows, 2, d), generator=torch.Generator().manual_seed(223))
+    q = q * 2.0 ** power if power is not None else q * 0
+    table = _i32(np.concatenate([pool.table, np.full((1, wide), -1)], 1))
+    args = (pool.device(), _i32([0, rows]), _i32([held]), table)
+    kw = dict(q_first=_i32([held - rows - 9]), scale=scale)
+    o, lse = cpa.kv4_cache_attn(q.to(DEV), *args, **kw)
+    v = pool.tokens_of(0, held)[1][:, 0]
+    w = torch.zeros((pool.n_pages, 1, 32), device=DEV)
+    cpa.kv4_cache_weigh(q.to(DEV), lse, args[0], w, *args[1:], **kw)
+    gathered = pool.gather(0, held, w.double().cpu().numpy())[:, 0]
+    want = np.zeros(held)
+    for i in range(rows):
+        n = held - rows - 9 + i + 1
+        want[:n] += 2 / n
+        ref, mean = v[:n].mean(0), np.abs(v[:n]).mean(0)
+        for h in range(2):
+            assert np.all(np.abs(o[i, h].double().cpu().numpy() - ref) <= mean * (2.0 ** -21 + n * 2.0 ** -27 + 2.0 ** -20)
+                          + np.abs(ref) * 2.0 ** -24)
+            assert abs(float(lse[i, h]) - np.log(n)) <= 2.0 ** -20 + 2.0 ** -22 * np.log(n)
+    # exp(s - LSE) is off by 2^-22 LSE + 2^-20 of itself, eight of them are added
+    assert np.all(np.abs(gathered - want) <= want * (2.0 ** -22 * np.log(held) * 2 + 2.0 ** -20 + 10 * 2.0 ** -24))

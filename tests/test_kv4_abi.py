@@ -235,3 +235,13 @@ def test_oracle_eviction_keeps_the_heaviest():
         assert all(i == j for j, i in enumerate(got[:z]) if i < z)
         fills = [i for i in got[:z] if i >= z]
         assert fills == sorted(fills)
+
+
+def test_softmax_scales_beyond_base_2_are_refused():
+    lib = api.load_library()
+    for scale in (3e38, 2.4e38, float("inf")):
+        assert lib.cp_kv4_cache_attn(ctypes.byref(_attn(scale=scale)), None) == BAD
+        assert lib.cp_kv4_cache_weigh(ctypes.byref(_weigh(scale=scale)), None) == BAD
+    nothing = _rows(n_rows=0)
+    assert lib.cp_kv4_cache_attn(ctypes.byref(_attn(scale=2e38, rows=nothing)), None) == api.CP_OK
+    assert lib.cp_kv4_cache_weigh(ctypes.byref(_weigh(scale=2e38, rows=nothing)), None) == api.CP_OK
