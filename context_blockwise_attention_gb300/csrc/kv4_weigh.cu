@@ -221,7 +221,13 @@ __global__ void __launch_bounds__(WeighShape<D, NT, QP>::kWarps * 32, 1)
       const bool gives = fabsf(lse) < INFINITY;
       const float l2 = gives ? lse * kLog2e : INFINITY;
       if (live) lmin = min(lmin, lm);
-      const float f = query_operands<D, QP>(p, out * D, gives, tig, &qf[n * QP]);
+      const float f = query_operands<D, QP>(p, out * D, live, tig, &qf[n * QP]);  // loads that do not wait for the LSE
+      if (!gives) {
+#pragma unroll
+        for (int part = 0; part < QP; ++part)
+#pragma unroll
+          for (int j = 0; j < kMt; ++j) qf[n * QP + part][j][0] = qf[n * QP + part][j][1] = 0u;
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         fac[n][r] = __shfl_sync(kFull, f, (2 * tig + r) * 4);
