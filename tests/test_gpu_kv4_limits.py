@@ -161,3 +161,27 @@ def test_softmax_scales_of_any_size(wide, d, scale, power):
             assert abs(float(lse[i, h]) - np.log(n)) <= 2.0 ** -20 + 2.0 ** -22 * np.log(n)
     # exp(s - LSE) is off by 2^-22 LSE + 2^-20 of itself, eight of them are added
     assert np.all(np.abs(gathered - want) <= want * (2.0 ** -22 * np.log(held) * 2 + 2.0 ** -20 + 10 * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("n,wide", [(100, 0), (100, 1000), (0, 0), (-4, 600), (9999, 0)])
+def test_evict_to_the_largest_keep(n, wide):
+    """No limit: nothing is evicted, every slot is answered, nothing is written in front of `kept` or behind it, and the
+    workspace is as large as the page table needs.  (9999: more tokens than the table has pages for.)"""
+    keep, guard = 2 ** 31 - 1, 4096
+    pool = Pool(1, [100], 16, 1, 64, 251)
+    pool.fill([100], 252)
+    cache = pool.device()
+    table = _i32(np.concatenate([pool.table, np.full((1, wide), -1)], 1))
+    assert cpa.kv4_cache_evict_workspace(cache, 1, table.shape[1], keep) < 1 << 20
+    buf = torch.full((guard + keep + guard,), 77, dtype=torch.int32, device=DEV)
+    kept = buf[guard:guard + keep].view(1, keep)
+    w = torch.rand((pool.n_pages, 1, 16), device=DEV)
+    before = w.clone()
+    _, lens = cpa.kv4_cache_evict(cache, w, _i32([n]), table, keep, 10, kept=kept)
+    assert lens.item() == max(0, n) and torch.equal(w, before)
+    kv4._same_cache(cache, pool)
+    assert bool((buf[:guard] == 77).all()) and bool((buf[guard + keep:] == 77).all())
+    m = max(0, n)
+    assert torch.equal(kept[0, :m], torch.arange(m, dtype=torch.int32, device=DEV))
+    for part in kept[0, m:].split(1 << 28):
+        assert bool((part == -1).all())
