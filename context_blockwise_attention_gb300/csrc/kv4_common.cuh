@@ -17,10 +17,10 @@ constexpr int kRow = D / 2 + D / 16;  // bytes of a row: 72 or 36
 constexpr uint32_t kNaN = 255;         // scale byte of a group with a number that is not finite
 constexpr uint32_t kMostScale = 0xe2;  // 10240: 6 times the next one is beyond f16
 
-// x times a constant c given in two parts, hi = c rounded (or nearly) and lo = c - hi: off by 2^-47 before its one
-// rounding (Brisebarre and Muller's multiplication by a constant of twice the precision).  So x / 6 and x / scale, taken
-// by the reciprocals, are never rounded onto a tie of the next step but where they are one: numbers that are a divisor
-// times a tie are exact in fp32, and the next number of fp32 is at least 0.53 of a step of the quotient away.
+// x times a constant c given in two parts, hi near c and lo = c - hi: off by 2^-42 before its one rounding (Brisebarre and
+// Muller's multiplication by a constant of twice the precision).  So x / 6 and x / scale, taken by the reciprocals, are
+// never rounded onto a tie of the next step but where they are one: numbers that are a divisor times a tie are exact in fp32,
+// and the next number of fp32 is at least 0.53 of a step of the quotient away.
 __device__ __forceinline__ float times(float x, float hi, float lo) { return __fmaf_rn(x, hi, __fmul_rn(x, lo)); }
 
 // The byte of the scale nearest to amax / 6 (ties to even).
@@ -38,9 +38,11 @@ __device__ __forceinline__ float scale_of(uint32_t code) {
   return f;
 }
 
-// The reciprocal of a scale in two parts.
+// The reciprocal of a scale in two parts.  hi is the approximation less two steps of fp32, which is below the reciprocal, as
+// the approximation is off by one at most: with lo above 0 the sum of a minus zero's two products is a minus zero.
 __device__ __forceinline__ void reciprocal(float scale, float& hi, float& lo) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(scale));
+  hi = __uint_as_float(__float_as_uint(hi) - 2u);
   lo = __fmul_rn(__fmaf_rn(-scale, hi, 1.0f), hi);
 }
 

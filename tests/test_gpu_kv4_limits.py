@@ -185,3 +185,27 @@ def test_evict_to_the_largest_keep(n, wide):
     assert torch.equal(kept[0, :m], torch.arange(m, dtype=torch.int32, device=DEV))
     for part in kept[0, m:].split(1 << 28):
         assert bool((part == -1).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_zeros_keep_their_sign(d, dtype):
+    """Minus zero, and what is rounded to it, in a group of every scale."""
+    scales = o4.SCALE[1:o4.MOST + 1]
+    x = np.zeros((len(scales), 1, d))
+    x[:, 0, 0::16] = 6 * scales[:, None]
+    x[:, 0, 1::16] = -0.0
+    x[:, 0, 2::16] = -0.2 * scales[:, None]
+    x[:, 0, 3::16] = 0.2 * scales[:, None]
+    x[:, 0, 15::16] = -0.0
+    x = torch.from_numpy(x).to(dtype)
+    rows = x.shape[0]
+    pool = Pool(1, [rows], 16, 1, d, 231)
+    cache = pool.device()
+    args = (_i32([0, rows]), _i32([0]), _i32(pool.table))
+    cpa.kv4_cache_write(cache, x.to(DEV), (-x).to(DEV), *args)
+    o4.cache_write(pool.rows[0], x.double().numpy(), [0, rows], [0], pool.table)
+    o4.cache_write(pool.rows[1], -x.double().numpy(), [0, rows], [0], pool.table)
+    kv4._same_cache(cache, pool)
+    k, v = cpa.kv4_cache_read(cache, *args, rows, dtype=dtype)
+    assert torch.equal(torch.signbit(k).cpu(), torch.signbit(x)) and torch.equal(torch.signbit(v).cpu(), torch.signbit(-x))
