@@ -2,6 +2,8 @@
 other tests unless one is derived here.
 """
 
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -209,3 +211,24 @@ def test_zeros_keep_their_sign(d, dtype):
     kv4._same_cache(cache, pool)
     k, v = cpa.kv4_cache_read(cache, *args, rows, dtype=dtype)
     assert torch.equal(torch.signbit(k).cpu(), torch.signbit(x)) and torch.equal(torch.signbit(v).cpu(), torch.signbit(-x))
+
+
+def test_the_readme_s_serving_example_runs():
+    with open(os.path.join(helpers.ROOT, "README.md")) as f:
+        text = f.read()
+    code = text[text.index("# serving, one rank"):]
+    code = code[:code.index("```")]
+    n_pages, page_size, hkv, hq, d, cp, rank = 20, 16, 2, 4, 64, 1, 0
+    new, pages = [70, 3], 6
+    gen = torch.Generator().manual_seed(261)
+    names = dict(cpa=cpa, torch=torch, n_pages=n_pages, page_size=page_size, hkv=hkv, d=d, cp=cp, rank=rank,
+                 q=torch.randn((73, hq, d), generator=gen).to(BF16).to(DEV), k=torch.randn((73, hkv, d), generator=gen).to(BF16).to(DEV),
+                 v=torch.randn((73, hkv, d), generator=gen).to(BF16).to(DEV), row_start=_i32([0, 70, 73]), cached=_i32([0, 0]),
+                 kv_lens=_i32(new), q_positions=_i32([0, 0]), positions=_i32(list(range(70)) + list(range(3))),
+                 inv_freq=tuple(10000.0 ** (-i / 32) for i in range(32)), page_table=_i32(np.arange(2 * pages).reshape(2, pages)),
+                 all_ranks_o=[torch.zeros((73, hq, d), device=DEV)], all_ranks_lse=[torch.zeros((73, hq), device=DEV)],
+                 rows=_i32([0, 70, 73]), first=_i32([0, 0]), n_rows=73)
+    exec(code, names)
+    assert names["kp"].shape == names["vp"].shape == (73, hkv, d) and names["kept_lens"].tolist() == new
+    # the prefix is what was written, to e4m3's half step at a page's scale
+    assert bool(((names["kp"].float() - names["k"].float()).abs() <= names["k"].float().abs() * 2.0 ** -4 + 2.0 ** -7).all())
