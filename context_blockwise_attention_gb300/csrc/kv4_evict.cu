@@ -50,9 +50,8 @@ struct EvictParams {
   int32_t* new_tokens;
   int32_t* status;
   Sequence* seqs;      // workspace: [n_seqs]
-  int32_t* holes;      // [n_seqs, most_holes]
+  int32_t* holes;      // [n_seqs, keep]; none where keep is as much as the page table has room for
   uint32_t* store;     // [n_seqs, cluster] of room + 3 room / 32 words, where shared memory is too small; else null
-  int32_t most_holes;  // as many as keep, or as the page table has room for
   int32_t cluster, room;  // room: tokens of a block, a multiple of 32
   int32_t ordered;     // blocks of the second kernel that move recent tokens
   int32_t per_seq;     // blocks of a sequence that move fills
@@ -142,8 +141,9 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
   int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
   // A sequence that stays as it is.
   const auto leave = [&]() {
-    // in 64 bits: keep may be the largest number of 32
-    for (int64_t i = rank * kThreads + tid; i < p.keep; i += cluster * kThreads) kept[i] = i < n ? static_cast<int32_t>(i) : -1;
+    // unsigned: keep may be the largest signed number
+    for (uint32_t i = rank * kThreads + tid; i < static_cast<uint32_t>(p.keep); i += cluster * kThreads)
+      kept[i] = i < static_cast<uint32_t>(n) ? static_cast<int32_t>(i) : -1;
     if (rank == 0 && tid == 0) {
       p.new_tokens[b] = n;
       p.seqs[b] = Sequence{n, 0, 0, 0};
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
       fills += of[r];
     }
   }
-  int32_t* const list = p.holes + static_cast<int64_t>(b) * p.most_holes;
+  int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
   for (int w = warp; w < words; w += kWarps) {
     const int at = from + 32 * w + lane;
     const uint32_t s = stay[w];
@@ -366,7 +366,7 @@ __device__ __forceinline__ void move_in_order(const EvictParams& p, int b, int h
   const Sequence s = p.seqs[b];
   if (s.recent == 0) return;
   const int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
-  const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.most_holes;
+  const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
   const int fills = min(s.fills, s.recent), by = s.n - p.keep, mine = threadIdx.x / 10, e = threadIdx.x % 10;
   const bool weight = e == 9;
   uint8_t* const base = weight ? reinterpret_cast<uint8_t*>(p.weight)
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv4_move_kernel(const __grid_
   const int b = block / p.per_seq, first = (block % p.per_seq) * (kMoveThreads / 32) + (threadIdx.x >> 5);
   const int fills = __ldg(&p.seqs[b].fills);
   const int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
-  const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.most_holes;
+  const int32_t* const list = p.holes + static_cast<int64_t>(b) * p.keep;
   uint8_t* const base = lane < 18 ? static_cast<uint8_t*>(lane < 9 ? p.c.k : p.c.v) +
                                         (lane < 9 ? lane : lane - 9) * static_cast<int>(sizeof(Piece<D>))
                                   : reinterpret_cast<uint8_t*>(p.weight);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv4_move_kernel(const __grid_
 }
 
 struct Layout {
-  int cluster, room, per_seq, most_holes;
+  int cluster, room, per_seq;
   int64_t holes_off, store_off, bytes;
   int smem;
 };
@@ -469,8 +469,8 @@ Layout layout_of(const cp_kv4_evict_desc& d, int sms) {
   const int64_t per = kMoveThreads / 32, share = (8 * static_cast<int64_t>(sms) + seqs - 1) / seqs;
   r.per_seq = static_cast<int>((fills + per - 1) / per < share ? (fills + per - 1) / per : share);
   r.holes_off = (seqs * static_cast<int64_t>(sizeof(Sequence)) + 255) / 256 * 256;
-  r.most_holes = static_cast<int>(most < d.keep ? most : d.keep);
-  r.store_off = r.holes_off + (seqs * r.most_holes * 4 + 255) / 256 * 256;
+  const int64_t holes = most > d.keep ? d.keep : 0;
+  r.store_off = r.holes_off + (seqs * holes * 4 + 255) / 256 * 256;
   r.bytes = r.store_off + (fits ? 0 : seqs * r.cluster * words * 4);
   return r;
 }
@@ -498,7 +498,6 @@ cp_status launch_kv4_evict(const cp_kv4_evict_desc& d, int num_sms, cudaStream_t
   p.seqs = reinterpret_cast<Sequence*>(ws);
   p.holes = reinterpret_cast<int32_t*>(ws + l.holes_off);
   p.store = l.smem == 0 ? reinterpret_cast<uint32_t*>(ws + l.store_off) : nullptr;
-  p.most_holes = l.most_holes;
   p.cluster = l.cluster;
   p.room = l.room;
   p.ordered = d.recent > 0 ? d.n_seqs * d.cache.hkv * 2 : 0;
