@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) kv4_select_kernel(const __grid_const
   };
   ptx::wait_dependencies();
   ptx::launch_dependents();
-  const int held = __ldg(p.tokens + b);
+  const int held = p.tokens[b];  // no read-only load: the answer may take its place
   const int n = held < 0 ? 0 : held;
   const bool over = n > static_cast<int64_t>(p.max_pages) << p.page_log2;
   int32_t* const kept = p.kept + static_cast<int64_t>(b) * p.keep;
