@@ -232,3 +232,38 @@ def test_the_readme_s_serving_example_runs():
     assert names["kp"].shape == names["vp"].shape == (73, hkv, d) and names["kept_lens"].tolist() == new
     # the prefix is what was written, to e4m3's half step at a page's scale
     assert bool(((names["kp"].float() - names["k"].float()).abs() <= names["k"].float().abs() * 2.0 ** -4 + 2.0 ** -7).all())
+
+
+@pytest.mark.parametrize("d,page,hq,hkv,dtype", [(64, 16, 8, 2, BF16), (64, 128, 4, 4, F32), (128, 64, 10, 2, BF16), (128, 32, 6, 1, F32)])
+def test_weights_of_a_prompt(d, page, hq, hkv, dtype):
+    """A prompt's rows over its own tokens, a chunk of one over a longer cache, and single tokens in the same call."""
+    rows, held = [300, 1, 130, 1, 2], [300, 420, 500, 1, 33]
+    pool = Pool(5, held, page, hkv, d, 271)
+    pool.fill(held, 272)
+    q = torch.randn((sum(rows), hq, d), generator=torch.Generator().manual_seed(273)).to(dtype)
+    first = [m - n for n, m in zip(rows, held)]
+    kv4._check_weigh(pool, q, rows, held, first, PosMap(0, 1), [0, 419, 370, 0, 31], 0.75, 274)
+    kv4._check_attn(pool, pool.device(), q, rows, held, first, PosMap(0, 1), dtype)
+
+
+def test_many_heads():
+    """1030 KV heads: more items, units of work and moving blocks than the SMs hold at once."""
+    rows, held, hkv = [1, 3], [40, 7], 1030
+    pool = Pool(2, [40, 7], 16, hkv, 64, 281)
+    gen = torch.Generator().manual_seed(282)
+    x = [torch.randn((47, hkv, 64), generator=gen).to(BF16) for _ in range(2)]
+    cache = pool.device()
+    args = (_i32([0, 40, 47]), _i32([0, 0]), _i32(pool.table))
+    cpa.kv4_cache_write(cache, x[0].to(DEV), x[1].to(DEV), *args)
+    for w in range(2):
+        o4.cache_write(pool.rows[w], x[w].double().numpy(), [0, 40, 47], [0, 0], pool.table)
+    kv4._same_cache(cache, pool)
+    k, v = cpa.kv4_cache_read(cache, *args, 47, dtype=F32)
+    for w, got in enumerate((k, v)):
+        want = np.concatenate([pool.tokens_of(b, n)[w] for b, n in enumerate(held)])
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    q = torch.randn((4, 2 * hkv, 64), generator=gen).to(BF16)
+    kv4._check_attn(pool, cache, q, rows, held, [39, 4], PosMap(0, 1), F32)
+    kv4._check_weigh(pool, q, rows, held, [39, 4], PosMap(0, 1), None, 1.0, 283)
+    w = np.random.default_rng(284).uniform(0, 1, (pool.n_pages, hkv, 16)).astype(np.float32)
+    kv4._check_evict(pool, held, 20, 5, w)
