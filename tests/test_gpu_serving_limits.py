@@ -386,3 +386,39 @@ def test_two_tiles_of_rows_put_their_sums_aside(d, g, din, dout):
         for h in range(g):
             _check_row(o[i, h], float(lse[i, h]) - np.log(repeats), q[i, h].double().numpy(), k[:, 0], v[:, 0], scales,
                        d ** -0.5, dout, acc)
+
+
+@pytest.mark.parametrize("path,rows", [("one", 2), ("cluster", 2), ("split", 24)])
+@pytest.mark.parametrize("d,page,g,din,dout", [(64, 64, 4, BF16, BF16), (64, 16, 4, F32, F32), (128, 32, 8, BF16, F32),
+                                               (128, 64, 8, BF16, BF16)])
+def test_scores_up_to_the_largest(d, page, g, din, dout, path, rows):
+    """Rows whose largest score in base 2 is just below 2^23, where fp32 has steps of a half: that of all tokens with one key,
+    in pages of different value scales.  Equal keys have scores within two steps (one of the product, one where the value's
+    scale is added), so a row is a mean of these tokens' values with weights within a factor of 4."""
+    held = 300
+    pool = Pool(1, [held], page, 1, d, 301)
+    rng = np.random.default_rng(302)
+    key = rng.choice([-1.0, 1.0], (1, 1, d)) * rng.uniform(0.5, 1, (1, 1, d)) * 2.0 ** 7
+    kind = rng.choice([1.0, 1.0, -1.0, 0.0], held)
+    values = rng.standard_normal((held, 1, d)) * np.repeat(2.0 ** rng.integers(-3, 4, -(-held // page)), page)[:held, None, None]
+    for w, x in ((0, kind[:, None, None] * key), (1, values)):
+        oc.cache_write(pool.bytes[w], pool.scale[w], x.astype(np.float32).astype(np.float64), [0, held], [0], pool.table)
+    k, v = (t[:, 0] for t in pool.tokens_of(0, held))
+    x = np.sign(key) * rng.uniform(0.5, 1, (rows, g, d))
+    one = k[kind == 1.0][0]
+    target = 2.0 ** 23 * np.log(2) * rng.uniform(0.5, 0.99, (rows, g, 1)) * d ** 0.5
+    q = torch.from_numpy(x * (target / (x @ one)[..., None])).to(din)
+    table = _table(pool, path, q, rows)
+    o, lse = cpa.kv_cache_attn(q.to(DEV), pool.device(), _i32([0, rows]), _i32([held]), table, o_dtype=dout)
+    top = v[kind == 1.0]
+    for i in range(rows):
+        for h in range(g):
+            qd = q[i, h].double().numpy()
+            s = float(one @ qd) * d ** -0.5
+            assert 2.0 ** 21.9 < s / np.log(2) < 2.0 ** 23
+            got = o[i, h].double().cpu().numpy()
+            # the mean with weights up to 4 times too large above it and too small below
+            above, below = np.maximum(top, 0).mean(0), np.minimum(top, 0).mean(0)
+            tol = np.abs(top).mean(0) * 2.0 ** -6
+            assert np.all(got <= 4 * above + below / 4 + tol) and np.all(got >= 4 * below + above / 4 - tol), (i, h, s)
+            assert abs(float(lse[i, h]) - s) <= 2.0 ** -19 * s + np.log(held)
