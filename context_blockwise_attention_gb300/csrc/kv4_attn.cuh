@@ -26,9 +26,9 @@
 // Bound.  Each cached byte is used for twice as many products as in the 8-bit cache, and conversions and scales are half
 // of some 580 instructions for a granule and tile of rows: the SMs issue at 57 % of their rate and the ALU pipe is busy for
 // 49 % of the time, beside memory at two thirds of its rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8
-// heads, D = 128, bf16: 69 us for 328 MB, 4.7 TB/s (the 8-bit cache: 86): copies begin at 4 us, the first data are there
-// at 8, the warps end at 53 to 64 and the second kernel at 68; 6 TB/s between.  8 x 90000-131072, 64/8, D = 64, fp32
-// partials: 114 us for 513 MB, 4.5 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 97 us; one token over 1000: 8 us.
+// heads, D = 128, bf16: 70 us for 328 MB, 4.7 TB/s (the 8-bit cache: 86): copies begin at 4 us, the first data are there
+// at 8, the warps end at 53 to 65 and the second kernel at 69; 6 TB/s between.  8 x 90000-131072, 64/8, D = 64, fp32
+// partials: 115 us for 513 MB, 4.4 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 97.5 us; one token over 1000: 8 us.
 // Slower: K and V in slots of their own with 16 warps (73, 118 and 122 us: they spill or hold less in flight).
 #pragma once
 

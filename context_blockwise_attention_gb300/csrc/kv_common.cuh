@@ -1,5 +1,5 @@
-// What the 8-bit cache kernels share: the checked view of a batch's rows and pages, e4m3
-// conversions, and the power-of-two scales.
+// What the kernels of the paged caches share: the checked view of a batch's rows and pages and powers of two;
+// and what the 8-bit ones do: e4m3 conversions and the power-of-two scales.
 #pragma once
 
 #include <cuda_bf16.h>

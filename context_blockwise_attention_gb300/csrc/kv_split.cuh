@@ -216,7 +216,8 @@ struct Plan {
 };
 
 // Sums the partials of the items that several workers shared, and answers the rows that see nothing.  Launched behind
-// the attention kernel of `workers` workers, as its programmatic dependent.  RT is 8 or 16.
+// the attention kernel of `workers` workers, as its programmatic dependent.  RT is 8, 16 or, at
+// D = 128, 24.
 template <int D, int RT>
 cp_status launch_sum(const Params& p, int64_t workers, int64_t items, int num_sms, cudaStream_t s);
 

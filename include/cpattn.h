@@ -646,9 +646,10 @@ cp_status cp_kv4_cache_weigh(const cp_kv4_weigh_desc* desc, cudaStream_t stream)
 /*
  * cp_kv4_cache_evict -- shortens every sequence of more than `keep` tokens to `keep`: its last `recent` tokens stay, and of
  * the others the z = keep - recent whose weight, summed over the KV heads, is largest (of equal ones the earlier; NaN is
- * below everything).  Rows of K and V and their weights move: of the slots below z those whose token stays are as they
- * were, the others receive, in order, the tokens that stay from slot z on; the recent tokens follow from slot z on in
- * their order.  What slots from `keep` on hold then belongs to no token.
+ * below everything; the sum is right to (hkv 2^-24)^2 of itself, then rounded to fp32).  Rows of K and V and their weights
+ * move: of the slots below z those whose token stays are as they were, the others receive, in order, the tokens that stay
+ * from slot z on; the recent tokens follow from slot z on in their order.  What slots from `keep` on hold then belongs to
+ * no token.
  *   tokens      device int32 [n_seqs]: tokens of each sequence
  *   page_table  device int32 [n_seqs, max_pages]; no page may belong to two sequences or stand twice in a table
  *   kept        device int32 [n_seqs, keep], written: the slot that each slot's token had, -1 behind the sequence's end
@@ -656,8 +657,8 @@ cp_status cp_kv4_cache_weigh(const cp_kv4_weigh_desc* desc, cudaStream_t stream)
  *   workspace   device memory, 16-byte aligned, of at least cp_kv4_cache_evict_workspace bytes; it need not be initialised
  *               and holds nothing afterwards.  Calls that may overlap need one each.
  *   status      device int32 or NULL: CP_ERR_INVALID_ARG | (site << 8) where a sequence has a negative count (taken for 0),
- *               more tokens than its table has pages for, or a page outside [0, n_pages).  The latter two are left as they
- *               are, with `kept` naming their first slots.
+ *               more tokens than its table has pages for, or, where it is too long, a page outside [0, n_pages).  The latter
+ *               two are left as they are, with `kept` naming their first slots.
  * Since keys are stored rotated, where a token stands does not matter to later rows that see all of the cache.  Causal rows
  * are right as long as every evicted sequence's q_first[b] is lowered by kv_pos.stride for each token that it lost and no
  * row stands before a token that was not among the recent ones.
