@@ -28,7 +28,7 @@
 // 49 % of the time, beside memory at two thirds of its rate.  Measured (GB300, in a graph): 64 x 256-8192 tokens, 32/8
 // heads, D = 128, bf16: 70 us for 328 MB, 4.7 TB/s (the 8-bit cache: 86): copies begin at 4 us, the first data are there
 // at 8, the warps end at 53 to 65 and the second kernel at 69; 6 TB/s between.  8 x 90000-131072, 64/8, D = 64, fp32
-// partials: 115 us for 513 MB, 4.4 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 97.5 us; one token over 1000: 8 us.
+// partials: 115 us for 513 MB, 4.4 TB/s; 16 x 2-6 rows over 1000-20000, 32/8, D = 128: 98 us; one token over 1000: 8 us.
 // Slower: K and V in slots of their own with 16 warps (73, 118 and 122 us: they spill or hold less in flight).
 #pragma once
 
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          const float low = fabsf(x) >= kLarge ? fmaf(fabsf(x), -0x1p-22f, x) : x;
+          // an infinite score makes m infinite and its row NaN
+          const float low = fabsf(x) >= kLarge && x < INFINITY ? fmaf(fabsf(x), -0x1p-22f, x) : x;
           const float now = x > m[n][r] + kSlack ? fmaxf(floorf(low), m[n][r]) : m[n][r];
           c[r] = now > m[n][r] ? ex2(m[n][r] - now) : 1.0f;
           m[n][r] = now;
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
         sum += __shfl_xor_sync(kFull, sum, 4);
         sum += __shfl_xor_sync(kFull, sum, 8);
         sum += __shfl_xor_sync(kFull, sum, 16);
+        if (m[n][r] == INFINITY) sum = __int_as_float(0x7fffffff);  // a finite product that is no finite score leaves 0
         const int local = n * 8 + 2 * tig + r;
         const int rho = row_q + local;
         if (rho >= n_rows) continue;

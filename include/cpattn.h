@@ -578,8 +578,8 @@ cp_status cp_kv4_cache_read(const cp_kv4_cache* cache, const cp_kv_rows* rows, v
  * Precision: sums and softmax statistics are fp32.  Queries are taken exactly (bf16) or to 22 bits (fp32), but no finer
  * than 2^-38 of their row's largest element.  Weights are taken to 11 bits for a bf16 output and to 22 for an fp32 one, but
  * no finer than 2^-37 of the row's largest.
- * Scores may be as large as fp32 allows (log2 e times them below 3.4e38); from 7e5 on those that differ by less than some
- * fp32 steps, 2^-20 of them, may count as equal.
+ * Scores may be as large as fp32 allows (log2 e times them below 3.4e38; a row with one above it is NaN); from 7e5 on those
+ * that differ by less than some fp32 steps, 2^-20 of them, may count as equal.
  */
 typedef struct {
   cp_kv4_cache cache;

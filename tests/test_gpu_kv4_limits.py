@@ -267,3 +267,36 @@ def test_many_heads():
     kv4._check_weigh(pool, q, rows, held, [39, 4], PosMap(0, 1), None, 1.0, 283)
     w = np.random.default_rng(284).uniform(0, 1, (pool.n_pages, hkv, 16)).astype(np.float32)
     kv4._check_evict(pool, held, 20, 5, w)
+
+
+@pytest.mark.parametrize("wide,rows", [(0, 2), (600, 2), (2500, 2), (2500, 9)])
+@pytest.mark.parametrize("d,page,din,dout", [(64, 16, BF16, BF16), (128, 64, F32, F32), (128, 32, BF16, F32)])
+def test_infinite_scores_make_a_row_nan(d, page, din, dout, wide, rows):
+    """By an infinity in a query that meets no zero and one sign of keys, and by finite products beyond fp32.  A bf16 query of
+    minus infinity gives its tokens no weight; an fp32 one is NaN too, as its low part, -inf - -inf, is.  Other rows are as
+    they were, to the bit."""
+    held = 333
+    pool = Pool(1, [held], page, 1, d, 291)
+    rng = np.random.default_rng(292)
+    k = rng.uniform(1, 2, (held, 1, d))
+    o4.cache_write(pool.rows[0], k, [0, held], [0], pool.table)
+    o4.cache_write(pool.rows[1], rng.standard_normal((held, 1, d)), [0, held], [0], pool.table)
+    q = torch.randn((rows, 4, d), generator=torch.Generator().manual_seed(293)).to(din)
+    table = _i32(np.concatenate([pool.table, np.full((1, wide), -1)], 1))
+    args = (pool.device(), _i32([0, rows]), _i32([held]), table)
+    want, lwant = cpa.kv4_cache_attn(q.to(DEV), *args, o_dtype=dout)
+    assert bool(want.isfinite().all())
+    q[0, 1, 7] = float("inf")
+    q[1, 2] = 3e38  # a sum of d products of 3e38 or more
+    q[1, 0, 3] = -float("inf")
+    o, lse = cpa.kv4_cache_attn(q.to(DEV), *args, o_dtype=dout)
+    left = torch.ones((rows, 4), dtype=torch.bool, device=DEV)
+    for i, h in ((0, 1), (1, 2)):
+        left[i, h] = False
+        assert bool(o[i, h].isnan().all()) and bool(lse[i, h].isnan())
+    left[1, 0] = False
+    if din == BF16:
+        assert bool((o[1, 0] == 0).all()) and lse[1, 0].item() == -float("inf")
+    else:
+        assert bool(o[1, 0].isnan().all()) and bool(lse[1, 0].isnan())
+    assert torch.equal(o[left], want[left]) and torch.equal(lse[left], lwant[left])
