@@ -21,7 +21,9 @@
 // an fp32 row is split into a high and a low part, 22 bits.  Weights are held relative to a whole number m_i that is at
 // most kSlack below the row's largest score, times 2^12: one f16 part for a bf16 output (off by 2^-11 at most, against the
 // output's 2^-8), two for an fp32 one.  f16 ends at 2^-24, so a weight is off by 2^-37 of the row's largest besides.
-// Sums, maxima and the accumulators are fp32.
+// Sums, maxima and the accumulators are fp32; l is a sum of granules' sums, since single weights vanish next to a heavy token's
+// (8 x 90000-131072 tokens, 64/8, D = 64, over 16 draws: 4.1e-7 to 1.4e-6 relative to the exact outputs key by key, 3.8e-7 to
+// 4.2e-7 so, in 0.5 us more).
 //
 // Bound.  Each cached byte is used for twice as many products as in the 8-bit cache, and conversions and scales are half
 // of some 580 instructions for a granule and tile of rows: the SMs issue at 57 % of their rate and the ALU pipe is busy for
@@ -67,7 +69,7 @@ struct Shape4 {
   static constexpr int kRows = NT * 8;  // RT
   // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: the accumulators are added
   // to others every kFlush granules, in registers where there are some left (kHold), else in the workspace.  Every 2 or 4
-  // with kHold, on the 8 long sequences above: 4.2e-7 to 7.0e-7 or 5.5e-7 to 7.5e-7 relative to the exact outputs, and
+  // with kHold, on the 8 long sequences above, l as it was: 4.2e-7 to 7.0e-7 or 5.5e-7 to 7.5e-7 relative to the exact outputs, and
   // 0.3 us between them.
   static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
   static constexpr int kFlush = PP == 1 ? 64 : kHold ? 2 : D == 128 ? 16 : 8;
@@ -446,7 +448,8 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
       // two rows at a time
       const uint64_t ref = ptx::f2_pack(m[n][0] == -INFINITY ? 0.0f : -m[n][0], m[n][1] == -INFINITY ? 0.0f : -m[n][1]);
       const uint64_t both = ptx::f2_pack(fac[n][0], fac[n][1]), unit = ptx::f2_pack(kPUnit, kPUnit);
-      uint64_t sum = ptx::f2_pack(l[n][0], l[n][1]);
+      // the granule's weights are summed on their own: next to a large l most of them would be less than half a step
+      uint64_t sum = 0;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
           float w[2];
           ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[n][i][2 * u], s[n][i][2 * u + 1]), both, ref), w[0], w[1]);
           const uint64_t w2 = ptx::f2_pack(ex2(at_most(w[0], kMost)), ex2(at_most(w[1], kMost))), x2 = ptx::f2_mul(w2, unit);
-          sum = ptx::f2_add(sum, w2);
+          sum = i == 0 && u == 0 ? w2 : ptx::f2_add(sum, w2);
           float a, b;
           ptx::f2_unpack(x2, a, b);
           const uint32_t h = to_f16x2(a, b);
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(Shape4<D, NT, QP, PP>::kWarps * 32, 1)
             pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(a, b));
           }
         }
-      ptx::f2_unpack(sum, l[n][0], l[n][1]);
+      ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(l[n][0], l[n][1]), sum), l[n][0], l[n][1]);
     }
     // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll
