@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float ref[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+      float sum[2];  // of the granule: next to a large l most weights would be less than half a step
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float w = ex2(fmaf(s[n][i][2 * u + r], f2[n][r][i], -ref[r]));
-            l[n][r] += w;
+            sum[r] = i == 0 && u == 0 ? w : sum[r] + w;
             pv[r] = w * vf[i];
           }
           const uint32_t h = to_f16x2(pv[0], pv[1]);
@@ -686,6 +687,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, PP>::kWarps * 32, 1)
             pb[n][1][i][u] = ptx::transpose8x8(to_f16x2(pv[0] - back.x, pv[1] - back.y));
           }
         }
+      l[n][0] += sum[0];
+      l[n][1] += sum[1];
     }
     // O^T += V^T P^T: rows gid and gid + 8 of tile w are columns kCols gid + 2 w and + 1 of O
 #pragma unroll

@@ -422,3 +422,30 @@ def test_scores_up_to_the_largest(d, page, g, din, dout, path, rows):
             tol = np.abs(top).mean(0) * 2.0 ** -6
             assert np.all(got <= 4 * above + below / 4 + tol) and np.all(got >= 4 * below + above / 4 - tol), (i, h, s)
             assert abs(float(lse[i, h]) - s) <= 2.0 ** -19 * s + np.log(held)
+
+
+@pytest.mark.parametrize("d,din,dout", [(64, BF16, F32), (64, BF16, BF16), (128, BF16, F32), (128, F32, F32)])
+def test_light_tokens_count_beside_a_heavy_one(d, din, dout):
+    """One token of weight 1 and two million of 2^-24.2, less than half a step of fp32 next to it.  The heavy key is zero, so its
+    score is exact.  A warp adds a granule's weights up before they join its sum, which is off by half a step for each of its
+    granules then, and not by a weight for each of its keys, of which a lane has 4 or 8 in a granule: (G + 8) 2^-24, and 2^-20
+    for the rest."""
+    page, hkv, n = 128, 8, 2000000 // 128 * 128
+    cache = cpa.kv_cache_empty(2, page, hkv, d)
+    k = torch.zeros((2 * page, hkv, d))
+    k[1:, :, 0] = -6.0
+    v = torch.ones((2 * page, hkv, d))
+    cpa.kv_cache_write(cache, k.to(DEV), v.to(DEV), _i32([0, 2 * page]), _i32([0]), _i32([[0, 1]]))
+    q = torch.zeros((1, hkv, d))
+    q[:, :, 0] = 1.0
+    scale = float(np.float32(24.2 * np.log(2) / 6))
+    table = torch.ones((1, n // page), dtype=torch.int32, device=DEV)
+    table[0, 0] = 0
+    o, lse = cpa.kv_cache_attn(q.to(din).to(DEV), cache, _i32([0, 1]), _i32([n]), table, scale=scale, o_dtype=dout)
+    light = np.exp(-6 * scale)
+    share = hkv * (n * d // 4096 + 1) / (12 * torch.cuda.get_device_properties(DEV).multi_processor_count)
+    keys = 512 // d  # of a lane in a granule
+    assert light < 2.0 ** -24 and (share - 1) * (keys * light - 2.0 ** -24) / (1 + n * light) > 2.0 ** -20  # what would be lost
+    want = np.log1p((n - 1) * light)
+    assert bool(((lse.double() - want).abs() <= (share + 8) * 2.0 ** -24 + 2.0 ** -20).all()), (lse - want).abs().max()
+    assert bool(((o.double() - 1).abs() <= 2.0 ** -8).all())
