@@ -49,8 +49,8 @@ constexpr float kSlack = 3.0f;     // largest s - m
 // m goes by scores that are rounded to fp32 and weights by fma(product, factor, -m), which is not: they differ by 2^-4 at most
 // where |m| is below kLarge, but by 8 from 2^27 on.  So from kLarge on m is set 2 to 4 fp32 steps below the score, the exponent
 // stays at or above 0 for the largest, and ends at kMost, below which f16 holds the weight: scores of a large magnitude that
-// are some steps of fp32 apart, which is less than they are off, count as equal.  (Ending the exponents costs 1 % of the batch
-// below and 0 to 1 % of the other calls; a path of their own for such rows, with rounded scores, 2 to 4 %.)
+// are some steps of fp32 apart, which is less than they are off, count as equal.  (Ending the exponents costs 1 to 1.6 % of the
+// batch and the 16 sequences above and 0 to 1 % of other calls; a path of their own for such rows, with rounded scores, 2 to 4 %.)
 constexpr float kLarge = 1048576.0f;
 constexpr float kMost = 3.9f;
 __device__ __forceinline__ float at_most(float x, float most) {  // NaN stays
@@ -69,8 +69,8 @@ struct Shape4 {
   static constexpr int kRows = NT * 8;  // RT
   // The tensor cores' fp32 sums are truncated, an error that grows with the length of a sum: the accumulators are added
   // to others every kFlush granules, in registers where there are some left (kHold), else in the workspace.  Every 2 or 4
-  // with kHold, on the 8 long sequences above, l as it was: 4.2e-7 to 7.0e-7 or 5.5e-7 to 7.5e-7 relative to the exact outputs, and
-  // 0.3 us between them.
+  // with kHold, on the 8 long sequences above, when l was a sum of keys: 4.2e-7 to 7.0e-7 or 5.5e-7 to 7.5e-7 relative to
+  // the exact outputs, and 0.3 us between them.
   static constexpr bool kHold = PP == 2 && D == 64 && NT == 1;
   static constexpr int kFlush = PP == 1 ? 64 : kHold ? 2 : D == 128 ? 16 : 8;
   static constexpr int kKeys = Granule<D>::kKeys;

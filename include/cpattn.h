@@ -495,8 +495,8 @@ cp_status cp_kv_cache_read(const cp_kv_cache* cache, const cp_kv_rows* rows, voi
  * Precision: sums and softmax statistics are fp32.  Queries are taken exactly (bf16) or to 22 bits (fp32), but no finer
  * than 2^-38 of their row's largest element.  Weights are taken to 11 bits for a bf16 output and to 22 for an fp32 one;
  * a token's weight times its page's V scale no finer than 2^-39 of the row's largest such product.  A weight below 2^-45
- * of the row's largest may count as zero.  Scores (scale q . k) may be up to 5e6 in magnitude: beyond, where fp32 has no halves,
- * a row may come out infinite or NaN (cp_kv4_cache_attn has no such limit).
+ * of the row's largest may count as zero.  Scores (scale q . k) may be up to 5e6 in magnitude: beyond, where fp32 has no
+ * halves, a row may come out infinite or NaN (cp_kv4_cache_attn has no such limit).
  * Rows of a sequence beyond a few dozen (long prompts) are answered, but cp_kv_cache_read followed
  * by cp_partial_attn is the faster way for them.
  * max_pages * page_size is at most 2e9, n_rows * hq below 2^31.
@@ -613,7 +613,8 @@ cp_status cp_kv4_cache_attn_workspace(const cp_kv4_attn_desc* desc, int64_t* byt
  *   weight   device fp32 [n_pages, hkv, page_size]: laid out as the cache, 16-byte aligned
  *   q, lse   device [n_rows, hq, d] (in_dtype), 16-byte aligned; fp32 [n_rows, hq]: the rows' final LSE, merged over the
  *            ranks, so that the weights of all ranks' tokens add up to 1 for each row and query head.  A row and head
- *            whose lse is not finite gives nothing, whatever its query holds.
+ *            whose lse is not finite gives nothing, whatever its query holds.  Scores and lse are fp32: a weight is off by
+ *            up to 2^-22 (|score| + |lse|) of itself besides the score's own error.
  *   known    device int32 [n_seqs] or NULL: how many of the tokens have gathered weight already; the memory of the others
  *            need not be initialised.  NULL: all.  With decay 0 no old weight is looked at.
  *   decay    in [0, 1]
